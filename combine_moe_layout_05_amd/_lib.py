@@ -29,6 +29,11 @@ MOE_F32 = 0
 MOE_BF16 = 1
 MOE_WEIGHTS_ROW_MAJOR = 0
 MOE_WEIGHTS_TILED = 1
+MOE_GEMM_ZERO_TAIL = 1
+MOE_GEMM_ACCUMULATE = 2
+MOE_MAX_GEMM_WIDTH = 1 << 22
+MOE_ACT_SILU = 0
+MOE_ACT_GELU_TANH = 1
 
 MOE_MAX_EXPERTS = 1024
 MOE_MAX_TOPK = 16
@@ -78,6 +83,20 @@ SIGNATURES = {
     "moe_grouped_gemm": (_int, [_vp, _vp, _vp, _i32, _i64, _i32, _i32, _vp, _i32, _i32, _vp]),
     "moe_tiled_weights_bytes": (_i64, [_i32, _i32, _i32]),
     "moe_tile_expert_weights": (_int, [_vp, _i32, _i32, _i32, _vp, _vp]),
+    "moe_gated_grouped_gemm": (_int, [_vp, _vp, _vp, _i32, _i64, _i32, _i32, _i32, _vp, _vp,
+                                      _i32, _vp]),
+    "moe_grouped_gemm_forward": (_int, [_vp, _vp, _vp, _i32, _i64, _i32, _i32, _vp, _i32, _vp]),
+    "moe_grouped_gemm_backward_input": (_int, [_vp, _vp, _vp, _i32, _i64, _i32, _i32, _vp, _i32,
+                                               _vp]),
+    "moe_gated_grouped_gemm_backward": (_int, [_vp, _vp, _vp, _vp, _i32, _i64, _i32, _i32, _i32,
+                                               _vp, _i32, _vp]),
+    "moe_grouped_gemm_backward_weight": (_int, [_vp, _vp, _vp, _i32, _i64, _i32, _i32, _i32, _vp,
+                                                _i32, _vp]),
+    "moe_mxfp4_weights_bytes": (_i64, [_i32, _i32, _i32]),
+    "moe_pack_mxfp4_weights": (_int, [_vp, _vp, _i32, _i32, _i32, _vp, _vp]),
+    "moe_grouped_gemm_mxfp4": (_int, [_vp, _vp, _vp, _i32, _i64, _i32, _i32, _vp, _i32, _vp]),
+    "moe_gated_grouped_gemm_mxfp4": (_int, [_vp, _vp, _vp, _i32, _i64, _i32, _i32, _i32, _vp,
+                                            _i32, _vp]),
     "moe_set_tuning": (_int, [_vp, C.POINTER(MoeTuning)]),
     "moe_get_tuning": (_int, [_vp, C.POINTER(MoeTuning)]),
     "moe_ceil_div": (_i64, [_i64, _i64]),

@@ -23,6 +23,9 @@ from typing import Optional
 
 import torch
 
+from .experts import (_activation, _offsets, _rows, _weights, gated_grouped_gemm,
+                      gated_grouped_gemm_backward, grouped_gemm_backward_input,
+                      grouped_gemm_backward_weight, grouped_gemm_forward)
 from .moe import MoeDispatcher
 
 
@@ -115,3 +118,64 @@ class MoeTokenDispatcher:
             raise RuntimeError("combine() needs a preceding dispatch() on this layer")
         return _Combine.apply(y_e.contiguous(), topk_scores.contiguous(), self._row_map,
                               self._total, self.disp, self._ntpr, self._generation)
+
+
+class _ExpertFfn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, w_gate_up, w_down, offsets, activation: str):
+        # The layout's offsets are a persistent buffer the next layout
+        # rewrites: the backward keeps its own copy.
+        offsets = offsets.clone()
+        pre = torch.empty((x.shape[0], w_gate_up.shape[1]), dtype=torch.float32,
+                          device=x.device)
+        h = gated_grouped_gemm(x, w_gate_up, offsets, activation=activation, pre=pre)
+        ctx.save_for_backward(x, w_gate_up, w_down, offsets, pre, h)
+        ctx.activation = activation
+        return grouped_gemm_forward(h, w_down, offsets)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad_y):
+        x, w_gate_up, w_down, offsets, pre, h = ctx.saved_tensors
+        need_x, need_gate_up, need_down = ctx.needs_input_grad[:3]
+        g = grad_y.contiguous()
+        grad_x = grad_gate_up = grad_down = None
+        if need_down:
+            grad_down = grouped_gemm_backward_weight(g, h, offsets)
+        if need_x or need_gate_up:
+            grad_pre = gated_grouped_gemm_backward(g, w_down, pre, offsets,
+                                                   activation=ctx.activation)
+            if need_gate_up:
+                grad_gate_up = grouped_gemm_backward_weight(grad_pre, x, offsets)
+            if need_x:
+                grad_x = grouped_gemm_backward_input(grad_pre, w_gate_up, offsets)
+        return grad_x, grad_gate_up, grad_down, None, None
+
+
+def expert_ffn(x_expert: torch.Tensor, w_gate_up: torch.Tensor, w_down: torch.Tensor,
+               offsets: torch.Tensor, activation: str = "silu") -> torch.Tensor:
+    """Differentiable gated feed-forward block of the experts, between
+    dispatch and combine: for the rows r of expert e,
+        y[r] = (act(x[r] @ Wg[e].T) * (x[r] @ Wu[e].T)) @ Wd[e].T
+
+    x_expert bf16 [R, k_in]; w_gate_up bf16 [E, 2 n_hidden, k_in] (the gate's
+    rows first); w_down bf16 [E, n_out, n_hidden]; offsets int32 [E+1] (e.g.
+    Layout.offsets); y bf16 [R, n_out], its rows from offsets[E] on zero.
+    Gradients reach x_expert and both weights (bf16, in one rounding of an fp32
+    sum). Between the kernels h = act(g) * u and, in the backward, the gradients
+    of g and u are rounded to bf16: they are operands of matrix-core products.
+    g and u themselves are kept in fp32."""
+    dev = x_expert.device
+    _activation(activation)
+    E, n2, k_in = _weights("w_gate_up", w_gate_up, dev)
+    E2, _, hidden = _weights("w_down", w_down, dev)
+    if E2 != E or 2 * hidden != n2:
+        raise ValueError("shapes: w_gate_up [E, 2 n_hidden, k_in], w_down [E, n_out, n_hidden]; "
+                         f"got {tuple(w_gate_up.shape)}, {tuple(w_down.shape)}")
+    _rows("x_expert", x_expert, k_in, dev)
+    _offsets(offsets, E, dev)
+    if torch.is_grad_enabled() and (x_expert.requires_grad or w_gate_up.requires_grad
+                                    or w_down.requires_grad):
+        return _ExpertFfn.apply(x_expert, w_gate_up, w_down, offsets, activation)
+    h = gated_grouped_gemm(x_expert, w_gate_up, offsets, activation=activation)
+    return grouped_gemm_forward(h, w_down, offsets)

@@ -1,0 +1,236 @@
+// C ABI entry points of the expert feed-forward block (include/moe.h): host
+// argument checks and the choice of kernel. No entry point touches the device
+// before every check has passed.
+#include <hip/hip_runtime.h>
+
+#include <climits>
+#include <cstdint>
+
+#include "expert_kernels.h"
+#include "moe.h"
+
+namespace {
+
+bool misaligned(const void* p, uintptr_t a) {
+    return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0;
+}
+
+bool width_ok(int32_t n, int32_t multiple) {
+    return n >= 8 && n <= MOE_MAX_GEMM_WIDTH && n % multiple == 0;
+}
+
+bool experts_ok(int32_t E) { return E >= 1 && E <= MOE_MAX_EXPERTS; }
+
+bool activation_ok(int32_t a) { return a == MOE_ACT_SILU || a == MOE_ACT_GELU_TANH; }
+
+// bf16 buffers every call of the family needs, with its offsets.
+bool buffers_ok(const void* a, const void* b, const void* c, const int32_t* offsets) {
+    return a && b && c && offsets && !misaligned(a, 16) && !misaligned(b, 16) &&
+           !misaligned(c, 16) && !misaligned(offsets, 4);
+}
+
+int status_of(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_ERR_HIP; }
+
+// Few rows per expert: the form that streams the weights (16-row tiles).
+bool stream_bf16(int64_t max_rows, int32_t E) {
+    return max_rows <= 16 || max_rows <= int64_t(8) * E;
+}
+
+int run_gemm(moe::ExpertOp op, const void* rows, const void* w, const int32_t* offsets, int32_t E,
+             int64_t max_rows, int32_t red, int32_t feats, int32_t activation, void* out,
+             float* pre, int32_t flags, void* stream) {
+    const bool forward = op == moe::ExpertOp::kPlain || op == moe::ExpertOp::kGated;
+    if (forward && stream_bf16(max_rows, E)) {
+        moe::ExpertStreamArgs a;
+        a.mxfp4 = false;
+        a.gated = op == moe::ExpertOp::kGated;
+        a.rows = rows;
+        a.w = w;
+        a.offsets = offsets;
+        a.E = E;
+        a.max_rows = max_rows;
+        a.red = red;
+        a.feats = feats;
+        a.activation = activation;
+        a.out = out;
+        a.pre = pre;
+        a.zero_tail = (flags & MOE_GEMM_ZERO_TAIL) != 0;
+        if (moe::expert_stream_grid(a) > INT32_MAX) return MOE_ERR_INVALID_ARG;
+        return status_of(moe::launch_expert_stream(a, static_cast<hipStream_t>(stream)));
+    }
+    moe::ExpertGemmArgs a;
+    a.op = op;
+    a.rows = rows;
+    a.w = w;
+    a.offsets = offsets;
+    a.E = E;
+    a.max_rows = max_rows;
+    a.red = red;
+    a.feats = feats;
+    a.activation = activation;
+    a.out = out;
+    a.pre = pre;
+    a.zero_tail = (flags & MOE_GEMM_ZERO_TAIL) != 0;
+    if (moe::expert_gemm_grid(a) > INT32_MAX) return MOE_ERR_INVALID_ARG;
+    return status_of(moe::launch_expert_gemm(a, static_cast<hipStream_t>(stream)));
+}
+
+int run_mxfp4(bool gated, const void* rows, const void* packed, const int32_t* offsets, int32_t E,
+              int64_t max_rows, int32_t red, int32_t feats, int32_t activation, void* out,
+              int32_t flags, void* stream) {
+    if (moe_mxfp4_weights_bytes(E, gated ? 2 * feats : feats, red) < 0) return MOE_ERR_INVALID_ARG;
+    if (max_rows < 0 || max_rows > INT32_MAX || (flags & ~MOE_GEMM_ZERO_TAIL))
+        return MOE_ERR_INVALID_ARG;
+    if (max_rows == 0) return MOE_OK;
+    if (!buffers_ok(rows, packed, out, offsets)) return MOE_ERR_INVALID_ARG;
+    moe::ExpertStreamArgs a;
+    a.mxfp4 = true;
+    a.gated = gated;
+    a.rows = rows;
+    a.w = packed;
+    a.offsets = offsets;
+    a.E = E;
+    a.max_rows = max_rows;
+    a.red = red;
+    a.feats = feats;
+    a.activation = activation;
+    a.out = out;
+    a.pre = nullptr;
+    a.zero_tail = (flags & MOE_GEMM_ZERO_TAIL) != 0;
+    if (moe::expert_stream_grid(a) > INT32_MAX) return MOE_ERR_INVALID_ARG;
+    return status_of(moe::launch_expert_stream(a, static_cast<hipStream_t>(stream)));
+}
+
+}  // namespace
+
+extern "C" {
+
+int moe_gated_grouped_gemm(const void* d_x_expert, const void* d_weights,
+                           const int32_t* d_offsets, int32_t num_experts, int64_t max_rows,
+                           int32_t k_in, int32_t n_hidden, int32_t activation, void* d_h,
+                           float* d_pre, int32_t flags, void* stream) {
+    if (!experts_ok(num_experts) || !width_ok(k_in, 8) || !width_ok(n_hidden, 8) ||
+        !activation_ok(activation) || max_rows < 0 || max_rows > INT32_MAX ||
+        (flags & ~MOE_GEMM_ZERO_TAIL))
+        return MOE_ERR_INVALID_ARG;
+    if (max_rows == 0) return MOE_OK;
+    if (!buffers_ok(d_x_expert, d_weights, d_h, d_offsets) || (d_pre && misaligned(d_pre, 16)))
+        return MOE_ERR_INVALID_ARG;
+    return run_gemm(moe::ExpertOp::kGated, d_x_expert, d_weights, d_offsets, num_experts, max_rows,
+                    k_in, n_hidden, activation, d_h, d_pre, flags, stream);
+}
+
+int moe_grouped_gemm_forward(const void* d_x_expert, const void* d_weights,
+                             const int32_t* d_offsets, int32_t num_experts, int64_t max_rows,
+                             int32_t k_in, int32_t n_out, void* d_out, int32_t flags,
+                             void* stream) {
+    if (!experts_ok(num_experts) || !width_ok(k_in, 8) || !width_ok(n_out, 8) || max_rows < 0 ||
+        max_rows > INT32_MAX || (flags & ~MOE_GEMM_ZERO_TAIL))
+        return MOE_ERR_INVALID_ARG;
+    if (max_rows == 0) return MOE_OK;
+    if (!buffers_ok(d_x_expert, d_weights, d_out, d_offsets)) return MOE_ERR_INVALID_ARG;
+    return run_gemm(moe::ExpertOp::kPlain, d_x_expert, d_weights, d_offsets, num_experts, max_rows,
+                    k_in, n_out, MOE_ACT_SILU, d_out, nullptr, flags, stream);
+}
+
+int moe_grouped_gemm_backward_input(const void* d_grad_out, const void* d_weights,
+                                    const int32_t* d_offsets, int32_t num_experts,
+                                    int64_t max_rows, int32_t k_in, int32_t n_out,
+                                    void* d_grad_x, int32_t flags, void* stream) {
+    if (!experts_ok(num_experts) || !width_ok(k_in, 8) || !width_ok(n_out, 8) || max_rows < 0 ||
+        max_rows > INT32_MAX || (flags & ~MOE_GEMM_ZERO_TAIL))
+        return MOE_ERR_INVALID_ARG;
+    if (max_rows == 0) return MOE_OK;
+    if (!buffers_ok(d_grad_out, d_weights, d_grad_x, d_offsets)) return MOE_ERR_INVALID_ARG;
+    return run_gemm(moe::ExpertOp::kInputGrad, d_grad_out, d_weights, d_offsets, num_experts,
+                    max_rows, n_out, k_in, MOE_ACT_SILU, d_grad_x, nullptr, flags, stream);
+}
+
+int moe_gated_grouped_gemm_backward(const void* d_grad_out, const void* d_weights,
+                                    const float* d_pre, const int32_t* d_offsets,
+                                    int32_t num_experts, int64_t max_rows, int32_t n_hidden,
+                                    int32_t n_out, int32_t activation, void* d_grad_pre,
+                                    int32_t flags, void* stream) {
+    if (!experts_ok(num_experts) || !width_ok(n_hidden, 8) || !width_ok(n_out, 8) ||
+        !activation_ok(activation) || max_rows < 0 || max_rows > INT32_MAX ||
+        (flags & ~MOE_GEMM_ZERO_TAIL))
+        return MOE_ERR_INVALID_ARG;
+    if (max_rows == 0) return MOE_OK;
+    if (!buffers_ok(d_grad_out, d_weights, d_grad_pre, d_offsets) || !d_pre ||
+        misaligned(d_pre, 16))
+        return MOE_ERR_INVALID_ARG;
+    return run_gemm(moe::ExpertOp::kGatedGrad, d_grad_out, d_weights, d_offsets, num_experts,
+                    max_rows, n_out, n_hidden, activation, d_grad_pre,
+                    const_cast<float*>(d_pre), flags, stream);
+}
+
+int moe_grouped_gemm_backward_weight(const void* d_grad_out, const void* d_x_expert,
+                                     const int32_t* d_offsets, int32_t num_experts,
+                                     int64_t max_rows, int32_t k_in, int32_t n_out,
+                                     int32_t grad_dtype, void* d_grad_w, int32_t flags,
+                                     void* stream) {
+    if (!experts_ok(num_experts) || !width_ok(k_in, 8) || !width_ok(n_out, 8) || max_rows < 0 ||
+        max_rows > INT32_MAX || (grad_dtype != MOE_BF16 && grad_dtype != MOE_F32) ||
+        (flags & ~MOE_GEMM_ACCUMULATE))
+        return MOE_ERR_INVALID_ARG;
+    if (!d_grad_w || !d_offsets || misaligned(d_grad_w, 16) || misaligned(d_offsets, 4))
+        return MOE_ERR_INVALID_ARG;
+    // Without rows nothing is read: the gradient is zero (or stays).
+    if (max_rows > 0 && (!d_grad_out || !d_x_expert || misaligned(d_grad_out, 16) ||
+                         misaligned(d_x_expert, 16)))
+        return MOE_ERR_INVALID_ARG;
+    moe::ExpertWgradArgs a;
+    a.dy = d_grad_out;
+    a.x = d_x_expert;
+    a.offsets = d_offsets;
+    a.E = num_experts;
+    a.max_rows = max_rows;
+    a.N = n_out;
+    a.K = k_in;
+    a.f32 = grad_dtype == MOE_F32;
+    a.accumulate = (flags & MOE_GEMM_ACCUMULATE) != 0;
+    a.dw = d_grad_w;
+    if (moe::expert_wgrad_grid(a) > INT32_MAX) return MOE_ERR_INVALID_ARG;
+    return status_of(moe::launch_expert_wgrad(a, static_cast<hipStream_t>(stream)));
+}
+
+int64_t moe_mxfp4_weights_bytes(int32_t num_experts, int32_t n_out, int32_t k_in) {
+    if (!experts_ok(num_experts) || !width_ok(n_out, 8) || !width_ok(k_in, 32)) return -1;
+    // The packing launch has a thread per packed dword.
+    if (moe::mxfp4_bytes(num_experts, n_out, k_in) / 4 / 256 >= INT32_MAX) return -1;
+    return moe::mxfp4_bytes(num_experts, n_out, k_in);
+}
+
+int moe_pack_mxfp4_weights(const void* d_values, const void* d_scales, int32_t num_experts,
+                           int32_t n_out, int32_t k_in, void* d_packed, void* stream) {
+    if (moe_mxfp4_weights_bytes(num_experts, n_out, k_in) < 0) return MOE_ERR_INVALID_ARG;
+    if (!d_values || !d_scales || !d_packed || misaligned(d_values, 4) || misaligned(d_packed, 16))
+        return MOE_ERR_INVALID_ARG;
+    moe::PackMxfp4Args a;
+    a.blocks = d_values;
+    a.scales = d_scales;
+    a.E = num_experts;
+    a.N = n_out;
+    a.K = k_in;
+    a.dst = d_packed;
+    return status_of(moe::launch_pack_mxfp4(a, static_cast<hipStream_t>(stream)));
+}
+
+int moe_grouped_gemm_mxfp4(const void* d_x_expert, const void* d_packed, const int32_t* d_offsets,
+                           int32_t num_experts, int64_t max_rows, int32_t k_in, int32_t n_out,
+                           void* d_out, int32_t flags, void* stream) {
+    return run_mxfp4(false, d_x_expert, d_packed, d_offsets, num_experts, max_rows, k_in, n_out,
+                     MOE_ACT_SILU, d_out, flags, stream);
+}
+
+int moe_gated_grouped_gemm_mxfp4(const void* d_x_expert, const void* d_packed,
+                                 const int32_t* d_offsets, int32_t num_experts, int64_t max_rows,
+                                 int32_t k_in, int32_t n_hidden, int32_t activation, void* d_h,
+                                 int32_t flags, void* stream) {
+    if (!width_ok(n_hidden, 16) || n_hidden > MOE_MAX_GEMM_WIDTH / 2 || !activation_ok(activation))
+        return MOE_ERR_INVALID_ARG;
+    return run_mxfp4(true, d_x_expert, d_packed, d_offsets, num_experts, max_rows, k_in, n_hidden,
+                     activation, d_h, flags, stream);
+}
+
+}  // extern "C"

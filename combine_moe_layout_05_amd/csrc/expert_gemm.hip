@@ -1,0 +1,296 @@
+// Products of the gated expert feed-forward block on gfx950, and their
+// gradients with respect to the rows: grouped GEMMs over the expert-major rows
+// with the block's element-wise part in the epilogue.
+#include "expert_kernels.h"
+#include "expert_mma.h"
+
+#include <type_traits>
+
+namespace moe {
+namespace {
+
+constexpr int kWaves = 8;
+constexpr int kWavesF = 4;              // wavefronts along the features
+constexpr int kWavesR = 2;              // and along the rows
+constexpr int kTileF = 256;             // weight positions per workgroup
+constexpr int kBlkF = kTileF / kWavesF / 16;
+constexpr int kXcdChunk = 32;
+constexpr int kBand = 8;
+
+constexpr bool strided(ExpertOp op) {
+    return op == ExpertOp::kInputGrad || op == ExpertOp::kGatedGrad;
+}
+// Output features per workgroup: the gated product holds gate and up rows.
+constexpr int tile_feats(ExpertOp op) { return op == ExpertOp::kGated ? kTileF / 2 : kTileF; }
+
+template <bool STRIDED>
+struct WeightOperand {
+    typedef PackedOperand<kTileF, kWaves> type;
+};
+template <>
+struct WeightOperand<true> {
+    typedef StridedOperand<kTileF, kWaves> type;
+};
+
+template <ExpertOp OP, int BT>
+__global__ __launch_bounds__(kWaves * 64, 2)
+void expert_gemm_kernel(const char* __restrict__ rows, const char* __restrict__ w,
+                        const int32_t* __restrict__ offsets, int32_t E, int32_t max_rows,
+                        int32_t red, int32_t feats, int32_t ftiles, int32_t act,
+                        char* __restrict__ out, float* __restrict__ pre, int32_t zero_tail) {
+    constexpr int kBlkR = BT / kWavesR / 16;
+    constexpr int kStages = BT == 256 ? 2 : 3;
+    typedef typename WeightOperand<strided(OP)>::type Weights;
+    typedef PackedOperand<BT, kWaves> Rows;
+    __shared__ v4i w0[Weights::kChunks], w1[Weights::kChunks];
+    __shared__ v4i w2[kStages > 2 ? Weights::kChunks : 1];
+    __shared__ v4i r0[Rows::kChunks], r1[Rows::kChunks];
+    __shared__ v4i r2[kStages > 2 ? Rows::kChunks : 1];
+    __shared__ int32_t info[4];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+
+    const int64_t number = expert_tile_number(kXcdChunk);
+    if (wave == 0) {
+        const ExpertTile t =
+            expert_find_tile(offsets, E, max_rows, BT, ftiles, kBand, number);
+        if (lane == 0) {
+            info[0] = t.e;
+            info[1] = t.f;
+            info[2] = t.row0;
+            info[3] = t.rows;
+        }
+    }
+    __syncthreads();
+    const int32_t e = __builtin_amdgcn_readfirstlane(info[0]);
+    const int32_t ft = __builtin_amdgcn_readfirstlane(info[1]);
+    const int32_t row0 = __builtin_amdgcn_readfirstlane(info[2]);
+    const int32_t nrows = __builtin_amdgcn_readfirstlane(info[3]);
+    const int64_t out_pitch = int64_t(feats) * (OP == ExpertOp::kGatedGrad ? 4 : 2);
+    if (e < 0) {
+        if (zero_tail)
+            expert_zero_tail(reinterpret_cast<v4i*>(out), row0, max_rows,
+                             static_cast<int32_t>(out_pitch / 16), ft, int64_t(gridDim.x) - nrows);
+        return;
+    }
+    const int32_t f0 = ft * tile_feats(OP);
+    const int64_t red_pitch = int64_t(red) * 2;
+
+    Weights wt;
+    Rows rt;
+    if constexpr (strided(OP)) {
+        // w[e] is [red][feats], features contiguous.
+        const char* base = w + (int64_t(e) * red * feats + f0) * 2;
+        wt.init(wave, lane, int64_t(feats) * 2, base, min(kTileF, feats - f0));
+    } else if constexpr (OP == ExpertOp::kGated) {
+        // Each wavefront's 64 positions are 32 gate rows and the 32 up rows of
+        // the same features, so the epilogue finds both in its own registers.
+        const char* gate = w + (int64_t(e) * 2 * feats + f0) * red_pitch;
+        const char* up = gate + int64_t(feats) * red_pitch;
+        const int last = feats - f0 - 1;
+        wt.init(wave, lane, red_pitch, [&](int p0) { return (p0 & 32) ? up : gate; },
+                [&](int p) { return min((p >> 6) * 32 + (p & 31), last); });
+    } else {
+        const char* base = w + (int64_t(e) * feats + f0) * red_pitch;
+        const int last = feats - f0 - 1;
+        wt.init(wave, lane, red_pitch, [&](int) { return base; },
+                [&](int p) { return min(p, last); });
+    }
+    {
+        const char* base = rows + int64_t(row0) * red_pitch;
+        rt.init(wave, lane, red_pitch, [&](int) { return base; },
+                [&](int p) { return min(p, nrows - 1); });
+    }
+    const int wf = wave % kWavesF, wr = wave / kWavesF;
+
+    f32x4 acc[kBlkF][kBlkR];
+#pragma unroll
+    for (int a = 0; a < kBlkF; ++a)
+#pragma unroll
+        for (int b = 0; b < kBlkR; ++b) acc[a][b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+    auto compute = [&](const v4i* wb, const v4i* rb) {
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            bf16x8 fa[kBlkF], fb[kBlkR];
+#pragma unroll
+            for (int a = 0; a < kBlkF; ++a) fa[a] = wt.frag(wb, wf * kBlkF + a, s);
+#pragma unroll
+            for (int b = 0; b < kBlkR; ++b) fb[b] = rt.frag(rb, wr * kBlkR + b, s);
+#pragma unroll
+            for (int b = 0; b < kBlkR; ++b)
+#pragma unroll
+                for (int a = 0; a < kBlkF; ++a)
+                    acc[a][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[a], fb[b], acc[a][b], 0,
+                                                                        0, 0);
+        }
+    };
+    constexpr int kLoads = Weights::kLoads + Rows::kLoads;
+    const int32_t full = red / 64;
+    // Stage P of the ring: its own arrays, so that the compiler sees that
+    // loads into one stage do not touch the stage being read.
+    auto issue = [&](auto p, int64_t t) {
+        constexpr int P = decltype(p)::value % kStages;
+        wt.issue(t, P == 0 ? w0 : P == 1 ? w1 : w2);
+        rt.issue(t, P == 0 ? r0 : P == 1 ? r1 : r2);
+    };
+    auto use = [&](auto p) {
+        constexpr int P = decltype(p)::value % kStages;
+        compute(P == 0 ? w0 : P == 1 ? w1 : w2, P == 0 ? r0 : P == 1 ? r1 : r2);
+    };
+    using std::integral_constant;
+    if (full > 0) {
+        issue(integral_constant<int, 0>{}, 0);
+        if (kStages > 2 && full > 1) issue(integral_constant<int, 1>{}, 1);
+        int32_t t = 0;
+        auto step = [&](auto p, int32_t at) {
+            constexpr int P = decltype(p)::value;
+            wait_loads<kLoads * (kStages - 2)>();
+            step_barrier();
+            issue(integral_constant<int, P + kStages - 1>{}, at + kStages - 1);
+            // Keeps the loads here: sunk to the end of the step, as the
+            // scheduler would have it, their latency would not be covered.
+            __builtin_amdgcn_sched_barrier(0);
+            use(p);
+        };
+        for (; t + 2 * kStages - 2 < full; t += kStages) {
+            step(integral_constant<int, 0>{}, t);
+            step(integral_constant<int, 1>{}, t + 1);
+            if constexpr (kStages > 2) step(integral_constant<int, 2>{}, t + 2);
+        }
+        // The last steps: fewer loads are in flight, all are waited for.
+        auto last = [&](auto p, int32_t at) {
+            constexpr int P = decltype(p)::value;
+            if (at >= full) return;
+            wait_loads<0>();
+            step_barrier();
+            if (at + kStages - 1 < full)
+                issue(integral_constant<int, P + kStages - 1>{}, at + kStages - 1);
+            __builtin_amdgcn_sched_barrier(0);
+            use(p);
+        };
+        last(integral_constant<int, 0>{}, t);
+        last(integral_constant<int, 1>{}, t + 1);
+        if constexpr (kStages > 2) {
+            last(integral_constant<int, 2>{}, t + 2);
+            last(integral_constant<int, 3>{}, t + 3);
+        }
+    }
+    if (full * 64 < red) {
+        __syncthreads();
+        if constexpr (strided(OP))
+            wt.tail(full, red, lane, w0);
+        else
+            wt.tail(full, red / 8, lane, w0);
+        rt.tail(full, red / 8, lane, r0);
+        __syncthreads();
+        compute(w0, r0);
+    }
+
+    // acc[a][b][t] belongs to row 16b + lane % 16 and position 16a + 4 (lane /
+    // 16) + t of the wavefront.
+    const int i = lane & 15, g = lane >> 4;
+#pragma unroll
+    for (int b = 0; b < kBlkR; ++b) {
+        const int r = (wr * kBlkR + b) * 16 + i;
+        if (r >= nrows) continue;
+        char* orow = out + int64_t(row0 + r) * out_pitch;
+        if constexpr (OP == ExpertOp::kGated) {
+            float* prow = pre + int64_t(row0 + r) * feats * 2;
+#pragma unroll
+            for (int a = 0; a < kBlkF / 2; ++a) {
+                const int32_t f = f0 + wf * 32 + a * 16 + g * 4;
+                if (f >= feats) continue;
+                const f32x4 gv = acc[a][b], uv = acc[a + kBlkF / 2][b];
+                float h[4];
+#pragma unroll
+                for (int t = 0; t < 4; ++t) h[t] = activate(act, gv[t]) * uv[t];
+                *reinterpret_cast<v2i*>(orow + int64_t(f) * 2) = pack_bf16x4(h[0], h[1], h[2], h[3]);
+                if (pre) {
+                    *reinterpret_cast<f32x4*>(prow + f) = gv;
+                    *reinterpret_cast<f32x4*>(prow + feats + f) = uv;
+                }
+            }
+        } else {
+#pragma unroll
+            for (int a = 0; a < kBlkF; ++a) {
+                const int32_t f = f0 + (wf * kBlkF + a) * 16 + g * 4;
+                if (f >= feats) continue;
+                const f32x4 v = acc[a][b];
+                if constexpr (OP == ExpertOp::kGatedGrad) {
+                    const float* prow = pre + int64_t(row0 + r) * feats * 2;
+                    const f32x4 gv = *reinterpret_cast<const f32x4*>(prow + f);
+                    const f32x4 uv = *reinterpret_cast<const f32x4*>(prow + feats + f);
+                    float dg[4], du[4];
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) {
+                        float value, slope;
+                        activate_grad(act, gv[t], value, slope);
+                        dg[t] = v[t] * uv[t] * slope;
+                        du[t] = v[t] * value;
+                    }
+                    *reinterpret_cast<v2i*>(orow + int64_t(f) * 2) =
+                        pack_bf16x4(dg[0], dg[1], dg[2], dg[3]);
+                    *reinterpret_cast<v2i*>(orow + (int64_t(feats) + f) * 2) =
+                        pack_bf16x4(du[0], du[1], du[2], du[3]);
+                } else {
+                    *reinterpret_cast<v2i*>(orow + int64_t(f) * 2) =
+                        pack_bf16x4(v[0], v[1], v[2], v[3]);
+                }
+            }
+        }
+    }
+}
+
+int32_t row_tile(const ExpertGemmArgs& a) {
+    const int64_t average = a.max_rows / a.E;
+    return average >= 192 ? 256 : average >= 96 ? 128 : 64;
+}
+
+int64_t feature_tiles(const ExpertGemmArgs& a) {
+    const int32_t per = tile_feats(a.op);
+    return (int64_t(a.feats) + per - 1) / per;
+}
+
+template <ExpertOp OP, int BT>
+hipError_t launch_bt(const ExpertGemmArgs& a, hipStream_t stream) {
+    hipLaunchKernelGGL((expert_gemm_kernel<OP, BT>), dim3(static_cast<uint32_t>(expert_gemm_grid(a))),
+                       dim3(kWaves * 64), 0, stream, static_cast<const char*>(a.rows),
+                       static_cast<const char*>(a.w), a.offsets, a.E,
+                       static_cast<int32_t>(a.max_rows), a.red, a.feats,
+                       static_cast<int32_t>(feature_tiles(a)), a.activation,
+                       static_cast<char*>(a.out), a.pre, a.zero_tail ? 1 : 0);
+    return hipGetLastError();
+}
+
+template <ExpertOp OP>
+hipError_t launch_op(const ExpertGemmArgs& a, hipStream_t stream) {
+    switch (row_tile(a)) {
+        case 64: return launch_bt<OP, 64>(a, stream);
+        case 128: return launch_bt<OP, 128>(a, stream);
+        default: return launch_bt<OP, 256>(a, stream);
+    }
+}
+
+}  // namespace
+
+int64_t expert_gemm_grid(const ExpertGemmArgs& a) {
+    const int32_t bt = row_tile(a);
+    // A segment of c rows takes ceil(c / bt) row tiles, at most one more per
+    // expert with rows than the rows fill.
+    const int64_t experts = a.max_rows < a.E ? a.max_rows : a.E;
+    const int64_t tiles = feature_tiles(a) * ((a.max_rows + bt - 1) / bt + experts);
+    const int64_t unit = int64_t(kExpertXcds) * kXcdChunk;
+    return (tiles + unit - 1) / unit * unit;
+}
+
+hipError_t launch_expert_gemm(const ExpertGemmArgs& a, hipStream_t stream) {
+    switch (a.op) {
+        case ExpertOp::kPlain: return launch_op<ExpertOp::kPlain>(a, stream);
+        case ExpertOp::kGated: return launch_op<ExpertOp::kGated>(a, stream);
+        case ExpertOp::kInputGrad: return launch_op<ExpertOp::kInputGrad>(a, stream);
+        default: return launch_op<ExpertOp::kGatedGrad>(a, stream);
+    }
+}
+
+}  // namespace moe

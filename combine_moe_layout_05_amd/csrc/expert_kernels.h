@@ -1,0 +1,96 @@
+// Internal declarations of the expert feed-forward kernels: the gated block's
+// products, their backward, and the products with 4-bit weights. Not part of
+// the public C ABI (include/moe.h).
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+namespace moe {
+
+// What an expert product writes.
+//   kPlain       out[r][n] = sum over k of rows[r][k] * w[e][n][k]
+//   kGated       the weight holds 2F rows, gate then up: out[r][f] =
+//                act(g) * u, optionally pre[r] = [g | u]
+//   kInputGrad   out[r][k] = sum over n of rows[r][n] * w[e][n][k]
+//   kGatedGrad   the same sum as dh, then out[r] = [dh*u*act'(g) | dh*act(g)]
+//                from pre[r] = [g | u]
+enum class ExpertOp { kPlain, kGated, kInputGrad, kGatedGrad };
+
+struct ExpertGemmArgs {
+    ExpertOp op;
+    const void* rows;       // bf16 [max_rows][red]
+    const void* w;          // bf16 [E][n][k] as the operation reads it
+    const int32_t* offsets; // [E+1], device
+    int32_t E;
+    int64_t max_rows;       // 1 .. INT32_MAX
+    int32_t red;            // length of the sums, multiple of 8
+    int32_t feats;          // features of the output (F for kGated), multiple of 8
+    int32_t activation;     // moe_activation
+    void* out;              // bf16 [max_rows][feats], kGatedGrad: [max_rows][2 feats]
+    float* pre;             // [max_rows][2 feats] or null
+    bool zero_tail;         // rows from offsets[E] on get +0.0
+};
+hipError_t launch_expert_gemm(const ExpertGemmArgs& a, hipStream_t stream);
+// Workgroups such a launch takes (checked against the grid limit).
+int64_t expert_gemm_grid(const ExpertGemmArgs& a);
+
+struct ExpertWgradArgs {
+    const void* dy;         // bf16 [max_rows][N]
+    const void* x;          // bf16 [max_rows][K]
+    const int32_t* offsets; // [E+1], device
+    int32_t E;
+    int64_t max_rows;       // 0 .. INT32_MAX
+    int32_t N;              // multiple of 8
+    int32_t K;              // multiple of 8
+    bool f32;               // element type of dw: fp32, else bf16
+    bool accumulate;        // add to what dw holds
+    void* dw;               // [E][N][K]
+};
+hipError_t launch_expert_wgrad(const ExpertWgradArgs& a, hipStream_t stream);
+int64_t expert_wgrad_grid(const ExpertWgradArgs& a);
+
+// Packed 4-bit weights: for 16-feature block b and 128-k step t one KiB, lane
+// l's 16 bytes being feature 16b + l % 16, dword s (0..3) the 8 values of k =
+// 128t + 32s + 8 (l / 16) .. + 8 (the A fragment of the matrix-core product
+// over the 32 k of scale group s). After all values, for each (b, t) the 16
+// features' scales of the step's 4 groups, a dword each. Features past N and
+// k past K hold zeros with scale 1.
+constexpr int32_t kMxfp4Step = 128;
+inline int64_t mxfp4_tiles(int32_t E, int32_t N, int32_t K) {
+    return int64_t(E) * ((int64_t(N) + 15) / 16) * ((int64_t(K) + kMxfp4Step - 1) / kMxfp4Step);
+}
+inline int64_t mxfp4_bytes(int32_t E, int32_t N, int32_t K) { return mxfp4_tiles(E, N, K) * 1088; }
+struct PackMxfp4Args {
+    const void* blocks;     // uint8 [E][N][K/2]
+    const void* scales;     // uint8 [E][N][K/32]
+    int32_t E;
+    int32_t N;
+    int32_t K;              // multiple of 32
+    void* dst;              // mxfp4_bytes(E, N, K)
+};
+hipError_t launch_pack_mxfp4(const PackMxfp4Args& a, hipStream_t stream);
+
+// Products for few rows per expert: the weights are streamed once from HBM
+// straight into fragment registers, the sum split over a workgroup's
+// wavefronts.
+struct ExpertStreamArgs {
+    bool mxfp4;             // w is packed 4-bit, else bf16 [E][n][red]
+    bool gated;             // act(g) * u, else the plain product
+    const void* rows;       // bf16 [max_rows][red]
+    const void* w;
+    const int32_t* offsets; // [E+1], device
+    int32_t E;
+    int64_t max_rows;       // 1 .. INT32_MAX
+    int32_t red;            // multiple of 8 (mxfp4: of 32)
+    int32_t feats;          // features of the output, multiple of 8 (mxfp4 gated: of 16)
+    int32_t activation;
+    void* out;              // bf16 [max_rows][feats]
+    float* pre;             // gated: [max_rows][2 feats] or null
+    bool zero_tail;
+};
+hipError_t launch_expert_stream(const ExpertStreamArgs& a, hipStream_t stream);
+int64_t expert_stream_grid(const ExpertStreamArgs& a);
+
+}  // namespace moe

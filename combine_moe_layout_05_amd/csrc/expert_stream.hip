@@ -1,0 +1,348 @@
+// Expert products for few rows per expert on gfx950, and the packing of 4-bit
+// expert weights.
+#include "expert_kernels.h"
+#include "expert_mma.h"
+
+#include <type_traits>
+
+namespace moe {
+namespace {
+
+constexpr int kWaves = 8;               // wavefronts of a workgroup, splitting the sum
+constexpr int kBlocks = 4;              // 16-feature blocks per workgroup
+constexpr int kRows = 16;               // rows per workgroup
+constexpr int kXcdChunk = 32;
+
+// Sum elements per step, the 32-element products in it and 16-byte chunks.
+template <bool MXFP4>
+struct Step {
+    static constexpr int kElems = MXFP4 ? kMxfp4Step : 64;
+    static constexpr int kProducts = kElems / 32;
+    static constexpr int kRowChunks = kElems / 8;
+    static constexpr int kRowLoads = kRows * kRowChunks / 64;
+    static constexpr int kRowsPerLoad = 64 / kRowChunks;
+};
+
+// One step of a 16-feature block in registers.
+template <bool MXFP4>
+struct Weights;
+template <>
+struct Weights<true> {
+    v4i q;
+    uint32_t scale;
+    __device__ bf16x8 frag(int s) const {
+        // The scale's exponent byte is the exponent field of a float; the
+        // conversion is exact (2-bit significands times a power of two).
+        const float f = __uint_as_float(((scale >> (8 * s)) & 0xFFu) << 23);
+        const uint32_t v = static_cast<uint32_t>(q[s]);
+        typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+        const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v, f, 0);
+        const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v, f, 1);
+        const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v, f, 2);
+        const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v, f, 3);
+        return bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+    }
+};
+template <>
+struct Weights<false> {
+    v4i q[2];
+    __device__ bf16x8 frag(int s) const { return __builtin_bit_cast(bf16x8, q[s]); }
+};
+
+template <bool MXFP4, bool GATED>
+__global__ __launch_bounds__(kWaves * 64, 4)
+void expert_stream_kernel(const char* __restrict__ rows, const char* __restrict__ w,
+                          const char* __restrict__ scales, const int32_t* __restrict__ offsets,
+                          int32_t E, int32_t max_rows, int32_t red, int32_t feats, int32_t ftiles,
+                          int32_t act, char* __restrict__ out, float* __restrict__ pre,
+                          int32_t zero_tail) {
+    typedef Step<MXFP4> S;
+    constexpr int kFeatBlocks = GATED ? kBlocks / 2 : kBlocks;  // of the output
+    constexpr int kXs = kRows * S::kRowChunks;                  // chunks of a row step
+    __shared__ v4i x0[kWaves][kXs], x1[kWaves][kXs];
+    // The wavefronts' sums, [wave][block][lane]; with 4-bit weights they take
+    // the place of the wavefront's own rows, so that two workgroups fit a CU.
+    constexpr int kPart = kBlocks * 64;
+    static_assert(!MXFP4 || kXs == kPart, "the sums fill the place of the rows");
+    __shared__ v4i sums[MXFP4 ? 1 : kWaves][MXFP4 ? 1 : kPart];
+    __shared__ int32_t info[4];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t number = expert_tile_number(kXcdChunk);
+    if (wave == 0) {
+        // Feature tiles fastest: neighbouring workgroups read neighbouring
+        // weights; the row tiles of a longer segment follow each other.
+        const ExpertTile t = expert_find_tile(offsets, E, max_rows, kRows, ftiles, 4, number);
+        if (lane == 0) {
+            info[0] = t.e;
+            info[1] = t.f;
+            info[2] = t.row0;
+            info[3] = t.rows;
+        }
+    }
+    __syncthreads();
+    const int32_t e = __builtin_amdgcn_readfirstlane(info[0]);
+    const int32_t ft = __builtin_amdgcn_readfirstlane(info[1]);
+    const int32_t row0 = __builtin_amdgcn_readfirstlane(info[2]);
+    const int32_t nrows = __builtin_amdgcn_readfirstlane(info[3]);
+    if (e < 0) {
+        if (zero_tail)
+            expert_zero_tail(reinterpret_cast<v4i*>(out), row0, max_rows, feats / 8, ft,
+                             int64_t(gridDim.x) - nrows);
+        return;
+    }
+    const int i = lane & 15, g = lane >> 4;
+    const int32_t f0 = ft * kFeatBlocks * 16;
+    const int32_t steps = (red + S::kElems - 1) / S::kElems;
+    const int32_t full = red / S::kElems;
+
+    // Weight addresses of the 16-feature blocks; blocks past the matrix read
+    // its last one and are not stored.
+    const char* wb[kBlocks];
+    const char* sb[kBlocks];
+#pragma unroll
+    for (int b = 0; b < kBlocks; ++b) {
+        const int ob = GATED ? b % kFeatBlocks : b;         // output block
+        const bool up = GATED && b >= kFeatBlocks;
+        if constexpr (MXFP4) {
+            const int32_t nb = (feats + 15) / 16;
+            const int64_t blk = int64_t(e) * nb * (GATED ? 2 : 1) + (up ? nb : 0) +
+                                min(f0 / 16 + ob, nb - 1);
+            wb[b] = w + blk * steps * 1024 + lane * 16;
+            sb[b] = scales + blk * steps * 64 + i * 4;
+        } else {
+            const int32_t f = min(f0 + ob * 16 + i, feats - 1) + (up ? feats : 0);
+            wb[b] = w + (int64_t(e) * feats * (GATED ? 2 : 1) + f) * (int64_t(red) * 2) + g * 16;
+            sb[b] = nullptr;
+        }
+    }
+    const int64_t pitch = int64_t(red) * 2;
+    auto load_w = [&](int32_t t, Weights<MXFP4> (&d)[kBlocks]) {
+#pragma unroll
+        for (int b = 0; b < kBlocks; ++b) {
+            if constexpr (MXFP4) {
+                d[b].q = __builtin_nontemporal_load(
+                    reinterpret_cast<const v4i*>(wb[b] + int64_t(t) * 1024));
+                d[b].scale = *reinterpret_cast<const uint32_t*>(sb[b] + int64_t(t) * 64);
+            } else {
+#pragma unroll
+                for (int s = 0; s < 2; ++s)
+                    d[b].q[s] = *reinterpret_cast<const v4i*>(wb[b] + int64_t(t) * 128 + s * 64);
+            }
+        }
+    };
+    // Rows: chunk c of row r sits at chunk c ^ swizzle(r) of the row's step,
+    // so that 16 rows at one chunk fall into distinct LDS banks.
+    auto swz = [](int r) { return MXFP4 ? r : ((r ^ (r >> 3)) & 7); };
+    const int lr = lane / S::kRowChunks, lp = lane % S::kRowChunks;
+    const char* xbase = rows + int64_t(row0) * pitch;
+    auto load_x = [&](int32_t t, v4i* buf) {
+#pragma unroll
+        for (int j = 0; j < S::kRowLoads; ++j) {
+            const int r = lr + j * S::kRowsPerLoad;
+            if (j * S::kRowsPerLoad < nrows)
+                load_to_lds(xbase + min(r, nrows - 1) * pitch + int64_t(t) * (S::kElems * 2) +
+                                (lp ^ swz(r)) * 16,
+                            buf + j * 64);
+        }
+    };
+    f32x4 acc[kBlocks];
+#pragma unroll
+    for (int b = 0; b < kBlocks; ++b) acc[b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    auto compute = [&](const Weights<MXFP4> (&d)[kBlocks], const v4i* buf) {
+#pragma unroll
+        for (int s = 0; s < S::kProducts; ++s) {
+            const bf16x8 fx =
+                __builtin_bit_cast(bf16x8, buf[i * S::kRowChunks + ((4 * s + g) ^ swz(i))]);
+#pragma unroll
+            for (int b = 0; b < kBlocks; ++b)
+                acc[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(d[b].frag(s), fx, acc[b], 0, 0, 0);
+        }
+    };
+    // Wavefront w takes steps w, w + 8, ...: the workgroup reads consecutive
+    // weights. Two steps are in flight; LDS is this wavefront's own, so the
+    // loop has no barrier.
+    Weights<MXFP4> d0[kBlocks], d1[kBlocks];
+    v4i* b0 = x0[wave];
+    v4i* b1 = x1[wave];
+    const int32_t n = full > wave ? (full - wave + kWaves - 1) / kWaves : 0;
+    auto at = [&](int32_t k) { return wave + k * kWaves; };
+    // A step's row loads go out before its weight loads, of which there are
+    // kWeightLoads, and at least one row load: with the next step's behind
+    // them, this step's rows have landed once no more than these are left.
+    constexpr int kWeightLoads = 2 * kBlocks;
+    auto load = [&](int32_t t, Weights<MXFP4> (&d)[kBlocks], v4i* buf) {
+        wait_lds_reads();           // the buffer's last reads have returned
+        load_x(t, buf);
+        __builtin_amdgcn_sched_barrier(0);
+        load_w(t, d);
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    if (n > 0) {
+        load(at(0), d0, b0);
+        if (n > 1) load(at(1), d1, b1);
+        int32_t k = 0;
+        for (; k + 3 < n; k += 2) {
+            wait_loads<kWeightLoads + 1>();
+            compute(d0, b0);
+            load(at(k + 2), d0, b0);
+            wait_loads<kWeightLoads + 1>();
+            compute(d1, b1);
+            load(at(k + 3), d1, b1);
+        }
+        // One to three steps are left, the first two of them loaded.
+        wait_loads<0>();
+        compute(d0, b0);
+        if (k + 2 < n) load(at(k + 2), d0, b0);
+        if (k + 1 < n) compute(d1, b1);
+        if (k + 2 < n) {
+            wait_loads<0>();
+            compute(d0, b0);
+        }
+    }
+    // The last, partial step: row chunks past the row are zero, and so are the
+    // weights there (packed weights hold zeros already).
+    if (full < steps && wave == full % kWaves) {
+        const v4i zero = {0, 0, 0, 0};
+        const int32_t left = (red - full * S::kElems) / 8;
+        wait_loads<0>();            // nothing still writes or reads b0
+#pragma unroll
+        for (int j = 0; j < S::kRowLoads; ++j) {
+            const int r = lr + j * S::kRowsPerLoad;
+            const int c = lp ^ swz(r);
+            v4i v = zero;
+            if (c < left)
+                v = *reinterpret_cast<const v4i*>(xbase + min(r, nrows - 1) * pitch +
+                                                  int64_t(full) * (S::kElems * 2) + c * 16);
+            b0[j * 64 + lane] = v;
+        }
+        if constexpr (MXFP4) {
+            load_w(full, d0);
+        } else {
+#pragma unroll
+            for (int b = 0; b < kBlocks; ++b)
+#pragma unroll
+                for (int s = 0; s < 2; ++s)
+                    d0[b].q[s] = 4 * s + g < left ? *reinterpret_cast<const v4i*>(
+                                                        wb[b] + int64_t(full) * 128 + s * 64)
+                                                  : zero;
+        }
+        compute(d0, b0);
+    }
+
+    // Join the wavefronts' sums, in wavefront order.
+    f32x4(*part)[kBlocks][64] =
+        reinterpret_cast<f32x4(*)[kBlocks][64]>(MXFP4 ? &x0[0][0] : &sums[0][0]);
+    wait_loads<0>();
+#pragma unroll
+    for (int b = 0; b < kBlocks; ++b) part[wave][b][lane] = acc[b];
+    __syncthreads();
+    if (wave >= kFeatBlocks) return;
+    f32x4 v = part[0][wave][lane];
+    f32x4 u = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int p = 1; p < kWaves; ++p) v += part[p][wave][lane];
+    if constexpr (GATED) {
+        u = part[0][wave + kFeatBlocks][lane];
+#pragma unroll
+        for (int p = 1; p < kWaves; ++p) u += part[p][wave + kFeatBlocks][lane];
+    }
+    const int32_t f = f0 + wave * 16 + g * 4;
+    if (i >= nrows || f >= feats) return;
+    v2i* o = reinterpret_cast<v2i*>(out + (int64_t(row0 + i) * feats + f) * 2);
+    if constexpr (GATED) {
+        float h[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) h[t] = activate(act, v[t]) * u[t];
+        *o = pack_bf16x4(h[0], h[1], h[2], h[3]);
+        if (pre) {
+            float* p = pre + int64_t(row0 + i) * feats * 2 + f;
+            *reinterpret_cast<f32x4*>(p) = v;
+            *reinterpret_cast<f32x4*>(p + feats) = u;
+        }
+    } else {
+        *o = pack_bf16x4(v[0], v[1], v[2], v[3]);
+    }
+}
+
+// One dword of the packed values per thread, then one dword of the scales.
+__global__ __launch_bounds__(256)
+void pack_mxfp4_kernel(const uint8_t* __restrict__ blocks, const uint8_t* __restrict__ scales,
+                       int32_t N, int32_t K, int32_t nb, int32_t steps, int64_t tiles,
+                       uint32_t* __restrict__ dst) {
+    const int64_t q = int64_t(blockIdx.x) * 256 + threadIdx.x;
+    const int64_t values = tiles * 256;
+    if (q >= values + tiles * 16) return;
+    const bool is_scale = q >= values;
+    const int64_t p = is_scale ? q - values : q;
+    const int64_t tile = is_scale ? p >> 4 : p >> 8;
+    const int32_t t = static_cast<int32_t>(tile % steps);
+    const int64_t eb = tile / steps;
+    const int32_t b = static_cast<int32_t>(eb % nb);
+    const int64_t e = eb / nb;
+    uint32_t v = is_scale ? 0x7F7F7F7Fu : 0u;
+    if (!is_scale) {
+        const int l = static_cast<int>(p >> 2) & 63, s = static_cast<int>(p) & 3;
+        const int32_t f = 16 * b + (l & 15);
+        const int32_t k = t * kMxfp4Step + 32 * s + 8 * (l >> 4);
+        if (f < N && k < K)
+            v = *reinterpret_cast<const uint32_t*>(blocks + ((e * N + f) * K + k) / 2);
+    } else {
+        const int32_t f = 16 * b + (static_cast<int>(p) & 15);
+        if (f < N)
+            for (int s = 0; s < 4; ++s) {
+                const int32_t grp = 4 * t + s;
+                if (grp < K / 32) {
+                    const uint32_t x = scales[(e * N + f) * (K / 32) + grp];
+                    v = (v & ~(0xFFu << (8 * s))) | (x << (8 * s));
+                }
+            }
+    }
+    dst[q] = v;
+}
+
+int64_t stream_feature_tiles(const ExpertStreamArgs& a) {
+    const int32_t per = (a.gated ? kBlocks / 2 : kBlocks) * 16;
+    return (int64_t(a.feats) + per - 1) / per;
+}
+
+template <bool MXFP4, bool GATED>
+hipError_t launch_stream(const ExpertStreamArgs& a, hipStream_t stream) {
+    const char* w = static_cast<const char*>(a.w);
+    const char* scales = w + mxfp4_tiles(a.E, a.gated ? 2 * a.feats : a.feats, a.red) * 1024;
+    hipLaunchKernelGGL((expert_stream_kernel<MXFP4, GATED>),
+                       dim3(static_cast<uint32_t>(expert_stream_grid(a))), dim3(kWaves * 64), 0,
+                       stream, static_cast<const char*>(a.rows), w, scales, a.offsets, a.E,
+                       static_cast<int32_t>(a.max_rows), a.red, a.feats,
+                       static_cast<int32_t>(stream_feature_tiles(a)), a.activation,
+                       static_cast<char*>(a.out), a.pre, a.zero_tail ? 1 : 0);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+int64_t expert_stream_grid(const ExpertStreamArgs& a) {
+    const int64_t experts = a.max_rows < a.E ? a.max_rows : a.E;
+    const int64_t tiles =
+        stream_feature_tiles(a) * ((a.max_rows + kRows - 1) / kRows + experts);
+    const int64_t unit = int64_t(kExpertXcds) * kXcdChunk;
+    return (tiles + unit - 1) / unit * unit;
+}
+
+hipError_t launch_expert_stream(const ExpertStreamArgs& a, hipStream_t stream) {
+    if (a.mxfp4)
+        return a.gated ? launch_stream<true, true>(a, stream) : launch_stream<true, false>(a, stream);
+    return a.gated ? launch_stream<false, true>(a, stream) : launch_stream<false, false>(a, stream);
+}
+
+hipError_t launch_pack_mxfp4(const PackMxfp4Args& a, hipStream_t stream) {
+    const int64_t tiles = mxfp4_tiles(a.E, a.N, a.K);
+    const int64_t dwords = tiles * 272;
+    hipLaunchKernelGGL(pack_mxfp4_kernel, dim3(static_cast<uint32_t>((dwords + 255) / 256)),
+                       dim3(256), 0, stream, static_cast<const uint8_t*>(a.blocks),
+                       static_cast<const uint8_t*>(a.scales), a.N, a.K, (a.N + 15) / 16,
+                       (a.K + kMxfp4Step - 1) / kMxfp4Step, tiles, static_cast<uint32_t*>(a.dst));
+    return hipGetLastError();
+}
+
+}  // namespace moe

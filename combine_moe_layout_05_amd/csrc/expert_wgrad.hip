@@ -1,0 +1,158 @@
+// Gradient of the expert weights on gfx950: for every expert e
+//     dw[e][n][k] = sum over rows r of e's segment of dy[r][n] * x[r][k]
+// (plus what dw holds, on request), one rounding of the fp32 sum.
+#include "expert_kernels.h"
+#include "expert_mma.h"
+
+#include <type_traits>
+
+namespace moe {
+namespace {
+
+constexpr int kWaves = 8;
+constexpr int kWavesK = 4;
+constexpr int kWavesN = 2;
+constexpr int kTileK = 256;
+constexpr int kTileN = 256;
+constexpr int kBlkK = kTileK / kWavesK / 16;
+constexpr int kBlkN = kTileN / kWavesN / 16;
+constexpr int kXcdChunk = 32;
+
+template <bool F32, bool ACCUMULATE>
+__global__ __launch_bounds__(kWaves * 64, 2)
+void expert_wgrad_kernel(const char* __restrict__ dy, const char* __restrict__ x,
+                         const int32_t* __restrict__ offsets, int32_t max_rows, int32_t N,
+                         int32_t K, int32_t ntiles, int32_t ktiles, int64_t tiles, char* __restrict__ dw) {
+    typedef StridedOperand<kTileK, kWaves> Kop;
+    typedef StridedOperand<kTileN, kWaves> Nop;
+    __shared__ v4i k0[Kop::kChunks], k1[Kop::kChunks];
+    __shared__ v4i n0[Nop::kChunks], n1[Nop::kChunks];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t u = expert_tile_number(kXcdChunk);
+    if (u >= tiles) return;
+    const int32_t per = ntiles * ktiles;
+    const int32_t e = static_cast<int32_t>(u / per);
+    const int32_t in = static_cast<int32_t>(u - int64_t(e) * per);
+    const int32_t nt0 = (in / ktiles) * kTileN, kt0 = (in % ktiles) * kTileK;
+    int32_t s0, s1;
+    expert_segment(offsets, e, max_rows, s0, s1);
+    const int32_t count = s1 - s0;
+    if (ACCUMULATE && count == 0) return;
+
+    Kop ko;
+    Nop no;
+    ko.init(wave, lane, int64_t(K) * 2, x + (int64_t(s0) * K + kt0) * 2, min(kTileK, K - kt0));
+    no.init(wave, lane, int64_t(N) * 2, dy + (int64_t(s0) * N + nt0) * 2, min(kTileN, N - nt0));
+    const int wk = wave % kWavesK, wn = wave / kWavesK;
+
+    f32x4 acc[kBlkK][kBlkN];
+#pragma unroll
+    for (int a = 0; a < kBlkK; ++a)
+#pragma unroll
+        for (int b = 0; b < kBlkN; ++b) acc[a][b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    auto compute = [&](const v4i* kb, const v4i* nb) {
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            bf16x8 fa[kBlkK], fb[kBlkN];
+#pragma unroll
+            for (int a = 0; a < kBlkK; ++a) fa[a] = ko.frag(kb, wk * kBlkK + a, s);
+#pragma unroll
+            for (int b = 0; b < kBlkN; ++b) fb[b] = no.frag(nb, wn * kBlkN + b, s);
+#pragma unroll
+            for (int b = 0; b < kBlkN; ++b)
+#pragma unroll
+                for (int a = 0; a < kBlkK; ++a)
+                    acc[a][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[a], fb[b], acc[a][b], 0,
+                                                                        0, 0);
+        }
+    };
+    const int32_t full = count / 64;
+    if (full > 0) {
+        ko.issue(0, k0);
+        no.issue(0, n0);
+        for (int32_t t = 0; t < full; t += 2) {
+            wait_loads<0>();
+            step_barrier();
+            if (t + 1 < full) {
+                ko.issue(t + 1, k1);
+                no.issue(t + 1, n1);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            compute(k0, n0);
+            if (t + 1 >= full) break;
+            wait_loads<0>();
+            step_barrier();
+            if (t + 2 < full) {
+                ko.issue(t + 2, k0);
+                no.issue(t + 2, n0);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            compute(k1, n1);
+        }
+    }
+    if (full * 64 < count) {
+        __syncthreads();
+        ko.tail(full, count, lane, k0);
+        no.tail(full, count, lane, n0);
+        __syncthreads();
+        compute(k0, n0);
+    }
+
+    const int i = lane & 15, g = lane >> 4;
+#pragma unroll
+    for (int b = 0; b < kBlkN; ++b) {
+        const int32_t n = nt0 + (wn * kBlkN + b) * 16 + i;
+        if (n >= N) continue;
+#pragma unroll
+        for (int a = 0; a < kBlkK; ++a) {
+            const int32_t k = kt0 + (wk * kBlkK + a) * 16 + g * 4;
+            if (k >= K) continue;
+            const int64_t at = (int64_t(e) * N + n) * K + k;
+            f32x4 v = acc[a][b];
+            if constexpr (F32) {
+                f32x4* p = reinterpret_cast<f32x4*>(dw + at * 4);
+                if constexpr (ACCUMULATE) v = *p + v;
+                *p = v;
+            } else {
+                v2i* p = reinterpret_cast<v2i*>(dw + at * 2);
+                if constexpr (ACCUMULATE) {
+                    const v2i o = *p;
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) {
+                        const uint32_t word = static_cast<uint32_t>(o[t >> 1]);
+                        v[t] += (t & 1) ? bf16_hi(word) : bf16_lo(word);
+                    }
+                }
+                *p = pack_bf16x4(v[0], v[1], v[2], v[3]);
+            }
+        }
+    }
+}
+
+int64_t wgrad_tiles(const ExpertWgradArgs& a) {
+    const int64_t nt = (int64_t(a.N) + kTileN - 1) / kTileN;
+    const int64_t kt = (int64_t(a.K) + kTileK - 1) / kTileK;
+    return nt * kt * a.E;
+}
+
+}  // namespace
+
+int64_t expert_wgrad_grid(const ExpertWgradArgs& a) {
+    const int64_t unit = int64_t(kExpertXcds) * kXcdChunk;
+    return (wgrad_tiles(a) + unit - 1) / unit * unit;
+}
+
+hipError_t launch_expert_wgrad(const ExpertWgradArgs& a, hipStream_t stream) {
+    auto kernel = a.f32 ? (a.accumulate ? expert_wgrad_kernel<true, true> : expert_wgrad_kernel<true, false>)
+                        : (a.accumulate ? expert_wgrad_kernel<false, true> : expert_wgrad_kernel<false, false>);
+    hipLaunchKernelGGL(kernel, dim3(static_cast<uint32_t>(expert_wgrad_grid(a))),
+                       dim3(kWaves * 64), 0, stream, static_cast<const char*>(a.dy),
+                       static_cast<const char*>(a.x), a.offsets, static_cast<int32_t>(a.max_rows),
+                       a.N, a.K, static_cast<int32_t>((int64_t(a.N) + kTileN - 1) / kTileN),
+                       static_cast<int32_t>((int64_t(a.K) + kTileK - 1) / kTileK), wgrad_tiles(a),
+                       static_cast<char*>(a.dw));
+    return hipGetLastError();
+}
+
+}  // namespace moe

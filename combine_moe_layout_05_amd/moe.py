@@ -103,6 +103,69 @@ def tile_expert_weights(weights: torch.Tensor) -> TiledExpertWeights:
     return TiledExpertWeights(data, E, n_out, k_in)
 
 
+def _call(name: str, dev: torch.device, *args) -> None:
+    """A library call on dev's current stream. Kernels launch on the current
+    device, so that is switched where the tensors live on another one."""
+    fn = getattr(L.load(), name)
+    if torch.cuda.current_device() == dev.index:
+        status = fn(*args, _stream(dev))
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, _stream(dev))
+    L.check(status, name)
+
+
+def _check_rows(name: str, t: torch.Tensor, dtype: torch.dtype, dim: int,
+                dev: torch.device) -> None:
+    if not t.is_cuda or t.device != dev:
+        raise ValueError(f"{name} must be on {dev if dev.type == 'cuda' else 'a GPU'}, "
+                         f"got {t.device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != dim or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dim}-d tensor")
+
+
+class Mxfp4ExpertWeights(NamedTuple):
+    """4-bit expert weights in the order the kernels read (mxfp4_expert_weights)."""
+    data: torch.Tensor       # uint8 [moe_mxfp4_weights_bytes], device
+    num_experts: int
+    n_out: int
+    k_in: int
+
+    def check(self, dev: torch.device) -> None:
+        """The kernels trust the packed buffer's size: it is checked here."""
+        _check_rows("packed weights", self.data, torch.uint8, 1, dev)
+        need = int(L.load().moe_mxfp4_weights_bytes(self.num_experts, self.n_out, self.k_in))
+        if self.data.numel() != need:
+            raise ValueError(f"packed weights must hold {need} bytes (moe_mxfp4_weights_bytes("
+                             f"{self.num_experts}, {self.n_out}, {self.k_in})), "
+                             f"got {self.data.numel()}")
+
+
+def _grouped_gemm_mxfp4(x_expert, weights: Mxfp4ExpertWeights, offsets, out, row_tile: int):
+    dev = x_expert.device
+    weights.check(dev)
+    _check_rows("x_expert", x_expert, torch.bfloat16, 2, dev)
+    _check_rows("offsets", offsets, torch.int32, 1, dev)
+    E, n_out, k_in = weights.num_experts, weights.n_out, weights.k_in
+    R = x_expert.shape[0]
+    if x_expert.shape[1] != k_in or offsets.shape[0] != E + 1:
+        raise ValueError("shapes: x_expert [R, k_in], weights [E, n_out, k_in], offsets [E+1]")
+    if row_tile != 0:
+        raise ValueError("4-bit weights take no row_tile")
+    flags = 0
+    if out is None:
+        out, flags = x_expert.new_empty((R, n_out)), L.MOE_GEMM_ZERO_TAIL
+    else:
+        _check_rows("out", out, torch.bfloat16, 2, dev)
+        if tuple(out.shape) != (R, n_out):
+            raise ValueError(f"out must be a contiguous bf16 [{R}, {n_out}] tensor on {dev}")
+    _call("moe_grouped_gemm_mxfp4", dev, x_expert.data_ptr(), weights.data.data_ptr(),
+          offsets.data_ptr(), E, R, k_in, n_out, out.data_ptr(), flags)
+    return out
+
+
 def grouped_gemm(x_expert: torch.Tensor, weights, offsets: torch.Tensor,
                  out: Optional[torch.Tensor] = None, *, row_tile: int = 0) -> torch.Tensor:
     """Expert step between dispatch and combine (moe_grouped_gemm): for each
@@ -112,8 +175,12 @@ def grouped_gemm(x_expert: torch.Tensor, weights, offsets: torch.Tensor,
     segment keep what `out` held.
 
     x_expert bf16 [R, k_in]; weights bf16 [E, n_out, k_in] or the
-    TiledExpertWeights of them (same results, faster); offsets int32 [E+1];
-    out bf16 [R, n_out] (allocated with torch.empty if None)."""
+    TiledExpertWeights of them (same results, faster), or 4-bit weights as
+    Mxfp4ExpertWeights (moe_grouped_gemm_mxfp4; rows from offsets[E] on of an
+    output it allocates are zero); offsets int32 [E+1]; out bf16 [R, n_out]
+    (allocated with torch.empty if None)."""
+    if isinstance(weights, Mxfp4ExpertWeights):
+        return _grouped_gemm_mxfp4(x_expert, weights, offsets, out, int(row_tile))
     dev = x_expert.device
     if isinstance(weights, TiledExpertWeights):
         E, n_out, k_in = weights.num_experts, weights.n_out, weights.k_in

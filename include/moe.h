@@ -401,6 +401,122 @@ int64_t moe_tiled_weights_bytes(int32_t num_experts, int32_t n_out, int32_t k_in
 int moe_tile_expert_weights(const void *d_weights, int32_t num_experts, int32_t n_out,
                             int32_t k_in, void *d_tiled, void *stream);
 
+/* ---- Expert feed-forward block -------------------------------------------
+ * The gated block on the expert-major rows: for every expert e and every row r
+ * of its segment [offsets[e], offsets[e+1]),
+ *   g = x[r] Wg[e]^T,  u = x[r] Wu[e]^T,  h[r] = act(g) * u,  y[r] = h[r] Wd[e]^T
+ * its gradients, and the same products with 4-bit weights. All calls below:
+ *   - rows, weights and outputs are bf16 unless stated, sums and the
+ *     activation fp32, each output rounded once to nearest even. The order of
+ *     a sum depends on the sizes of the call only, so equal calls give equal
+ *     bits;
+ *   - d_offsets int32 [num_experts + 1] in device memory, as for
+ *     moe_grouped_gemm (segments are clamped to [0, max_rows));
+ *   - rows outside every segment are never read. They are not written either,
+ *     except that MOE_GEMM_ZERO_TAIL sets the rows from offsets[num_experts]
+ *     on to +0.0;
+ *   - 0 <= max_rows <= INT32_MAX; with max_rows == 0 nothing is enqueued
+ *     (moe_grouped_gemm_backward_weight still writes its zeros);
+ *   - widths are multiples of 8 (more where stated) from 8 to
+ *     MOE_MAX_GEMM_WIDTH, 1 <= num_experts <= MOE_MAX_EXPERTS;
+ *   - bf16 and packed buffers are 16-byte aligned, outputs overlap no input;
+ *   - no context and no workspace. Violations: MOE_ERR_INVALID_ARG. */
+#define MOE_MAX_GEMM_WIDTH  (1 << 22)
+#define MOE_GEMM_ZERO_TAIL  1    /* +0.0 into the rows from offsets[num_experts] on */
+#define MOE_GEMM_ACCUMULATE 2    /* add to what the weight gradient holds */
+
+typedef enum moe_activation {
+    MOE_ACT_SILU = 0,            /* g / (1 + exp(-g)) */
+    MOE_ACT_GELU_TANH = 1        /* g/2 (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) */
+} moe_activation;
+
+/* First half of the block: h from x, both projections, the activation and the
+ * product in one launch.
+ *   d_x_expert  [max_rows][k_in]
+ *   d_weights   [num_experts][2 * n_hidden][k_in]: the gate rows, then the up
+ *               rows
+ *   d_h         [max_rows][n_hidden]
+ *   d_pre       float32 [max_rows][2 * n_hidden] receives [g | u] for the
+ *               backward (16-byte aligned), or NULL. Its rows outside the
+ *               segments are never written. In fp32, since a second rounding
+ *               to bf16 here would add as much error to the gradients as the
+ *               rounding of the gradient of [g | u] itself */
+int moe_gated_grouped_gemm(const void *d_x_expert, const void *d_weights,
+                           const int32_t *d_offsets, int32_t num_experts, int64_t max_rows,
+                           int32_t k_in, int32_t n_hidden, int32_t activation, void *d_h,
+                           float *d_pre, int32_t flags, void *stream);
+
+/* Second half of the block: out[r] = x[r] W[e]^T with row-major weights
+ * [num_experts][n_out][k_in], as moe_grouped_gemm computes it (another order
+ * of the sums), with the flags of this family. */
+int moe_grouped_gemm_forward(const void *d_x_expert, const void *d_weights,
+                             const int32_t *d_offsets, int32_t num_experts, int64_t max_rows,
+                             int32_t k_in, int32_t n_out, void *d_out, int32_t flags,
+                             void *stream);
+
+/* Gradient of out[r] = x[r] W[e]^T with respect to the rows:
+ *   d_grad_x[r][k] = sum over n of d_grad_out[r][n] * W[e][n][k]
+ *   d_grad_out [max_rows][n_out], d_weights [num_experts][n_out][k_in],
+ *   d_grad_x [max_rows][k_in] */
+int moe_grouped_gemm_backward_input(const void *d_grad_out, const void *d_weights,
+                                    const int32_t *d_offsets, int32_t num_experts,
+                                    int64_t max_rows, int32_t k_in, int32_t n_out,
+                                    void *d_grad_x, int32_t flags, void *stream);
+
+/* Gradient of the block's second half and of the gate in one launch: with
+ * dh = grad_out[r] Wd[e] (kept in fp32) and [g | u] = pre[r],
+ *   d_grad_pre[r] = [dh * u * act'(g) | dh * act(g)]
+ * the gradient of [g | u]; moe_grouped_gemm_backward_input with the first
+ * half's weights turns it into the gradient of x.
+ *   d_grad_out [max_rows][n_out], d_weights (Wd) [num_experts][n_out][n_hidden],
+ *   d_pre float32 and d_grad_pre bf16 [max_rows][2 * n_hidden] */
+int moe_gated_grouped_gemm_backward(const void *d_grad_out, const void *d_weights,
+                                    const float *d_pre, const int32_t *d_offsets,
+                                    int32_t num_experts, int64_t max_rows, int32_t n_hidden,
+                                    int32_t n_out, int32_t activation, void *d_grad_pre,
+                                    int32_t flags, void *stream);
+
+/* Gradient of out[r] = x[r] W[e]^T with respect to the weights:
+ *   d_grad_w[e][n][k] = sum over rows r of e's segment of
+ *                       d_grad_out[r][n] * d_x_expert[r][k]
+ * +0.0 for an expert without rows; with MOE_GEMM_ACCUMULATE the sum is added
+ * to what d_grad_w holds (one rounding of the total), and an expert without
+ * rows keeps its values. d_grad_w is [num_experts][n_out][k_in] of grad_dtype
+ * (MOE_BF16 or MOE_F32). MOE_GEMM_ZERO_TAIL does not apply. */
+int moe_grouped_gemm_backward_weight(const void *d_grad_out, const void *d_x_expert,
+                                     const int32_t *d_offsets, int32_t num_experts,
+                                     int64_t max_rows, int32_t k_in, int32_t n_out,
+                                     int32_t grad_dtype, void *d_grad_w, int32_t flags,
+                                     void *stream);
+
+/* 4-bit weights (the OCP microscaling format MXFP4): each value is 4 bits,
+ * e2m1 (0, 0.5, 1, 1.5, 2, 3, 4, 6 and a sign in bit 3), each 32 consecutive
+ * inputs of a row share a scale 2^(b - 127) given by its byte b (255: NaN).
+ * They are packed once into the order the kernels read and take
+ * moe_mxfp4_weights_bytes(...) bytes (-1 for sizes not supported); k_in is a
+ * multiple of 32.
+ *   d_values  uint8 [num_experts][n_out][k_in / 2], input 2i in the low half
+ *             of byte i (4-byte aligned)
+ *   d_scales  uint8 [num_experts][n_out][k_in / 32]
+ *   d_packed  16-byte aligned */
+int64_t moe_mxfp4_weights_bytes(int32_t num_experts, int32_t n_out, int32_t k_in);
+int moe_pack_mxfp4_weights(const void *d_values, const void *d_scales, int32_t num_experts,
+                           int32_t n_out, int32_t k_in, void *d_packed, void *stream);
+
+/* out[r] = x[r] W[e]^T with packed 4-bit weights; the weights' values are
+ * exact, x and out bf16. */
+int moe_grouped_gemm_mxfp4(const void *d_x_expert, const void *d_packed,
+                           const int32_t *d_offsets, int32_t num_experts, int64_t max_rows,
+                           int32_t k_in, int32_t n_out, void *d_out, int32_t flags,
+                           void *stream);
+
+/* moe_gated_grouped_gemm with packed 4-bit weights of n_out = 2 * n_hidden
+ * (gate rows, then up rows); n_hidden is a multiple of 16. */
+int moe_gated_grouped_gemm_mxfp4(const void *d_x_expert, const void *d_packed,
+                                 const int32_t *d_offsets, int32_t num_experts,
+                                 int64_t max_rows, int32_t k_in, int32_t n_hidden,
+                                 int32_t activation, void *d_h, int32_t flags, void *stream);
+
 /* Launch shape tuning (optional). moe_create picks every default from the
  * context's sizes (measured on MI355X); moe_get_tuning reports them. Each
  * token row is split into `segments` wavefront work items (1..16) and

@@ -1,0 +1,140 @@
+"""CPU tests of the expert block's host side: every refusal of the C entry
+points and of the Python binding happens before anything is enqueued."""
+import ctypes as C
+
+import pytest
+import torch
+
+import combine_moe_layout_05_amd as moe
+from combine_moe_layout_05_amd import _lib as L
+
+P = 1 << 40                # a device address that is never dereferenced
+OK, BAD = L.MOE_OK, L.MOE_ERR_INVALID_ARG
+MAX = L.MOE_MAX_GEMM_WIDTH
+
+
+@pytest.fixture(scope="module")
+def lib():
+    return L.load()
+
+
+# Each call with valid arguments but max_rows = 0, so that nothing launches.
+CALLS = {
+    "moe_gated_grouped_gemm": dict(
+        x=P, w=P, offsets=P, E=4, rows=0, k=64, n=32, act=0, out=P, pre=P, flags=1, stream=None),
+    "moe_grouped_gemm_forward": dict(
+        x=P, w=P, offsets=P, E=4, rows=0, k=64, n=32, out=P, flags=1, stream=None),
+    "moe_grouped_gemm_backward_input": dict(
+        x=P, w=P, offsets=P, E=4, rows=0, k=64, n=32, out=P, flags=1, stream=None),
+    "moe_gated_grouped_gemm_backward": dict(
+        x=P, w=P, pre=P, offsets=P, E=4, rows=0, k=32, n=64, act=1, out=P, flags=1, stream=None),
+    "moe_grouped_gemm_mxfp4": dict(
+        x=P, w=P, offsets=P, E=4, rows=0, k=64, n=32, out=P, flags=1, stream=None),
+    "moe_gated_grouped_gemm_mxfp4": dict(
+        x=P, w=P, offsets=P, E=4, rows=0, k=64, n=32, act=0, out=P, flags=1, stream=None),
+}
+
+
+def _bad_values(name, args):
+    """(argument, value) pairs the call must refuse."""
+    bad = [("E", 0), ("E", -1), ("E", L.MOE_MAX_EXPERTS + 1), ("rows", -1), ("rows", 1 << 31),
+           ("k", 0), ("k", 12), ("k", MAX + 8), ("n", 0), ("n", 20), ("n", MAX + 8), ("flags", 2),
+           ("flags", 4)]
+    if "mxfp4" in name:
+        bad += [("k", 40), ("k", 16)]
+    if name == "moe_gated_grouped_gemm_mxfp4":
+        bad += [("n", 24), ("n", MAX // 2 + 16)]
+    if "act" in args:
+        bad += [("act", 2), ("act", -1)]
+    return bad
+
+
+@pytest.mark.parametrize("name", sorted(CALLS))
+def test_entry_points_refuse_bad_sizes(lib, name):
+    fn, args = getattr(lib, name), CALLS[name]
+    assert fn(*args.values()) == OK
+    for key, value in _bad_values(name, args):
+        assert fn(*dict(args, **{key: value}).values()) == BAD, (key, value)
+
+
+@pytest.mark.parametrize("name", sorted(CALLS))
+def test_entry_points_refuse_bad_pointers(lib, name):
+    fn, args = getattr(lib, name), dict(CALLS[name], rows=8)
+    for key in ("x", "w", "offsets", "out", "pre"):
+        if key not in args:
+            continue
+        if not (key == "pre" and name == "moe_gated_grouped_gemm"):
+            assert fn(*dict(args, **{key: None}).values()) == BAD, key
+        off = 2 if key == "offsets" else 8
+        assert fn(*dict(args, **{key: P + off}).values()) == BAD, key
+
+
+def test_weight_gradient_refusals(lib):
+    args = dict(dy=P, x=P, offsets=P, E=4, rows=8, k=64, n=32, dtype=L.MOE_F32, out=P, flags=1,
+                stream=None)
+    fn = lib.moe_grouped_gemm_backward_weight
+    # flag 1 (the tail) does not apply here
+    assert fn(*args.values()) == BAD
+    args["flags"] = 2
+    for key, value in [("E", 0), ("E", L.MOE_MAX_EXPERTS + 1), ("rows", -1), ("rows", 1 << 31),
+                       ("k", 4), ("k", MAX + 8), ("n", 9), ("n", MAX + 8), ("dtype", 2),
+                       ("flags", 6), ("dy", None), ("x", None), ("offsets", None), ("out", None),
+                       ("dy", P + 8), ("x", P + 2), ("offsets", P + 1), ("out", P + 4),
+                       # more tiles than a launch takes
+                       ("n", MAX)]:
+        bad = dict(args, **{key: value})
+        if (key, value) == ("n", MAX):
+            bad.update(k=MAX, E=1024)
+        assert fn(*bad.values()) == BAD, (key, value)
+
+
+def test_grid_limit_is_refused(lib):
+    n = MAX
+    args = dict(CALLS["moe_grouped_gemm_forward"], rows=(1 << 31) - 1, k=64, n=n, E=1)
+    assert lib.moe_grouped_gemm_forward(*args.values()) == BAD
+
+
+def test_packed_sizes(lib):
+    size = lib.moe_mxfp4_weights_bytes
+    for E, N, K in [(1, 8, 32), (3, 24, 128), (256, 4096, 7168), (7, 2880, 2880)]:
+        blocks, steps = -(-N // 16), -(-K // 128)
+        assert size(E, N, K) == E * blocks * steps * (1024 + 64)
+    for bad in [(0, 8, 32), (1025, 8, 32), (1, 4, 32), (1, 12, 32), (1, 8, 16), (1, 8, 40),
+                (1, 8, 0), (1, MAX + 8, 32), (1, 8, MAX + 32), (1024, MAX, MAX)]:
+        assert size(*bad) == -1, bad
+
+
+def test_packing_refusals(lib):
+    fn = lib.moe_pack_mxfp4_weights
+    for args in [(None, P, 1, 8, 32, P), (P, None, 1, 8, 32, P), (P, P, 1, 8, 32, None),
+                 (P + 2, P, 1, 8, 32, P), (P, P, 1, 8, 32, P + 8), (P, P, 1, 8, 48, P)]:
+        assert fn(*args, None) == BAD, args
+
+
+def _cpu(*shape, dtype=torch.bfloat16):
+    return torch.zeros(shape, dtype=dtype)
+
+
+def test_binding_refuses_host_tensors():
+    off = _cpu(3, dtype=torch.int32)
+    x, w1, w2 = _cpu(4, 32), _cpu(2, 32, 32), _cpu(2, 32, 16)
+    packed = moe.Mxfp4ExpertWeights(_cpu(2 * 2 * 1088, dtype=torch.uint8), 2, 32, 32)
+    calls = [lambda: moe.gated_grouped_gemm(x, w1, off),
+             lambda: moe.grouped_gemm_forward(x, w1, off),
+             lambda: moe.grouped_gemm_backward_input(x, w1, off),
+             lambda: moe.gated_grouped_gemm_backward(x, w2, x, off),
+             lambda: moe.grouped_gemm_backward_weight(x, x, off),
+             lambda: moe.expert_ffn(x, w1, w2, off),
+             lambda: moe.grouped_gemm(x, packed, off),
+             lambda: moe.gated_grouped_gemm(x, packed, off),
+             lambda: moe.mxfp4_expert_weights(_cpu(2, 32, 16, dtype=torch.uint8),
+                                              _cpu(2, 32, 1, dtype=torch.uint8))]
+    for call in calls:
+        with pytest.raises(ValueError, match="GPU"):
+            call()
+
+
+def test_unknown_activation_is_refused():
+    with pytest.raises(ValueError, match="activation"):
+        moe.gated_grouped_gemm(_cpu(4, 32), _cpu(2, 32, 32), _cpu(3, dtype=torch.int32),
+                               activation="relu")
