@@ -4,8 +4,6 @@
 #include "expert_kernels.h"
 #include "expert_mma.h"
 
-#include <type_traits>
-
 namespace moe {
 namespace {
 
@@ -38,7 +36,6 @@ void expert_gemm_kernel(const char* __restrict__ rows, const char* __restrict__ 
                         const int32_t* __restrict__ offsets, int32_t E, int32_t max_rows,
                         int32_t red, int32_t feats, int32_t ftiles, int32_t act,
                         char* __restrict__ out, float* __restrict__ pre, int32_t zero_tail) {
-    constexpr int kBlkR = BT / kWavesR / 16;
     constexpr int kStages = BT == 256 ? 2 : 3;
     typedef typename WeightOperand<strided(OP)>::type Weights;
     typedef PackedOperand<BT, kWaves> Rows;
@@ -76,116 +73,47 @@ void expert_gemm_kernel(const char* __restrict__ rows, const char* __restrict__ 
     const int32_t f0 = ft * tile_feats(OP);
     const int64_t red_pitch = int64_t(red) * 2;
 
+    const int wf = wave % kWavesF, wr = wave / kWavesF;
     Weights wt;
-    Rows rt;
     if constexpr (strided(OP)) {
         // w[e] is [red][feats], features contiguous.
         const char* base = w + (int64_t(e) * red * feats + f0) * 2;
-        wt.init(wave, lane, int64_t(feats) * 2, base, min(kTileF, feats - f0));
+        wt.init(wave, lane, wf * kBlkF, int64_t(feats) * 2, base, min(kTileF, feats - f0));
     } else if constexpr (OP == ExpertOp::kGated) {
         // Each wavefront's 64 positions are 32 gate rows and the 32 up rows of
         // the same features, so the epilogue finds both in its own registers.
         const char* gate = w + (int64_t(e) * 2 * feats + f0) * red_pitch;
         const char* up = gate + int64_t(feats) * red_pitch;
         const int last = feats - f0 - 1;
-        wt.init(wave, lane, red_pitch, [&](int p0) { return (p0 & 32) ? up : gate; },
+        wt.init(wave, lane, wf * kBlkF, red_pitch, [&](int p0) { return (p0 & 32) ? up : gate; },
                 [&](int p) { return min((p >> 6) * 32 + (p & 31), last); });
     } else {
         const char* base = w + (int64_t(e) * feats + f0) * red_pitch;
         const int last = feats - f0 - 1;
-        wt.init(wave, lane, red_pitch, [&](int) { return base; },
+        wt.init(wave, lane, wf * kBlkF, red_pitch, [&](int) { return base; },
                 [&](int p) { return min(p, last); });
     }
-    {
-        const char* base = rows + int64_t(row0) * red_pitch;
-        rt.init(wave, lane, red_pitch, [&](int) { return base; },
-                [&](int p) { return min(p, nrows - 1); });
-    }
-    const int wf = wave % kWavesF, wr = wave / kWavesF;
-
+    // The loop exists for each 64-row count up to the tile's and is chosen once
+    // per workgroup, so that a segment's last tile costs what its rows need.
+    auto run = [&](auto parts) {
+    constexpr int kRowsUsed = decltype(parts)::value * 64;
+    constexpr int kBlkR = kRowsUsed / kWavesR / 16;
+    PackedOperand<kRowsUsed, kWaves> rt;
+    const char* rbase = rows + int64_t(row0) * red_pitch;
+    rt.init(wave, lane, wr * kBlkR, red_pitch, [&](int) { return rbase; },
+            [&](int p) { return min(p, nrows - 1); });
     f32x4 acc[kBlkF][kBlkR];
-#pragma unroll
-    for (int a = 0; a < kBlkF; ++a)
-#pragma unroll
-        for (int b = 0; b < kBlkR; ++b) acc[a][b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-
-    auto compute = [&](const v4i* wb, const v4i* rb) {
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            bf16x8 fa[kBlkF], fb[kBlkR];
-#pragma unroll
-            for (int a = 0; a < kBlkF; ++a) fa[a] = wt.frag(wb, wf * kBlkF + a, s);
-#pragma unroll
-            for (int b = 0; b < kBlkR; ++b) fb[b] = rt.frag(rb, wr * kBlkR + b, s);
-#pragma unroll
-            for (int b = 0; b < kBlkR; ++b)
-#pragma unroll
-                for (int a = 0; a < kBlkF; ++a)
-                    acc[a][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[a], fb[b], acc[a][b], 0,
-                                                                        0, 0);
-        }
-    };
-    constexpr int kLoads = Weights::kLoads + Rows::kLoads;
     const int32_t full = red / 64;
-    // Stage P of the ring: its own arrays, so that the compiler sees that
-    // loads into one stage do not touch the stage being read.
-    auto issue = [&](auto p, int64_t t) {
-        constexpr int P = decltype(p)::value % kStages;
-        wt.issue(t, P == 0 ? w0 : P == 1 ? w1 : w2);
-        rt.issue(t, P == 0 ? r0 : P == 1 ? r1 : r2);
-    };
-    auto use = [&](auto p) {
-        constexpr int P = decltype(p)::value % kStages;
-        compute(P == 0 ? w0 : P == 1 ? w1 : w2, P == 0 ? r0 : P == 1 ? r1 : r2);
-    };
-    using std::integral_constant;
-    if (full > 0) {
-        issue(integral_constant<int, 0>{}, 0);
-        if (kStages > 2 && full > 1) issue(integral_constant<int, 1>{}, 1);
-        int32_t t = 0;
-        auto step = [&](auto p, int32_t at) {
-            constexpr int P = decltype(p)::value;
-            wait_loads<kLoads * (kStages - 2)>();
-            step_barrier();
-            issue(integral_constant<int, P + kStages - 1>{}, at + kStages - 1);
-            // Keeps the loads here: sunk to the end of the step, as the
-            // scheduler would have it, their latency would not be covered.
-            __builtin_amdgcn_sched_barrier(0);
-            use(p);
-        };
-        for (; t + 2 * kStages - 2 < full; t += kStages) {
-            step(integral_constant<int, 0>{}, t);
-            step(integral_constant<int, 1>{}, t + 1);
-            if constexpr (kStages > 2) step(integral_constant<int, 2>{}, t + 2);
-        }
-        // The last steps: fewer loads are in flight, all are waited for.
-        auto last = [&](auto p, int32_t at) {
-            constexpr int P = decltype(p)::value;
-            if (at >= full) return;
-            wait_loads<0>();
-            step_barrier();
-            if (at + kStages - 1 < full)
-                issue(integral_constant<int, P + kStages - 1>{}, at + kStages - 1);
-            __builtin_amdgcn_sched_barrier(0);
-            use(p);
-        };
-        last(integral_constant<int, 0>{}, t);
-        last(integral_constant<int, 1>{}, t + 1);
-        if constexpr (kStages > 2) {
-            last(integral_constant<int, 2>{}, t + 2);
-            last(integral_constant<int, 3>{}, t + 3);
-        }
-    }
-    if (full * 64 < red) {
-        __syncthreads();
-        if constexpr (strided(OP))
-            wt.tail(full, red, lane, w0);
-        else
-            wt.tail(full, red / 8, lane, w0);
-        rt.tail(full, red / 8, lane, r0);
-        __syncthreads();
-        compute(w0, r0);
-    }
+    accumulate<kStages>(
+        wt, rt, Buffers{w0, w1, w2}, Buffers{r0, r1, r2}, full, full * 64 < red,
+        [&] {
+            if constexpr (strided(OP))
+                wt.tail(full, red, lane, w0);
+            else
+                wt.tail(full, red / 8, lane, w0);
+            rt.tail(full, red / 8, lane, r0);
+        },
+        acc);
 
     // acc[a][b][t] belongs to row 16b + lane % 16 and position 16a + 4 (lane /
     // 16) + t of the wavefront.
@@ -240,6 +168,16 @@ void expert_gemm_kernel(const char* __restrict__ rows, const char* __restrict__ 
             }
         }
     }
+    };
+    const int parts = (nrows + 63) / 64;
+    if constexpr (BT > 64) {
+        if (parts == 2) return run(std::integral_constant<int, 2>{});
+    }
+    if constexpr (BT > 128) {
+        if (parts == 3) return run(std::integral_constant<int, 3>{});
+        if (parts == 4) return run(std::integral_constant<int, 4>{});
+    }
+    run(std::integral_constant<int, 1>{});
 }
 
 int32_t row_tile(const ExpertGemmArgs& a) {

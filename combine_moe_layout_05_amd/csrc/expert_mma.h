@@ -6,6 +6,7 @@
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "moe_lanes.h"
 
@@ -115,13 +116,27 @@ __device__ __forceinline__ void expert_zero_tail(v4i* out, int64_t row0, int64_t
 typedef __attribute__((address_space(3))) v4i lds_v4i;
 typedef __attribute__((address_space(3))) bf16x4 lds_bf16x4;
 
-// Asynchronous 16-byte load of every lane into LDS: lane l's bytes land at
-// dst + 16 l (dst is the same for the whole wavefront).
-__device__ __forceinline__ void load_to_lds(const char* src, v4i* dst) {
+// Asynchronous 16-byte load of every lane into LDS: lane l reads base + off and
+// its bytes land at dst + 16 l (base and dst are the same for the whole
+// wavefront).
+__device__ __forceinline__ void load_to_lds(const char* base, uint32_t off, v4i* dst) {
     __builtin_amdgcn_global_load_lds(
-        (const __attribute__((address_space(1))) void*)(src),
+        (const __attribute__((address_space(1))) void*)(base + off),
         (__attribute__((address_space(3))) void*)(dst), 16, 0, 0);
 }
+
+// base + bytes in scalar registers (base is uniform over the wavefront). The
+// empty asm keeps the compiler from adding a lane's offset to base ahead of a
+// loop, which would hold a 64-bit address per load in vector registers.
+__device__ __forceinline__ const char* scalar_address(const char* base, int64_t bytes) {
+    uint64_t p = reinterpret_cast<uint64_t>(base) + static_cast<uint64_t>(bytes);
+    asm("" : "+s"(p));
+    return reinterpret_cast<const char*>(p);
+}
+
+// The value of a register, as something the compiler knows nothing about: what
+// is computed from it stays behind this point.
+__device__ __forceinline__ void reform(uint32_t& v) { asm volatile("" : "+v"(v)); }
 
 // Barrier without the full memory drain of __syncthreads(): loads in flight
 // into other buffers stay in flight. The empty asm statements keep the
@@ -147,58 +162,65 @@ __device__ __forceinline__ void wait_lds_reads() {
 
 // An operand whose sum index is contiguous in memory: EXT positions (rows or
 // features) x 64 elements of the sum, 128 bytes per position. 16-byte chunk c
-// of position p sits at chunk c ^ swz(p), which makes the fragment reads (16
-// consecutive positions at one chunk) hit 16 distinct bank groups. A direct
+// of position p sits at chunk c ^ swz(p). A 16-byte LDS read serves 16 lanes at
+// a time, lanes 0-3, 12-15, 20-23 and 24-27 of a half wavefront together, then
+// the others; with p / 2 % 8 both sets, which hold all 16 positions of a
+// fragment at chunks c and c ^ 1, fall into 16 distinct bank groups. A direct
 // load writes 64 consecutive chunks, so the swizzle is applied to the address
 // each lane reads.
 template <int EXT, int WAVES>
 struct PackedOperand {
     static constexpr int kChunks = EXT * 8;
     static constexpr int kLoads = EXT / (8 * WAVES);
+    static constexpr int kFragReads = 1;
     static_assert(EXT % (8 * WAVES) == 0, "whole wavefront loads");
     const char* base[kLoads];  // wavefront-uniform
     uint32_t off[kLoads];
-    int32_t chunk[kLoads];
     int wave;
-    uint32_t frag_at[2];       // chunk of this lane's fragment, halves of a step
+    uint32_t frag_at;          // byte of this lane's fragment of block blk0, first half
 
-    __device__ static int swz(int p) { return ((p & 15) ^ ((p & 15) >> 3)) & 7; }
+    __device__ static int swz(int p) { return (p >> 1) & 7; }
 
+    // The chunk lane `lane` loads for load j.
+    __device__ int chunk_of(int j, int lane) const {
+        return (lane & 7) ^ swz((wave + WAVES * j) * 8 + (lane >> 3));
+    }
     // row(p) gives the matrix row of position p relative to base_of(p); both
     // are uniform over groups of 8 positions except for the row itself.
     template <class Base, class Row>
-    __device__ void init(int wave_, int lane, int64_t pitch, Base base_of, Row row) {
+    __device__ void init(int wave_, int lane, int blk0, int64_t pitch, Base base_of, Row row) {
         wave = wave_;
 #pragma unroll
         for (int j = 0; j < kLoads; ++j) {
             const int p0 = (wave + WAVES * j) * 8;
             const int p = p0 + (lane >> 3);
-            chunk[j] = (lane & 7) ^ swz(p);
             base[j] = base_of(p0);
-            off[j] = static_cast<uint32_t>(row(p) * pitch) + chunk[j] * 16;
+            off[j] = static_cast<uint32_t>(row(p) * pitch) + chunk_of(j, lane) * 16;
         }
         const int i = lane & 15, g = lane >> 4;
-#pragma unroll
-        for (int s = 0; s < 2; ++s) frag_at[s] = i * 8 + ((4 * s + g) ^ swz(i));
+        frag_at = ((blk0 * 16 + i) * 8 + (g ^ swz(i))) * 16;
     }
     __device__ void issue(int64_t step, v4i* buf) const {
 #pragma unroll
         for (int j = 0; j < kLoads; ++j)
-            load_to_lds(base[j] + step * 128 + off[j], buf + (wave + WAVES * j) * 64);
+            load_to_lds(scalar_address(base[j], step * 128), off[j],
+                        buf + (wave + WAVES * j) * 64);
     }
     // The last, partial step: chunks at or past `chunks` of the row are zero.
     __device__ void tail(int64_t step, int32_t chunks, int lane, v4i* buf) const {
 #pragma unroll
         for (int j = 0; j < kLoads; ++j) {
             v4i v = {0, 0, 0, 0};
-            if (step * 8 + chunk[j] < chunks)
+            if (step * 8 + chunk_of(j, lane) < chunks)
                 v = *reinterpret_cast<const v4i*>(base[j] + step * 128 + off[j]);
             buf[(wave + WAVES * j) * 64 + lane] = v;
         }
     }
-    // Positions [16 blk, 16 blk + 16), half s of the step.
-    __device__ bf16x8 frag(const v4i* buf, int blk, int s) const {
-        return __builtin_bit_cast(bf16x8, buf[frag_at[s] + blk * 128]);
+    // Positions [16 (blk0 + b), + 16), half s of the step: chunk 4s + g, so
+    // the halves differ in one address bit.
+    __device__ bf16x8 frag(const v4i* buf, int b, int s) const {
+        const char* p = reinterpret_cast<const char*>(buf) + (frag_at ^ (64 * s)) + b * 2048;
+        return __builtin_bit_cast(bf16x8, *reinterpret_cast<const v4i*>(p));
     }
 };
 
@@ -213,19 +235,21 @@ struct StridedOperand {
     static constexpr int kRowChunks = EXT / 8;
     static constexpr int kChunks = 64 * kRowChunks;
     static constexpr int kLoads = kChunks / (64 * WAVES);
+    static constexpr int kFragReads = 2;
     static_assert(EXT % 128 == 0 && kChunks % (64 * WAVES) == 0, "whole wavefront loads");
     const char* base;          // wavefront-uniform
     int64_t step_bytes;
     uint32_t off[kLoads];
     int wave;
-    uint32_t frag_row;         // byte of this lane's first sum row
-    int fx;                    // this lane's block swizzle
+    uint32_t frag_at;          // byte of this lane's fragment of block blk0, first half
 
     __device__ static int fswz(int k) { return (k & 3) | ((k >> 1) & 4); }
 
     // base_: element (first sum row, first position) of the tile; positions
-    // at or past `width` (a multiple of 8) read the last valid chunk.
-    __device__ void init(int wave_, int lane, int64_t pitch, const char* base_, int32_t width) {
+    // at or past `width` (a multiple of 8) read the last valid chunk. blk0 is
+    // a multiple of the number of blocks read from it (a power of two).
+    __device__ void init(int wave_, int lane, int blk0, int64_t pitch, const char* base_,
+                         int32_t width) {
         wave = wave_;
         base = base_;
         step_bytes = pitch * 64;
@@ -237,13 +261,13 @@ struct StridedOperand {
             off[j] = static_cast<uint32_t>(k * pitch) + min(c, width / 8 - 1) * 16;
         }
         const int i = lane & 15, g = lane >> 4;
-        fx = (i >> 2) | ((g & 1) << 2);
-        frag_row = (8 * g + (i >> 2)) * (EXT * 2) + (i & 3) * 8;
+        const int fx = (i >> 2) | ((g & 1) << 2);
+        frag_at = (8 * g + (i >> 2)) * (EXT * 2) + (i & 3) * 8 + ((blk0 ^ fx) * 32);
     }
     __device__ void issue(int64_t step, v4i* buf) const {
+        const char* at = scalar_address(base, step * step_bytes);
 #pragma unroll
-        for (int j = 0; j < kLoads; ++j)
-            load_to_lds(base + step * step_bytes + off[j], buf + (wave + WAVES * j) * 64);
+        for (int j = 0; j < kLoads; ++j) load_to_lds(at, off[j], buf + (wave + WAVES * j) * 64);
     }
     // The last, partial step: sum rows at or past `rows` (counted from the
     // first step) are zero.
@@ -257,14 +281,137 @@ struct StridedOperand {
             buf[q] = v;
         }
     }
-    __device__ bf16x8 frag(const v4i* buf, int blk, int s) const {
-        const char* p = reinterpret_cast<const char*>(buf) + frag_row + ((blk ^ fx) * 32) +
-                        s * (32 * EXT * 2);
+    __device__ bf16x8 frag(const v4i* buf, int b, int s) const {
+        const char* p = reinterpret_cast<const char*>(buf) + (frag_at ^ (b * 32)) + s * (32 * EXT * 2);
         const bf16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4*)(p));
         const bf16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4*)(p + 4 * EXT * 2));
         return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
     }
 };
+
+// The LDS buffers of an operand's stages: distinct arrays, so that the compiler
+// sees that loads into one stage do not touch the stage being read.
+struct Buffers {
+    v4i* stage[3];
+};
+
+// acc[a][b] = the products of A's 16-position block blk0 + a with B's block
+// blk0 + b, summed over `full` steps of 64 and, with has_tail, a partial one
+// that write_tail() puts into the first buffers. Every wavefront of the
+// workgroup calls it.
+//
+// A step is two halves of 32. While the products of one half run, the LDS reads
+// of the next half go out between them, so the matrix cores wait neither for
+// LDS nor for memory: the second half is read during the first one's products;
+// then every wavefront has read the whole step, and after the step's one
+// barrier its buffers take the loads of step + STAGES, and the next step's
+// first half is read during the second one's products.
+template <int STAGES, int NA, int NB, class A, class B, class Tail>
+__device__ __forceinline__ void accumulate(const A& opa, const B& opb, const Buffers& bufa,
+                                           const Buffers& bufb, int32_t full, bool has_tail,
+                                           Tail write_tail,
+                                           f32x4 (&acc)[NA][NB]) {
+    struct Frags {
+        bf16x8 a[NA], b[NB];
+    };
+    constexpr int kLoads = A::kLoads + B::kLoads;
+    constexpr int kReads = NA * A::kFragReads + NB * B::kFragReads;  // LDS reads of a half
+#pragma unroll
+    for (int a = 0; a < NA; ++a)
+#pragma unroll
+        for (int b = 0; b < NB; ++b) acc[a][b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    auto multiply = [&](const Frags& d) {
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int a = 0; a < NA; ++a)
+                acc[a][b] =
+                    __builtin_amdgcn_mfma_f32_16x16x32_bf16(d.a[a], d.b[b], acc[a][b], 0, 0, 0);
+    };
+    // Every half forms its addresses anew from a few registers: what the
+    // compiler would form ahead of the loop does not fit the registers.
+    auto issue = [&](int stage, int64_t t) {
+        A oa = opa;
+        B ob = opb;
+#pragma unroll
+        for (int j = 0; j < A::kLoads; ++j) reform(oa.off[j]);
+#pragma unroll
+        for (int j = 0; j < B::kLoads; ++j) reform(ob.off[j]);
+        oa.issue(t, bufa.stage[stage]);
+        ob.issue(t, bufb.stage[stage]);
+    };
+    auto fetch_half = [&](int stage, int s, Frags& d) {
+        A oa = opa;
+        B ob = opb;
+        reform(oa.frag_at);
+        reform(ob.frag_at);
+#pragma unroll
+        for (int a = 0; a < NA; ++a) d.a[a] = oa.frag(bufa.stage[stage], a, s);
+#pragma unroll
+        for (int b = 0; b < NB; ++b) d.b[b] = ob.frag(bufb.stage[stage], b, s);
+    };
+    // The order within a half: an LDS read after every few products.
+    auto spread = [&] {
+        constexpr int per = NA * NB / kReads > 0 ? NA * NB / kReads : 1;
+#pragma unroll
+        for (int q = 0; q < kReads; ++q) {
+            __builtin_amdgcn_sched_group_barrier(0x008, per, 0);
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    Frags lo, hi;
+    auto step = [&](auto p, int32_t at) {
+        constexpr int P = decltype(p)::value;
+        fetch_half(P, 1, hi);
+        multiply(lo);
+        spread();
+        // The next step has landed: at most the loads of the ones after it
+        // are in flight.
+        if (STAGES > 2 && at + STAGES - 1 < full)
+            wait_loads<kLoads*(STAGES - 2)>();
+        else
+            wait_loads<0>();
+        step_barrier();
+        if (at + STAGES < full) issue(P, at + STAGES);
+        // After the last step this reads what an earlier one left; it is not
+        // used.
+        fetch_half((P + 1) % STAGES, 0, lo);
+        multiply(hi);
+        spread();
+    };
+    if (full > 0) {
+        issue(0, 0);
+        if (full > 1) issue(1, 1);
+        if (STAGES > 2 && full > 2) issue(2, 2);
+        if (full >= STAGES)
+            wait_loads<kLoads*(STAGES - 1)>();
+        else
+            wait_loads<0>();
+        step_barrier();
+        fetch_half(0, 0, lo);
+        using std::integral_constant;
+        for (int32_t t = 0;; t += STAGES) {
+            step(integral_constant<int, 0>{}, t);
+            if (t + 1 >= full) break;
+            step(integral_constant<int, 1>{}, t + 1);
+            if (t + 2 >= full) break;
+            if constexpr (STAGES > 2) {
+                step(integral_constant<int, 2>{}, t + 2);
+                if (t + 3 >= full) break;
+            }
+        }
+    }
+    if (has_tail) {
+        __syncthreads();
+        write_tail();
+        __syncthreads();
+        fetch_half(0, 0, lo);
+        fetch_half(0, 1, hi);
+        multiply(lo);
+        multiply(hi);
+    }
+}
 
 // act(g) and its derivative in fp32. silu(g) = g sigmoid(g); the tanh form of
 // gelu is g sigmoid(2z) with z = sqrt(2/pi) (g + 0.044715 g^3), which loses no

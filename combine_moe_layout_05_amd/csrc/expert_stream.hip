@@ -133,7 +133,7 @@ void expert_stream_kernel(const char* __restrict__ rows, const char* __restrict_
     };
     // Rows: chunk c of row r sits at chunk c ^ swizzle(r) of the row's step,
     // so that 16 rows at one chunk fall into distinct LDS banks.
-    auto swz = [](int r) { return MXFP4 ? r : ((r ^ (r >> 3)) & 7); };
+    auto swz = [](int r) { return MXFP4 ? r : (r >> 1) & 7; };
     const int lr = lane / S::kRowChunks, lp = lane % S::kRowChunks;
     const char* xbase = rows + int64_t(row0) * pitch;
     auto load_x = [&](int32_t t, v4i* buf) {
@@ -141,9 +141,8 @@ void expert_stream_kernel(const char* __restrict__ rows, const char* __restrict_
         for (int j = 0; j < S::kRowLoads; ++j) {
             const int r = lr + j * S::kRowsPerLoad;
             if (j * S::kRowsPerLoad < nrows)
-                load_to_lds(xbase + min(r, nrows - 1) * pitch + int64_t(t) * (S::kElems * 2) +
-                                (lp ^ swz(r)) * 16,
-                            buf + j * 64);
+                load_to_lds(xbase + min(r, nrows - 1) * pitch + int64_t(t) * (S::kElems * 2),
+                            (lp ^ swz(r)) * 16, buf + j * 64);
         }
     };
     f32x4 acc[kBlocks];

@@ -4,8 +4,6 @@
 #include "expert_kernels.h"
 #include "expert_mma.h"
 
-#include <type_traits>
-
 namespace moe {
 namespace {
 
@@ -42,62 +40,19 @@ void expert_wgrad_kernel(const char* __restrict__ dy, const char* __restrict__ x
 
     Kop ko;
     Nop no;
-    ko.init(wave, lane, int64_t(K) * 2, x + (int64_t(s0) * K + kt0) * 2, min(kTileK, K - kt0));
-    no.init(wave, lane, int64_t(N) * 2, dy + (int64_t(s0) * N + nt0) * 2, min(kTileN, N - nt0));
     const int wk = wave % kWavesK, wn = wave / kWavesK;
+    ko.init(wave, lane, wk * kBlkK, int64_t(K) * 2, x + (int64_t(s0) * K + kt0) * 2, min(kTileK, K - kt0));
+    no.init(wave, lane, wn * kBlkN, int64_t(N) * 2, dy + (int64_t(s0) * N + nt0) * 2, min(kTileN, N - nt0));
 
     f32x4 acc[kBlkK][kBlkN];
-#pragma unroll
-    for (int a = 0; a < kBlkK; ++a)
-#pragma unroll
-        for (int b = 0; b < kBlkN; ++b) acc[a][b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    auto compute = [&](const v4i* kb, const v4i* nb) {
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            bf16x8 fa[kBlkK], fb[kBlkN];
-#pragma unroll
-            for (int a = 0; a < kBlkK; ++a) fa[a] = ko.frag(kb, wk * kBlkK + a, s);
-#pragma unroll
-            for (int b = 0; b < kBlkN; ++b) fb[b] = no.frag(nb, wn * kBlkN + b, s);
-#pragma unroll
-            for (int b = 0; b < kBlkN; ++b)
-#pragma unroll
-                for (int a = 0; a < kBlkK; ++a)
-                    acc[a][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[a], fb[b], acc[a][b], 0,
-                                                                        0, 0);
-        }
-    };
     const int32_t full = count / 64;
-    if (full > 0) {
-        ko.issue(0, k0);
-        no.issue(0, n0);
-        for (int32_t t = 0; t < full; t += 2) {
-            wait_loads<0>();
-            step_barrier();
-            if (t + 1 < full) {
-                ko.issue(t + 1, k1);
-                no.issue(t + 1, n1);
-            }
-            __builtin_amdgcn_sched_barrier(0);
-            compute(k0, n0);
-            if (t + 1 >= full) break;
-            wait_loads<0>();
-            step_barrier();
-            if (t + 2 < full) {
-                ko.issue(t + 2, k0);
-                no.issue(t + 2, n0);
-            }
-            __builtin_amdgcn_sched_barrier(0);
-            compute(k1, n1);
-        }
-    }
-    if (full * 64 < count) {
-        __syncthreads();
-        ko.tail(full, count, lane, k0);
-        no.tail(full, count, lane, n0);
-        __syncthreads();
-        compute(k0, n0);
-    }
+    accumulate<2>(
+        ko, no, Buffers{k0, k1, k0}, Buffers{n0, n1, n0}, full, full * 64 < count,
+        [&] {
+            ko.tail(full, count, lane, k0);
+            no.tail(full, count, lane, n0);
+        },
+        acc);
 
     const int i = lane & 15, g = lane >> 4;
 #pragma unroll
