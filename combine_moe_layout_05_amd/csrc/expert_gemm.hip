@@ -38,11 +38,7 @@ void expert_gemm_kernel(const char* __restrict__ rows, const char* __restrict__ 
                         char* __restrict__ out, float* __restrict__ pre, int32_t zero_tail) {
     constexpr int kStages = BT == 256 ? 2 : 3;
     typedef typename WeightOperand<strided(OP)>::type Weights;
-    typedef PackedOperand<BT, kWaves> Rows;
-    __shared__ v4i w0[Weights::kChunks], w1[Weights::kChunks];
-    __shared__ v4i w2[kStages > 2 ? Weights::kChunks : 1];
-    __shared__ v4i r0[Rows::kChunks], r1[Rows::kChunks];
-    __shared__ v4i r2[kStages > 2 ? Rows::kChunks : 1];
+    __shared__ v4i lds[kStages * (Weights::kChunks + PackedOperand<BT, kWaves>::kChunks)];
     __shared__ int32_t info[4];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -103,17 +99,10 @@ void expert_gemm_kernel(const char* __restrict__ rows, const char* __restrict__ 
     rt.init(wave, lane, wr * kBlkR, red_pitch, [&](int) { return rbase; },
             [&](int p) { return min(p, nrows - 1); });
     f32x4 acc[kBlkF][kBlkR];
-    const int32_t full = red / 64;
-    accumulate<kStages>(
-        wt, rt, Buffers{w0, w1, w2}, Buffers{r0, r1, r2}, full, full * 64 < red,
-        [&] {
-            if constexpr (strided(OP))
-                wt.tail(full, red, lane, w0);
-            else
-                wt.tail(full, red / 8, lane, w0);
-            rt.tail(full, red / 8, lane, r0);
-        },
-        acc);
+    const Accumulator<kStages, kBlkF, kBlkR, Weights, PackedOperand<kRowsUsed, kWaves>> sums{lds,
+                                                                                             lane};
+    sums.start(wt, rt, red);
+    sums.template run<0>(wt, rt, red, false, acc);
 
     // acc[a][b][t] belongs to row 16b + lane % 16 and position 16a + 4 (lane /
     // 16) + t of the wavefront.

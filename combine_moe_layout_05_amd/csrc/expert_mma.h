@@ -118,20 +118,23 @@ typedef __attribute__((address_space(3))) bf16x4 lds_bf16x4;
 
 // Asynchronous 16-byte load of every lane into LDS: lane l reads base + off and
 // its bytes land at dst + 16 l (base and dst are the same for the whole
-// wavefront).
+// wavefront). The instruction has no register result; its bytes are in LDS once
+// wait_loads() has seen it finish (and, for other wavefronts, after a barrier
+// behind that); m0 is a register the compiler never keeps a value in. Written
+// out, since the compiler's own form of it makes every
+// later LDS read wait for all such loads wherever control flow joins, which
+// takes the loads of later steps out of flight.
 __device__ __forceinline__ void load_to_lds(const char* base, uint32_t off, v4i* dst) {
-    __builtin_amdgcn_global_load_lds(
-        (const __attribute__((address_space(1))) void*)(base + off),
-        (__attribute__((address_space(3))) void*)(dst), 16, 0, 0);
-}
-
-// base + bytes in scalar registers (base is uniform over the wavefront). The
-// empty asm keeps the compiler from adding a lane's offset to base ahead of a
-// loop, which would hold a 64-bit address per load in vector registers.
-__device__ __forceinline__ const char* scalar_address(const char* base, int64_t bytes) {
-    uint64_t p = reinterpret_cast<uint64_t>(base) + static_cast<uint64_t>(bytes);
-    asm("" : "+s"(p));
-    return reinterpret_cast<const char*>(p);
+    const uint32_t lds = static_cast<uint32_t>(
+        reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) void*)(dst)));
+    const uint64_t b = reinterpret_cast<uint64_t>(base);
+    const uint64_t lo = static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<uint32_t>(b)));
+    const uint64_t hi =
+        static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<uint32_t>(b >> 32)));
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+                 :
+                 : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(off), "s"(lo | (hi << 32))
+                 : "memory");
 }
 
 // The value of a register, as something the compiler knows nothing about: what
@@ -155,8 +158,8 @@ __device__ __forceinline__ void wait_loads() {
     __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4));
 }
 
-// Waits until all this wavefront's LDS reads have returned.
-__device__ __forceinline__ void wait_lds_reads() {
+// Waits until all this wavefront's LDS accesses are done.
+__device__ __forceinline__ void wait_lds() {
     __builtin_amdgcn_s_waitcnt(15 | (3 << 14) | (7 << 4));
 }
 
@@ -203,18 +206,25 @@ struct PackedOperand {
     __device__ void issue(int64_t step, v4i* buf) const {
 #pragma unroll
         for (int j = 0; j < kLoads; ++j)
-            load_to_lds(scalar_address(base[j], step * 128), off[j],
+            load_to_lds(base[j] + step * 128, off[j],
                         buf + (wave + WAVES * j) * 64);
     }
-    // The last, partial step: chunks at or past `chunks` of the row are zero.
-    __device__ void tail(int64_t step, int32_t chunks, int lane, v4i* buf) const {
+    // The last, partial step holds `left` (1..63) of the sum. Its loads read
+    // something valid past them, which fix() replaces by zeros in LDS.
+    __device__ void issue_partial(int64_t step, int left, int lane, v4i* buf) const {
 #pragma unroll
         for (int j = 0; j < kLoads; ++j) {
-            v4i v = {0, 0, 0, 0};
-            if (step * 8 + chunk_of(j, lane) < chunks)
-                v = *reinterpret_cast<const v4i*>(base[j] + step * 128 + off[j]);
-            buf[(wave + WAVES * j) * 64 + lane] = v;
+            const uint32_t c = chunk_of(j, lane);
+            load_to_lds(base[j] + step * 128,
+                        off[j] - (c * 8 < static_cast<uint32_t>(left) ? 0 : c * 16),
+                        buf + (wave + WAVES * j) * 64);
         }
+    }
+    __device__ void fix(int left, int lane, v4i* buf) const {
+#pragma unroll
+        for (int j = 0; j < kLoads; ++j)
+            if (chunk_of(j, lane) * 8 >= left)
+                buf[(wave + WAVES * j) * 64 + lane] = v4i{0, 0, 0, 0};
     }
     // Positions [16 (blk0 + b), + 16), half s of the step: chunk 4s + g, so
     // the halves differ in one address bit.
@@ -265,21 +275,29 @@ struct StridedOperand {
         frag_at = (8 * g + (i >> 2)) * (EXT * 2) + (i & 3) * 8 + ((blk0 ^ fx) * 32);
     }
     __device__ void issue(int64_t step, v4i* buf) const {
-        const char* at = scalar_address(base, step * step_bytes);
+        const char* at = base + step * step_bytes;
 #pragma unroll
         for (int j = 0; j < kLoads; ++j) load_to_lds(at, off[j], buf + (wave + WAVES * j) * 64);
     }
-    // The last, partial step: sum rows at or past `rows` (counted from the
-    // first step) are zero.
-    __device__ void tail(int64_t step, int64_t rows, int lane, v4i* buf) const {
+    // The last, partial step holds `left` (1..63) sum rows. The loads past
+    // them read its first row, which fix() replaces by zeros in LDS.
+    __device__ int row_of(int j, int lane) const {
+        return ((wave + WAVES * j) * 64 + lane) / kRowChunks;
+    }
+    __device__ void issue_partial(int64_t step, int left, int lane, v4i* buf) const {
+        const char* at = base + step * step_bytes;
+        const uint32_t pitch = static_cast<uint32_t>(step_bytes / 64);
 #pragma unroll
         for (int j = 0; j < kLoads; ++j) {
-            const int q = (wave + WAVES * j) * 64 + lane;
-            v4i v = {0, 0, 0, 0};
-            if (step * 64 + q / kRowChunks < rows)
-                v = *reinterpret_cast<const v4i*>(base + step * step_bytes + off[j]);
-            buf[q] = v;
+            const int k = row_of(j, lane);
+            load_to_lds(at, off[j] - (k < left ? 0 : k * pitch), buf + (wave + WAVES * j) * 64);
         }
+    }
+    __device__ void fix(int left, int lane, v4i* buf) const {
+#pragma unroll
+        for (int j = 0; j < kLoads; ++j)
+            if (row_of(j, lane) >= left)
+                buf[(wave + WAVES * j) * 64 + lane] = v4i{0, 0, 0, 0};
     }
     __device__ bf16x8 frag(const v4i* buf, int b, int s) const {
         const char* p = reinterpret_cast<const char*>(buf) + (frag_at ^ (b * 32)) + s * (32 * EXT * 2);
@@ -289,15 +307,8 @@ struct StridedOperand {
     }
 };
 
-// The LDS buffers of an operand's stages: distinct arrays, so that the compiler
-// sees that loads into one stage do not touch the stage being read.
-struct Buffers {
-    v4i* stage[3];
-};
-
-// acc[a][b] = the products of A's 16-position block blk0 + a with B's block
-// blk0 + b, summed over `full` steps of 64 and, with has_tail, a partial one
-// that write_tail() puts into the first buffers. Every wavefront of the
+// The products of A's 16-position blocks blk0 + a with B's blocks blk0 + b,
+// summed over `length` elements in steps of 64. Every wavefront of the
 // workgroup calls it.
 //
 // A step is two halves of 32. While the products of one half run, the LDS reads
@@ -306,52 +317,61 @@ struct Buffers {
 // then every wavefront has read the whole step, and after the step's one
 // barrier its buffers take the loads of step + STAGES, and the next step's
 // first half is read during the second one's products.
-template <int STAGES, int NA, int NB, class A, class B, class Tail>
-__device__ __forceinline__ void accumulate(const A& opa, const B& opb, const Buffers& bufa,
-                                           const Buffers& bufb, int32_t full, bool has_tail,
-                                           Tail write_tail,
-                                           f32x4 (&acc)[NA][NB]) {
+template <int STAGES, int NA, int NB, class A, class B>
+struct Accumulator {
+    static constexpr int kLoads = A::kLoads + B::kLoads;
+    static constexpr int kReads = NA * A::kFragReads + NB * B::kFragReads;  // of a half
     struct Frags {
         bf16x8 a[NA], b[NB];
     };
-    constexpr int kLoads = A::kLoads + B::kLoads;
-    constexpr int kReads = NA * A::kFragReads + NB * B::kFragReads;  // LDS reads of a half
+    // LDS of the stages, each A's part, then B's.
+    static constexpr int kStage = A::kChunks + B::kChunks;
+    static constexpr int kLdsChunks = STAGES * kStage;
+    v4i* lds;
+    int lane;
+
+    __device__ static int32_t steps_of(int64_t length) {
+        return static_cast<int32_t>((length + 63) / 64);
+    }
+    // A partial step (length not a multiple of 64) comes first, so that the
+    // loop holds whole steps only: step t of the loop is step t - 1 of memory
+    // then.
+    __device__ static int left_of(int64_t length) { return static_cast<int>(length & 63); }
+    __device__ __forceinline__ void issue(const A& opa, const B& opb, int stage, int32_t t) const {
+        opa.issue(t, lds + stage * kStage);
+        opb.issue(t, lds + stage * kStage + A::kChunks);
+    }
+    // The first steps' loads: what run() starts from.
+    __device__ __forceinline__ void start(const A& opa, const B& opb, int64_t length) const {
+        const int32_t steps = steps_of(length);
+        const int left = left_of(length);
+        if (left != 0) {
+            opa.issue_partial(steps - 1, left, lane, lds);
+            opb.issue_partial(steps - 1, left, lane, lds + A::kChunks);
+        } else if (steps > 0) {
+            issue(opa, opb, 0, 0);
+        }
+        const int32_t skip = left != 0 ? 1 : 0;
 #pragma unroll
-    for (int a = 0; a < NA; ++a)
-#pragma unroll
-        for (int b = 0; b < NB; ++b) acc[a][b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    auto multiply = [&](const Frags& d) {
-#pragma unroll
-        for (int b = 0; b < NB; ++b)
-#pragma unroll
-            for (int a = 0; a < NA; ++a)
-                acc[a][b] =
-                    __builtin_amdgcn_mfma_f32_16x16x32_bf16(d.a[a], d.b[b], acc[a][b], 0, 0, 0);
-    };
-    // Every half forms its addresses anew from a few registers: what the
-    // compiler would form ahead of the loop does not fit the registers.
-    auto issue = [&](int stage, int64_t t) {
-        A oa = opa;
-        B ob = opb;
-#pragma unroll
-        for (int j = 0; j < A::kLoads; ++j) reform(oa.off[j]);
-#pragma unroll
-        for (int j = 0; j < B::kLoads; ++j) reform(ob.off[j]);
-        oa.issue(t, bufa.stage[stage]);
-        ob.issue(t, bufb.stage[stage]);
-    };
-    auto fetch_half = [&](int stage, int s, Frags& d) {
+        for (int t = 1; t < STAGES; ++t)
+            if (t < steps) issue(opa, opb, t, t - skip);
+    }
+    __device__ __forceinline__ void fetch_half(const A& opa, const B& opb, int stage, int s,
+                                               Frags& d) const {
+        // The blocks' addresses are formed here from a register each: what the
+        // compiler would form ahead of the loop does not fit the registers.
         A oa = opa;
         B ob = opb;
         reform(oa.frag_at);
         reform(ob.frag_at);
+        const v4i* buf = lds + stage * kStage;
 #pragma unroll
-        for (int a = 0; a < NA; ++a) d.a[a] = oa.frag(bufa.stage[stage], a, s);
+        for (int a = 0; a < NA; ++a) d.a[a] = oa.frag(buf, a, s);
 #pragma unroll
-        for (int b = 0; b < NB; ++b) d.b[b] = ob.frag(bufb.stage[stage], b, s);
-    };
+        for (int b = 0; b < NB; ++b) d.b[b] = ob.frag(buf + A::kChunks, b, s);
+    }
     // The order within a half: an LDS read after every few products.
-    auto spread = [&] {
+    __device__ __forceinline__ static void spread() {
         constexpr int per = NA * NB / kReads > 0 ? NA * NB / kReads : 1;
 #pragma unroll
         for (int q = 0; q < kReads; ++q) {
@@ -359,59 +379,67 @@ __device__ __forceinline__ void accumulate(const A& opa, const B& opb, const Buf
             __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
         }
         __builtin_amdgcn_sched_barrier(0);
-    };
-    Frags lo, hi;
-    auto step = [&](auto p, int32_t at) {
-        constexpr int P = decltype(p)::value;
-        fetch_half(P, 1, hi);
-        multiply(lo);
-        spread();
-        // The next step has landed: at most the loads of the ones after it
-        // are in flight.
-        if (STAGES > 2 && at + STAGES - 1 < full)
-            wait_loads<kLoads*(STAGES - 2)>();
-        else
+    }
+    // Sums into acc (cleared first); start() has been called with the same
+    // operands. `younger` (then kYounger) other memory operations were issued
+    // after start()'s loads. On return no wavefront needs LDS any more.
+    template <int kYounger>
+    __device__ __forceinline__ void run(const A& opa, const B& opb, int64_t length, bool younger,
+                                        f32x4 (&acc)[NA][NB]) const {
+#pragma unroll
+        for (int a = 0; a < NA; ++a)
+#pragma unroll
+            for (int b = 0; b < NB; ++b) acc[a][b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        const int32_t steps = steps_of(length);
+        const int left = left_of(length);
+        if (steps == 0) return;
+        const int32_t ahead = left != 0 ? STAGES - 1 : STAGES;
+        auto multiply = [&](const Frags& d) {
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int a = 0; a < NA; ++a)
+                    acc[a][b] =
+                        __builtin_amdgcn_mfma_f32_16x16x32_bf16(d.a[a], d.b[b], acc[a][b], 0, 0, 0);
+        };
+        Frags lo, hi;
+        if (steps < STAGES)
             wait_loads<0>();
-        step_barrier();
-        if (at + STAGES < full) issue(P, at + STAGES);
-        // After the last step this reads what an earlier one left; it is not
-        // used.
-        fetch_half((P + 1) % STAGES, 0, lo);
-        multiply(hi);
-        spread();
-    };
-    if (full > 0) {
-        issue(0, 0);
-        if (full > 1) issue(1, 1);
-        if (STAGES > 2 && full > 2) issue(2, 2);
-        if (full >= STAGES)
+        else if (kYounger > 0 && younger)
+            wait_loads<kLoads*(STAGES - 1) + kYounger>();
+        else
             wait_loads<kLoads*(STAGES - 1)>();
-        else
-            wait_loads<0>();
         step_barrier();
-        fetch_half(0, 0, lo);
-        using std::integral_constant;
-        for (int32_t t = 0;; t += STAGES) {
-            step(integral_constant<int, 0>{}, t);
-            if (t + 1 >= full) break;
-            step(integral_constant<int, 1>{}, t + 1);
-            if (t + 2 >= full) break;
-            if constexpr (STAGES > 2) {
-                step(integral_constant<int, 2>{}, t + 2);
-                if (t + 3 >= full) break;
-            }
+        if (left != 0) {
+            opa.fix(left, lane, lds);
+            opb.fix(left, lane, lds + A::kChunks);
+            wait_lds();
+            step_barrier();
+        }
+        fetch_half(opa, opb, 0, 0, lo);
+        int stage = 0;
+        for (int32_t t = 0; t < steps; ++t) {
+            fetch_half(opa, opb, stage, 1, hi);
+            multiply(lo);
+            spread();
+            // At most the loads of the steps after the next one are in flight.
+            if (STAGES > 2 && t + STAGES - 1 < steps)
+                wait_loads<kLoads*(STAGES - 2)>();
+            else if (kYounger > 0 && younger && t == 0)
+                wait_loads<kYounger>();
+            else
+                wait_loads<0>();
+            step_barrier();
+            if (t + STAGES < steps) issue(opa, opb, stage, t + ahead);
+            stage = stage + 1 == STAGES ? 0 : stage + 1;
+            // After the last step this reads what an earlier one left; it is
+            // not used.
+            fetch_half(opa, opb, stage, 0, lo);
+            multiply(hi);
+            spread();
         }
     }
-    if (has_tail) {
-        __syncthreads();
-        write_tail();
-        __syncthreads();
-        fetch_half(0, 0, lo);
-        fetch_half(0, 1, hi);
-        multiply(lo);
-        multiply(hi);
-    }
-}
+};
 
 // act(g) and its derivative in fp32. silu(g) = g sigmoid(g); the tanh form of
 // gelu is g sigmoid(2z) with z = sqrt(2/pi) (g + 0.044715 g^3), which loses no

@@ -141,8 +141,9 @@ void expert_stream_kernel(const char* __restrict__ rows, const char* __restrict_
         for (int j = 0; j < S::kRowLoads; ++j) {
             const int r = lr + j * S::kRowsPerLoad;
             if (j * S::kRowsPerLoad < nrows)
-                load_to_lds(xbase + min(r, nrows - 1) * pitch + int64_t(t) * (S::kElems * 2),
-                            (lp ^ swz(r)) * 16, buf + j * 64);
+                load_to_lds(xbase + int64_t(t) * (S::kElems * 2),
+                            static_cast<uint32_t>(min(r, nrows - 1) * pitch) + (lp ^ swz(r)) * 16,
+                            buf + j * 64);
         }
     };
     f32x4 acc[kBlocks];
@@ -171,7 +172,7 @@ void expert_stream_kernel(const char* __restrict__ rows, const char* __restrict_
     // them, this step's rows have landed once no more than these are left.
     constexpr int kWeightLoads = 2 * kBlocks;
     auto load = [&](int32_t t, Weights<MXFP4> (&d)[kBlocks], v4i* buf) {
-        wait_lds_reads();           // the buffer's last reads have returned
+        wait_lds();           // the buffer's last reads have returned
         load_x(t, buf);
         __builtin_amdgcn_sched_barrier(0);
         load_w(t, d);

@@ -20,19 +20,22 @@ template <bool F32, bool ACCUMULATE>
 __global__ __launch_bounds__(kWaves * 64, 2)
 void expert_wgrad_kernel(const char* __restrict__ dy, const char* __restrict__ x,
                          const int32_t* __restrict__ offsets, int32_t max_rows, int32_t N,
-                         int32_t K, int32_t ntiles, int32_t ktiles, int64_t tiles, char* __restrict__ dw) {
+                         int32_t K, int32_t ntiles, int32_t ktiles, int32_t strip, int64_t tiles, char* __restrict__ dw) {
     typedef StridedOperand<kTileK, kWaves> Kop;
     typedef StridedOperand<kTileN, kWaves> Nop;
-    __shared__ v4i k0[Kop::kChunks], k1[Kop::kChunks];
-    __shared__ v4i n0[Nop::kChunks], n1[Nop::kChunks];
+    typedef Accumulator<2, kBlkK, kBlkN, Kop, Nop> Sums;
+    __shared__ v4i lds[Sums::kLdsChunks];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t u = expert_tile_number(kXcdChunk);
     if (u >= tiles) return;
-    const int32_t per = ntiles * ktiles;
+    const int32_t strips = (ktiles + strip - 1) / strip;
+    const int32_t per = ntiles * strips;
     const int32_t e = static_cast<int32_t>(u / per);
     const int32_t in = static_cast<int32_t>(u - int64_t(e) * per);
-    const int32_t nt0 = (in / ktiles) * kTileN, kt0 = (in % ktiles) * kTileK;
+    const int32_t nt0 = (in / strips) * kTileN;
+    const int32_t first = (in % strips) * strip;
+    const int32_t end = min(first + strip, ktiles);
     int32_t s0, s1;
     expert_segment(offsets, e, max_rows, s0, s1);
     const int32_t count = s1 - s0;
@@ -41,18 +44,28 @@ void expert_wgrad_kernel(const char* __restrict__ dy, const char* __restrict__ x
     Kop ko;
     Nop no;
     const int wk = wave % kWavesK, wn = wave / kWavesK;
-    ko.init(wave, lane, wk * kBlkK, int64_t(K) * 2, x + (int64_t(s0) * K + kt0) * 2, min(kTileK, K - kt0));
-    no.init(wave, lane, wn * kBlkN, int64_t(N) * 2, dy + (int64_t(s0) * N + nt0) * 2, min(kTileN, N - nt0));
-
+    auto at_tile = [&](int32_t t) {
+        ko.init(wave, lane, wk * kBlkK, int64_t(K) * 2,
+                x + (int64_t(s0) * K + int64_t(t) * kTileK) * 2, min(kTileK, K - t * kTileK));
+    };
+    no.init(wave, lane, wn * kBlkN, int64_t(N) * 2, dy + (int64_t(s0) * N + nt0) * 2,
+            min(kTileN, N - nt0));
     f32x4 acc[kBlkK][kBlkN];
-    const int32_t full = count / 64;
-    accumulate<2>(
-        ko, no, Buffers{k0, k1, k0}, Buffers{n0, n1, n0}, full, full * 64 < count,
-        [&] {
-            ko.tail(full, count, lane, k0);
-            no.tail(full, count, lane, n0);
-        },
-        acc);
+    const Sums sums{lds, lane};
+    at_tile(first);
+    sums.start(ko, no, count);
+    constexpr int kStores = kBlkK * kBlkN;
+    bool whole = false;     // the previous tile's stores went out in full
+    for (int32_t t = first; t < end; ++t) {
+    const int32_t kt0 = t * kTileK;
+    // The next tile's first loads are in flight while this one is stored, and
+    // its first products run while the stores drain.
+    sums.template run<(ACCUMULATE ? 0 : kStores)>(ko, no, count, whole, acc);
+    if (t + 1 < end) {
+        at_tile(t + 1);
+        sums.start(ko, no, count);
+    }
+    whole = nt0 + kTileN <= N && kt0 + kTileK <= K;
 
     const int i = lane & 15, g = lane >> 4;
 #pragma unroll
@@ -83,19 +96,30 @@ void expert_wgrad_kernel(const char* __restrict__ dy, const char* __restrict__ x
             }
         }
     }
+    }
 }
 
-int64_t wgrad_tiles(const ExpertWgradArgs& a) {
-    const int64_t nt = (int64_t(a.N) + kTileN - 1) / kTileN;
-    const int64_t kt = (int64_t(a.K) + kTileK - 1) / kTileK;
-    return nt * kt * a.E;
+int32_t k_tiles(const ExpertWgradArgs& a) {
+    return static_cast<int32_t>((int64_t(a.K) + kTileK - 1) / kTileK);
+}
+int32_t n_tiles(const ExpertWgradArgs& a) {
+    return static_cast<int32_t>((int64_t(a.N) + kTileN - 1) / kTileN);
+}
+// Tiles along K per workgroup.
+int32_t strip_of(const ExpertWgradArgs& a) {
+    const int64_t tiles = int64_t(n_tiles(a)) * k_tiles(a) * a.E;
+    return tiles >= 8192 ? 4 : tiles >= 2048 ? 2 : 1;
+}
+int64_t strip_count(const ExpertWgradArgs& a) {
+    const int32_t strip = strip_of(a);
+    return int64_t(n_tiles(a)) * ((k_tiles(a) + strip - 1) / strip) * a.E;
 }
 
 }  // namespace
 
 int64_t expert_wgrad_grid(const ExpertWgradArgs& a) {
     const int64_t unit = int64_t(kExpertXcds) * kXcdChunk;
-    return (wgrad_tiles(a) + unit - 1) / unit * unit;
+    return (strip_count(a) + unit - 1) / unit * unit;
 }
 
 hipError_t launch_expert_wgrad(const ExpertWgradArgs& a, hipStream_t stream) {
@@ -104,8 +128,7 @@ hipError_t launch_expert_wgrad(const ExpertWgradArgs& a, hipStream_t stream) {
     hipLaunchKernelGGL(kernel, dim3(static_cast<uint32_t>(expert_wgrad_grid(a))),
                        dim3(kWaves * 64), 0, stream, static_cast<const char*>(a.dy),
                        static_cast<const char*>(a.x), a.offsets, static_cast<int32_t>(a.max_rows),
-                       a.N, a.K, static_cast<int32_t>((int64_t(a.N) + kTileN - 1) / kTileN),
-                       static_cast<int32_t>((int64_t(a.K) + kTileK - 1) / kTileK), wgrad_tiles(a),
+                       a.N, a.K, n_tiles(a), k_tiles(a), strip_of(a), strip_count(a),
                        static_cast<char*>(a.dw));
     return hipGetLastError();
 }
