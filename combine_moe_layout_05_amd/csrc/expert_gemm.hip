@@ -112,47 +112,61 @@ void expert_gemm_kernel(const char* __restrict__ rows, const char* __restrict__ 
         const int r = (wr * kBlkR + b) * 16 + i;
         if (r >= nrows) continue;
         char* orow = out + int64_t(row0 + r) * out_pitch;
+        // Two 16-feature blocks at a time: every lane ends up with eight
+        // neighbouring features, which begin `at` features into the pair.
+        const int at = (g & 1) * 16 + (g >> 1) * 8;
         if constexpr (OP == ExpertOp::kGated) {
-            float* prow = pre + int64_t(row0 + r) * feats * 2;
+            static_assert(kBlkF == 4, "a pair of gate blocks, then their up blocks");
+            const int32_t f = f0 + wf * 32;
+            v2i h[2];
 #pragma unroll
-            for (int a = 0; a < kBlkF / 2; ++a) {
-                const int32_t f = f0 + wf * 32 + a * 16 + g * 4;
-                if (f >= feats) continue;
-                const f32x4 gv = acc[a][b], uv = acc[a + kBlkF / 2][b];
-                float h[4];
+            for (int a = 0; a < 2; ++a) {
+                const f32x4 gv = acc[a][b], uv = acc[a + 2][b];
+                f32x4 v;
 #pragma unroll
-                for (int t = 0; t < 4; ++t) h[t] = activate(act, gv[t]) * uv[t];
-                *reinterpret_cast<v2i*>(orow + int64_t(f) * 2) = pack_bf16x4(h[0], h[1], h[2], h[3]);
-                if (pre) {
-                    *reinterpret_cast<f32x4*>(prow + f) = gv;
-                    *reinterpret_cast<f32x4*>(prow + feats + f) = uv;
+                for (int t = 0; t < 4; ++t) v[t] = activate(act, gv[t]) * uv[t];
+                h[a] = pack_bf16x4(v);
+                const int32_t fq = f + a * 16 + g * 4;
+                if (pre && fq < feats) {
+                    float* p = pre + int64_t(row0 + r) * feats * 2 + fq;
+                    *reinterpret_cast<f32x4*>(p) = gv;
+                    *reinterpret_cast<f32x4*>(p + feats) = uv;
                 }
             }
+            const v4i v = pair_blocks(h[0], h[1]);
+            if (f + at < feats) *reinterpret_cast<v4i*>(orow + int64_t(f + at) * 2) = v;
         } else {
 #pragma unroll
-            for (int a = 0; a < kBlkF; ++a) {
-                const int32_t f = f0 + (wf * kBlkF + a) * 16 + g * 4;
-                if (f >= feats) continue;
-                const f32x4 v = acc[a][b];
+            for (int a = 0; a < kBlkF; a += 2) {
+                const int32_t f = f0 + (wf * kBlkF + a) * 16;
                 if constexpr (OP == ExpertOp::kGatedGrad) {
-                    const float* prow = pre + int64_t(row0 + r) * feats * 2;
-                    const f32x4 gv = *reinterpret_cast<const f32x4*>(prow + f);
-                    const f32x4 uv = *reinterpret_cast<const f32x4*>(prow + feats + f);
-                    float dg[4], du[4];
+                    v2i dg[2], du[2];
 #pragma unroll
-                    for (int t = 0; t < 4; ++t) {
-                        float value, slope;
-                        activate_grad(act, gv[t], value, slope);
-                        dg[t] = v[t] * uv[t] * slope;
-                        du[t] = v[t] * value;
+                    for (int c = 0; c < 2; ++c) {
+                        const int32_t fq = min(f + c * 16 + g * 4, feats - 4);
+                        const float* p = pre + int64_t(row0 + r) * feats * 2 + fq;
+                        const f32x4 gv = *reinterpret_cast<const f32x4*>(p);
+                        const f32x4 uv = *reinterpret_cast<const f32x4*>(p + feats);
+                        const f32x4 v = acc[a + c][b];
+                        f32x4 vg, vu;
+#pragma unroll
+                        for (int t = 0; t < 4; ++t) {
+                            float value, slope;
+                            activate_grad(act, gv[t], value, slope);
+                            vg[t] = v[t] * uv[t] * slope;
+                            vu[t] = v[t] * value;
+                        }
+                        dg[c] = pack_bf16x4(vg);
+                        du[c] = pack_bf16x4(vu);
                     }
-                    *reinterpret_cast<v2i*>(orow + int64_t(f) * 2) =
-                        pack_bf16x4(dg[0], dg[1], dg[2], dg[3]);
-                    *reinterpret_cast<v2i*>(orow + (int64_t(feats) + f) * 2) =
-                        pack_bf16x4(du[0], du[1], du[2], du[3]);
+                    const v4i og = pair_blocks(dg[0], dg[1]), ou = pair_blocks(du[0], du[1]);
+                    if (f + at < feats) {
+                        *reinterpret_cast<v4i*>(orow + int64_t(f + at) * 2) = og;
+                        *reinterpret_cast<v4i*>(orow + (int64_t(feats) + f + at) * 2) = ou;
+                    }
                 } else {
-                    *reinterpret_cast<v2i*>(orow + int64_t(f) * 2) =
-                        pack_bf16x4(v[0], v[1], v[2], v[3]);
+                    const v4i v = pair_blocks(pack_bf16x4(acc[a][b]), pack_bf16x4(acc[a + 1][b]));
+                    if (f + at < feats) *reinterpret_cast<v4i*>(orow + int64_t(f + at) * 2) = v;
                 }
             }
         }

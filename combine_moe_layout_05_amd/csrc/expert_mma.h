@@ -469,11 +469,21 @@ __device__ __forceinline__ void activate_grad(int act, float g, float& value, fl
     slope = pq == 0.0f ? p : __builtin_fmaf(g * pq, dz, p);
 }
 
-__device__ __forceinline__ v2i pack_bf16x4(float a, float b, float c, float d) {
-    v2i v;
-    v[0] = static_cast<int32_t>(f32_to_bf16_bits(a) | (f32_to_bf16_bits(b) << 16));
-    v[1] = static_cast<int32_t>(f32_to_bf16_bits(c) | (f32_to_bf16_bits(d) << 16));
-    return v;
+// Rounded to nearest even (a NaN stays one), element 2i in the low half.
+__device__ __forceinline__ v2i pack_bf16x4(f32x4 v) {
+    return __builtin_bit_cast(v2i, __builtin_convertvector(v, bf16x4));
+}
+
+// Four bf16 of block a and of the next block per lane (lane group g holds
+// elements 4g .. 4g + 3 of each, of one row), exchanged between groups 0 and 1
+// and between 2 and 3 so that every lane holds eight neighbours: elements
+// 8 (g / 2) .. + 8 of block a + g % 2. Stores then take half as many
+// instructions and cover 64 contiguous bytes of a row instead of 32.
+__device__ __forceinline__ v4i pair_blocks(v2i a, v2i b) {
+    const auto lo = __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false);
+    const auto hi = __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false);
+    return v4i{static_cast<int32_t>(lo[0]), static_cast<int32_t>(hi[0]),
+               static_cast<int32_t>(lo[1]), static_cast<int32_t>(hi[1])};
 }
 
 }  // namespace moe

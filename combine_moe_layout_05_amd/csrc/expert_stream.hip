@@ -251,17 +251,17 @@ void expert_stream_kernel(const char* __restrict__ rows, const char* __restrict_
     if (i >= nrows || f >= feats) return;
     v2i* o = reinterpret_cast<v2i*>(out + (int64_t(row0 + i) * feats + f) * 2);
     if constexpr (GATED) {
-        float h[4];
+        f32x4 h;
 #pragma unroll
         for (int t = 0; t < 4; ++t) h[t] = activate(act, v[t]) * u[t];
-        *o = pack_bf16x4(h[0], h[1], h[2], h[3]);
+        *o = pack_bf16x4(h);
         if (pre) {
             float* p = pre + int64_t(row0 + i) * feats * 2 + f;
             *reinterpret_cast<f32x4*>(p) = v;
             *reinterpret_cast<f32x4*>(p + feats) = u;
         }
     } else {
-        *o = pack_bf16x4(v[0], v[1], v[2], v[3]);
+        *o = pack_bf16x4(v);
     }
 }
 

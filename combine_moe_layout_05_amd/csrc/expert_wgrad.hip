@@ -54,7 +54,7 @@ void expert_wgrad_kernel(const char* __restrict__ dy, const char* __restrict__ x
     const Sums sums{lds, lane};
     at_tile(first);
     sums.start(ko, no, count);
-    constexpr int kStores = kBlkK * kBlkN;
+    constexpr int kStores = kBlkK * kBlkN / (F32 ? 1 : 2);
     bool whole = false;     // the previous tile's stores went out in full
     for (int32_t t = first; t < end; ++t) {
     const int32_t kt0 = t * kTileK;
@@ -72,27 +72,38 @@ void expert_wgrad_kernel(const char* __restrict__ dy, const char* __restrict__ x
     for (int b = 0; b < kBlkN; ++b) {
         const int32_t n = nt0 + (wn * kBlkN + b) * 16 + i;
         if (n >= N) continue;
+        const int64_t row = (int64_t(e) * N + n) * K;
 #pragma unroll
-        for (int a = 0; a < kBlkK; ++a) {
-            const int32_t k = kt0 + (wk * kBlkK + a) * 16 + g * 4;
-            if (k >= K) continue;
-            const int64_t at = (int64_t(e) * N + n) * K + k;
-            f32x4 v = acc[a][b];
+        for (int a = 0; a < kBlkK; a += 2) {
             if constexpr (F32) {
-                f32x4* p = reinterpret_cast<f32x4*>(dw + at * 4);
-                if constexpr (ACCUMULATE) v = *p + v;
-                *p = v;
-            } else {
-                v2i* p = reinterpret_cast<v2i*>(dw + at * 2);
-                if constexpr (ACCUMULATE) {
+#pragma unroll
+                for (int c = a; c < a + 2; ++c) {
+                    const int32_t k = kt0 + (wk * kBlkK + c) * 16 + g * 4;
+                    if (k >= K) continue;
+                    f32x4* p = reinterpret_cast<f32x4*>(dw + (row + k) * 4);
+                    f32x4 v = acc[c][b];
+                    if constexpr (ACCUMULATE) v = *p + v;
+                    *p = v;
+                }
+            } else if constexpr (ACCUMULATE) {
+#pragma unroll
+                for (int c = a; c < a + 2; ++c) {
+                    const int32_t k = kt0 + (wk * kBlkK + c) * 16 + g * 4;
+                    if (k >= K) continue;
+                    v2i* p = reinterpret_cast<v2i*>(dw + (row + k) * 2);
+                    f32x4 v = acc[c][b];
                     const v2i o = *p;
 #pragma unroll
-                    for (int t = 0; t < 4; ++t) {
-                        const uint32_t word = static_cast<uint32_t>(o[t >> 1]);
-                        v[t] += (t & 1) ? bf16_hi(word) : bf16_lo(word);
+                    for (int q = 0; q < 4; ++q) {
+                        const uint32_t word = static_cast<uint32_t>(o[q >> 1]);
+                        v[q] += (q & 1) ? bf16_hi(word) : bf16_lo(word);
                     }
+                    *p = pack_bf16x4(v);
                 }
-                *p = pack_bf16x4(v[0], v[1], v[2], v[3]);
+            } else {
+                const int32_t k = kt0 + (wk * kBlkK + a + (g & 1)) * 16 + (g >> 1) * 8;
+                const v4i v = pair_blocks(pack_bf16x4(acc[a][b]), pack_bf16x4(acc[a + 1][b]));
+                if (k < K) *reinterpret_cast<v4i*>(dw + (row + k) * 2) = v;
             }
         }
     }
