@@ -27,7 +27,7 @@ struct WeightOperand {
 };
 template <>
 struct WeightOperand<true> {
-    typedef StridedOperand<kTileF, kWaves> type;
+    typedef StridedOperand<kTileF, kWaves, 64> type;
 };
 
 template <ExpertOp OP, int BT>
@@ -101,8 +101,7 @@ void expert_gemm_kernel(const char* __restrict__ rows, const char* __restrict__ 
     f32x4 acc[kBlkF][kBlkR];
     const Accumulator<kStages, kBlkF, kBlkR, Weights, PackedOperand<kRowsUsed, kWaves>> sums{lds,
                                                                                              lane};
-    sums.start(wt, rt, red);
-    sums.template run<0>(wt, rt, red, false, acc);
+    sums.run(wt, rt, red, acc);
 
     // acc[a][b][t] belongs to row 16b + lane % 16 and position 16a + 4 (lane /
     // 16) + t of the wavefront.

@@ -234,16 +234,16 @@ struct PackedOperand {
     }
 };
 
-// An operand whose sum index strides in memory: 64 rows of the sum x EXT
-// contiguous positions. Fragments come out of LDS transposed (ds_read_b64_tr:
+// An operand whose sum index strides in memory: a step of ROWS (32 or 64) rows
+// of the sum x EXT contiguous positions. Fragments come out of LDS transposed (ds_read_b64_tr:
 // a group of 16 lanes reads 4 sum rows of 32 bytes and each lane receives one
 // position's 4 elements). The 32-byte blocks of a sum row are stored at block
 // b ^ f(row) with f(row) = row % 4 + 4 * (row / 8 % 2): the 8 sum rows two
 // lane groups read together then lie in distinct banks.
-template <int EXT, int WAVES>
+template <int EXT, int WAVES, int ROWS>
 struct StridedOperand {
     static constexpr int kRowChunks = EXT / 8;
-    static constexpr int kChunks = 64 * kRowChunks;
+    static constexpr int kChunks = ROWS * kRowChunks;
     static constexpr int kLoads = kChunks / (64 * WAVES);
     static constexpr int kFragReads = 2;
     static_assert(EXT % 128 == 0 && kChunks % (64 * WAVES) == 0, "whole wavefront loads");
@@ -262,7 +262,7 @@ struct StridedOperand {
                          int32_t width) {
         wave = wave_;
         base = base_;
-        step_bytes = pitch * 64;
+        step_bytes = pitch * ROWS;
 #pragma unroll
         for (int j = 0; j < kLoads; ++j) {
             const int q = (wave + WAVES * j) * 64 + lane;
@@ -279,14 +279,14 @@ struct StridedOperand {
 #pragma unroll
         for (int j = 0; j < kLoads; ++j) load_to_lds(at, off[j], buf + (wave + WAVES * j) * 64);
     }
-    // The last, partial step holds `left` (1..63) sum rows. The loads past
+    // The last, partial step holds `left` (fewer) sum rows. The loads past
     // them read its first row, which fix() replaces by zeros in LDS.
     __device__ int row_of(int j, int lane) const {
         return ((wave + WAVES * j) * 64 + lane) / kRowChunks;
     }
     __device__ void issue_partial(int64_t step, int left, int lane, v4i* buf) const {
         const char* at = base + step * step_bytes;
-        const uint32_t pitch = static_cast<uint32_t>(step_bytes / 64);
+        const uint32_t pitch = static_cast<uint32_t>(step_bytes / ROWS);
 #pragma unroll
         for (int j = 0; j < kLoads; ++j) {
             const int k = row_of(j, lane);
@@ -341,7 +341,7 @@ struct Accumulator {
         opa.issue(t, lds + stage * kStage);
         opb.issue(t, lds + stage * kStage + A::kChunks);
     }
-    // The first steps' loads: what run() starts from.
+    // The first steps' loads.
     __device__ __forceinline__ void start(const A& opa, const B& opb, int64_t length) const {
         const int32_t steps = steps_of(length);
         const int left = left_of(length);
@@ -380,11 +380,8 @@ struct Accumulator {
         }
         __builtin_amdgcn_sched_barrier(0);
     }
-    // Sums into acc (cleared first); start() has been called with the same
-    // operands. `younger` (then kYounger) other memory operations were issued
-    // after start()'s loads. On return no wavefront needs LDS any more.
-    template <int kYounger>
-    __device__ __forceinline__ void run(const A& opa, const B& opb, int64_t length, bool younger,
+    // Sums into acc (cleared first).
+    __device__ __forceinline__ void run(const A& opa, const B& opb, int64_t length,
                                         f32x4 (&acc)[NA][NB]) const {
 #pragma unroll
         for (int a = 0; a < NA; ++a)
@@ -403,10 +400,9 @@ struct Accumulator {
                         __builtin_amdgcn_mfma_f32_16x16x32_bf16(d.a[a], d.b[b], acc[a][b], 0, 0, 0);
         };
         Frags lo, hi;
+        start(opa, opb, length);
         if (steps < STAGES)
             wait_loads<0>();
-        else if (kYounger > 0 && younger)
-            wait_loads<kLoads*(STAGES - 1) + kYounger>();
         else
             wait_loads<kLoads*(STAGES - 1)>();
         step_barrier();
@@ -425,8 +421,6 @@ struct Accumulator {
             // At most the loads of the steps after the next one are in flight.
             if (STAGES > 2 && t + STAGES - 1 < steps)
                 wait_loads<kLoads*(STAGES - 2)>();
-            else if (kYounger > 0 && younger && t == 0)
-                wait_loads<kYounger>();
             else
                 wait_loads<0>();
             step_barrier();

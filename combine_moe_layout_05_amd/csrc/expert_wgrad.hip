@@ -7,65 +7,153 @@
 namespace moe {
 namespace {
 
-constexpr int kWaves = 8;
-constexpr int kWavesK = 4;
+constexpr int kWaves = 4;
+constexpr int kWavesK = 2;
 constexpr int kWavesN = 2;
 constexpr int kTileK = 256;
-constexpr int kTileN = 256;
+constexpr int kTileN = 128;
 constexpr int kBlkK = kTileK / kWavesK / 16;
 constexpr int kBlkN = kTileN / kWavesN / 16;
-constexpr int kXcdChunk = 32;
+constexpr int kStep = 32;               // rows per step: one matrix-core product deep
+constexpr int kStages = 3;              // 72 KiB of LDS: two workgroups per CU
+constexpr int kXcdChunk = 64;
+
+typedef StridedOperand<kTileK, kWaves, kStep> Kop;
+typedef StridedOperand<kTileN, kWaves, kStep> Nop;
+constexpr int kLoads = Kop::kLoads + Nop::kLoads;
+constexpr int kStageChunks = Kop::kChunks + Nop::kChunks;
+
+struct Frags {
+    bf16x8 k[kBlkK], n[kBlkN];
+};
+
+__device__ __forceinline__ void fetch(const Kop& ko, const Nop& no, const v4i* buf, Frags& d) {
+    // The blocks' addresses are formed here from a register each: what the
+    // compiler would form ahead of the loop does not fit the registers.
+    Kop kk = ko;
+    Nop nn = no;
+    reform(kk.frag_at);
+    reform(nn.frag_at);
+#pragma unroll
+    for (int a = 0; a < kBlkK; ++a) d.k[a] = kk.frag(buf, a, 0);
+#pragma unroll
+    for (int b = 0; b < kBlkN; ++b) d.n[b] = nn.frag(buf + Kop::kChunks, b, 0);
+}
 
 template <bool F32, bool ACCUMULATE>
 __global__ __launch_bounds__(kWaves * 64, 2)
 void expert_wgrad_kernel(const char* __restrict__ dy, const char* __restrict__ x,
                          const int32_t* __restrict__ offsets, int32_t max_rows, int32_t N,
-                         int32_t K, int32_t ntiles, int32_t ktiles, int32_t strip, int64_t tiles, char* __restrict__ dw) {
-    typedef StridedOperand<kTileK, kWaves> Kop;
-    typedef StridedOperand<kTileN, kWaves> Nop;
-    typedef Accumulator<2, kBlkK, kBlkN, Kop, Nop> Sums;
-    __shared__ v4i lds[Sums::kLdsChunks];
+                         int32_t K, int32_t ntiles, int32_t ktiles, int64_t tiles,
+                         char* __restrict__ dw) {
+    __shared__ v4i lds[kStages * kStageChunks];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t u = expert_tile_number(kXcdChunk);
     if (u >= tiles) return;
-    const int32_t strips = (ktiles + strip - 1) / strip;
-    const int32_t per = ntiles * strips;
+    const int32_t per = ntiles * ktiles;
     const int32_t e = static_cast<int32_t>(u / per);
     const int32_t in = static_cast<int32_t>(u - int64_t(e) * per);
-    const int32_t nt0 = (in / strips) * kTileN;
-    const int32_t first = (in % strips) * strip;
-    const int32_t end = min(first + strip, ktiles);
     int32_t s0, s1;
     expert_segment(offsets, e, max_rows, s0, s1);
     const int32_t count = s1 - s0;
     if (ACCUMULATE && count == 0) return;
+    // Tiles along K first where a segment is short: what runs at once then
+    // writes long contiguous pieces of dw. From 2048 rows on the rows' reads
+    // weigh more, and bands of 8 tiles along N share them in the L2 cache.
+    const int32_t deep = count >= 2048 ? 8 : 1;
+    const int32_t band = in / (ktiles * deep);
+    const int32_t inside = in - band * ktiles * deep;
+    const int32_t height = min(deep, ntiles - band * deep);
+    const int32_t nt0 = (band * deep + inside % height) * kTileN;
+    const int32_t kt0 = inside / height * kTileK;
 
     Kop ko;
     Nop no;
     const int wk = wave % kWavesK, wn = wave / kWavesK;
-    auto at_tile = [&](int32_t t) {
-        ko.init(wave, lane, wk * kBlkK, int64_t(K) * 2,
-                x + (int64_t(s0) * K + int64_t(t) * kTileK) * 2, min(kTileK, K - t * kTileK));
-    };
+    ko.init(wave, lane, wk * kBlkK, int64_t(K) * 2, x + (int64_t(s0) * K + kt0) * 2,
+            min(kTileK, K - kt0));
     no.init(wave, lane, wn * kBlkN, int64_t(N) * 2, dy + (int64_t(s0) * N + nt0) * 2,
             min(kTileN, N - nt0));
     f32x4 acc[kBlkK][kBlkN];
-    const Sums sums{lds, lane};
-    at_tile(first);
-    sums.start(ko, no, count);
-    constexpr int kStores = kBlkK * kBlkN / (F32 ? 1 : 2);
-    bool whole = false;     // the previous tile's stores went out in full
-    for (int32_t t = first; t < end; ++t) {
-    const int32_t kt0 = t * kTileK;
-    // The next tile's first loads are in flight while this one is stored, and
-    // its first products run while the stores drain.
-    sums.template run<(ACCUMULATE ? 0 : kStores)>(ko, no, count, whole, acc);
-    if (t + 1 < end) {
-        at_tile(t + 1);
-        sums.start(ko, no, count);
+#pragma unroll
+    for (int a = 0; a < kBlkK; ++a)
+#pragma unroll
+        for (int b = 0; b < kBlkN; ++b) acc[a][b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+    const int32_t steps = (count + kStep - 1) / kStep;
+    if (steps > 0) {
+        auto issue = [&](int stage, int32_t t) {
+            ko.issue(t, lds + stage * kStageChunks);
+            no.issue(t, lds + stage * kStageChunks + Kop::kChunks);
+        };
+        // A partial step comes first, so that the loop holds whole steps only:
+        // step t of the loop is step t - 1 of memory then.
+        const int left = count % kStep;
+        const int32_t skip = left != 0 ? 1 : 0;
+        if (left != 0) {
+            ko.issue_partial(steps - 1, left, lane, lds);
+            no.issue_partial(steps - 1, left, lane, lds + Kop::kChunks);
+        } else {
+            issue(0, 0);
+        }
+#pragma unroll
+        for (int t = 1; t < kStages; ++t)
+            if (t < steps) issue(t, t - skip);
+        if (steps < kStages)
+            wait_loads<0>();
+        else
+            wait_loads<kLoads*(kStages - 1)>();
+        step_barrier();
+        if (left != 0) {
+            ko.fix(left, lane, lds);
+            no.fix(left, lane, lds + Kop::kChunks);
+            wait_lds();
+            step_barrier();
+        }
+        Frags even, odd;
+        fetch(ko, no, lds, even);
+        int stage = 0;
+        // Products of one step, while the next one's fragments are read.
+        auto step = [&](const Frags& now, Frags& next, int32_t t) {
+            // The next step has landed (at most the loads of those after it
+            // are in flight) and this one's reads have returned.
+            if (t + kStages - 1 < steps)
+                wait_loads<kLoads*(kStages - 2)>();
+            else
+                wait_loads<0>();
+            step_barrier();
+            if (t + kStages < steps) issue(stage, t + kStages - skip);
+            stage = stage + 1 == kStages ? 0 : stage + 1;
+            // After the last step this reads what an earlier one left; it is
+            // not used.
+            fetch(ko, no, lds + stage * kStageChunks, next);
+#pragma unroll
+            for (int b = 0; b < kBlkN; ++b)
+#pragma unroll
+                for (int a = 0; a < kBlkK; ++a)
+                    acc[a][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(now.k[a], now.n[b],
+                                                                        acc[a][b], 0, 0, 0);
+            // An LDS read (two to a fragment) after each product.
+#pragma unroll
+            for (int q = 0; q < 2 * (kBlkK + kBlkN); ++q) {
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        // Two steps a turn; an odd number ends with a step of zeros.
+        for (int32_t t = 0; t < steps; t += 2) {
+            step(even, odd, t);
+            if (t + 1 >= steps) {
+#pragma unroll
+                for (int a = 0; a < kBlkK; ++a) odd.k[a] = bf16x8{};
+#pragma unroll
+                for (int b = 0; b < kBlkN; ++b) odd.n[b] = bf16x8{};
+            }
+            step(odd, even, t + 1);
+        }
     }
-    whole = nt0 + kTileN <= N && kt0 + kTileK <= K;
 
     const int i = lane & 15, g = lane >> 4;
 #pragma unroll
@@ -103,10 +191,12 @@ void expert_wgrad_kernel(const char* __restrict__ dy, const char* __restrict__ x
             } else {
                 const int32_t k = kt0 + (wk * kBlkK + a + (g & 1)) * 16 + (g >> 1) * 8;
                 const v4i v = pair_blocks(pack_bf16x4(acc[a][b]), pack_bf16x4(acc[a + 1][b]));
-                if (k < K) *reinterpret_cast<v4i*>(dw + (row + k) * 2) = v;
+                // Streamed past the caches: the gradient is as large as the
+                // weights and is not read here.
+                if (k < K)
+                    __builtin_nontemporal_store(v, reinterpret_cast<v4i*>(dw + (row + k) * 2));
             }
         }
-    }
     }
 }
 
@@ -116,21 +206,13 @@ int32_t k_tiles(const ExpertWgradArgs& a) {
 int32_t n_tiles(const ExpertWgradArgs& a) {
     return static_cast<int32_t>((int64_t(a.N) + kTileN - 1) / kTileN);
 }
-// Tiles along K per workgroup.
-int32_t strip_of(const ExpertWgradArgs& a) {
-    const int64_t tiles = int64_t(n_tiles(a)) * k_tiles(a) * a.E;
-    return tiles >= 8192 ? 4 : tiles >= 2048 ? 2 : 1;
-}
-int64_t strip_count(const ExpertWgradArgs& a) {
-    const int32_t strip = strip_of(a);
-    return int64_t(n_tiles(a)) * ((k_tiles(a) + strip - 1) / strip) * a.E;
-}
+int64_t tile_count(const ExpertWgradArgs& a) { return int64_t(n_tiles(a)) * k_tiles(a) * a.E; }
 
 }  // namespace
 
 int64_t expert_wgrad_grid(const ExpertWgradArgs& a) {
     const int64_t unit = int64_t(kExpertXcds) * kXcdChunk;
-    return (strip_count(a) + unit - 1) / unit * unit;
+    return (tile_count(a) + unit - 1) / unit * unit;
 }
 
 hipError_t launch_expert_wgrad(const ExpertWgradArgs& a, hipStream_t stream) {
@@ -139,7 +221,7 @@ hipError_t launch_expert_wgrad(const ExpertWgradArgs& a, hipStream_t stream) {
     hipLaunchKernelGGL(kernel, dim3(static_cast<uint32_t>(expert_wgrad_grid(a))),
                        dim3(kWaves * 64), 0, stream, static_cast<const char*>(a.dy),
                        static_cast<const char*>(a.x), a.offsets, static_cast<int32_t>(a.max_rows),
-                       a.N, a.K, n_tiles(a), k_tiles(a), strip_of(a), strip_count(a),
+                       a.N, a.K, n_tiles(a), k_tiles(a), tile_count(a),
                        static_cast<char*>(a.dw));
     return hipGetLastError();
 }
