@@ -21,10 +21,11 @@ INCLUDE = os.path.join(ROOT, "include")
 
 SOURCES = ["layout.hip", "dispatch.hip", "combine.hip", "combine_backward.hip", "routing_map.hip",
            "grouped_gemm.hip", "noalloc.hip",
-           "expert_gemm.hip", "expert_wgrad.hip", "expert_stream.hip",
+           "expert_gemm.hip", "expert_wgrad.hip", "expert_stream.hip", "expert_mxfp4.hip",
            "moe_api.cpp", "expert_api.cpp"]
 HEADERS = [os.path.join(CSRC, "moe_kernels.h"), os.path.join(CSRC, "moe_lanes.h"),
            os.path.join(CSRC, "expert_kernels.h"), os.path.join(CSRC, "expert_mma.h"),
+           os.path.join(CSRC, "expert_mxfp4.h"),
            os.path.join(INCLUDE, "moe.h")]
 # The benchmark's traffic reference kernels, built into a library of their own.
 PROBE_SOURCES = ["traffic_probe.hip"]

@@ -92,5 +92,8 @@ struct ExpertStreamArgs {
 };
 hipError_t launch_expert_stream(const ExpertStreamArgs& a, hipStream_t stream);
 int64_t expert_stream_grid(const ExpertStreamArgs& a);
+// The same products with packed 4-bit weights for many rows per expert.
+hipError_t launch_expert_mxfp4(const ExpertStreamArgs& a, hipStream_t stream);
+int64_t expert_mxfp4_grid(const ExpertStreamArgs& a);
 
 }  // namespace moe

@@ -2,6 +2,7 @@
 // expert weights.
 #include "expert_kernels.h"
 #include "expert_mma.h"
+#include "expert_mxfp4.h"
 
 #include <type_traits>
 
@@ -27,22 +28,7 @@ struct Step {
 template <bool MXFP4>
 struct Weights;
 template <>
-struct Weights<true> {
-    v4i q;
-    uint32_t scale;
-    __device__ bf16x8 frag(int s) const {
-        // The scale's exponent byte is the exponent field of a float; the
-        // conversion is exact (2-bit significands times a power of two).
-        const float f = __uint_as_float(((scale >> (8 * s)) & 0xFFu) << 23);
-        const uint32_t v = static_cast<uint32_t>(q[s]);
-        typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-        const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v, f, 0);
-        const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v, f, 1);
-        const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v, f, 2);
-        const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v, f, 3);
-        return bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
-    }
-};
+struct Weights<true> : Mxfp4Step {};
 template <>
 struct Weights<false> {
     v4i q[2];
