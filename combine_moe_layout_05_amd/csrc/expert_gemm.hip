@@ -36,9 +36,9 @@ void expert_gemm_kernel(const char* __restrict__ rows, const char* __restrict__ 
                         const int32_t* __restrict__ offsets, int32_t E, int32_t max_rows,
                         int32_t red, int32_t feats, int32_t ftiles, int32_t act,
                         char* __restrict__ out, float* __restrict__ pre, int32_t zero_tail) {
-    constexpr int kStages = BT == 256 ? 2 : 3;
     typedef typename WeightOperand<strided(OP)>::type Weights;
-    __shared__ v4i lds[kStages * (Weights::kChunks + PackedOperand<BT, kWaves>::kChunks)];
+    // Three stages up to 128 rows, two above.
+    __shared__ v4i lds[BT > 128 ? 9216 : 3 * (Weights::kChunks + PackedOperand<BT, kWaves>::kChunks)];
     __shared__ int32_t info[4];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -94,6 +94,7 @@ void expert_gemm_kernel(const char* __restrict__ rows, const char* __restrict__ 
     auto run = [&](auto parts) {
     constexpr int kRowsUsed = decltype(parts)::value * 64;
     constexpr int kBlkR = kRowsUsed / kWavesR / 16;
+    constexpr int kStages = kRowsUsed > 128 ? 2 : 3;
     PackedOperand<kRowsUsed, kWaves> rt;
     const char* rbase = rows + int64_t(row0) * red_pitch;
     rt.init(wave, lane, wr * kBlkR, red_pitch, [&](int) { return rbase; },

@@ -70,7 +70,7 @@ void expert_mxfp4_kernel(const char* __restrict__ rows, const char* __restrict__
         constexpr int NB = decltype(row_blocks)::value;
         typedef PackedOperand<(NB > 4 ? 128 : 64), kWaves> Rows;
         constexpr int kLoads = 2 * Rows::kLoads;                // of a step
-        constexpr int kGroup = NB < 4 ? NB : 4;                 // row blocks fetched at once
+        constexpr int kGroup = NB % 3 == 0 ? 3 : NB < 4 ? NB : 4;   // row blocks fetched at once
         constexpr int kFetches = 4 * NB / kGroup;               // per step
         Rows rt;
         const int64_t pitch = int64_t(red) * 2;
@@ -98,16 +98,24 @@ void expert_mxfp4_kernel(const char* __restrict__ rows, const char* __restrict__
             }
         };
         auto load_w = [&](int32_t t, Mxfp4Step (&d)[kBlocks]) {
+            // A uniform address and a 32-bit offset per lane (a register, not
+            // an address pair per load).
+            uint32_t qo = lane * 16, so = i * 4;
+            reform(qo);
+            reform(so);
 #pragma unroll
             for (int b = 0; b < kBlocks; ++b) {
-                d[b].q = *reinterpret_cast<const v4i*>(wb[b] + int64_t(t) * 1024 + lane * 16);
-                d[b].scale = *reinterpret_cast<const uint32_t*>(sb[b] + int64_t(t) * 64 + i * 4);
+                d[b].q = *reinterpret_cast<const v4i*>(wb[b] + int64_t(t) * 1024 + qo);
+                d[b].scale = *reinterpret_cast<const uint32_t*>(sb[b] + int64_t(t) * 64 + so);
             }
         };
-        auto fix = [&](int stage) {
+        // Zeros into what the loads of step t put past the rows' end, or into
+        // all of a step that does not exist (an odd number of them ends with
+        // one of zeros).
+        auto clear = [&](int32_t t, int stage) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const int left = red - (2 * (steps - 1) + h) * 64;
+                const int left = min(red - (2 * t + h) * 64, 64);
                 if (left < 64) rt.fix(max(left, 0), lane, stage_of(stage) + h * Rows::kChunks);
             }
             wait_lds();
@@ -115,25 +123,25 @@ void expert_mxfp4_kernel(const char* __restrict__ rows, const char* __restrict__
         };
         const bool partial = red % kMxfp4Step != 0;
 
-        Mxfp4Step now[kBlocks], next[kBlocks], later[kBlocks];
-        load_w(0, now);
+        Mxfp4Step even[kBlocks], odd[kBlocks];
         issue_rows(0, 0);
-        load_w(min(1, steps - 1), next);
         if (steps > 1) issue_rows(1, 1);
-        wait_loads<0>();
+        load_w(0, even);
+        load_w(min(1, steps - 1), odd);
+        wait_loads<4 * kBlocks>();
         step_barrier();
-        if (partial && steps == 1) fix(0);
+        if (partial && steps == 1) clear(0, 0);
         int stage = 0;
-        for (int32_t t = 0; t < steps; ++t) {
+        auto step = [&](Mxfp4Step (&mine)[kBlocks], int32_t t) {
             const int after = stage + 1 == kStages ? 0 : stage + 1;
             const int free = after + 1 == kStages ? 0 : after + 1;
-            // Two steps ahead: weights into registers, rows into the stage read
-            // last, weights first (a load is waited for together with all that
-            // were issued before it).
-            const bool more = t + 2 < steps;
-            load_w(min(t + 2, steps - 1), later);
-            if (more) issue_rows(t + 2, free);
+            bf16x8 wf[kBlocks];
+#pragma unroll
+            for (int a = 0; a < kBlocks; ++a) wf[a] = mine[a].frag(0);
             __builtin_amdgcn_sched_barrier(0);
+            // Behind the first use of this step's weights: what waits for them
+            // must not wait for these loads.
+            if (t + 2 < steps) issue_rows(t + 2, free);
             const v4i* buf = stage_of(stage);
             auto fetch = [&](int n, bf16x8 (&d)[kGroup]) {
                 const int s = n * kGroup / NB, b0 = n * kGroup % NB;
@@ -141,15 +149,15 @@ void expert_mxfp4_kernel(const char* __restrict__ rows, const char* __restrict__
                 for (int b = 0; b < kGroup; ++b)
                     d[b] = rt.frag(buf + (s >> 1) * Rows::kChunks, b0 + b, s & 1);
             };
-            bf16x8 cur[kGroup], nxt[kGroup], wf[kBlocks];
+            bf16x8 cur[kGroup], nxt[kGroup];
             fetch(0, cur);
 #pragma unroll
             for (int n = 0; n < kFetches; ++n) {
                 if (n + 1 < kFetches) fetch(n + 1, nxt);
                 const int s = n * kGroup / NB, b0 = n * kGroup % NB;
-                if (b0 == 0) {
+                if (b0 == 0 && s > 0) {
 #pragma unroll
-                    for (int a = 0; a < kBlocks; ++a) wf[a] = now[a].frag(s);
+                    for (int a = 0; a < kBlocks; ++a) wf[a] = mine[a].frag(s);
                 }
 #pragma unroll
                 for (int b = 0; b < kGroup; ++b)
@@ -161,21 +169,27 @@ void expert_mxfp4_kernel(const char* __restrict__ rows, const char* __restrict__
                 for (int b = 0; b < kGroup; ++b) cur[b] = nxt[b];
             }
             __builtin_amdgcn_sched_barrier(0);
-            // The next step's rows have landed: behind them only the loads of
-            // the one after it are in flight.
-            if (more)
-                wait_loads<kLoads + 2 * kBlocks>();
+            load_w(min(t + 2, steps - 1), mine);
+            __builtin_amdgcn_sched_barrier(0);
+            // The next step's rows have landed: behind them are two steps'
+            // weights and the rows of the step after it, if there are any.
+            if (t + 2 < steps)
+                wait_loads<kLoads + 4 * kBlocks>();
             else
-                wait_loads<0>();
+                wait_loads<4 * kBlocks>();
             step_barrier();
-            if (partial && t + 2 == steps) fix(after);
-#pragma unroll
-            for (int b = 0; b < kBlocks; ++b) {
-                now[b] = next[b];
-                next[b] = later[b];
-            }
+            if ((partial && t + 2 == steps) || t + 1 == steps) clear(t + 1, after);
             stage = after;
+        };
+        for (int32_t t = 0; t < steps; t += 2) {
+            step(even, t);
+            if (t + 1 >= steps) {
+#pragma unroll
+                for (int b = 0; b < kBlocks; ++b) odd[b].q = v4i{0, 0, 0, 0};
+            }
+            step(odd, t + 1);
         }
+        wait_loads<0>();
 
         const int at = (g & 1) * 16 + (g >> 1) * 8;
 #pragma unroll
@@ -210,8 +224,12 @@ void expert_mxfp4_kernel(const char* __restrict__ rows, const char* __restrict__
         run(std::integral_constant<int, 1>{});
     else if (nrows <= 32)
         run(std::integral_constant<int, 2>{});
+    else if (nrows <= 48)
+        run(std::integral_constant<int, 3>{});
     else if (nrows <= 64)
         run(std::integral_constant<int, 4>{});
+    else if (nrows <= 96)
+        run(std::integral_constant<int, 6>{});
     else
         run(std::integral_constant<int, 8>{});
 }
