@@ -32,15 +32,15 @@ bool buffers_ok(const void* a, const void* b, const void* c, const int32_t* offs
 int status_of(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_ERR_HIP; }
 
 // Few rows per expert: the form that streams the weights (16-row tiles).
-bool few_rows(int64_t max_rows, int32_t E) {
-    return max_rows <= 16 || max_rows <= int64_t(8) * E;
+bool few_rows(bool mxfp4, int64_t max_rows, int32_t E) {
+    return max_rows <= 64 || (mxfp4 && max_rows <= int64_t(8) * E);
 }
 
 int run_gemm(moe::ExpertOp op, const void* rows, const void* w, const int32_t* offsets, int32_t E,
              int64_t max_rows, int32_t red, int32_t feats, int32_t activation, void* out,
              float* pre, int32_t flags, void* stream) {
     const bool forward = op == moe::ExpertOp::kPlain || op == moe::ExpertOp::kGated;
-    if (forward && few_rows(max_rows, E)) {
+    if (forward && few_rows(false, max_rows, E)) {
         moe::ExpertStreamArgs a;
         a.mxfp4 = false;
         a.gated = op == moe::ExpertOp::kGated;
@@ -97,7 +97,7 @@ int run_mxfp4(bool gated, const void* rows, const void* packed, const int32_t* o
     a.out = out;
     a.pre = nullptr;
     a.zero_tail = (flags & MOE_GEMM_ZERO_TAIL) != 0;
-    if (few_rows(max_rows, E)) {
+    if (few_rows(true, max_rows, E)) {
         if (moe::expert_stream_grid(a) > INT32_MAX) return MOE_ERR_INVALID_ARG;
         return status_of(moe::launch_expert_stream(a, static_cast<hipStream_t>(stream)));
     }

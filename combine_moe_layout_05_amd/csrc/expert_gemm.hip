@@ -11,8 +11,9 @@ constexpr int kWaves = 8;
 constexpr int kWavesF = 4;              // wavefronts along the features
 constexpr int kWavesR = 2;              // and along the rows
 constexpr int kTileF = 256;             // weight positions per workgroup
+constexpr int kTileR = 256;             // rows per workgroup
 constexpr int kBlkF = kTileF / kWavesF / 16;
-constexpr int kXcdChunk = 32;
+constexpr int kXcdChunk = 16;
 constexpr int kBand = 8;
 
 constexpr bool strided(ExpertOp op) {
@@ -30,7 +31,7 @@ struct WeightOperand<true> {
     typedef StridedOperand<kTileF, kWaves, 64> type;
 };
 
-template <ExpertOp OP, int BT>
+template <ExpertOp OP>
 __global__ __launch_bounds__(kWaves * 64, 2)
 void expert_gemm_kernel(const char* __restrict__ rows, const char* __restrict__ w,
                         const int32_t* __restrict__ offsets, int32_t E, int32_t max_rows,
@@ -38,7 +39,9 @@ void expert_gemm_kernel(const char* __restrict__ rows, const char* __restrict__ 
                         char* __restrict__ out, float* __restrict__ pre, int32_t zero_tail) {
     typedef typename WeightOperand<strided(OP)>::type Weights;
     // Three stages up to 128 rows, two above.
-    __shared__ v4i lds[BT > 128 ? 9216 : 3 * (Weights::kChunks + PackedOperand<BT, kWaves>::kChunks)];
+    constexpr int kLds2 = 2 * (Weights::kChunks + PackedOperand<kTileR, kWaves>::kChunks);
+    constexpr int kLds3 = 3 * (Weights::kChunks + PackedOperand<kTileR / 2, kWaves>::kChunks);
+    __shared__ v4i lds[kLds3 > kLds2 ? kLds3 : kLds2];
     __shared__ int32_t info[4];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -46,7 +49,7 @@ void expert_gemm_kernel(const char* __restrict__ rows, const char* __restrict__ 
     const int64_t number = expert_tile_number(kXcdChunk);
     if (wave == 0) {
         const ExpertTile t =
-            expert_find_tile(offsets, E, max_rows, BT, ftiles, kBand, number);
+            expert_find_tile(offsets, E, max_rows, kTileR, ftiles, kBand, number);
         if (lane == 0) {
             info[0] = t.e;
             info[1] = t.f;
@@ -173,19 +176,14 @@ void expert_gemm_kernel(const char* __restrict__ rows, const char* __restrict__ 
     }
     };
     const int parts = (nrows + 63) / 64;
-    if constexpr (BT > 64) {
-        if (parts == 2) return run(std::integral_constant<int, 2>{});
-    }
-    if constexpr (BT > 128) {
-        if (parts == 3) return run(std::integral_constant<int, 3>{});
-        if (parts == 4) return run(std::integral_constant<int, 4>{});
-    }
-    run(std::integral_constant<int, 1>{});
-}
-
-int32_t row_tile(const ExpertGemmArgs& a) {
-    const int64_t average = a.max_rows / a.E;
-    return average >= 192 ? 256 : average >= 96 ? 128 : 64;
+    if (parts == 1)
+        run(std::integral_constant<int, 1>{});
+    else if (parts == 2)
+        run(std::integral_constant<int, 2>{});
+    else if (parts == 3)
+        run(std::integral_constant<int, 3>{});
+    else
+        run(std::integral_constant<int, 4>{});
 }
 
 int64_t feature_tiles(const ExpertGemmArgs& a) {
@@ -193,9 +191,9 @@ int64_t feature_tiles(const ExpertGemmArgs& a) {
     return (int64_t(a.feats) + per - 1) / per;
 }
 
-template <ExpertOp OP, int BT>
-hipError_t launch_bt(const ExpertGemmArgs& a, hipStream_t stream) {
-    hipLaunchKernelGGL((expert_gemm_kernel<OP, BT>), dim3(static_cast<uint32_t>(expert_gemm_grid(a))),
+template <ExpertOp OP>
+hipError_t launch_op(const ExpertGemmArgs& a, hipStream_t stream) {
+    hipLaunchKernelGGL((expert_gemm_kernel<OP>), dim3(static_cast<uint32_t>(expert_gemm_grid(a))),
                        dim3(kWaves * 64), 0, stream, static_cast<const char*>(a.rows),
                        static_cast<const char*>(a.w), a.offsets, a.E,
                        static_cast<int32_t>(a.max_rows), a.red, a.feats,
@@ -204,23 +202,13 @@ hipError_t launch_bt(const ExpertGemmArgs& a, hipStream_t stream) {
     return hipGetLastError();
 }
 
-template <ExpertOp OP>
-hipError_t launch_op(const ExpertGemmArgs& a, hipStream_t stream) {
-    switch (row_tile(a)) {
-        case 64: return launch_bt<OP, 64>(a, stream);
-        case 128: return launch_bt<OP, 128>(a, stream);
-        default: return launch_bt<OP, 256>(a, stream);
-    }
-}
-
 }  // namespace
 
 int64_t expert_gemm_grid(const ExpertGemmArgs& a) {
-    const int32_t bt = row_tile(a);
-    // A segment of c rows takes ceil(c / bt) row tiles, at most one more per
+    // A segment of c rows takes ceil(c / kTileR) row tiles, at most one more per
     // expert with rows than the rows fill.
     const int64_t experts = a.max_rows < a.E ? a.max_rows : a.E;
-    const int64_t tiles = feature_tiles(a) * ((a.max_rows + bt - 1) / bt + experts);
+    const int64_t tiles = feature_tiles(a) * ((a.max_rows + kTileR - 1) / kTileR + experts);
     const int64_t unit = int64_t(kExpertXcds) * kXcdChunk;
     return (tiles + unit - 1) / unit * unit;
 }

@@ -37,18 +37,32 @@ struct ExpertTile {
 // Finds tile number u of the launch (wavefront 0 calls it; every lane gets the
 // result). Expert e owns ceil(rows / bt) * ftiles consecutive numbers; inside
 // an expert, blocks of up to `band` row tiles: all feature tiles of a band,
-// each with the band's row tiles fastest.
+// each with the band's row tiles fastest. A lane holds up to 16 neighbouring
+// experts; their offsets are loaded in groups of 4, together, since every
+// workgroup waits for this before its first useful load.
 __device__ inline ExpertTile expert_find_tile(const int32_t* offsets, int32_t E, int32_t max_rows,
                                               int32_t bt, int32_t ftiles, int32_t band, int64_t u) {
+    constexpr int kGroup = 4;
     const int lane = threadIdx.x & 63;
     const int per = (E + 63) / 64;
     const int e_lo = min(E, lane * per);
     const int e_hi = min(E, e_lo + per);
+    int32_t first[kGroup + 1];              // first row of the group's experts
+    auto load_group = [&](int e0) {
+#pragma unroll
+        for (int k = 0; k <= kGroup; ++k) first[k] = offsets[min(e0 + k, E)];
+#pragma unroll
+        for (int k = 0; k <= kGroup; ++k) first[k] = min(max(first[k], 0), max_rows);
+    };
+    auto tiles_of = [&](int e0, int k) -> int32_t {
+        return e0 + k < e_hi ? (max(first[k + 1] - first[k], 0) + bt - 1) / bt : 0;
+    };
+    const int32_t end = min(max(offsets[E], 0), max_rows);
     int64_t local = 0;
-    for (int e = e_lo; e < e_hi; ++e) {
-        int32_t s0, s1;
-        expert_segment(offsets, e, max_rows, s0, s1);
-        local += int64_t((s1 - s0 + bt - 1) / bt) * ftiles;
+    for (int e0 = e_lo; e0 < max(e_hi, e_lo + 1); e0 += kGroup) {
+        load_group(e0);
+#pragma unroll
+        for (int k = 0; k < kGroup; ++k) local += int64_t(tiles_of(e0, k)) * ftiles;
     }
     int64_t incl = local;
 #pragma unroll
@@ -61,30 +75,29 @@ __device__ inline ExpertTile expert_find_tile(const int32_t* offsets, int32_t E,
     if (u >= total) {
         t.f = static_cast<int32_t>(u - total);
         t.rows = static_cast<int32_t>(total);
-        const int32_t end = offsets[E];
-        t.row0 = min(max(end, 0), max_rows);
+        t.row0 = end;
         return t;
     }
     int64_t base = incl - local;
     const bool mine = u >= base && u < incl;
     if (mine) {
-        for (int e = e_lo; e < e_hi; ++e) {
-            int32_t s0, s1;
-            expert_segment(offsets, e, max_rows, s0, s1);
-            const int32_t mt = (s1 - s0 + bt - 1) / bt;
-            const int64_t n = int64_t(mt) * ftiles;
-            if (u < base + n) {
+        for (int e0 = e_lo; e0 < e_hi; e0 += kGroup) {
+            if (per > kGroup) load_group(e0);
+#pragma unroll
+            for (int k = 0; k < kGroup; ++k) {
+                const int32_t mt = tiles_of(e0, k);
                 const int64_t rem = u - base;
-                const int32_t mb = static_cast<int32_t>(rem / (int64_t(ftiles) * band));
-                const int32_t in = static_cast<int32_t>(rem - int64_t(mb) * ftiles * band);
-                const int32_t mbe = min(band, mt - mb * band);
-                t.e = e;
-                t.f = in / mbe;
-                t.row0 = s0 + (mb * band + in % mbe) * bt;
-                t.rows = min(bt, s1 - t.row0);
-                break;
+                base += int64_t(mt) * ftiles;
+                if (rem >= 0 && rem < int64_t(mt) * ftiles) {
+                    const int32_t mb = static_cast<int32_t>(rem / (int64_t(ftiles) * band));
+                    const int32_t in = static_cast<int32_t>(rem - int64_t(mb) * ftiles * band);
+                    const int32_t mbe = min(band, mt - mb * band);
+                    t.e = e0 + k;
+                    t.f = in / mbe;
+                    t.row0 = first[k] + (mb * band + in % mbe) * bt;
+                    t.rows = min(bt, first[k + 1] - t.row0);
+                }
             }
-            base += n;
         }
     }
     const int src = __ffsll(static_cast<unsigned long long>(__ballot(mine))) - 1;
