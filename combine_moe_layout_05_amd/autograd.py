@@ -23,10 +23,9 @@ from typing import Optional
 
 import torch
 
-from .experts import (_activation, _offsets, _rows, _weights, gated_grouped_gemm,
-                      gated_grouped_gemm_backward, grouped_gemm_backward_input,
-                      grouped_gemm_backward_weight, grouped_gemm_forward)
-from .moe import MoeDispatcher
+from . import _lib as L
+from .experts import _activation, _offsets, _rows, _weights
+from .moe import MoeDispatcher, _call
 
 
 class _Dispatch(torch.autograd.Function):
@@ -120,35 +119,65 @@ class MoeTokenDispatcher:
                               self._total, self.disp, self._ntpr, self._generation)
 
 
+def _ffn_forward(x, w_gate_up, w_down, offsets, act: int, pre: Optional[torch.Tensor]):
+    """(h, y) of checked arguments: the calls of gated_grouped_gemm and
+    grouped_gemm_forward. h's rows behind the last segment stay unwritten, y's
+    are zero."""
+    dev, off = x.device, offsets.data_ptr()
+    R, k_in = x.shape
+    E, n_out, hidden = w_down.shape
+    h, y = x.new_empty((R, hidden)), x.new_empty((R, n_out))
+    _call("moe_gated_grouped_gemm", dev, x.data_ptr(), w_gate_up.data_ptr(), off, E, R, k_in,
+          hidden, act, h.data_ptr(), 0 if pre is None else pre.data_ptr(), 0)
+    _call("moe_grouped_gemm_forward", dev, h.data_ptr(), w_down.data_ptr(), off, E, R, hidden,
+          n_out, y.data_ptr(), L.MOE_GEMM_ZERO_TAIL)
+    return h, y
+
+
 class _ExpertFfn(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, w_gate_up, w_down, offsets, activation: str):
+    def forward(ctx, x, w_gate_up, w_down, offsets, act: int):
         # The layout's offsets are a persistent buffer the next layout
         # rewrites: the backward keeps its own copy.
         offsets = offsets.clone()
         pre = torch.empty((x.shape[0], w_gate_up.shape[1]), dtype=torch.float32,
                           device=x.device)
-        h = gated_grouped_gemm(x, w_gate_up, offsets, activation=activation, pre=pre)
+        h, y = _ffn_forward(x, w_gate_up, w_down, offsets, act, pre)
         ctx.save_for_backward(x, w_gate_up, w_down, offsets, pre, h)
-        ctx.activation = activation
-        return grouped_gemm_forward(h, w_down, offsets)
+        ctx.act = act
+        return y
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, grad_y):
+        # The forward has checked every size; these are the calls of
+        # grouped_gemm_backward_weight, gated_grouped_gemm_backward and
+        # grouped_gemm_backward_input.
         x, w_gate_up, w_down, offsets, pre, h = ctx.saved_tensors
         need_x, need_gate_up, need_down = ctx.needs_input_grad[:3]
         g = grad_y.contiguous()
+        dev, off = x.device, offsets.data_ptr()
+        R, k_in = x.shape
+        E, n_out, hidden = w_down.shape
         grad_x = grad_gate_up = grad_down = None
         if need_down:
-            grad_down = grouped_gemm_backward_weight(g, h, offsets)
+            grad_down = torch.empty_like(w_down)
+            _call("moe_grouped_gemm_backward_weight", dev, g.data_ptr(), h.data_ptr(), off, E, R,
+                  hidden, n_out, L.MOE_BF16, grad_down.data_ptr(), 0)
         if need_x or need_gate_up:
-            grad_pre = gated_grouped_gemm_backward(g, w_down, pre, offsets,
-                                                   activation=ctx.activation)
+            # Rows behind the last segment are read by neither product below.
+            grad_pre = x.new_empty((R, 2 * hidden))
+            _call("moe_gated_grouped_gemm_backward", dev, g.data_ptr(), w_down.data_ptr(),
+                  pre.data_ptr(), off, E, R, hidden, n_out, ctx.act, grad_pre.data_ptr(), 0)
             if need_gate_up:
-                grad_gate_up = grouped_gemm_backward_weight(grad_pre, x, offsets)
+                grad_gate_up = torch.empty_like(w_gate_up)
+                _call("moe_grouped_gemm_backward_weight", dev, grad_pre.data_ptr(), x.data_ptr(),
+                      off, E, R, k_in, 2 * hidden, L.MOE_BF16, grad_gate_up.data_ptr(), 0)
             if need_x:
-                grad_x = grouped_gemm_backward_input(grad_pre, w_gate_up, offsets)
+                grad_x = torch.empty_like(x)
+                _call("moe_grouped_gemm_backward_input", dev, grad_pre.data_ptr(),
+                      w_gate_up.data_ptr(), off, E, R, k_in, 2 * hidden, grad_x.data_ptr(),
+                      L.MOE_GEMM_ZERO_TAIL)
         return grad_x, grad_gate_up, grad_down, None, None
 
 
@@ -166,7 +195,7 @@ def expert_ffn(x_expert: torch.Tensor, w_gate_up: torch.Tensor, w_down: torch.Te
     of g and u are rounded to bf16: they are operands of matrix-core products.
     g and u themselves are kept in fp32."""
     dev = x_expert.device
-    _activation(activation)
+    act = _activation(activation)
     E, n2, k_in = _weights("w_gate_up", w_gate_up, dev)
     E2, _, hidden = _weights("w_down", w_down, dev)
     if E2 != E or 2 * hidden != n2:
@@ -176,6 +205,5 @@ def expert_ffn(x_expert: torch.Tensor, w_gate_up: torch.Tensor, w_down: torch.Te
     _offsets(offsets, E, dev)
     if torch.is_grad_enabled() and (x_expert.requires_grad or w_gate_up.requires_grad
                                     or w_down.requires_grad):
-        return _ExpertFfn.apply(x_expert, w_gate_up, w_down, offsets, activation)
-    h = gated_grouped_gemm(x_expert, w_gate_up, offsets, activation=activation)
-    return grouped_gemm_forward(h, w_down, offsets)
+        return _ExpertFfn.apply(x_expert, w_gate_up, w_down, offsets, act)
+    return _ffn_forward(x_expert, w_gate_up, w_down, offsets, act, None)[1]

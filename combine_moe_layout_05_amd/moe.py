@@ -103,16 +103,25 @@ def tile_expert_weights(weights: torch.Tensor) -> TiledExpertWeights:
     return TiledExpertWeights(data, E, n_out, k_in)
 
 
+# The current device's index; the private getter skips the public one's lazy
+# initialisation check, which the tensors on the device make unnecessary.
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_entry_points: dict = {}
+
+
 def _call(name: str, dev: torch.device, *args) -> None:
     """A library call on dev's current stream. Kernels launch on the current
     device, so that is switched where the tensors live on another one."""
-    fn = getattr(L.load(), name)
-    if torch.cuda.current_device() == dev.index:
+    fn = _entry_points.get(name)
+    if fn is None:
+        fn = _entry_points[name] = getattr(L.load(), name)
+    if _current_device() == dev.index:
         status = fn(*args, _stream(dev))
     else:
         with torch.cuda.device(dev):
             status = fn(*args, _stream(dev))
-    L.check(status, name)
+    if status != L.MOE_OK:
+        L.check(status, name)
 
 
 def _check_rows(name: str, t: torch.Tensor, dtype: torch.dtype, dim: int,
