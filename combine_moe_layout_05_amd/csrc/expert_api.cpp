@@ -200,15 +200,15 @@ int moe_grouped_gemm_backward_weight(const void* d_grad_out, const void* d_x_exp
 
 int64_t moe_mxfp4_weights_bytes(int32_t num_experts, int32_t n_out, int32_t k_in) {
     if (!experts_ok(num_experts) || !width_ok(n_out, 8) || !width_ok(k_in, 32)) return -1;
-    // The packing launch has a thread per packed dword.
-    if (moe::mxfp4_bytes(num_experts, n_out, k_in) / 4 / 256 >= INT32_MAX) return -1;
+    // The packing launch has a thread per feature and step.
+    if (moe::mxfp4_tiles(num_experts, n_out, k_in) / 16 >= INT32_MAX) return -1;
     return moe::mxfp4_bytes(num_experts, n_out, k_in);
 }
 
 int moe_pack_mxfp4_weights(const void* d_values, const void* d_scales, int32_t num_experts,
                            int32_t n_out, int32_t k_in, void* d_packed, void* stream) {
     if (moe_mxfp4_weights_bytes(num_experts, n_out, k_in) < 0) return MOE_ERR_INVALID_ARG;
-    if (!d_values || !d_scales || !d_packed || misaligned(d_values, 4) || misaligned(d_packed, 16))
+    if (!d_values || !d_scales || !d_packed || misaligned(d_values, 16) || misaligned(d_packed, 16))
         return MOE_ERR_INVALID_ARG;
     moe::PackMxfp4Args a;
     a.blocks = d_values;

@@ -256,40 +256,40 @@ void expert_stream_kernel(const char* __restrict__ rows, const char* __restrict_
     }
 }
 
-// One dword of the packed values per thread, then one dword of the scales.
+// One (feature, step) per thread: 64 bytes of values, rearranged from groups of
+// 32 inputs into the lanes' 16 bytes, and the step's four scales. Lanes run
+// over the 16 features of a block first, then over the steps, so that a
+// wavefront reads 256 contiguous bytes of each feature and writes whole pieces
+// of 256 bytes.
 __global__ __launch_bounds__(256)
-void pack_mxfp4_kernel(const uint8_t* __restrict__ blocks, const uint8_t* __restrict__ scales,
+void pack_mxfp4_kernel(const char* __restrict__ blocks, const uint8_t* __restrict__ scales,
                        int32_t N, int32_t K, int32_t nb, int32_t steps, int64_t tiles,
-                       uint32_t* __restrict__ dst) {
+                       char* __restrict__ dst) {
     const int64_t q = int64_t(blockIdx.x) * 256 + threadIdx.x;
-    const int64_t values = tiles * 256;
-    if (q >= values + tiles * 16) return;
-    const bool is_scale = q >= values;
-    const int64_t p = is_scale ? q - values : q;
-    const int64_t tile = is_scale ? p >> 4 : p >> 8;
+    if (q >= tiles * 16) return;
+    const int i = static_cast<int>(q & 15);
+    const int64_t tile = q >> 4;
     const int32_t t = static_cast<int32_t>(tile % steps);
     const int64_t eb = tile / steps;
-    const int32_t b = static_cast<int32_t>(eb % nb);
-    const int64_t e = eb / nb;
-    uint32_t v = is_scale ? 0x7F7F7F7Fu : 0u;
-    if (!is_scale) {
-        const int l = static_cast<int>(p >> 2) & 63, s = static_cast<int>(p) & 3;
-        const int32_t f = 16 * b + (l & 15);
-        const int32_t k = t * kMxfp4Step + 32 * s + 8 * (l >> 4);
-        if (f < N && k < K)
-            v = *reinterpret_cast<const uint32_t*>(blocks + ((e * N + f) * K + k) / 2);
-    } else {
-        const int32_t f = 16 * b + (static_cast<int>(p) & 15);
-        if (f < N)
-            for (int s = 0; s < 4; ++s) {
-                const int32_t grp = 4 * t + s;
-                if (grp < K / 32) {
-                    const uint32_t x = scales[(e * N + f) * (K / 32) + grp];
-                    v = (v & ~(0xFFu << (8 * s))) | (x << (8 * s));
-                }
-            }
+    const int32_t f = 16 * static_cast<int32_t>(eb % nb) + i;
+    const int64_t row = (eb / nb) * N + f;
+    v4i v[4];
+    uint32_t scale = 0x7F7F7F7Fu;
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+        const int32_t group = 4 * t + s;
+        v[s] = v4i{0, 0, 0, 0};
+        if (f < N && group < K / 32) {
+            v[s] = *reinterpret_cast<const v4i*>(blocks + row * (K / 2) + group * 16);
+            scale = (scale & ~(0xFFu << (8 * s))) |
+                    (uint32_t(scales[row * (K / 32) + group]) << (8 * s));
+        }
     }
-    dst[q] = v;
+#pragma unroll
+    for (int g = 0; g < 4; ++g)
+        *reinterpret_cast<v4i*>(dst + tile * 1024 + (g * 16 + i) * 16) =
+            v4i{v[0][g], v[1][g], v[2][g], v[3][g]};
+    *reinterpret_cast<uint32_t*>(dst + tiles * 1024 + tile * 64 + i * 4) = scale;
 }
 
 int64_t stream_feature_tiles(const ExpertStreamArgs& a) {
@@ -328,11 +328,10 @@ hipError_t launch_expert_stream(const ExpertStreamArgs& a, hipStream_t stream) {
 
 hipError_t launch_pack_mxfp4(const PackMxfp4Args& a, hipStream_t stream) {
     const int64_t tiles = mxfp4_tiles(a.E, a.N, a.K);
-    const int64_t dwords = tiles * 272;
-    hipLaunchKernelGGL(pack_mxfp4_kernel, dim3(static_cast<uint32_t>((dwords + 255) / 256)),
-                       dim3(256), 0, stream, static_cast<const uint8_t*>(a.blocks),
+    hipLaunchKernelGGL(pack_mxfp4_kernel, dim3(static_cast<uint32_t>((tiles * 16 + 255) / 256)),
+                       dim3(256), 0, stream, static_cast<const char*>(a.blocks),
                        static_cast<const uint8_t*>(a.scales), a.N, a.K, (a.N + 15) / 16,
-                       (a.K + kMxfp4Step - 1) / kMxfp4Step, tiles, static_cast<uint32_t*>(a.dst));
+                       (a.K + kMxfp4Step - 1) / kMxfp4Step, tiles, static_cast<char*>(a.dst));
     return hipGetLastError();
 }
 

@@ -496,7 +496,7 @@ int moe_grouped_gemm_backward_weight(const void *d_grad_out, const void *d_x_exp
  * moe_mxfp4_weights_bytes(...) bytes (-1 for sizes not supported); k_in is a
  * multiple of 32.
  *   d_values  uint8 [num_experts][n_out][k_in / 2], input 2i in the low half
- *             of byte i (4-byte aligned)
+ *             of byte i (16-byte aligned)
  *   d_scales  uint8 [num_experts][n_out][k_in / 32]
  *   d_packed  16-byte aligned */
 int64_t moe_mxfp4_weights_bytes(int32_t num_experts, int32_t n_out, int32_t k_in);
