@@ -11,8 +11,8 @@ constexpr int kWaves = 8;               // along the features
 constexpr int kBlocks = 4;              // 16-feature blocks per wavefront
 constexpr int kRowTile = 128;
 constexpr int kStages = 3;              // 128-element steps of rows in LDS
-constexpr int kXcdChunk = 32;
-constexpr int kBand = 4;
+constexpr int kXcdChunk = 8;
+constexpr int kBand = 8;
 
 template <bool GATED>
 __global__ __launch_bounds__(kWaves * 64, 2)

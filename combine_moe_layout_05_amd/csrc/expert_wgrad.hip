@@ -40,6 +40,31 @@ __device__ __forceinline__ void fetch(const Kop& ko, const Nop& no, const v4i* b
     for (int b = 0; b < kBlkN; ++b) d.n[b] = nn.frag(buf + Kop::kChunks, b, 0);
 }
 
+// A tile's results on their way out through LDS: rows of CHUNKS 16-byte chunks,
+// chunk c of row r at c ^ (r % 16), so that writes of one chunk of 16 rows and
+// reads of whole rows both spread over the banks. From there whole rows go out,
+// CHUNKS * 16 contiguous bytes each; from the products' own lanes they would
+// leave in pieces of 64 bytes. Streamed past the caches: the gradient is as
+// large as the weights and is not read here.
+template <int ROWS, int CHUNKS>
+struct OutTile {
+    __device__ static int at(int row, int chunk) { return row * CHUNKS + (chunk ^ (row & 15)); }
+    // Rows [0, rows) to dst, `pitch` bytes apart, their first `chunks` chunks.
+    __device__ __forceinline__ static void store(const v4i* lds, char* dst, int64_t pitch,
+                                                 int rows, int chunks, int wave, int lane) {
+        constexpr int kRows = 64 / CHUNKS;          // of one store
+        const int c = lane % CHUNKS;
+        const int r0 = wave * (ROWS / kWaves) + lane / CHUNKS;
+#pragma unroll
+        for (int q = 0; q < ROWS / kWaves / kRows; ++q) {
+            const int r = r0 + q * kRows;
+            const v4i v = lds[at(r, c)];
+            if (r < rows && c < chunks)
+                __builtin_nontemporal_store(v, reinterpret_cast<v4i*>(dst + r * pitch) + c);
+        }
+    }
+};
+
 template <bool F32, bool ACCUMULATE>
 __global__ __launch_bounds__(kWaves * 64, 2)
 void expert_wgrad_kernel(const char* __restrict__ dy, const char* __restrict__ x,
@@ -156,30 +181,25 @@ void expert_wgrad_kernel(const char* __restrict__ dy, const char* __restrict__ x
     }
 
     const int i = lane & 15, g = lane >> 4;
+    char* tile = dw + ((int64_t(e) * N + nt0) * K + kt0) * (F32 ? 4 : 2);
+    const int rows = min(kTileN, N - nt0), width = min(kTileK, K - kt0);
+    if constexpr (ACCUMULATE) {
+        // Every lane adds to four neighbours of one row.
 #pragma unroll
-    for (int b = 0; b < kBlkN; ++b) {
-        const int32_t n = nt0 + (wn * kBlkN + b) * 16 + i;
-        if (n >= N) continue;
-        const int64_t row = (int64_t(e) * N + n) * K;
+        for (int b = 0; b < kBlkN; ++b) {
+            const int n = (wn * kBlkN + b) * 16 + i;
+            if (n >= rows) continue;
 #pragma unroll
-        for (int a = 0; a < kBlkK; a += 2) {
-            if constexpr (F32) {
-#pragma unroll
-                for (int c = a; c < a + 2; ++c) {
-                    const int32_t k = kt0 + (wk * kBlkK + c) * 16 + g * 4;
-                    if (k >= K) continue;
-                    f32x4* p = reinterpret_cast<f32x4*>(dw + (row + k) * 4);
-                    f32x4 v = acc[c][b];
-                    if constexpr (ACCUMULATE) v = *p + v;
-                    *p = v;
-                }
-            } else if constexpr (ACCUMULATE) {
-#pragma unroll
-                for (int c = a; c < a + 2; ++c) {
-                    const int32_t k = kt0 + (wk * kBlkK + c) * 16 + g * 4;
-                    if (k >= K) continue;
-                    v2i* p = reinterpret_cast<v2i*>(dw + (row + k) * 2);
-                    f32x4 v = acc[c][b];
+            for (int a = 0; a < kBlkK; ++a) {
+                const int k = (wk * kBlkK + a) * 16 + g * 4;
+                if (k >= width) continue;
+                char* at = tile + (int64_t(n) * K + k) * (F32 ? 4 : 2);
+                f32x4 v = acc[a][b];
+                if constexpr (F32) {
+                    f32x4* p = reinterpret_cast<f32x4*>(at);
+                    *p = *p + v;
+                } else {
+                    v2i* p = reinterpret_cast<v2i*>(at);
                     const v2i o = *p;
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
@@ -188,15 +208,39 @@ void expert_wgrad_kernel(const char* __restrict__ dy, const char* __restrict__ x
                     }
                     *p = pack_bf16x4(v);
                 }
-            } else {
-                const int32_t k = kt0 + (wk * kBlkK + a + (g & 1)) * 16 + (g >> 1) * 8;
-                const v4i v = pair_blocks(pack_bf16x4(acc[a][b]), pack_bf16x4(acc[a + 1][b]));
-                // Streamed past the caches: the gradient is as large as the
-                // weights and is not read here.
-                if (k < K)
-                    __builtin_nontemporal_store(v, reinterpret_cast<v4i*>(dw + (row + k) * 2));
             }
         }
+    } else if constexpr (F32) {
+        // 64 KiB at a time: the rows of half the blocks, then of the others.
+        typedef OutTile<kBlkN / 2 * 16, kTileK / 4> Out;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            if (half) __syncthreads();
+#pragma unroll
+            for (int b = 0; b < kBlkN / 2; ++b)
+#pragma unroll
+                for (int a = 0; a < kBlkK; ++a)
+                    lds[Out::at((wn * (kBlkN / 2) + b) * 16 + i, (wk * kBlkK + a) * 4 + g)] =
+                        __builtin_bit_cast(v4i, acc[a][half * (kBlkN / 2) + b]);
+            __syncthreads();
+#pragma unroll
+            for (int p = 0; p < kWavesN; ++p) {
+                const int first = (p * kBlkN + half * (kBlkN / 2)) * 16;
+                Out::store(lds + p * (kBlkN / 2) * 16 * (kTileK / 4),
+                           tile + int64_t(first) * K * 4, int64_t(K) * 4, rows - first, width / 4,
+                           wave, lane);
+            }
+        }
+    } else {
+        typedef OutTile<kTileN, kTileK / 8> Out;
+#pragma unroll
+        for (int b = 0; b < kBlkN; ++b)
+#pragma unroll
+            for (int a = 0; a < kBlkK; a += 2)
+                lds[Out::at((wn * kBlkN + b) * 16 + i, (wk * kBlkK + a + (g & 1)) * 2 + (g >> 1))] =
+                    pair_blocks(pack_bf16x4(acc[a][b]), pack_bf16x4(acc[a + 1][b]));
+        __syncthreads();
+        Out::store(lds, tile, int64_t(K) * 2, rows, width / 8, wave, lane);
     }
 }
 
