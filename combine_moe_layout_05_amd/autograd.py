@@ -25,7 +25,7 @@ import torch
 
 from . import _lib as L
 from .experts import _activation, _offsets, _rows, _weights
-from .moe import MoeDispatcher, _call
+from .moe import MoeDispatcher, _call, _stream
 
 
 class _Dispatch(torch.autograd.Function):
@@ -181,6 +181,31 @@ class _ExpertFfn(torch.autograd.Function):
         return grad_x, grad_gate_up, grad_down, None, None
 
 
+# Marks a leaf's gradient accumulator as made by a call on the default stream.
+_ON_DEFAULT_STREAM = "combine_moe_layout.default_stream"
+
+
+def _leaf_accumulators(tensors, stream: int):
+    """The gradient accumulators of the leaves among `tensors`, to be held until
+    the call's node holds them. The engine runs an accumulator on the stream it
+    was made on, and it lives as long as any graph that reaches it. One made on
+    the default stream cannot join a capture: the backward would fail inside
+    the engine and end the process, so such a capture is refused here."""
+    nodes = [torch.autograd.graph.get_gradient_edge(t).node
+             for t in tensors if t.requires_grad and t.is_leaf]
+    if torch.cuda.is_current_stream_capturing():
+        if any(n.metadata.get(_ON_DEFAULT_STREAM) for n in nodes):
+            raise RuntimeError(
+                "expert_ffn cannot be captured while the output of an earlier call on the default "
+                "stream that reaches the same leaf tensors is alive: its gradient accumulators "
+                "belong to that stream. Delete that output first, or run the calls before the "
+                "capture on a side stream.")
+    elif stream == 0:
+        for n in nodes:
+            n.metadata[_ON_DEFAULT_STREAM] = True
+    return nodes
+
+
 def expert_ffn(x_expert: torch.Tensor, w_gate_up: torch.Tensor, w_down: torch.Tensor,
                offsets: torch.Tensor, activation: str = "silu") -> torch.Tensor:
     """Differentiable gated feed-forward block of the experts, between
@@ -193,7 +218,11 @@ def expert_ffn(x_expert: torch.Tensor, w_gate_up: torch.Tensor, w_down: torch.Te
     Gradients reach x_expert and both weights (bf16, in one rounding of an fp32
     sum). Between the kernels h = act(g) * u and, in the backward, the gradients
     of g and u are rounded to bf16: they are operands of matrix-core products.
-    g and u themselves are kept in fp32."""
+    g and u themselves are kept in fp32.
+
+    A step can be captured into a graph (forward and backward together) after
+    warm-up calls on a side stream. While an output of a call on the default
+    stream that reaches the same leaves is alive, the capture is refused."""
     dev = x_expert.device
     act = _activation(activation)
     E, n2, k_in = _weights("w_gate_up", w_gate_up, dev)
@@ -205,5 +234,8 @@ def expert_ffn(x_expert: torch.Tensor, w_gate_up: torch.Tensor, w_down: torch.Te
     _offsets(offsets, E, dev)
     if torch.is_grad_enabled() and (x_expert.requires_grad or w_gate_up.requires_grad
                                     or w_down.requires_grad):
-        return _ExpertFfn.apply(x_expert, w_gate_up, w_down, offsets, act)
+        nodes = _leaf_accumulators((x_expert, w_gate_up, w_down), _stream(dev))
+        y = _ExpertFfn.apply(x_expert, w_gate_up, w_down, offsets, act)
+        del nodes
+        return y
     return _ffn_forward(x_expert, w_gate_up, w_down, offsets, act, None)[1]

@@ -637,3 +637,59 @@ def test_no_rows_and_one_expert():
     assert tuple(x.grad.shape) == (0, 32)
     assert (w1.grad == 0).all() and (w2.grad == 0).all()
     assert tuple(grouped_gemm(x.detach(), _mx(2, 64, 32, 1)[2], off_d).shape) == (0, 64)
+
+
+def _captured_step(leaves, off_d, dy):
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = expert_ffn(*leaves, off_d)
+        y.backward(dy)
+    return graph, y
+
+
+def test_training_step_in_a_captured_graph():
+    """Forward and backward in one graph, replayed on new inputs and compared
+    with the eager gradients; refused while an eager graph of the same leaves
+    from the default stream is alive."""
+    off, off_d = _off([40, 0, 90, 7])
+    total, D, F = off[-1], 136, 72
+    x = _rand((total, D), 1).to(DEV).requires_grad_(True)
+    w1 = _rand((4, 2 * F, D), 2, D ** -0.5).to(DEV).requires_grad_(True)
+    w2 = _rand((4, D, F), 3, F ** -0.5).to(DEV).requires_grad_(True)
+    dy = _rand((total, D), 4).to(DEV)
+    leaves = (x, w1, w2)
+
+    def eager():
+        copies = [t.detach().clone().requires_grad_(True) for t in leaves]
+        y = expert_ffn(*copies, off_d)
+        y.backward(dy)
+        return [y.detach(), *(t.grad for t in copies)]
+
+    kept = expert_ffn(*leaves, off_d)
+    note("capture beside an eager graph: refused")
+    with pytest.raises(RuntimeError, match="default stream"):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            expert_ffn(*leaves, off_d)
+    del kept, graph
+    sync_or_fail()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        expert_ffn(*leaves, off_d).backward(dy)
+    torch.cuda.current_stream().wait_stream(side)
+    for t in leaves:
+        t.grad = None
+    note("training step graph")
+    graph, y = _captured_step(leaves, off_d, dy)
+    for seed in range(10, 13):
+        with torch.no_grad():
+            x.copy_(_rand((total, D), seed)), dy.copy_(_rand((total, D), seed + 50))
+        for t in leaves:
+            t.grad.zero_()
+        graph.replay()
+        got = [t.detach().clone() for t in (y, x.grad, w1.grad, w2.grad)]
+        sync_or_fail()
+        for a, b in zip(got, eager()):
+            assert torch.equal(a, b)
+        sync_or_fail()
