@@ -7,41 +7,53 @@
 namespace moe {
 namespace {
 
-constexpr int kWaves = 8;
-constexpr int kWavesF = 4;              // wavefronts along the features
-constexpr int kWavesR = 2;              // and along the rows
-constexpr int kTileF = 256;             // weight positions per workgroup
-constexpr int kTileR = 256;             // rows per workgroup
-constexpr int kBlkF = kTileF / kWavesF / 16;
+constexpr int kWavesR = 2;              // wavefronts along the rows
+constexpr int kBlkF = 4;                // 16-position blocks of weights per wavefront
+
+// A workgroup's tile: WAVES_F wavefronts of 64 weight positions times ROWS rows.
+// The large one reads least per product; the small one makes up to eight times
+// as many workgroups of the same product, two to a CU.
+template <int WAVES_F, int ROWS>
+struct Shape {
+    static constexpr int kWavesF = WAVES_F;
+    static constexpr int kWaves = WAVES_F * kWavesR;
+    static constexpr int kTileF = WAVES_F * kBlkF * 16;
+    static constexpr int kTileR = ROWS;
+    // Stages of 64-element steps in LDS for a tile of `rows` rows.
+    static constexpr int stages(int rows) { return rows > 128 ? 2 : 3; }
+    // Output features: the gated product holds gate and up rows.
+    static constexpr int feats(ExpertOp op) { return op == ExpertOp::kGated ? kTileF / 2 : kTileF; }
+};
+typedef Shape<4, 256> Large;
+typedef Shape<2, 64> Small;
 constexpr int kXcdChunk = 16;
 constexpr int kBand = 8;
 
 constexpr bool strided(ExpertOp op) {
     return op == ExpertOp::kInputGrad || op == ExpertOp::kGatedGrad;
 }
-// Output features per workgroup: the gated product holds gate and up rows.
-constexpr int tile_feats(ExpertOp op) { return op == ExpertOp::kGated ? kTileF / 2 : kTileF; }
 
-template <bool STRIDED>
+template <class S, bool STRIDED>
 struct WeightOperand {
-    typedef PackedOperand<kTileF, kWaves> type;
+    typedef PackedOperand<S::kTileF, S::kWaves> type;
 };
-template <>
-struct WeightOperand<true> {
-    typedef StridedOperand<kTileF, kWaves, 64> type;
+template <class S>
+struct WeightOperand<S, true> {
+    typedef StridedOperand<S::kTileF, S::kWaves, 64> type;
 };
 
-template <ExpertOp OP>
-__global__ __launch_bounds__(kWaves * 64, 2)
+template <ExpertOp OP, class S>
+__global__ __launch_bounds__(S::kWaves * 64, 2)
 void expert_gemm_kernel(const char* __restrict__ rows, const char* __restrict__ w,
                         const int32_t* __restrict__ offsets, int32_t E, int32_t max_rows,
                         int32_t red, int32_t feats, int32_t ftiles, int32_t act,
                         char* __restrict__ out, float* __restrict__ pre, int32_t zero_tail) {
-    typedef typename WeightOperand<strided(OP)>::type Weights;
-    // Three stages up to 128 rows, two above.
-    constexpr int kLds2 = 2 * (Weights::kChunks + PackedOperand<kTileR, kWaves>::kChunks);
-    constexpr int kLds3 = 3 * (Weights::kChunks + PackedOperand<kTileR / 2, kWaves>::kChunks);
-    __shared__ v4i lds[kLds3 > kLds2 ? kLds3 : kLds2];
+    constexpr int kWaves = S::kWaves, kWavesF = S::kWavesF, kTileF = S::kTileF,
+                  kTileR = S::kTileR;
+    typedef typename WeightOperand<S, strided(OP)>::type Weights;
+    constexpr auto lds_of = [](int rows) { return S::stages(rows) * (Weights::kChunks + rows * 8); };
+    constexpr int kHalf = kTileR > 64 ? kTileR / 2 : kTileR;
+    __shared__ v4i lds[lds_of(kHalf) > lds_of(kTileR) ? lds_of(kHalf) : lds_of(kTileR)];
     __shared__ int32_t info[4];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -69,7 +81,7 @@ void expert_gemm_kernel(const char* __restrict__ rows, const char* __restrict__ 
                              static_cast<int32_t>(out_pitch / 16), ft, int64_t(gridDim.x) - nrows);
         return;
     }
-    const int32_t f0 = ft * tile_feats(OP);
+    const int32_t f0 = ft * S::feats(OP);
     const int64_t red_pitch = int64_t(red) * 2;
 
     const int wf = wave % kWavesF, wr = wave / kWavesF;
@@ -97,7 +109,7 @@ void expert_gemm_kernel(const char* __restrict__ rows, const char* __restrict__ 
     auto run = [&](auto parts) {
     constexpr int kRowsUsed = decltype(parts)::value * 64;
     constexpr int kBlkR = kRowsUsed / kWavesR / 16;
-    constexpr int kStages = kRowsUsed > 128 ? 2 : 3;
+    constexpr int kStages = S::stages(kRowsUsed);
     PackedOperand<kRowsUsed, kWaves> rt;
     const char* rbase = rows + int64_t(row0) * red_pitch;
     rt.init(wave, lane, wr * kBlkR, red_pitch, [&](int) { return rbase; },
@@ -176,41 +188,62 @@ void expert_gemm_kernel(const char* __restrict__ rows, const char* __restrict__ 
     }
     };
     const int parts = (nrows + 63) / 64;
-    if (parts == 1)
-        run(std::integral_constant<int, 1>{});
-    else if (parts == 2)
-        run(std::integral_constant<int, 2>{});
-    else if (parts == 3)
-        run(std::integral_constant<int, 3>{});
-    else
-        run(std::integral_constant<int, 4>{});
+    if constexpr (kTileR > 64) {
+        if (parts == 2) return run(std::integral_constant<int, 2>{});
+        if (parts == 3) return run(std::integral_constant<int, 3>{});
+        if (parts == 4) return run(std::integral_constant<int, 4>{});
+    }
+    run(std::integral_constant<int, 1>{});
 }
 
+template <class S>
 int64_t feature_tiles(const ExpertGemmArgs& a) {
-    const int32_t per = tile_feats(a.op);
+    const int32_t per = S::feats(a.op);
     return (int64_t(a.feats) + per - 1) / per;
+}
+
+template <class S>
+int64_t grid_of(const ExpertGemmArgs& a) {
+    // A segment of c rows takes ceil(c / kTileR) row tiles, at most one more
+    // per expert with rows than the rows fill.
+    const int64_t experts = a.max_rows < a.E ? a.max_rows : a.E;
+    const int64_t tiles =
+        feature_tiles<S>(a) * ((a.max_rows + S::kTileR - 1) / S::kTileR + experts);
+    const int64_t unit = int64_t(kExpertXcds) * kXcdChunk;
+    return (tiles + unit - 1) / unit * unit;
+}
+
+// The small shape where the large one would leave half the 256 CUs idle.
+// Measured on MI355X, one expert of 4096 -> 2 x 2048 gated: 24.8 against 84.1 us
+// at 256 rows (16 large tiles), 42.5 against 87.7 at 1024 (64), 81.0 against
+// 91.0 at 2048 (128), 156 against 112 us at 4096 (256); 16 experts of 1024 -> 2 x
+// 704: 24.8 against 29.0 us at 4096 rows (96), 38.0 against 32.6 at 8192 (192).
+bool use_small(const ExpertGemmArgs& a) {
+    const int64_t row_tiles = (a.max_rows + Large::kTileR - 1) / Large::kTileR;
+    const int64_t experts = a.max_rows < a.E ? a.max_rows : a.E;
+    return feature_tiles<Large>(a) * (row_tiles > experts ? row_tiles : experts) <= 128;
+}
+
+template <ExpertOp OP, class S>
+hipError_t launch_shape(const ExpertGemmArgs& a, hipStream_t stream) {
+    hipLaunchKernelGGL((expert_gemm_kernel<OP, S>), dim3(static_cast<uint32_t>(grid_of<S>(a))),
+                       dim3(S::kWaves * 64), 0, stream, static_cast<const char*>(a.rows),
+                       static_cast<const char*>(a.w), a.offsets, a.E,
+                       static_cast<int32_t>(a.max_rows), a.red, a.feats,
+                       static_cast<int32_t>(feature_tiles<S>(a)), a.activation,
+                       static_cast<char*>(a.out), a.pre, a.zero_tail ? 1 : 0);
+    return hipGetLastError();
 }
 
 template <ExpertOp OP>
 hipError_t launch_op(const ExpertGemmArgs& a, hipStream_t stream) {
-    hipLaunchKernelGGL((expert_gemm_kernel<OP>), dim3(static_cast<uint32_t>(expert_gemm_grid(a))),
-                       dim3(kWaves * 64), 0, stream, static_cast<const char*>(a.rows),
-                       static_cast<const char*>(a.w), a.offsets, a.E,
-                       static_cast<int32_t>(a.max_rows), a.red, a.feats,
-                       static_cast<int32_t>(feature_tiles(a)), a.activation,
-                       static_cast<char*>(a.out), a.pre, a.zero_tail ? 1 : 0);
-    return hipGetLastError();
+    return use_small(a) ? launch_shape<OP, Small>(a, stream) : launch_shape<OP, Large>(a, stream);
 }
 
 }  // namespace
 
 int64_t expert_gemm_grid(const ExpertGemmArgs& a) {
-    // A segment of c rows takes ceil(c / kTileR) row tiles, at most one more per
-    // expert with rows than the rows fill.
-    const int64_t experts = a.max_rows < a.E ? a.max_rows : a.E;
-    const int64_t tiles = feature_tiles(a) * ((a.max_rows + kTileR - 1) / kTileR + experts);
-    const int64_t unit = int64_t(kExpertXcds) * kXcdChunk;
-    return (tiles + unit - 1) / unit * unit;
+    return use_small(a) ? grid_of<Small>(a) : grid_of<Large>(a);
 }
 
 hipError_t launch_expert_gemm(const ExpertGemmArgs& a, hipStream_t stream) {

@@ -7,9 +7,15 @@
 namespace moe {
 namespace {
 
-constexpr int kWaves = 8;               // along the features
 constexpr int kBlocks = 4;              // 16-feature blocks per wavefront
-constexpr int kRowTile = 128;
+
+// Four wavefronts and 64 rows: two such workgroups fit a CU. Measured on MI355X
+// against eight wavefronts of 128 rows, one to a CU, and two of 64 rows: 43.8
+// against 90.9 and 52.4 us for one expert of 4096 -> 2 x 2048 at 1024 rows, 569
+// against 597 and 695 us for 128 such experts at 16384 rows, 971 against 976 and
+// 1214 us at 32768.
+constexpr int kWaves = 4;               // along the features
+constexpr int kRowTile = 64;
 constexpr int kStages = 3;              // 128-element steps of rows in LDS
 constexpr int kXcdChunk = 8;
 constexpr int kBand = 8;
@@ -68,10 +74,8 @@ void expert_mxfp4_kernel(const char* __restrict__ rows, const char* __restrict__
 
     auto run = [&](auto row_blocks) {
         constexpr int NB = decltype(row_blocks)::value;
-        typedef PackedOperand<(NB > 4 ? 128 : 64), kWaves> Rows;
+        typedef PackedOperand<kRowTile, kWaves> Rows;
         constexpr int kLoads = 2 * Rows::kLoads;                // of a step
-        constexpr int kGroup = NB % 3 == 0 ? 3 : NB < 4 ? NB : 4;   // row blocks fetched at once
-        constexpr int kFetches = 4 * NB / kGroup;               // per step
         Rows rt;
         const int64_t pitch = int64_t(red) * 2;
         const char* rbase = rows + int64_t(row0) * pitch;
@@ -143,30 +147,29 @@ void expert_mxfp4_kernel(const char* __restrict__ rows, const char* __restrict__
             // must not wait for these loads.
             if (t + 2 < steps) issue_rows(t + 2, free);
             const v4i* buf = stage_of(stage);
-            auto fetch = [&](int n, bf16x8 (&d)[kGroup]) {
-                const int s = n * kGroup / NB, b0 = n * kGroup % NB;
+            // The rows of scale group s, one product deep.
+            auto fetch = [&](int s, bf16x8 (&d)[NB]) {
 #pragma unroll
-                for (int b = 0; b < kGroup; ++b)
-                    d[b] = rt.frag(buf + (s >> 1) * Rows::kChunks, b0 + b, s & 1);
+                for (int b = 0; b < NB; ++b)
+                    d[b] = rt.frag(buf + (s >> 1) * Rows::kChunks, b, s & 1);
             };
-            bf16x8 cur[kGroup], nxt[kGroup];
+            bf16x8 cur[NB], nxt[NB];
             fetch(0, cur);
 #pragma unroll
-            for (int n = 0; n < kFetches; ++n) {
-                if (n + 1 < kFetches) fetch(n + 1, nxt);
-                const int s = n * kGroup / NB, b0 = n * kGroup % NB;
-                if (b0 == 0 && s > 0) {
+            for (int s = 0; s < 4; ++s) {
+                if (s < 3) fetch(s + 1, nxt);
+                if (s > 0) {
 #pragma unroll
                     for (int a = 0; a < kBlocks; ++a) wf[a] = mine[a].frag(s);
                 }
 #pragma unroll
-                for (int b = 0; b < kGroup; ++b)
+                for (int b = 0; b < NB; ++b)
 #pragma unroll
                     for (int a = 0; a < kBlocks; ++a)
-                        acc[a][b0 + b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                            wf[a], cur[b], acc[a][b0 + b], 0, 0, 0);
+                        acc[a][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf[a], cur[b],
+                                                                            acc[a][b], 0, 0, 0);
 #pragma unroll
-                for (int b = 0; b < kGroup; ++b) cur[b] = nxt[b];
+                for (int b = 0; b < NB; ++b) cur[b] = nxt[b];
             }
             __builtin_amdgcn_sched_barrier(0);
             load_w(min(t + 2, steps - 1), mine);
@@ -226,12 +229,8 @@ void expert_mxfp4_kernel(const char* __restrict__ rows, const char* __restrict__
         run(std::integral_constant<int, 2>{});
     else if (nrows <= 48)
         run(std::integral_constant<int, 3>{});
-    else if (nrows <= 64)
-        run(std::integral_constant<int, 4>{});
-    else if (nrows <= 96)
-        run(std::integral_constant<int, 6>{});
     else
-        run(std::integral_constant<int, 8>{});
+        run(std::integral_constant<int, 4>{});
 }
 
 int64_t feature_tiles(const ExpertStreamArgs& a) {

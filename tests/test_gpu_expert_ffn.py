@@ -174,6 +174,9 @@ MX = [
     ([300], 4, 640, 64),
     ([0, 0], 8, 64, 32),
     ([int(i % 5 == 0) * (i % 7) for i in range(300)], 5, 64, 48),
+    # many rows and features: the tiled form, last tiles of every size
+    ([16, 900, 33, 61, 500, 130], 11, 224, 1040),
+    ([2500], 4, 160, 784),
 ]
 
 
@@ -226,7 +229,7 @@ def test_mxfp4_gated(i, name):
     assert (fresh[total:].view(torch.int16) == 0).all()
 
 
-@pytest.mark.parametrize("rows", [2, 80, 300])
+@pytest.mark.parametrize("rows", [2, 80, 300, 900])
 def test_mxfp4_every_value_and_scale(rows):
     """x is a one in one place per row, so each output is one weight: every
     e2m1 value under every scale byte, exactly (bf16 holds them all)."""
