@@ -5,6 +5,7 @@
 
 #include <climits>
 #include <cstdint>
+#include <initializer_list>
 
 #include "expert_kernels.h"
 #include "moe.h"
@@ -22,6 +23,32 @@ bool width_ok(int32_t n, int32_t multiple) {
 bool experts_ok(int32_t E) { return E >= 1 && E <= MOE_MAX_EXPERTS; }
 
 bool activation_ok(int32_t a) { return a == MOE_ACT_SILU || a == MOE_ACT_GELU_TANH; }
+
+// Whether two buffers share a byte. The sizes stay below 2^56 bytes.
+bool overlap(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
+    const uintptr_t pa = reinterpret_cast<uintptr_t>(a), pb = reinterpret_cast<uintptr_t>(b);
+    return pa < pb ? pb - pa < static_cast<uintptr_t>(a_bytes)
+                   : pa - pb < static_cast<uintptr_t>(b_bytes);
+}
+
+// A buffer a call reads.
+struct Input {
+    const void* p;
+    int64_t bytes;
+};
+Input rows_of(const void* p, int64_t rows, int64_t width, int64_t elem = 2) {
+    return {p, rows * width * elem};
+}
+Input weights_of(const void* p, int64_t E, int64_t n, int64_t k) { return {p, E * n * k * 2}; }
+Input offsets_of(const int32_t* p, int32_t E) { return {p, (int64_t(E) + 1) * 4}; }
+
+// An output that shares bytes with none of the inputs: other workgroups still
+// read those when it is written.
+bool apart(const void* out, int64_t bytes, std::initializer_list<Input> inputs) {
+    for (const Input& in : inputs)
+        if (overlap(out, bytes, in.p, in.bytes)) return false;
+    return true;
+}
 
 // bf16 buffers every call of the family needs, with its offsets.
 bool buffers_ok(const void* a, const void* b, const void* c, const int32_t* offsets) {
@@ -93,11 +120,15 @@ int run_gemm(moe::ExpertOp op, const void* rows, const void* w, const int32_t* o
 int run_mxfp4(bool gated, const void* rows, const void* packed, const int32_t* offsets, int32_t E,
               int64_t max_rows, int32_t red, int32_t feats, int32_t activation, void* out,
               int32_t flags, void* stream) {
-    if (moe_mxfp4_weights_bytes(E, gated ? 2 * feats : feats, red) < 0) return MOE_ERR_INVALID_ARG;
+    const int64_t packed_bytes = moe_mxfp4_weights_bytes(E, gated ? 2 * feats : feats, red);
+    if (packed_bytes < 0) return MOE_ERR_INVALID_ARG;
     if (max_rows < 0 || max_rows > INT32_MAX || (flags & ~MOE_GEMM_ZERO_TAIL))
         return MOE_ERR_INVALID_ARG;
     if (max_rows == 0) return MOE_OK;
-    if (!buffers_ok(rows, packed, out, offsets)) return MOE_ERR_INVALID_ARG;
+    if (!buffers_ok(rows, packed, out, offsets) ||
+        !apart(out, max_rows * feats * 2,
+               {rows_of(rows, max_rows, red), {packed, packed_bytes}, offsets_of(offsets, E)}))
+        return MOE_ERR_INVALID_ARG;
     moe::ExpertStreamArgs a;
     a.mxfp4 = true;
     a.gated = gated;
@@ -135,6 +166,13 @@ int moe_gated_grouped_gemm(const void* d_x_expert, const void* d_weights,
     if (max_rows == 0) return MOE_OK;
     if (!buffers_ok(d_x_expert, d_weights, d_h, d_offsets) || (d_pre && misaligned(d_pre, 16)))
         return MOE_ERR_INVALID_ARG;
+    const Input x = rows_of(d_x_expert, max_rows, k_in);
+    const Input w = weights_of(d_weights, num_experts, int64_t(2) * n_hidden, k_in);
+    const Input off = offsets_of(d_offsets, num_experts);
+    const Input h = rows_of(d_h, max_rows, n_hidden);
+    if (!apart(d_h, h.bytes, {x, w, off}) ||
+        (d_pre && !apart(d_pre, max_rows * n_hidden * 8, {x, w, off, h})))
+        return MOE_ERR_INVALID_ARG;
     return run_gemm(moe::ExpertOp::kGated, d_x_expert, d_weights, d_offsets, num_experts, max_rows,
                     k_in, n_hidden, activation, d_h, d_pre, flags, stream);
 }
@@ -147,7 +185,12 @@ int moe_grouped_gemm_forward(const void* d_x_expert, const void* d_weights,
         max_rows > INT32_MAX || (flags & ~MOE_GEMM_ZERO_TAIL))
         return MOE_ERR_INVALID_ARG;
     if (max_rows == 0) return MOE_OK;
-    if (!buffers_ok(d_x_expert, d_weights, d_out, d_offsets)) return MOE_ERR_INVALID_ARG;
+    if (!buffers_ok(d_x_expert, d_weights, d_out, d_offsets) ||
+        !apart(d_out, max_rows * n_out * 2,
+               {rows_of(d_x_expert, max_rows, k_in),
+                weights_of(d_weights, num_experts, n_out, k_in),
+                offsets_of(d_offsets, num_experts)}))
+        return MOE_ERR_INVALID_ARG;
     return run_gemm(moe::ExpertOp::kPlain, d_x_expert, d_weights, d_offsets, num_experts, max_rows,
                     k_in, n_out, MOE_ACT_SILU, d_out, nullptr, flags, stream);
 }
@@ -160,7 +203,12 @@ int moe_grouped_gemm_backward_input(const void* d_grad_out, const void* d_weight
         max_rows > INT32_MAX || (flags & ~MOE_GEMM_ZERO_TAIL))
         return MOE_ERR_INVALID_ARG;
     if (max_rows == 0) return MOE_OK;
-    if (!buffers_ok(d_grad_out, d_weights, d_grad_x, d_offsets)) return MOE_ERR_INVALID_ARG;
+    if (!buffers_ok(d_grad_out, d_weights, d_grad_x, d_offsets) ||
+        !apart(d_grad_x, max_rows * k_in * 2,
+               {rows_of(d_grad_out, max_rows, n_out),
+                weights_of(d_weights, num_experts, n_out, k_in),
+                offsets_of(d_offsets, num_experts)}))
+        return MOE_ERR_INVALID_ARG;
     return run_gemm(moe::ExpertOp::kInputGrad, d_grad_out, d_weights, d_offsets, num_experts,
                     max_rows, n_out, k_in, MOE_ACT_SILU, d_grad_x, nullptr, flags, stream);
 }
@@ -176,7 +224,12 @@ int moe_gated_grouped_gemm_backward(const void* d_grad_out, const void* d_weight
         return MOE_ERR_INVALID_ARG;
     if (max_rows == 0) return MOE_OK;
     if (!buffers_ok(d_grad_out, d_weights, d_grad_pre, d_offsets) || !d_pre ||
-        misaligned(d_pre, 16))
+        misaligned(d_pre, 16) ||
+        !apart(d_grad_pre, max_rows * n_hidden * 4,
+               {rows_of(d_grad_out, max_rows, n_out),
+                weights_of(d_weights, num_experts, n_out, n_hidden),
+                rows_of(d_pre, max_rows, int64_t(2) * n_hidden, 4),
+                offsets_of(d_offsets, num_experts)}))
         return MOE_ERR_INVALID_ARG;
     return run_gemm(moe::ExpertOp::kGatedGrad, d_grad_out, d_weights, d_offsets, num_experts,
                     max_rows, n_out, n_hidden, activation, d_grad_pre,
@@ -197,6 +250,11 @@ int moe_grouped_gemm_backward_weight(const void* d_grad_out, const void* d_x_exp
     // Without rows nothing is read: the gradient is zero (or stays).
     if (max_rows > 0 && (!d_grad_out || !d_x_expert || misaligned(d_grad_out, 16) ||
                          misaligned(d_x_expert, 16)))
+        return MOE_ERR_INVALID_ARG;
+    if (!apart(d_grad_w,
+               int64_t(num_experts) * n_out * k_in * (grad_dtype == MOE_F32 ? 4 : 2),
+               {rows_of(d_grad_out, max_rows, n_out), rows_of(d_x_expert, max_rows, k_in),
+                offsets_of(d_offsets, num_experts)}))
         return MOE_ERR_INVALID_ARG;
     moe::ExpertWgradArgs a;
     a.dy = d_grad_out;
@@ -222,8 +280,12 @@ int64_t moe_mxfp4_weights_bytes(int32_t num_experts, int32_t n_out, int32_t k_in
 
 int moe_pack_mxfp4_weights(const void* d_values, const void* d_scales, int32_t num_experts,
                            int32_t n_out, int32_t k_in, void* d_packed, void* stream) {
-    if (moe_mxfp4_weights_bytes(num_experts, n_out, k_in) < 0) return MOE_ERR_INVALID_ARG;
+    const int64_t bytes = moe_mxfp4_weights_bytes(num_experts, n_out, k_in);
+    if (bytes < 0) return MOE_ERR_INVALID_ARG;
     if (!d_values || !d_scales || !d_packed || misaligned(d_values, 16) || misaligned(d_packed, 16))
+        return MOE_ERR_INVALID_ARG;
+    const int64_t values = int64_t(num_experts) * n_out * k_in;
+    if (!apart(d_packed, bytes, {{d_values, values / 2}, {d_scales, values / 32}}))
         return MOE_ERR_INVALID_ARG;
     moe::PackMxfp4Args a;
     a.blocks = d_values;

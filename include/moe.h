@@ -419,7 +419,8 @@ int moe_tile_expert_weights(const void *d_weights, int32_t num_experts, int32_t 
  *     (moe_grouped_gemm_backward_weight still writes its zeros);
  *   - widths are multiples of 8 (more where stated) from 8 to
  *     MOE_MAX_GEMM_WIDTH, 1 <= num_experts <= MOE_MAX_EXPERTS;
- *   - bf16 and packed buffers are 16-byte aligned, outputs overlap no input;
+ *   - bf16 and packed buffers are 16-byte aligned; an output shares no byte
+ *     with an input or another output;
  *   - no context and no workspace. Violations: MOE_ERR_INVALID_ARG. */
 #define MOE_MAX_GEMM_WIDTH  (1 << 22)
 #define MOE_GEMM_ZERO_TAIL  1    /* +0.0 into the rows from offsets[num_experts] on */

@@ -8,7 +8,7 @@ import torch
 import combine_moe_layout_05_amd as moe
 from combine_moe_layout_05_amd import _lib as L
 
-P = 1 << 40                # a device address that is never dereferenced
+P = 1 << 56                # a device address that is never dereferenced; buffers lie P apart
 OK, BAD = L.MOE_OK, L.MOE_ERR_INVALID_ARG
 MAX = L.MOE_MAX_GEMM_WIDTH
 
@@ -21,17 +21,20 @@ def lib():
 # Each call with valid arguments but max_rows = 0, so that nothing launches.
 CALLS = {
     "moe_gated_grouped_gemm": dict(
-        x=P, w=P, offsets=P, E=4, rows=0, k=64, n=32, act=0, out=P, pre=P, flags=1, stream=None),
+        x=P, w=2 * P, offsets=3 * P, E=4, rows=0, k=64, n=32, act=0, out=4 * P, pre=5 * P,
+        flags=1, stream=None),
     "moe_grouped_gemm_forward": dict(
-        x=P, w=P, offsets=P, E=4, rows=0, k=64, n=32, out=P, flags=1, stream=None),
+        x=P, w=2 * P, offsets=3 * P, E=4, rows=0, k=64, n=32, out=4 * P, flags=1, stream=None),
     "moe_grouped_gemm_backward_input": dict(
-        x=P, w=P, offsets=P, E=4, rows=0, k=64, n=32, out=P, flags=1, stream=None),
+        x=P, w=2 * P, offsets=3 * P, E=4, rows=0, k=64, n=32, out=4 * P, flags=1, stream=None),
     "moe_gated_grouped_gemm_backward": dict(
-        x=P, w=P, pre=P, offsets=P, E=4, rows=0, k=32, n=64, act=1, out=P, flags=1, stream=None),
+        x=P, w=2 * P, pre=5 * P, offsets=3 * P, E=4, rows=0, k=32, n=64, act=1, out=4 * P,
+        flags=1, stream=None),
     "moe_grouped_gemm_mxfp4": dict(
-        x=P, w=P, offsets=P, E=4, rows=0, k=64, n=32, out=P, flags=1, stream=None),
+        x=P, w=2 * P, offsets=3 * P, E=4, rows=0, k=64, n=32, out=4 * P, flags=1, stream=None),
     "moe_gated_grouped_gemm_mxfp4": dict(
-        x=P, w=P, offsets=P, E=4, rows=0, k=64, n=32, act=0, out=P, flags=1, stream=None),
+        x=P, w=2 * P, offsets=3 * P, E=4, rows=0, k=64, n=32, act=0, out=4 * P,
+        flags=1, stream=None),
 }
 
 
@@ -66,12 +69,51 @@ def test_entry_points_refuse_bad_pointers(lib, name):
         if not (key == "pre" and name == "moe_gated_grouped_gemm"):
             assert fn(*dict(args, **{key: None}).values()) == BAD, key
         off = 2 if key == "offsets" else 8
-        assert fn(*dict(args, **{key: P + off}).values()) == BAD, key
+        assert fn(*dict(args, **{key: args[key] + off}).values()) == BAD, key
+
+
+WEIGHT_GRADIENT = dict(dy=P, x=2 * P, offsets=3 * P, E=4, rows=8, k=64, n=32, dtype=L.MOE_F32,
+                       out=4 * P, flags=2, stream=None)
+
+# Bytes of each buffer of the calls above at 8 rows (4 experts).
+SIZES = {
+    "moe_gated_grouped_gemm": dict(x=8 * 64 * 2, w=4 * 64 * 64 * 2, offsets=20, out=8 * 32 * 2,
+                                   pre=8 * 64 * 4),
+    "moe_grouped_gemm_forward": dict(x=8 * 64 * 2, w=4 * 32 * 64 * 2, offsets=20, out=8 * 32 * 2),
+    "moe_grouped_gemm_backward_input": dict(x=8 * 32 * 2, w=4 * 32 * 64 * 2, offsets=20,
+                                            out=8 * 64 * 2),
+    "moe_gated_grouped_gemm_backward": dict(x=8 * 64 * 2, w=4 * 64 * 32 * 2, offsets=20,
+                                            pre=8 * 64 * 4, out=8 * 64 * 2),
+    "moe_grouped_gemm_mxfp4": dict(x=8 * 64 * 2, w=4 * 2 * 1088, offsets=20, out=8 * 32 * 2),
+    "moe_gated_grouped_gemm_mxfp4": dict(x=8 * 64 * 2, w=4 * 4 * 1088, offsets=20,
+                                         out=8 * 32 * 2),
+    "moe_grouped_gemm_backward_weight": dict(dy=8 * 32 * 2, x=8 * 64 * 2, offsets=20,
+                                             out=4 * 32 * 64 * 4),
+}
+
+
+def _overlaps(args, sizes, out):
+    """An output over another buffer's last bytes, or its last ones over the
+    other's first."""
+    for key in sizes:
+        if key != out:
+            for at in (args[key], args[key] + (sizes[key] - 1) // 16 * 16,
+                       args[key] + 16 - sizes[out]):
+                yield {out: at}
+
+
+@pytest.mark.parametrize("name", sorted(SIZES))
+def test_entry_points_refuse_overlapping_outputs(lib, name):
+    fn, sizes = getattr(lib, name), SIZES[name]
+    args = WEIGHT_GRADIENT if name not in CALLS else dict(CALLS[name], rows=8)
+    outs = ["out", "pre"] if name == "moe_gated_grouped_gemm" else ["out"]
+    for out in outs:
+        for at in _overlaps(args, sizes, out):
+            assert fn(*dict(args, **at).values()) == BAD, at
 
 
 def test_weight_gradient_refusals(lib):
-    args = dict(dy=P, x=P, offsets=P, E=4, rows=8, k=64, n=32, dtype=L.MOE_F32, out=P, flags=1,
-                stream=None)
+    args = dict(WEIGHT_GRADIENT, flags=1)
     fn = lib.moe_grouped_gemm_backward_weight
     # flag 1 (the tail) does not apply here
     assert fn(*args.values()) == BAD
@@ -79,7 +121,7 @@ def test_weight_gradient_refusals(lib):
     for key, value in [("E", 0), ("E", L.MOE_MAX_EXPERTS + 1), ("rows", -1), ("rows", 1 << 31),
                        ("k", 4), ("k", MAX + 8), ("n", 9), ("n", MAX + 8), ("dtype", 2),
                        ("flags", 6), ("dy", None), ("x", None), ("offsets", None), ("out", None),
-                       ("dy", P + 8), ("x", P + 2), ("offsets", P + 1), ("out", P + 4),
+                       ("dy", P + 8), ("x", 2 * P + 2), ("offsets", 3 * P + 1), ("out", 4 * P + 4),
                        # more tiles than a launch takes
                        ("n", MAX)]:
         bad = dict(args, **{key: value})
@@ -106,8 +148,12 @@ def test_packed_sizes(lib):
 
 def test_packing_refusals(lib):
     fn = lib.moe_pack_mxfp4_weights
-    for args in [(None, P, 1, 8, 32, P), (P, None, 1, 8, 32, P), (P, P, 1, 8, 32, None),
-                 (P + 2, P, 1, 8, 32, P), (P, P, 1, 8, 32, P + 8), (P, P, 1, 8, 48, P)]:
+    Q, D = 2 * P, 3 * P
+    for args in [(None, Q, 1, 8, 32, D), (P, None, 1, 8, 32, D), (P, Q, 1, 8, 32, None),
+                 (P + 2, Q, 1, 8, 32, D), (P, Q, 1, 8, 32, D + 8), (P, Q, 1, 8, 48, D),
+                 # 1088 packed bytes over the values or the scales
+                 (P, Q, 1, 8, 32, P), (P, Q, 1, 8, 32, P - 1072), (P, Q, 1, 8, 32, P + 112),
+                 (P, Q, 1, 8, 32, Q - 1072), (P, Q, 1, 8, 32, Q)]:
         assert fn(*args, None) == BAD, args
 
 
