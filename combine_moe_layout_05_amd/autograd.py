@@ -156,6 +156,8 @@ class _ExpertFfn(torch.autograd.Function):
         x, w_gate_up, w_down, offsets, pre, h = ctx.saved_tensors
         need_x, need_gate_up, need_down = ctx.needs_input_grad[:3]
         g = grad_y.contiguous()
+        if g.data_ptr() % 16 != 0:
+            g = g.clone()           # a slice of a larger gradient may begin anywhere
         dev, off = x.device, offsets.data_ptr()
         R, k_in = x.shape
         E, n_out, hidden = w_down.shape
@@ -222,7 +224,9 @@ def expert_ffn(x_expert: torch.Tensor, w_gate_up: torch.Tensor, w_down: torch.Te
 
     A step can be captured into a graph (forward and backward together) after
     warm-up calls on a side stream. While an output of a call on the default
-    stream that reaches the same leaves is alive, the capture is refused."""
+    stream that takes the same leaf tensors is alive, the capture is refused.
+    (Of inputs that are computed from other leaves only the caller can know
+    that: keep no such output alive across the capture.)"""
     dev = x_expert.device
     act = _activation(activation)
     E, n2, k_in = _weights("w_gate_up", w_gate_up, dev)

@@ -369,6 +369,26 @@ def test_broadcast_and_strided_upstream_gradient():
     assert torch.equal(*grads)
 
 
+@pytest.mark.parametrize("shift", [0, 1, 8])
+def test_upstream_gradient_that_begins_anywhere(shift):
+    """The gradient of a concatenation's part is a view into the whole one."""
+    off, off_d = _off([4, 3])
+    x, w1, w2 = (t.to(DEV) for t in (_rand((7, 32), 1), _rand((2, 32, 32), 2), _rand((2, 24, 16), 3)))
+    dy = _rand((7, 24), 4).to(DEV)
+    grads = []
+    for joined in (True, False):
+        leaves = [t.clone().requires_grad_(True) for t in (x, w1, w2)]
+        y = expert_ffn(*leaves, off_d)
+        if joined:
+            head = torch.zeros(shift, dtype=BF, device=DEV, requires_grad=True)
+            torch.cat((head, y.flatten())).backward(torch.cat((torch.zeros_like(head), dy.flatten())))
+        else:
+            y.backward(dy)
+        grads.append([t.grad for t in leaves])
+    for a, b in zip(*grads):
+        assert torch.equal(a, b)
+
+
 def test_offsets_are_kept_for_the_backward():
     """The caller's offsets (a layout's persistent buffer) may be rewritten
     between forward and backward."""
@@ -422,6 +442,81 @@ def test_repeats_and_streams_give_equal_bits():
     sync_or_fail()
     for a, b in zip(first, again):
         assert torch.equal(a, b)
+
+
+def test_two_streams_at_once():
+    """Calls share no state: two streams run the whole block side by side."""
+    cases = []
+    for seed, counts in ((1, [300, 0, 41]), (2, [9, 5, 290])):
+        off, off_d = _off(counts)
+        ts = [_rand((off[-1], 264), seed), _rand((3, 272, 264), seed + 2, 264 ** -0.5),
+              _rand((3, 264, 136), seed + 4, 136 ** -0.5), _rand((off[-1], 264), seed + 6)]
+        cases.append((off_d, [t.to(DEV) for t in ts]))
+
+    def step(off_d, ts):
+        leaves = [t.clone().requires_grad_(True) for t in ts[:3]]
+        y = expert_ffn(*leaves, off_d)
+        y.backward(ts[3])
+        return [y.detach(), *(t.grad for t in leaves)]
+
+    want = [step(*c) for c in cases]
+    sync_or_fail()
+    streams = [torch.cuda.Stream() for _ in cases]
+    got = [[], []]
+    for _ in range(4):
+        for j, c in enumerate(cases):
+            with torch.cuda.stream(streams[j]):
+                got[j].append(step(*c))
+    sync_or_fail()
+    for j in range(2):
+        for run in got[j]:
+            for a, b in zip(run, want[j]):
+                assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("rows", [40, 700, 9000])
+def test_as_many_experts_as_there_can_be(rows):
+    """1024 experts: a wavefront's lane looks after 16 of them."""
+    E, D, F = 1024, 64, 32
+    g = _gen(rows)
+    counts = torch.bincount(torch.randint(0, E, (rows,), generator=g), minlength=E)
+    counts[7] = 0
+    off, off_d = _off(counts.tolist())
+    total, R = off[-1], off[-1] + 6
+    note(f"1024 experts, {total} rows")
+    x, w = _rows(R, D, total, 1), _rand((E, 2 * F, D), 2, D ** -0.5)
+    h, err, pre, _ = ref.gated(x[:total], w, off, "silu")
+    got = gated_grouped_gemm(x.to(DEV), w.to(DEV), off_d)
+    sync_or_fail()
+    ref.check(got[:total], h, err, ref.B, "h")
+    assert (got[total:].view(torch.int16) == 0).all()
+    dy = _rows(R, F, total, 3)
+    want, err = ref.wgrad(dy, x, off)
+    ref.check(grouped_gemm_backward_weight(dy.to(DEV), x.to(DEV), off_d), want, err, ref.B, "dw")
+    values, scales, packed = _mx(E, 2 * F, D, 4)
+    h, err, _, _ = ref.gated(x[:total], ref.mxfp4_weights(values, scales), off, "silu")
+    got = gated_grouped_gemm(x.to(DEV), packed, off_d)
+    sync_or_fail()
+    ref.check(got[:total], h, err, ref.B, "4-bit h")
+
+
+def test_segments_are_clamped_to_the_rows():
+    """Offsets that begin behind row 0, before it or end past the last row."""
+    R, D, F = 150, 72, 40
+    x, w = _rand((R, D), 1), _rand((2, 2 * F, D), 2, D ** -0.5)
+    dy = _rand((R, F), 3)
+    for raw in ([20, 90, 150], [-7, 90, 150], [0, 90, 1 << 30], [-(1 << 30), -5, 1 << 30]):
+        off = [min(max(o, 0), R) for o in raw]
+        off_d = torch.tensor(raw, dtype=torch.int32, device=DEV)
+        note(f"offsets {raw}")
+        out = _poisoned(R, F)
+        gated_grouped_gemm(x.to(DEV), w.to(DEV), off_d, out)
+        h, err, _, _ = ref.gated(x, w, off, "silu")
+        sync_or_fail()
+        assert _is_poison(out[:off[0]])
+        ref.check(out[off[0]:], h[off[0]:], err[off[0]:], ref.B, "h")
+        want, err = ref.wgrad(dy, x, off)
+        ref.check(grouped_gemm_backward_weight(dy.to(DEV), x.to(DEV), off_d), want, err, ref.B, "dw")
 
 
 def test_buffers_past_32_bits():
