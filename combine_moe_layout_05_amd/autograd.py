@@ -187,25 +187,23 @@ class _ExpertFfn(torch.autograd.Function):
 _ON_DEFAULT_STREAM = "combine_moe_layout.default_stream"
 
 
-def _leaf_accumulators(tensors, stream: int):
-    """The gradient accumulators of the leaves among `tensors`, to be held until
-    the call's node holds them. The engine runs an accumulator on the stream it
-    was made on, and it lives as long as any graph that reaches it. One made on
-    the default stream cannot join a capture: the backward would fail inside
-    the engine and end the process, so such a capture is refused here."""
-    nodes = [torch.autograd.graph.get_gradient_edge(t).node
-             for t in tensors if t.requires_grad and t.is_leaf]
+def _watch_accumulators(node, stream: int) -> None:
+    """Looks at the gradient accumulators of the leaves that a call's node
+    leads to. The engine runs an accumulator on the stream it was made on, and
+    it lives as long as any graph that reaches it. One made on the default
+    stream cannot join a capture: the backward would fail inside the engine and
+    end the process, so such a capture is refused here."""
+    leaves = [fn for fn, _ in node.next_functions if hasattr(fn, "variable")]
     if torch.cuda.is_current_stream_capturing():
-        if any(n.metadata.get(_ON_DEFAULT_STREAM) for n in nodes):
+        if any(fn.metadata.get(_ON_DEFAULT_STREAM) for fn in leaves):
             raise RuntimeError(
                 "expert_ffn cannot be captured while the output of an earlier call on the default "
                 "stream that reaches the same leaf tensors is alive: its gradient accumulators "
                 "belong to that stream. Delete that output first, or run the calls before the "
                 "capture on a side stream.")
     elif stream == 0:
-        for n in nodes:
-            n.metadata[_ON_DEFAULT_STREAM] = True
-    return nodes
+        for fn in leaves:
+            fn.metadata[_ON_DEFAULT_STREAM] = True
 
 
 def expert_ffn(x_expert: torch.Tensor, w_gate_up: torch.Tensor, w_down: torch.Tensor,
@@ -238,8 +236,7 @@ def expert_ffn(x_expert: torch.Tensor, w_gate_up: torch.Tensor, w_down: torch.Te
     _offsets(offsets, E, dev)
     if torch.is_grad_enabled() and (x_expert.requires_grad or w_gate_up.requires_grad
                                     or w_down.requires_grad):
-        nodes = _leaf_accumulators((x_expert, w_gate_up, w_down), _stream(dev))
         y = _ExpertFfn.apply(x_expert, w_gate_up, w_down, offsets, act)
-        del nodes
+        _watch_accumulators(y.grad_fn, _stream(dev))
         return y
     return _ffn_forward(x_expert, w_gate_up, w_down, offsets, act, None)[1]
