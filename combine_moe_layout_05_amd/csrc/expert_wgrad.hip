@@ -1,6 +1,26 @@
 // Gradient of the expert weights on gfx950: for every expert e
 //     dw[e][n][k] = sum over rows r of e's segment of dy[r][n] * x[r][k]
 // (plus what dw holds, on request), one rounding of the fp32 sum.
+//
+// Both operands stride along the sum (the rows), which the matrix cores want
+// contiguous: LDS is read transposed. A workgroup owns a tile of one expert's
+// gradient and walks its rows, so no sum is shared between workgroups, nothing
+// is joined afterwards and the order of a sum is the rows' order.
+//
+// Bound. The gradient is written once, and a segment of c rows gives c operations
+// per byte of it in bf16: its bytes count up to some 200 rows per expert, the
+// matrix cores above. 128 x 256 of four wavefronts, two workgroups to a CU: one
+// fills its first stages or writes its results while the other multiplies. Tried
+// at 512 rows per expert, 4096 x 4096: 256 x 256 with steps of 64 rows, one to a
+// CU, 3.13 against 2.84 ms; 128 x 128, three to a CU, 2.96 against 2.74 (at 128
+// rows and 2048 x 1408, which 128 divides better, 189 against 212 us; at 2816 x
+// 2048 378 against 366); workgroups that stay and load the next tile early, 3.5.
+//
+// Measured on MI355X (a large library product reaches 1438 TFLOP/s), behind other
+// products as in a training step: 128 experts of 512 rows, 4096 x 2048 1.31 ms
+// (0.84 PFLOP/s), 4096 x 4096 2.58 ms (0.85); of 128 rows, 2048 x 1408 241 us,
+// 2816 x 2048 420 us (3.9 TB/s). One expert of 65536 rows: 1.23 to 1.31 PFLOP/s.
+// LDS bank conflicts count 0.
 #include "expert_kernels.h"
 #include "expert_mma.h"
 
@@ -17,6 +37,7 @@ constexpr int kBlkN = kTileN / kWavesN / 16;
 constexpr int kStep = 32;               // rows per step: one matrix-core product deep
 constexpr int kStages = 3;              // 72 KiB of LDS: two workgroups per CU
 constexpr int kXcdChunk = 64;
+constexpr int kTouch = 16;              // workgroups that touch one expert's rows
 
 typedef StridedOperand<kTileK, kWaves, kStep> Kop;
 typedef StridedOperand<kTileN, kWaves, kStep> Nop;
@@ -65,23 +86,61 @@ struct OutTile {
     }
 };
 
+// Reads part `part` of kTouch of `bytes` (whole 16-byte chunks) and drops them:
+// they are in the memory-side cache then.
+__device__ __forceinline__ void touch_rows(const char* base, int64_t bytes, int part) {
+    constexpr int kThreads = kWaves * 64, kAtOnce = 8;
+    const v4i* p = reinterpret_cast<const v4i*>(base);
+    const int64_t chunks = bytes / 16, end = chunks * (part + 1) / kTouch;
+    int64_t i = chunks * part / kTouch + threadIdx.x;
+    int32_t seen = 0;
+    for (; i + (kAtOnce - 1) * kThreads < end; i += kAtOnce * kThreads) {
+        v4i v[kAtOnce];
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j) v[j] = p[i + j * kThreads];
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j) seen ^= v[j][0];
+    }
+    for (; i < end; i += kThreads) seen ^= p[i][0];
+    asm volatile("" ::"v"(seen));       // the loads have a use
+}
+
+// The launch's workgroups, in the order they start. With touch != 0 (kTouch):
+// first the ones that touch the rows of experts 0 .. ahead - 1, then for every
+// expert those that touch the rows of the expert `ahead` later, and its tiles.
 template <bool F32, bool ACCUMULATE>
 __global__ __launch_bounds__(kWaves * 64, 2)
 void expert_wgrad_kernel(const char* __restrict__ dy, const char* __restrict__ x,
                          const int32_t* __restrict__ offsets, int32_t max_rows, int32_t N,
-                         int32_t K, int32_t ntiles, int32_t ktiles, int64_t tiles,
-                         char* __restrict__ dw) {
+                         int32_t K, int32_t ntiles, int32_t ktiles, int32_t E, int32_t touch,
+                         int32_t ahead, int64_t jobs, char* __restrict__ dw) {
     __shared__ v4i lds[kStages * kStageChunks];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t u = expert_tile_number(kXcdChunk);
-    if (u >= tiles) return;
-    const int32_t per = ntiles * ktiles;
-    const int32_t e = static_cast<int32_t>(u / per);
-    const int32_t in = static_cast<int32_t>(u - int64_t(e) * per);
+    int64_t u = expert_tile_number(kXcdChunk);
+    if (u >= jobs) return;
+    const int64_t front = int64_t(touch) * ahead;
+    int32_t e, in;
+    if (u < front) {
+        e = static_cast<int32_t>(u / touch);
+        in = static_cast<int32_t>(u - int64_t(e) * touch);
+    } else {
+        const int32_t per = touch + ntiles * ktiles;
+        u -= front;
+        e = static_cast<int32_t>(u / per);
+        in = static_cast<int32_t>(u - int64_t(e) * per);
+        if (in < touch) e += ahead;
+    }
+    if (e >= E) return;
     int32_t s0, s1;
     expert_segment(offsets, e, max_rows, s0, s1);
     const int32_t count = s1 - s0;
+    if (in < touch) {
+        touch_rows(x + int64_t(s0) * K * 2, int64_t(count) * K * 2, in);
+        touch_rows(dy + int64_t(s0) * N * 2, int64_t(count) * N * 2, in);
+        return;
+    }
+    in -= touch;
     if (ACCUMULATE && count == 0) return;
     // Tiles along K first where a segment is short: what runs at once then
     // writes long contiguous pieces of dw. From 2048 rows on the rows' reads
@@ -250,13 +309,41 @@ int32_t k_tiles(const ExpertWgradArgs& a) {
 int32_t n_tiles(const ExpertWgradArgs& a) {
     return static_cast<int32_t>((int64_t(a.N) + kTileN - 1) / kTileN);
 }
-int64_t tile_count(const ExpertWgradArgs& a) { return int64_t(n_tiles(a)) * k_tiles(a) * a.E; }
+int64_t tiles_per_expert(const ExpertWgradArgs& a) { return int64_t(n_tiles(a)) * k_tiles(a); }
+
+// Whether rows are touched ahead of their tiles. A tile of a short segment is
+// little more than the latency of its reads, and where the rows are not in the
+// memory-side cache (another product has run since they were written) those
+// queue behind the gradient's own writes. Measured on MI355X behind a product of
+// other weights: 128 experts of 128 rows, 2048 x 1408, 296 us without and 241
+// with it, 2816 x 2048 490 and 420; 16 such experts 63.9 and 53.8; 256 of 8 rows,
+// 2048 x 7168, 1481 and 1239; 128 of 512 rows, 4096 x 2048 1400 and 1305, 4096 x
+// 4096 2801 and 2581. Longer segments read ahead in their own loops: 32 of 1024
+// rows, 4096 x 4096, 1070 and 1106, 16 of 4096 rows 1709 and 1880. Repeated on
+// rows that are in the cache it costs 3 to 6 % (128 rows: 212 and 219, 366 and
+// 389). 32 workgroups per expert instead of 16 lose at 2048 x 1408 (306).
+bool touches(const ExpertWgradArgs& a) { return a.max_rows <= int64_t(512) * a.E; }
+
+// How many experts ahead: all at once if the rows fit the memory-side cache (256
+// MB) with room for others, else what one or two rounds of workgroups take
+// (128 experts of 128 rows, one to two rounds ahead: 283 and 479 us). At 512
+// rows 2048 tiles ahead are as good as 1024, 8192 lose 5 %.
+int32_t touched_ahead(const ExpertWgradArgs& a) {
+    if (a.max_rows * (int64_t(a.N) + a.K) * 2 <= (int64_t(192) << 20)) return a.E;
+    const int64_t per = tiles_per_expert(a);
+    const int64_t ahead = (1024 + per - 1) / per;
+    return static_cast<int32_t>(ahead < a.E ? ahead : a.E);
+}
+int64_t job_count(const ExpertWgradArgs& a) {
+    const int64_t touch = touches(a) ? kTouch : 0;
+    return (tiles_per_expert(a) + touch) * a.E + touch * touched_ahead(a);
+}
 
 }  // namespace
 
 int64_t expert_wgrad_grid(const ExpertWgradArgs& a) {
     const int64_t unit = int64_t(kExpertXcds) * kXcdChunk;
-    return (tile_count(a) + unit - 1) / unit * unit;
+    return (job_count(a) + unit - 1) / unit * unit;
 }
 
 hipError_t launch_expert_wgrad(const ExpertWgradArgs& a, hipStream_t stream) {
@@ -265,8 +352,8 @@ hipError_t launch_expert_wgrad(const ExpertWgradArgs& a, hipStream_t stream) {
     hipLaunchKernelGGL(kernel, dim3(static_cast<uint32_t>(expert_wgrad_grid(a))),
                        dim3(kWaves * 64), 0, stream, static_cast<const char*>(a.dy),
                        static_cast<const char*>(a.x), a.offsets, static_cast<int32_t>(a.max_rows),
-                       a.N, a.K, n_tiles(a), k_tiles(a), tile_count(a),
-                       static_cast<char*>(a.dw));
+                       a.N, a.K, n_tiles(a), k_tiles(a), a.E, touches(a) ? kTouch : 0,
+                       touched_ahead(a), job_count(a), static_cast<char*>(a.dw));
     return hipGetLastError();
 }
 

@@ -519,6 +519,38 @@ def test_segments_are_clamped_to_the_rows():
         ref.check(grouped_gemm_backward_weight(dy.to(DEV), x.to(DEV), off_d), want, err, ref.B, "dw")
 
 
+@pytest.mark.parametrize("counts", [[1300], [600, 0, 1100]])
+def test_backward_weight_of_long_segments(counts):
+    """Segments too long for their rows to be touched ahead of the tiles."""
+    off, off_d = _off(counts)
+    total, D, F = off[-1], 264, 136
+    x, dy = _rows(total + 2, D, total, 1), _rows(total + 2, F, total, 2)
+    want, err = ref.wgrad(dy, x, off)
+    got = grouped_gemm_backward_weight(dy.to(DEV), x.to(DEV), off_d)
+    sync_or_fail()
+    ref.check(got, want, err, ref.B, "dw")
+
+
+def test_backward_weight_with_rows_touched_expert_by_expert():
+    """More rows than are touched at once: 210 MB in 64 experts."""
+    E, D, F = 64, 2048, 2048
+    counts = [400 + 8 * (e % 3) - 3 * (e % 5) for e in range(E)]
+    off, off_d = _off(counts)
+    total = off[-1]
+    assert total * (D + F) * 2 > 192 << 20
+    g = torch.Generator(device=DEV).manual_seed(5)
+    x = torch.randn(total, D, generator=g, device=DEV).to(BF)
+    dy = torch.randn(total, F, generator=g, device=DEV).to(BF)
+    note(f"64 experts, {total} rows")
+    got = grouped_gemm_backward_weight(dy, x, off_d)
+    sync_or_fail()
+    for e in range(E):
+        a, b = off[e], off[e + 1]
+        d, xe = dy[a:b].double().t().contiguous(), x[a:b].double()
+        err = ref.gamma(b - a) * (d.abs() @ xe.abs())
+        ref.check(got[e], (d @ xe).cpu(), err.cpu(), ref.B, f"dw[{e}]")
+
+
 def test_buffers_past_32_bits():
     """Outputs and rows beyond 4 GiB: the last rows are right."""
     D, F, E = 64, 8192, 2
