@@ -1,5 +1,20 @@
 // Expert products for few rows per expert on gfx950, and the packing of 4-bit
-// expert weights.
+// expert weights: with rows r of expert e, out[r] = x[r] W^T, or act(g) * u of
+// the two projections g and u.
+//
+// Bound: the bytes of the weights, each used for at most 16 rows. They go
+// straight from HBM into the registers the matrix cores read, never through
+// LDS: a workgroup takes 64 features, its wavefronts every n-th step of the sum
+// (consecutive weights, so that a workgroup's reads are one stream), and the
+// wavefronts' sums are joined in LDS in wavefront order. Splitting the sum gives
+// one token enough workgroups and loads in flight: 8 experts' 4096 features are
+// 512 workgroups of 8 wavefronts.
+//
+// Measured on MI355X, one token of 8 experts. bf16, 7168 -> 2 x 2048: 78.6 us for
+// 470 MB (6.0 TB/s; a large copy moves 4.9, an in-place update 6.0). 4 bits, 7168
+// -> 2 x 2048: 21.6 us for 125 MB (5.8 TB/s); 2048 -> 7168: 14.4 us for 63 MB
+// (4.4 TB/s), where the start of 7 rounds of loads is most of it. 64 tokens over
+// 256 experts at 4 bits: 353 us for 2.13 GB (6.0 TB/s).
 #include "expert_kernels.h"
 #include "expert_mma.h"
 #include "expert_mxfp4.h"
@@ -260,7 +275,8 @@ void expert_stream_kernel(const char* __restrict__ rows, const char* __restrict_
 // 32 inputs into the lanes' 16 bytes, and the step's four scales. Lanes run
 // over the 16 features of a block first, then over the steps, so that a
 // wavefront reads 256 contiguous bytes of each feature and writes whole pieces
-// of 256 bytes.
+// of 256 bytes. Bound by those bytes: 256 experts of 7168 -> 4096 (8.0 GB) take
+// 1.98 ms on MI355X, 4.0 TB/s.
 __global__ __launch_bounds__(256)
 void pack_mxfp4_kernel(const char* __restrict__ blocks, const uint8_t* __restrict__ scales,
                        int32_t N, int32_t K, int32_t nb, int32_t steps, int64_t tiles,
