@@ -823,3 +823,49 @@ def test_training_step_in_a_captured_graph():
         for a, b in zip(got, eager()):
             assert torch.equal(a, b)
         sync_or_fail()
+
+
+def test_layer_training_step_in_a_captured_graph():
+    """dispatch -> expert_ffn -> combine and back in one graph, replayed with
+    new rows and new routing, a padded extent included."""
+    T, ntpr, D, F, E, K = 53, 58, 64, 48, 6, 2
+    x, ids, s = _layer(T, D, F, E, K, 3)
+    w1 = _rand((E, 2 * F, D), 5, D ** -0.5).to(DEV).requires_grad_(True)
+    w2 = _rand((E, D, F), 6, F ** -0.5).to(DEV).requires_grad_(True)
+    dy = _rand((T, D), 7).to(DEV)
+    x, s = x.requires_grad_(True), s.requires_grad_(True)
+    leaves = (x, s, w1, w2)
+    layers = [MoeTokenDispatcher(MoeDispatcher(64, D, E, K, backward=True)) for _ in range(2)]
+
+    def step(layer, x, s, w1, w2):
+        x_e = layer.dispatch(x, s, ids, ntpr)
+        y = layer.combine(expert_ffn(x_e, w1, w2, layer.disp.offsets), s)
+        y.backward(dy)
+        return y.detach()
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(layers[0], *leaves)
+    torch.cuda.current_stream().wait_stream(side)
+    for t in leaves:
+        t.grad = None
+    sync_or_fail()
+    note("whole layer training step graph")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = step(layers[0], *leaves)
+    for seed in range(20, 24):
+        x2, ids2, s2 = _layer(T, D, F, E, K, seed)
+        with torch.no_grad():
+            x.copy_(x2), ids.copy_(ids2), s.copy_(s2)
+        for t in leaves:
+            t.grad.zero_()
+        graph.replay()
+        got = [t.clone() for t in (y, *(t.grad for t in leaves))]
+        sync_or_fail()
+        copies = [t.detach().clone().requires_grad_(True) for t in leaves]
+        want = [step(layers[1], *copies), *(t.grad for t in copies)]
+        sync_or_fail()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
