@@ -244,12 +244,19 @@ int64_t grid_of(const ExpertGemmArgs& a) {
     return (tiles + unit - 1) / unit * unit;
 }
 
-// The small shape where the large one would leave half the 256 CUs idle.
-// Measured on MI355X, one expert of 4096 -> 2 x 2048 gated: 24.8 against 84.1 us
-// at 256 rows (16 large tiles), 42.5 against 87.7 at 1024 (64), 81.0 against
-// 91.0 at 2048 (128), 156 against 112 us at 4096 (256); 16 experts of 1024 -> 2 x
-// 704: 24.8 against 29.0 us at 4096 rows (96), 38.0 against 32.6 at 8192 (192).
+// The small shape where segments are short, or where the large one would leave
+// half the 256 CUs idle. Measured on MI355X, weights from HBM, large against
+// small:
+//   - 8 rows per expert, skewed, 256 experts of 7168 -> 2 x 2048 gated 2371 and
+//     2248 us; 32 rows, skewed, 128 experts of 2048 -> 2 x 1408 353 and 292, its
+//     gradients towards the rows 213 and 158, 287 and 278; 256 experts 2597 and
+//     2610. At 64 rows 383 and 341 but 2771 and 2980.
+//   - one expert of 4096 -> 2 x 2048 gated: 98.6 and 34.2 us at 512 rows (32
+//     large tiles), 100 and 104 at 2048 (128), 135 and 201 at 4096 (256); 8 of
+//     100 rows 80.4 and 71.8 (128); 24 of 1992 -> 2 x 1000 60.7 and 70.1 at 92
+//     rows (192).
 bool use_small(const ExpertGemmArgs& a) {
+    if (a.max_rows <= int64_t(32) * a.E) return true;
     const int64_t row_tiles = (a.max_rows + Large::kTileR - 1) / Large::kTileR;
     const int64_t experts = a.max_rows < a.E ? a.max_rows : a.E;
     return feature_tiles<Large>(a) * (row_tiles > experts ? row_tiles : experts) <= 128;
