@@ -8,8 +8,8 @@ The compute lives in libmoe_layout.so (hand-written HIP kernels behind the C
 ABI of include/moe.h); this package is its thin Python binding.
 """
 from .moe import (  # noqa: F401
-    Dispatched, Layout, MoeDispatcher, Mxfp4ExpertWeights, TiledExpertWeights, ceil_div, grouped_gemm,
-    layout_noalloc, num_max_tokens_infer, num_max_tokens_pretrain, round_up4,
+    Dispatched, Layout, MoeDispatcher, Mxfp4ExpertWeights, TiledExpertWeights, ceil_div,
+    grouped_gemm, layout_noalloc, num_max_tokens_infer, num_max_tokens_pretrain, round_up4,
     tile_expert_weights, validate_num_max,
 )
 from ._lib import MoeError, load  # noqa: F401

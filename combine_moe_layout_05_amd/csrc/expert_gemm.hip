@@ -82,7 +82,9 @@ void expert_gemm_kernel(const char* __restrict__ rows, const char* __restrict__ 
     constexpr int kWaves = S::kWaves, kWavesF = S::kWavesF, kTileF = S::kTileF,
                   kTileR = S::kTileR;
     typedef typename WeightOperand<S, strided(OP)>::type Weights;
-    constexpr auto lds_of = [](int rows) { return S::stages(rows) * (Weights::kChunks + rows * 8); };
+    constexpr auto lds_of = [](int rows) {
+        return S::stages(rows) * (Weights::kChunks + rows * 8);
+    };
     constexpr int kHalf = kTileR > 64 ? kTileR / 2 : kTileR;
     __shared__ v4i lds[lds_of(kHalf) > lds_of(kTileR) ? lds_of(kHalf) : lds_of(kTileR)];
     __shared__ int32_t info[4];
@@ -138,85 +140,86 @@ void expert_gemm_kernel(const char* __restrict__ rows, const char* __restrict__ 
     // The loop exists for each 64-row count up to the tile's and is chosen once
     // per workgroup, so that a segment's last tile costs what its rows need.
     auto run = [&](auto parts) {
-    constexpr int kRowsUsed = decltype(parts)::value * 64;
-    constexpr int kBlkR = kRowsUsed / kWavesR / 16;
-    constexpr int kStages = S::stages(kRowsUsed);
-    PackedOperand<kRowsUsed, kWaves> rt;
-    const char* rbase = rows + int64_t(row0) * red_pitch;
-    rt.init(wave, lane, wr * kBlkR, red_pitch, [&](int) { return rbase; },
-            [&](int p) { return min(p, nrows - 1); });
-    f32x4 acc[kBlkF][kBlkR];
-    const Accumulator<kStages, kBlkF, kBlkR, Weights, PackedOperand<kRowsUsed, kWaves>> sums{lds,
-                                                                                             lane};
-    sums.run(wt, rt, red, acc);
+        constexpr int kRowsUsed = decltype(parts)::value * 64;
+        constexpr int kBlkR = kRowsUsed / kWavesR / 16;
+        constexpr int kStages = S::stages(kRowsUsed);
+        PackedOperand<kRowsUsed, kWaves> rt;
+        const char* rbase = rows + int64_t(row0) * red_pitch;
+        rt.init(wave, lane, wr * kBlkR, red_pitch, [&](int) { return rbase; },
+                [&](int p) { return min(p, nrows - 1); });
+        f32x4 acc[kBlkF][kBlkR];
+        typedef Accumulator<kStages, kBlkF, kBlkR, Weights, PackedOperand<kRowsUsed, kWaves>> Sums;
+        const Sums sums{lds, lane};
+        sums.run(wt, rt, red, acc);
 
-    // acc[a][b][t] belongs to row 16b + lane % 16 and position 16a + 4 (lane /
-    // 16) + t of the wavefront.
-    const int i = lane & 15, g = lane >> 4;
-#pragma unroll
-    for (int b = 0; b < kBlkR; ++b) {
-        const int r = (wr * kBlkR + b) * 16 + i;
-        if (r >= nrows) continue;
-        char* orow = out + int64_t(row0 + r) * out_pitch;
-        // Two 16-feature blocks at a time: every lane ends up with eight
-        // neighbouring features, which begin `at` features into the pair.
-        const int at = (g & 1) * 16 + (g >> 1) * 8;
-        if constexpr (OP == ExpertOp::kGated) {
-            static_assert(kBlkF == 4, "a pair of gate blocks, then their up blocks");
-            const int32_t f = f0 + wf * 32;
-            v2i h[2];
-#pragma unroll
-            for (int a = 0; a < 2; ++a) {
-                const f32x4 gv = acc[a][b], uv = acc[a + 2][b];
-                f32x4 v;
-#pragma unroll
-                for (int t = 0; t < 4; ++t) v[t] = activate(act, gv[t]) * uv[t];
-                h[a] = pack_bf16x4(v);
-                const int32_t fq = f + a * 16 + g * 4;
-                if (pre && fq < feats) {
-                    float* p = pre + int64_t(row0 + r) * feats * 2 + fq;
-                    *reinterpret_cast<f32x4*>(p) = gv;
-                    *reinterpret_cast<f32x4*>(p + feats) = uv;
+        // acc[a][b][t] belongs to row 16b + lane % 16 and position 16a + 4 (lane /
+        // 16) + t of the wavefront.
+        const int i = lane & 15, g = lane >> 4;
+    #pragma unroll
+        for (int b = 0; b < kBlkR; ++b) {
+            const int r = (wr * kBlkR + b) * 16 + i;
+            if (r >= nrows) continue;
+            char* orow = out + int64_t(row0 + r) * out_pitch;
+            // Two 16-feature blocks at a time: every lane ends up with eight
+            // neighbouring features, which begin `at` features into the pair.
+            const int at = (g & 1) * 16 + (g >> 1) * 8;
+            if constexpr (OP == ExpertOp::kGated) {
+                static_assert(kBlkF == 4, "a pair of gate blocks, then their up blocks");
+                const int32_t f = f0 + wf * 32;
+                v2i h[2];
+    #pragma unroll
+                for (int a = 0; a < 2; ++a) {
+                    const f32x4 gv = acc[a][b], uv = acc[a + 2][b];
+                    f32x4 v;
+    #pragma unroll
+                    for (int t = 0; t < 4; ++t) v[t] = activate(act, gv[t]) * uv[t];
+                    h[a] = pack_bf16x4(v);
+                    const int32_t fq = f + a * 16 + g * 4;
+                    if (pre && fq < feats) {
+                        float* p = pre + int64_t(row0 + r) * feats * 2 + fq;
+                        *reinterpret_cast<f32x4*>(p) = gv;
+                        *reinterpret_cast<f32x4*>(p + feats) = uv;
+                    }
                 }
-            }
-            const v4i v = pair_blocks(h[0], h[1]);
-            if (f + at < feats) *reinterpret_cast<v4i*>(orow + int64_t(f + at) * 2) = v;
-        } else {
-#pragma unroll
-            for (int a = 0; a < kBlkF; a += 2) {
-                const int32_t f = f0 + (wf * kBlkF + a) * 16;
-                if constexpr (OP == ExpertOp::kGatedGrad) {
-                    v2i dg[2], du[2];
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        const int32_t fq = min(f + c * 16 + g * 4, feats - 4);
-                        const float* p = pre + int64_t(row0 + r) * feats * 2 + fq;
-                        const f32x4 gv = *reinterpret_cast<const f32x4*>(p);
-                        const f32x4 uv = *reinterpret_cast<const f32x4*>(p + feats);
-                        const f32x4 v = acc[a + c][b];
-                        f32x4 vg, vu;
-#pragma unroll
-                        for (int t = 0; t < 4; ++t) {
-                            float value, slope;
-                            activate_grad(act, gv[t], value, slope);
-                            vg[t] = v[t] * uv[t] * slope;
-                            vu[t] = v[t] * value;
+                const v4i v = pair_blocks(h[0], h[1]);
+                if (f + at < feats) *reinterpret_cast<v4i*>(orow + int64_t(f + at) * 2) = v;
+            } else {
+    #pragma unroll
+                for (int a = 0; a < kBlkF; a += 2) {
+                    const int32_t f = f0 + (wf * kBlkF + a) * 16;
+                    if constexpr (OP == ExpertOp::kGatedGrad) {
+                        v2i dg[2], du[2];
+    #pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            const int32_t fq = min(f + c * 16 + g * 4, feats - 4);
+                            const float* p = pre + int64_t(row0 + r) * feats * 2 + fq;
+                            const f32x4 gv = *reinterpret_cast<const f32x4*>(p);
+                            const f32x4 uv = *reinterpret_cast<const f32x4*>(p + feats);
+                            const f32x4 v = acc[a + c][b];
+                            f32x4 vg, vu;
+    #pragma unroll
+                            for (int t = 0; t < 4; ++t) {
+                                float value, slope;
+                                activate_grad(act, gv[t], value, slope);
+                                vg[t] = v[t] * uv[t] * slope;
+                                vu[t] = v[t] * value;
+                            }
+                            dg[c] = pack_bf16x4(vg);
+                            du[c] = pack_bf16x4(vu);
                         }
-                        dg[c] = pack_bf16x4(vg);
-                        du[c] = pack_bf16x4(vu);
+                        const v4i og = pair_blocks(dg[0], dg[1]), ou = pair_blocks(du[0], du[1]);
+                        if (f + at < feats) {
+                            *reinterpret_cast<v4i*>(orow + int64_t(f + at) * 2) = og;
+                            *reinterpret_cast<v4i*>(orow + (int64_t(feats) + f + at) * 2) = ou;
+                        }
+                    } else {
+                        const v4i v =
+                            pair_blocks(pack_bf16x4(acc[a][b]), pack_bf16x4(acc[a + 1][b]));
+                        if (f + at < feats) *reinterpret_cast<v4i*>(orow + int64_t(f + at) * 2) = v;
                     }
-                    const v4i og = pair_blocks(dg[0], dg[1]), ou = pair_blocks(du[0], du[1]);
-                    if (f + at < feats) {
-                        *reinterpret_cast<v4i*>(orow + int64_t(f + at) * 2) = og;
-                        *reinterpret_cast<v4i*>(orow + (int64_t(feats) + f + at) * 2) = ou;
-                    }
-                } else {
-                    const v4i v = pair_blocks(pack_bf16x4(acc[a][b]), pack_bf16x4(acc[a + 1][b]));
-                    if (f + at < feats) *reinterpret_cast<v4i*>(orow + int64_t(f + at) * 2) = v;
                 }
             }
         }
-    }
     };
     const int parts = (nrows + 63) / 64;
     if constexpr (kTileR > 64) {

@@ -141,7 +141,8 @@ __device__ __forceinline__ void load_to_lds(const char* base, uint32_t off, v4i*
     const uint32_t lds = static_cast<uint32_t>(
         reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) void*)(dst)));
     const uint64_t b = reinterpret_cast<uint64_t>(base);
-    const uint64_t lo = static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<uint32_t>(b)));
+    const uint64_t lo =
+        static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<uint32_t>(b)));
     const uint64_t hi =
         static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<uint32_t>(b >> 32)));
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
@@ -313,7 +314,8 @@ struct StridedOperand {
                 buf[(wave + WAVES * j) * 64 + lane] = v4i{0, 0, 0, 0};
     }
     __device__ bf16x8 frag(const v4i* buf, int b, int s) const {
-        const char* p = reinterpret_cast<const char*>(buf) + (frag_at ^ (b * 32)) + s * (32 * EXT * 2);
+        const char* p =
+            reinterpret_cast<const char*>(buf) + (frag_at ^ (b * 32)) + s * (32 * EXT * 2);
         const bf16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4*)(p));
         const bf16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4*)(p + 4 * EXT * 2));
         return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);

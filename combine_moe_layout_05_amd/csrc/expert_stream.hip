@@ -318,8 +318,8 @@ hipError_t launch_stream(const ExpertStreamArgs& a, hipStream_t stream) {
     const char* w = static_cast<const char*>(a.w);
     const char* scales = w + mxfp4_tiles(a.E, a.gated ? 2 * a.feats : a.feats, a.red) * 1024;
     hipLaunchKernelGGL((expert_stream_kernel<MXFP4, GATED>),
-                       dim3(static_cast<uint32_t>(expert_stream_grid(a))), dim3(waves_of(MXFP4) * 64), 0,
-                       stream, static_cast<const char*>(a.rows), w, scales, a.offsets, a.E,
+                       dim3(static_cast<uint32_t>(expert_stream_grid(a))),
+                       dim3(waves_of(MXFP4) * 64), 0, stream, static_cast<const char*>(a.rows), w, scales, a.offsets, a.E,
                        static_cast<int32_t>(a.max_rows), a.red, a.feats,
                        static_cast<int32_t>(stream_feature_tiles(a)), a.activation,
                        static_cast<char*>(a.out), a.pre, a.zero_tail ? 1 : 0);
@@ -338,7 +338,8 @@ int64_t expert_stream_grid(const ExpertStreamArgs& a) {
 
 hipError_t launch_expert_stream(const ExpertStreamArgs& a, hipStream_t stream) {
     if (a.mxfp4)
-        return a.gated ? launch_stream<true, true>(a, stream) : launch_stream<true, false>(a, stream);
+        return a.gated ? launch_stream<true, true>(a, stream)
+                       : launch_stream<true, false>(a, stream);
     return a.gated ? launch_stream<false, true>(a, stream) : launch_stream<false, false>(a, stream);
 }
 

@@ -347,8 +347,10 @@ int64_t expert_wgrad_grid(const ExpertWgradArgs& a) {
 }
 
 hipError_t launch_expert_wgrad(const ExpertWgradArgs& a, hipStream_t stream) {
-    auto kernel = a.f32 ? (a.accumulate ? expert_wgrad_kernel<true, true> : expert_wgrad_kernel<true, false>)
-                        : (a.accumulate ? expert_wgrad_kernel<false, true> : expert_wgrad_kernel<false, false>);
+    auto kernel = a.f32 ? (a.accumulate ? expert_wgrad_kernel<true, true>
+                                        : expert_wgrad_kernel<true, false>)
+                        : (a.accumulate ? expert_wgrad_kernel<false, true>
+                                        : expert_wgrad_kernel<false, false>);
     hipLaunchKernelGGL(kernel, dim3(static_cast<uint32_t>(expert_wgrad_grid(a))),
                        dim3(kWaves * 64), 0, stream, static_cast<const char*>(a.dy),
                        static_cast<const char*>(a.x), a.offsets, static_cast<int32_t>(a.max_rows),

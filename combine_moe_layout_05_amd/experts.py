@@ -93,7 +93,8 @@ def gated_grouped_gemm(x_expert: torch.Tensor, weights: Union[torch.Tensor, Mxfp
     rows first, or the Mxfp4ExpertWeights of such rows (n_hidden a multiple of
     16); offsets int32 [E+1]; out bf16 [R, n_hidden]. activation "silu" or
     "gelu" (tanh form). pre, fp32 [R, 2 n_hidden], receives the projections
-    [g | u] of the segments' rows for the backward (bf16 weights only). Not differentiable by itself; see expert_ffn."""
+    [g | u] of the segments' rows for the backward (bf16 weights only). Not
+    differentiable by itself; see expert_ffn."""
     dev = x_expert.device
     act = _activation(activation)
     packed = isinstance(weights, Mxfp4ExpertWeights)
