@@ -322,7 +322,15 @@ int64_t tiles_per_expert(const ExpertWgradArgs& a) { return int64_t(n_tiles(a)) 
 // rows, 4096 x 4096, 1070 and 1106, 16 of 4096 rows 1709 and 1880. Repeated on
 // rows that are in the cache it costs 3 to 6 % (128 rows: 212 and 219, 366 and
 // 389). 32 workgroups per expert instead of 16 lose at 2048 x 1408 (306).
-bool touches(const ExpertWgradArgs& a) { return a.max_rows <= int64_t(512) * a.E; }
+// Not where an expert has few tiles beside the 16 workgroups (256 experts of 64
+// rows: 256 x 512, 4 tiles, 25.3 and 32.8 us; 512 x 1024, 16 tiles, 77.2 and 74.7;
+// 1024 x 1024, 32 tiles, 153 and 132), nor where all tiles start at once anyway
+// (one expert of 256 rows, 4096 x 4096, 512 tiles, 17.3 and 23.0 us; 8 of 128 rows,
+// 2816 x 2048, 1408 tiles, 33.6 and 32.2).
+bool touches(const ExpertWgradArgs& a) {
+    return a.max_rows <= int64_t(512) * a.E && tiles_per_expert(a) >= kTouch &&
+           tiles_per_expert(a) * a.E >= 1024;
+}
 
 // How many experts ahead: all at once if the rows fit the memory-side cache (256
 // MB) with room for others, else what one or two rounds of workgroups take
