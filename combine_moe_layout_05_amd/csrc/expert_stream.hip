@@ -13,8 +13,8 @@
 // Measured on MI355X, one token of 8 experts. bf16, 7168 -> 2 x 2048: 78.6 us for
 // 470 MB (6.0 TB/s; a large copy moves 4.9, an in-place update 6.0). 4 bits, 7168
 // -> 2 x 2048: 21.6 us for 125 MB (5.8 TB/s); 2048 -> 7168: 14.4 us for 63 MB
-// (4.4 TB/s), where the start of 7 rounds of loads is most of it. 64 tokens over
-// 256 experts at 4 bits: 353 us for 2.13 GB (6.0 TB/s).
+// (4.4 TB/s), where a wavefront has four steps and start and end weigh most. 64
+// tokens over 256 experts at 4 bits: 353 us for 2.13 GB (6.0 TB/s).
 #include "expert_kernels.h"
 #include "expert_mma.h"
 #include "expert_mxfp4.h"

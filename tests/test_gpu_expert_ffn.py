@@ -531,24 +531,35 @@ def test_backward_weight_of_long_segments(counts):
     ref.check(got, want, err, ref.B, "dw")
 
 
-def test_backward_weight_with_rows_touched_expert_by_expert():
-    """More rows than are touched at once: 210 MB in 64 experts."""
-    E, D, F = 64, 2048, 2048
-    counts = [400 + 8 * (e % 3) - 3 * (e % 5) for e in range(E)]
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("E, rows", [(64, 400), (8, 33)])
+def test_backward_weight_with_rows_touched_ahead(E, rows, accumulate):
+    """Enough tiles for the rows to be touched ahead of them: 210 MB of rows a
+    few experts ahead, 1.4 MB all at once."""
+    D, F = 2048, 2048
+    counts = [rows + 8 * (e % 3) - 3 * (e % 5) for e in range(E)]
+    counts[3] = 0
     off, off_d = _off(counts)
     total = off[-1]
-    assert total * (D + F) * 2 > 192 << 20
+    assert (total * (D + F) * 2 > 192 << 20) == (E == 64) and E * 128 >= 1024
     g = torch.Generator(device=DEV).manual_seed(5)
-    x = torch.randn(total, D, generator=g, device=DEV).to(BF)
-    dy = torch.randn(total, F, generator=g, device=DEV).to(BF)
-    note(f"64 experts, {total} rows")
-    got = grouped_gemm_backward_weight(dy, x, off_d)
+    x = torch.randn(total + 3, D, generator=g, device=DEV).to(BF)
+    dy = torch.randn(total + 3, F, generator=g, device=DEV).to(BF)
+    x[total:], dy[total:] = float("nan"), float("nan")
+    note(f"{E} experts, {total} rows")
+    before = torch.randn(E, F, D, generator=g, device=DEV) if accumulate else None
+    got = grouped_gemm_backward_weight(dy, x, off_d,
+                                       before.clone() if accumulate else None,
+                                       accumulate=accumulate)
     sync_or_fail()
     for e in range(E):
         a, b = off[e], off[e + 1]
         d, xe = dy[a:b].double().t().contiguous(), x[a:b].double()
-        err = ref.gamma(b - a) * (d.abs() @ xe.abs())
-        ref.check(got[e], (d @ xe).cpu(), err.cpu(), ref.B, f"dw[{e}]")
+        want = d @ xe if b > a else torch.zeros(F, D, dtype=torch.float64, device=DEV)
+        err = ref.gamma(b - a) * (d.abs() @ xe.abs()) if b > a else torch.zeros_like(want)
+        if accumulate:
+            want += before[e].double()
+        ref.check(got[e], want.cpu(), err.cpu(), ref.U if accumulate else ref.B, f"dw[{e}]")
 
 
 def test_buffers_past_32_bits():
