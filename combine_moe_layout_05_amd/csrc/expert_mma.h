@@ -344,17 +344,23 @@ struct Accumulator {
     static constexpr int kLdsChunks = STAGES * kStage;
     v4i* lds;
     int lane;
+    int32_t first;          // the whole steps are taken from this one on, then from 0
+    int32_t whole;          // how many there are
 
+    // Memory step of the t-th whole step.
+    __device__ __forceinline__ int32_t at(int32_t t) const {
+        t += first;
+        return t >= whole ? t - whole : t;
+    }
     __device__ static int32_t steps_of(int64_t length) {
         return static_cast<int32_t>((length + 63) / 64);
     }
     // A partial step (length not a multiple of 64) comes first, so that the
-    // loop holds whole steps only: step t of the loop is step t - 1 of memory
-    // then.
+    // loop holds whole steps only: step t of the loop is whole step t - 1 then.
     __device__ static int left_of(int64_t length) { return static_cast<int>(length & 63); }
     __device__ __forceinline__ void issue(const A& opa, const B& opb, int stage, int32_t t) const {
-        opa.issue(t, lds + stage * kStage);
-        opb.issue(t, lds + stage * kStage + A::kChunks);
+        opa.issue(at(t), lds + stage * kStage);
+        opb.issue(at(t), lds + stage * kStage + A::kChunks);
     }
     // The first steps' loads.
     __device__ __forceinline__ void start(const A& opa, const B& opb, int64_t length) const {

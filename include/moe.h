@@ -408,8 +408,8 @@ int moe_tile_expert_weights(const void *d_weights, int32_t num_experts, int32_t 
  * its gradients, and the same products with 4-bit weights. All calls below:
  *   - rows, weights and outputs are bf16 unless stated, sums and the
  *     activation fp32, each output rounded once to nearest even. The order of
- *     a sum depends on the sizes of the call only, so equal calls give equal
- *     bits;
+ *     a sum depends on the sizes of the call and the expert's number only, so
+ *     equal calls give equal bits;
  *   - d_offsets int32 [num_experts + 1] in device memory, as for
  *     moe_grouped_gemm (segments are clamped to [0, max_rows));
  *   - rows outside every segment are never read. They are not written either,
