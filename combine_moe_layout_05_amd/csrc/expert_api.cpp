@@ -26,6 +26,7 @@ bool activation_ok(int32_t a) { return a == MOE_ACT_SILU || a == MOE_ACT_GELU_TA
 
 // Whether two buffers share a byte. The sizes stay below 2^56 bytes.
 bool overlap(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
+    if (a_bytes == 0 || b_bytes == 0) return false;
     const uintptr_t pa = reinterpret_cast<uintptr_t>(a), pb = reinterpret_cast<uintptr_t>(b);
     return pa < pb ? pb - pa < static_cast<uintptr_t>(a_bytes)
                    : pa - pb < static_cast<uintptr_t>(b_bytes);

@@ -69,6 +69,9 @@ int main() {
     EXPECT(before == moe::g_gemm + moe::g_wgrad + moe::g_stream + moe::g_mxfp4);
     EXPECT(moe_grouped_gemm_forward(p, w, off, 1, 8, 64, 64, p + 1024, 0, nullptr) == MOE_OK);
     EXPECT(moe_grouped_gemm_forward(p, w, off, 1, 8, 64, 64, w - 1024, 0, nullptr) == MOE_OK);
+    // Without rows nothing is read, so nothing can be shared.
+    EXPECT(moe_grouped_gemm_backward_weight(out + 64, out + 64, off, 1, 0, 64, 64, MOE_F32, out, 0,
+                                            nullptr) == MOE_OK);
     EXPECT(moe_mxfp4_weights_bytes(2, 24, 160) == 2 * 2 * 2 * 1088);
     EXPECT(moe_mxfp4_weights_bytes(MOE_MAX_EXPERTS, MOE_MAX_GEMM_WIDTH, MOE_MAX_GEMM_WIDTH) == -1);
     EXPECT(moe_pack_mxfp4_weights(p, w, 2, 24, 160, out, nullptr) == MOE_OK && moe::g_pack == 1);
