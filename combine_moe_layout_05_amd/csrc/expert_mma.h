@@ -133,10 +133,15 @@ typedef __attribute__((address_space(3))) bf16x4 lds_bf16x4;
 // its bytes land at dst + 16 l (base and dst are the same for the whole
 // wavefront). The instruction has no register result; its bytes are in LDS once
 // wait_loads() has seen it finish (and, for other wavefronts, after a barrier
-// behind that); m0 is a register the compiler never keeps a value in. Written
-// out, since the compiler's own form of it makes every
+// behind that). Written out, since the compiler's own form of it makes every
 // later LDS read wait for all such loads wherever control flow joins, which
 // takes the loads of later steps out of flight.
+//
+// A memory instruction may read a scalar register no sooner than 5 wait states
+// after a vector instruction wrote it (here v_readfirstlane, with which the
+// compiler may form the base right in front); nothing but the code keeps that
+// distance, and the compiler does not look inside the statement. s_nop 4 is 5
+// wait states, one of which the write of m0 needs as well.
 __device__ __forceinline__ void load_to_lds(const char* base, uint32_t off, v4i* dst) {
     const uint32_t lds = static_cast<uint32_t>(
         reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) void*)(dst)));
@@ -145,10 +150,10 @@ __device__ __forceinline__ void load_to_lds(const char* base, uint32_t off, v4i*
         static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<uint32_t>(b)));
     const uint64_t hi =
         static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<uint32_t>(b >> 32)));
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %2"
                  :
                  : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(off), "s"(lo | (hi << 32))
-                 : "memory");
+                 : "memory", "m0");
 }
 
 // The value of a register, as something the compiler knows nothing about: what
