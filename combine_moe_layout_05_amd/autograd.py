@@ -22,6 +22,7 @@ from __future__ import annotations
 from typing import Optional
 
 import torch
+from torch.autograd import forward_ad
 
 from . import _lib as L
 from .experts import _activation, _offsets, _rows, _weights
@@ -218,7 +219,7 @@ def expert_ffn(x_expert: torch.Tensor, w_gate_up: torch.Tensor, w_down: torch.Te
     Gradients reach x_expert and both weights (bf16, in one rounding of an fp32
     sum). Between the kernels h = act(g) * u and, in the backward, the gradients
     of g and u are rounded to bf16: they are operands of matrix-core products.
-    g and u themselves are kept in fp32.
+    g and u themselves are kept in fp32. Forward-mode derivatives are refused.
 
     A step can be captured into a graph (forward and backward together) after
     warm-up calls on a side stream. While an output of a call on the default
@@ -234,6 +235,8 @@ def expert_ffn(x_expert: torch.Tensor, w_gate_up: torch.Tensor, w_down: torch.Te
                          f"got {tuple(w_gate_up.shape)}, {tuple(w_down.shape)}")
     _rows("x_expert", x_expert, k_in, dev)
     _offsets(offsets, E, dev)
+    if any(forward_ad.unpack_dual(t).tangent is not None for t in (x_expert, w_gate_up, w_down)):
+        raise NotImplementedError("expert_ffn has no forward-mode derivative")
     if torch.is_grad_enabled() and (x_expert.requires_grad or w_gate_up.requires_grad
                                     or w_down.requires_grad):
         y = _ExpertFfn.apply(x_expert, w_gate_up, w_down, offsets, act)

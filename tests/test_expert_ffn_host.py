@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import combine_moe_layout_05_amd as moe
-from combine_moe_layout_05_amd import _lib as L
+from combine_moe_layout_05_amd import _lib as L, autograd
 
 P = 1 << 56                # a device address that is never dereferenced; buffers lie P apart
 OK, BAD = L.MOE_OK, L.MOE_ERR_INVALID_ARG
@@ -184,3 +184,38 @@ def test_unknown_activation_is_refused():
     with pytest.raises(ValueError, match="activation"):
         moe.gated_grouped_gemm(_cpu(4, 32), _cpu(2, 32, 32), _cpu(3, dtype=torch.int32),
                                activation="relu")
+
+
+@pytest.fixture
+def stubbed(monkeypatch):
+    """expert_ffn on host tensors: what asks for a GPU and the library's calls
+    are replaced, the calls recorded."""
+    calls = []
+    monkeypatch.setattr(autograd, "_weights", lambda name, w, dev: w.shape)
+    monkeypatch.setattr(autograd, "_rows", lambda *a: None)
+    monkeypatch.setattr(autograd, "_offsets", lambda *a: None)
+    monkeypatch.setattr(autograd, "_stream", lambda dev: 1)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    monkeypatch.setattr(autograd, "_call", lambda name, dev, *a: calls.append(name))
+    return calls
+
+
+@pytest.mark.parametrize("which", [0, 1, 2])
+@pytest.mark.parametrize("grad", [False, True])
+def test_forward_mode_derivatives_are_refused(stubbed, which, grad):
+    """A tangent that cannot be followed is an error, whether or not another
+    input needs a gradient and whether or not gradients are recorded."""
+    args = [_cpu(4, 32), _cpu(2, 32, 32), _cpu(2, 32, 16)]
+    off = _cpu(3, dtype=torch.int32)
+    if grad:
+        args[(which + 1) % 3].requires_grad_(True)
+    with torch.autograd.forward_ad.dual_level():
+        moe.expert_ffn(*args, off)              # no tangent: an ordinary call
+        args[which] = torch.autograd.forward_ad.make_dual(args[which],
+                                                          torch.ones_like(args[which]))
+        stubbed.clear()
+        with pytest.raises(NotImplementedError, match="forward"):
+            moe.expert_ffn(*args, off)
+        with torch.no_grad(), pytest.raises(NotImplementedError, match="forward"):
+            moe.expert_ffn(*args, off)
+        assert not stubbed                      # refused before any kernel
