@@ -18,6 +18,12 @@ namespace moe {
 //                from pre[r] = [g | u]
 enum class ExpertOp { kPlain, kGated, kInputGrad, kGatedGrad };
 
+// Tiles or steps of `size` rows that `rows` (0 .. INT32_MAX) rows take. The sum
+// is formed in 32 unsigned bits, which it stays within.
+__host__ __device__ constexpr int32_t expert_row_parts(int32_t rows, uint32_t size) {
+    return static_cast<int32_t>((static_cast<uint32_t>(rows) + size - 1) / size);
+}
+
 struct ExpertGemmArgs {
     ExpertOp op;
     const void* rows;       // bf16 [max_rows][red]

@@ -8,6 +8,7 @@
 #include <cstdint>
 #include <type_traits>
 
+#include "expert_kernels.h"
 #include "moe_lanes.h"
 
 namespace moe {
@@ -55,7 +56,7 @@ __device__ inline ExpertTile expert_find_tile(const int32_t* offsets, int32_t E,
         for (int k = 0; k <= kGroup; ++k) first[k] = min(max(first[k], 0), max_rows);
     };
     auto tiles_of = [&](int e0, int k) -> int32_t {
-        return e0 + k < e_hi ? (max(first[k + 1] - first[k], 0) + bt - 1) / bt : 0;
+        return e0 + k < e_hi ? expert_row_parts(max(first[k + 1] - first[k], 0), bt) : 0;
     };
     const int32_t end = min(max(offsets[E], 0), max_rows);
     int64_t local = 0;

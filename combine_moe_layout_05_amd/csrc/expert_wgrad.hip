@@ -165,7 +165,7 @@ void expert_wgrad_kernel(const char* __restrict__ dy, const char* __restrict__ x
 #pragma unroll
         for (int b = 0; b < kBlkN; ++b) acc[a][b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
-    const int32_t steps = (count + kStep - 1) / kStep;
+    const int32_t steps = expert_row_parts(count, kStep);
     if (steps > 0) {
         auto issue = [&](int stage, int32_t t) {
             ko.issue(t, lds + stage * kStageChunks);
