@@ -98,7 +98,7 @@ int run_gemm(moe::ExpertOp op, const void* rows, const void* w, const int32_t* o
         a.out = out;
         a.pre = pre;
         a.zero_tail = (flags & MOE_GEMM_ZERO_TAIL) != 0;
-        if (moe::expert_stream_grid(a) > INT32_MAX) return MOE_ERR_INVALID_ARG;
+        if (moe::expert_stream_grid(a) > moe::kMaxGrid) return MOE_ERR_INVALID_ARG;
         return status_of(moe::launch_expert_stream(a, static_cast<hipStream_t>(stream)));
     }
     moe::ExpertGemmArgs a;
@@ -114,7 +114,7 @@ int run_gemm(moe::ExpertOp op, const void* rows, const void* w, const int32_t* o
     a.out = out;
     a.pre = pre;
     a.zero_tail = (flags & MOE_GEMM_ZERO_TAIL) != 0;
-    if (moe::expert_gemm_grid(a) > INT32_MAX) return MOE_ERR_INVALID_ARG;
+    if (moe::expert_gemm_grid(a) > moe::kMaxGrid) return MOE_ERR_INVALID_ARG;
     return status_of(moe::launch_expert_gemm(a, static_cast<hipStream_t>(stream)));
 }
 
@@ -145,10 +145,10 @@ int run_mxfp4(bool gated, const void* rows, const void* packed, const int32_t* o
     a.pre = nullptr;
     a.zero_tail = (flags & MOE_GEMM_ZERO_TAIL) != 0;
     if (stream_mxfp4(max_rows, E, gated ? int64_t(2) * feats : feats)) {
-        if (moe::expert_stream_grid(a) > INT32_MAX) return MOE_ERR_INVALID_ARG;
+        if (moe::expert_stream_grid(a) > moe::kMaxGrid) return MOE_ERR_INVALID_ARG;
         return status_of(moe::launch_expert_stream(a, static_cast<hipStream_t>(stream)));
     }
-    if (moe::expert_mxfp4_grid(a) > INT32_MAX) return MOE_ERR_INVALID_ARG;
+    if (moe::expert_mxfp4_grid(a) > moe::kMaxGrid) return MOE_ERR_INVALID_ARG;
     return status_of(moe::launch_expert_mxfp4(a, static_cast<hipStream_t>(stream)));
 }
 
@@ -268,14 +268,13 @@ int moe_grouped_gemm_backward_weight(const void* d_grad_out, const void* d_x_exp
     a.f32 = grad_dtype == MOE_F32;
     a.accumulate = (flags & MOE_GEMM_ACCUMULATE) != 0;
     a.dw = d_grad_w;
-    if (moe::expert_wgrad_grid(a) > INT32_MAX) return MOE_ERR_INVALID_ARG;
+    if (moe::expert_wgrad_grid(a) > moe::kMaxGrid) return MOE_ERR_INVALID_ARG;
     return status_of(moe::launch_expert_wgrad(a, static_cast<hipStream_t>(stream)));
 }
 
 int64_t moe_mxfp4_weights_bytes(int32_t num_experts, int32_t n_out, int32_t k_in) {
     if (!experts_ok(num_experts) || !width_ok(n_out, 8) || !width_ok(k_in, 32)) return -1;
-    // The packing launch has a thread per feature and step.
-    if (moe::mxfp4_tiles(num_experts, n_out, k_in) / 16 >= INT32_MAX) return -1;
+    if (moe::mxfp4_pack_grid(num_experts, n_out, k_in) > moe::kMaxGrid) return -1;
     return moe::mxfp4_bytes(num_experts, n_out, k_in);
 }
 

@@ -293,7 +293,8 @@ hipError_t launch_op(const ExpertGemmArgs& a, hipStream_t stream) {
 }  // namespace
 
 int64_t expert_gemm_grid(const ExpertGemmArgs& a) {
-    return use_small(a) ? grid_of<Small>(a) : grid_of<Large>(a);
+    return use_small(a) ? grid_of<Small>(a) * (Small::kWaves * 64)
+                        : grid_of<Large>(a) * (Large::kWaves * 64);
 }
 
 hipError_t launch_expert_gemm(const ExpertGemmArgs& a, hipStream_t stream) {

@@ -39,7 +39,9 @@ struct ExpertGemmArgs {
     bool zero_tail;         // rows from offsets[E] on get +0.0
 };
 hipError_t launch_expert_gemm(const ExpertGemmArgs& a, hipStream_t stream);
-// Workgroups such a launch takes (checked against the grid limit).
+// Work-items such a launch takes (workgroups times their threads); at most
+// kMaxGrid of them fit a launch.
+constexpr int64_t kMaxGrid = UINT32_MAX;
 int64_t expert_gemm_grid(const ExpertGemmArgs& a);
 
 struct ExpertWgradArgs {
@@ -76,6 +78,10 @@ struct PackMxfp4Args {
     int32_t K;              // multiple of 32
     void* dst;              // mxfp4_bytes(E, N, K)
 };
+// Work-items of the packing launch: one per feature of a block and step.
+inline int64_t mxfp4_pack_grid(int32_t E, int32_t N, int32_t K) {
+    return (mxfp4_tiles(E, N, K) * 16 + 255) / 256 * 256;
+}
 hipError_t launch_pack_mxfp4(const PackMxfp4Args& a, hipStream_t stream);
 
 // Products for few rows per expert: the weights are streamed once from HBM

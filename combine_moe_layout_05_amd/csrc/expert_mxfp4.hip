@@ -251,20 +251,22 @@ int64_t feature_tiles(const ExpertStreamArgs& a) {
     return (int64_t(a.feats) + per - 1) / per;
 }
 
-}  // namespace
-
-int64_t expert_mxfp4_grid(const ExpertStreamArgs& a) {
+int64_t grid_of(const ExpertStreamArgs& a) {
     const int64_t experts = a.max_rows < a.E ? a.max_rows : a.E;
     const int64_t tiles = feature_tiles(a) * ((a.max_rows + kRowTile - 1) / kRowTile + experts);
     const int64_t unit = int64_t(kExpertXcds) * kXcdChunk;
     return (tiles + unit - 1) / unit * unit;
 }
 
+}  // namespace
+
+int64_t expert_mxfp4_grid(const ExpertStreamArgs& a) { return grid_of(a) * (kWaves * 64); }
+
 hipError_t launch_expert_mxfp4(const ExpertStreamArgs& a, hipStream_t stream) {
     const char* w = static_cast<const char*>(a.w);
     const char* scales = w + mxfp4_tiles(a.E, a.gated ? 2 * a.feats : a.feats, a.red) * 1024;
     auto kernel = a.gated ? expert_mxfp4_kernel<true> : expert_mxfp4_kernel<false>;
-    hipLaunchKernelGGL(kernel, dim3(static_cast<uint32_t>(expert_mxfp4_grid(a))),
+    hipLaunchKernelGGL(kernel, dim3(static_cast<uint32_t>(grid_of(a))),
                        dim3(kWaves * 64), 0, stream, static_cast<const char*>(a.rows), w, scales,
                        a.offsets, a.E, static_cast<int32_t>(a.max_rows), a.red, a.feats,
                        static_cast<int32_t>(feature_tiles(a)), a.activation,

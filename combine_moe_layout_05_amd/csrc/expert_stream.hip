@@ -313,14 +313,22 @@ int64_t stream_feature_tiles(const ExpertStreamArgs& a) {
     return (int64_t(a.feats) + per - 1) / per;
 }
 
+int64_t stream_workgroups(const ExpertStreamArgs& a) {
+    const int64_t experts = a.max_rows < a.E ? a.max_rows : a.E;
+    const int64_t tiles =
+        stream_feature_tiles(a) * ((a.max_rows + kRows - 1) / kRows + experts);
+    const int64_t unit = int64_t(kExpertXcds) * kXcdChunk;
+    return (tiles + unit - 1) / unit * unit;
+}
+
 template <bool MXFP4, bool GATED>
 hipError_t launch_stream(const ExpertStreamArgs& a, hipStream_t stream) {
     const char* w = static_cast<const char*>(a.w);
     const char* scales = w + mxfp4_tiles(a.E, a.gated ? 2 * a.feats : a.feats, a.red) * 1024;
     hipLaunchKernelGGL((expert_stream_kernel<MXFP4, GATED>),
-                       dim3(static_cast<uint32_t>(expert_stream_grid(a))),
-                       dim3(waves_of(MXFP4) * 64), 0, stream, static_cast<const char*>(a.rows), w, scales, a.offsets, a.E,
-                       static_cast<int32_t>(a.max_rows), a.red, a.feats,
+                       dim3(static_cast<uint32_t>(stream_workgroups(a))),
+                       dim3(waves_of(MXFP4) * 64), 0, stream, static_cast<const char*>(a.rows), w,
+                       scales, a.offsets, a.E, static_cast<int32_t>(a.max_rows), a.red, a.feats,
                        static_cast<int32_t>(stream_feature_tiles(a)), a.activation,
                        static_cast<char*>(a.out), a.pre, a.zero_tail ? 1 : 0);
     return hipGetLastError();
@@ -329,11 +337,7 @@ hipError_t launch_stream(const ExpertStreamArgs& a, hipStream_t stream) {
 }  // namespace
 
 int64_t expert_stream_grid(const ExpertStreamArgs& a) {
-    const int64_t experts = a.max_rows < a.E ? a.max_rows : a.E;
-    const int64_t tiles =
-        stream_feature_tiles(a) * ((a.max_rows + kRows - 1) / kRows + experts);
-    const int64_t unit = int64_t(kExpertXcds) * kXcdChunk;
-    return (tiles + unit - 1) / unit * unit;
+    return stream_workgroups(a) * (waves_of(a.mxfp4) * 64);
 }
 
 hipError_t launch_expert_stream(const ExpertStreamArgs& a, hipStream_t stream) {
@@ -345,7 +349,8 @@ hipError_t launch_expert_stream(const ExpertStreamArgs& a, hipStream_t stream) {
 
 hipError_t launch_pack_mxfp4(const PackMxfp4Args& a, hipStream_t stream) {
     const int64_t tiles = mxfp4_tiles(a.E, a.N, a.K);
-    hipLaunchKernelGGL(pack_mxfp4_kernel, dim3(static_cast<uint32_t>((tiles * 16 + 255) / 256)),
+    hipLaunchKernelGGL(pack_mxfp4_kernel,
+                       dim3(static_cast<uint32_t>(mxfp4_pack_grid(a.E, a.N, a.K) / 256)),
                        dim3(256), 0, stream, static_cast<const char*>(a.blocks),
                        static_cast<const uint8_t*>(a.scales), a.N, a.K, (a.N + 15) / 16,
                        (a.K + kMxfp4Step - 1) / kMxfp4Step, tiles, static_cast<char*>(a.dst));

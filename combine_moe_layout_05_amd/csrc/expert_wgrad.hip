@@ -347,19 +347,21 @@ int64_t job_count(const ExpertWgradArgs& a) {
     return (tiles_per_expert(a) + touch) * a.E + touch * touched_ahead(a);
 }
 
-}  // namespace
-
-int64_t expert_wgrad_grid(const ExpertWgradArgs& a) {
+int64_t grid_of(const ExpertWgradArgs& a) {
     const int64_t unit = int64_t(kExpertXcds) * kXcdChunk;
     return (job_count(a) + unit - 1) / unit * unit;
 }
+
+}  // namespace
+
+int64_t expert_wgrad_grid(const ExpertWgradArgs& a) { return grid_of(a) * (kWaves * 64); }
 
 hipError_t launch_expert_wgrad(const ExpertWgradArgs& a, hipStream_t stream) {
     auto kernel = a.f32 ? (a.accumulate ? expert_wgrad_kernel<true, true>
                                         : expert_wgrad_kernel<true, false>)
                         : (a.accumulate ? expert_wgrad_kernel<false, true>
                                         : expert_wgrad_kernel<false, false>);
-    hipLaunchKernelGGL(kernel, dim3(static_cast<uint32_t>(expert_wgrad_grid(a))),
+    hipLaunchKernelGGL(kernel, dim3(static_cast<uint32_t>(grid_of(a))),
                        dim3(kWaves * 64), 0, stream, static_cast<const char*>(a.dy),
                        static_cast<const char*>(a.x), a.offsets, static_cast<int32_t>(a.max_rows),
                        a.N, a.K, n_tiles(a), k_tiles(a), a.E, touches(a) ? kTouch : 0,

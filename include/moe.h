@@ -421,6 +421,8 @@ int moe_tile_expert_weights(const void *d_weights, int32_t num_experts, int32_t 
  *     MOE_MAX_GEMM_WIDTH, 1 <= num_experts <= MOE_MAX_EXPERTS;
  *   - bf16 and packed buffers are 16-byte aligned; an output shares no byte
  *     with an input or another output;
+ *   - a launch holds fewer than 2^32 work-items (workgroups times threads);
+ *     sizes that need more are refused;
  *   - no context and no workspace. Violations: MOE_ERR_INVALID_ARG. */
 #define MOE_MAX_GEMM_WIDTH  (1 << 22)
 #define MOE_GEMM_ZERO_TAIL  1    /* +0.0 into the rows from offsets[num_experts] on */

@@ -3,6 +3,7 @@ import os
 
 import pytest
 
+from combine_moe_layout_05_amd import _lib as L
 from test_sanitizers import CLANG, ENV, ROOT, SAN, _check, _run
 
 
@@ -17,3 +18,35 @@ def test_row_counts_up_to_the_largest(tmp_path):
                  os.path.join(ROOT, "tests", "sanitize", "expert_limits.cpp"), "-o", exe]),
            "compile")
     assert "0 failures" in _check(_run([exe], env=ENV), "run")
+
+
+P = 1 << 56                # addresses that are never dereferenced, P bytes apart
+X, W, OFF, OUT, PRE = (n * P for n in range(1, 6))
+ROWS, WIDE = (1 << 31) - 1, L.MOE_MAX_GEMM_WIDTH
+
+
+@pytest.mark.parametrize("name, args", [
+    ("moe_grouped_gemm_forward", (X, W, OFF, 1, ROWS, 8, 8, OUT, 0)),
+    ("moe_grouped_gemm_backward_input", (X, W, OFF, 1, ROWS, 8, 8, OUT, 0)),
+    ("moe_gated_grouped_gemm", (X, W, OFF, 1, ROWS, 8, 8, 0, OUT, None, 0)),
+    ("moe_gated_grouped_gemm_backward", (X, W, PRE, OFF, 1, ROWS, 8, 8, 0, OUT, 0)),
+    # few rows: the streamed form
+    ("moe_gated_grouped_gemm", (X, W, OFF, 64, 64, 8, WIDE, 0, OUT, None, 0)),
+    ("moe_grouped_gemm_mxfp4", (X, W, OFF, 1024, 8192, 32, WIDE // 2, OUT, 0)),
+    ("moe_grouped_gemm_mxfp4", (X, W, OFF, 1, ROWS, 32, 8, OUT, 0)),
+    ("moe_gated_grouped_gemm_mxfp4", (X, W, OFF, 1, ROWS, 32, 16, 0, OUT, 0)),
+    ("moe_grouped_gemm_backward_weight", (X, W, OFF, 1024, 8, 1 << 17, 1 << 17, L.MOE_BF16, OUT,
+                                          0)),
+    # 2^28 tiles of packed weights
+    ("moe_pack_mxfp4_weights", (X, W, 1024, WIDE // 8, 1024, OUT)),
+])
+def test_launches_past_32_bits_of_work_items_are_refused(name, args):
+    """Workgroups times threads decide, and the refusal is an argument error
+    of the host, not a failed launch."""
+    assert getattr(L.load(), name)(*args, None) == L.MOE_ERR_INVALID_ARG
+
+
+def test_packed_size_limit():
+    size = L.load().moe_mxfp4_weights_bytes
+    assert size(1024, WIDE // 8, 1024) == -1
+    assert size(1023, WIDE // 8, 1024) == 1023 * (WIDE // 8 // 16) * 8 * 1088
