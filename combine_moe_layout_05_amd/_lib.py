@@ -31,6 +31,8 @@ MOE_WEIGHTS_ROW_MAJOR = 0
 MOE_WEIGHTS_TILED = 1
 MOE_GEMM_ZERO_TAIL = 1
 MOE_GEMM_ACCUMULATE = 2
+MOE_GEMM_ZERO_HEAD = 8
+MOE_GEMM_ZERO_OUTSIDE = MOE_GEMM_ZERO_TAIL | MOE_GEMM_ZERO_HEAD
 MOE_MAX_GEMM_WIDTH = 1 << 22
 MOE_ACT_SILU = 0
 MOE_ACT_GELU_TANH = 1

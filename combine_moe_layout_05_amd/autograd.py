@@ -122,8 +122,8 @@ class MoeTokenDispatcher:
 
 def _ffn_forward(x, w_gate_up, w_down, offsets, act: int, pre: Optional[torch.Tensor]):
     """(h, y) of checked arguments: the calls of gated_grouped_gemm and
-    grouped_gemm_forward. h's rows behind the last segment stay unwritten, y's
-    are zero."""
+    grouped_gemm_forward. h's rows outside the segments stay unwritten, y's are
+    zero."""
     dev, off = x.device, offsets.data_ptr()
     R, k_in = x.shape
     E, n_out, hidden = w_down.shape
@@ -131,7 +131,7 @@ def _ffn_forward(x, w_gate_up, w_down, offsets, act: int, pre: Optional[torch.Te
     _call("moe_gated_grouped_gemm", dev, x.data_ptr(), w_gate_up.data_ptr(), off, E, R, k_in,
           hidden, act, h.data_ptr(), 0 if pre is None else pre.data_ptr(), 0)
     _call("moe_grouped_gemm_forward", dev, h.data_ptr(), w_down.data_ptr(), off, E, R, hidden,
-          n_out, y.data_ptr(), L.MOE_GEMM_ZERO_TAIL)
+          n_out, y.data_ptr(), L.MOE_GEMM_ZERO_OUTSIDE)
     return h, y
 
 
@@ -168,7 +168,7 @@ class _ExpertFfn(torch.autograd.Function):
             _call("moe_grouped_gemm_backward_weight", dev, g.data_ptr(), h.data_ptr(), off, E, R,
                   hidden, n_out, L.MOE_BF16, grad_down.data_ptr(), 0)
         if need_x or need_gate_up:
-            # Rows behind the last segment are read by neither product below.
+            # Rows outside the segments are read by neither product below.
             grad_pre = x.new_empty((R, 2 * hidden))
             _call("moe_gated_grouped_gemm_backward", dev, g.data_ptr(), w_down.data_ptr(),
                   pre.data_ptr(), off, E, R, hidden, n_out, ctx.act, grad_pre.data_ptr(), 0)
@@ -180,7 +180,7 @@ class _ExpertFfn(torch.autograd.Function):
                 grad_x = torch.empty_like(x)
                 _call("moe_grouped_gemm_backward_input", dev, grad_pre.data_ptr(),
                       w_gate_up.data_ptr(), off, E, R, k_in, 2 * hidden, grad_x.data_ptr(),
-                      L.MOE_GEMM_ZERO_TAIL)
+                      L.MOE_GEMM_ZERO_OUTSIDE)
         return grad_x, grad_gate_up, grad_down, None, None
 
 
@@ -215,7 +215,8 @@ def expert_ffn(x_expert: torch.Tensor, w_gate_up: torch.Tensor, w_down: torch.Te
 
     x_expert bf16 [R, k_in]; w_gate_up bf16 [E, 2 n_hidden, k_in] (the gate's
     rows first); w_down bf16 [E, n_out, n_hidden]; offsets int32 [E+1] (e.g.
-    Layout.offsets); y bf16 [R, n_out], its rows from offsets[E] on zero.
+    Layout.offsets); y bf16 [R, n_out], its rows of no segment (from offsets[E] on
+    and before offsets[0]) zero.
     Gradients reach x_expert and both weights (bf16, in one rounding of an fp32
     sum). Between the kernels h = act(g) * u and, in the backward, the gradients
     of g and u are rounded to bf16: they are operands of matrix-core products.

@@ -57,6 +57,12 @@ bool buffers_ok(const void* a, const void* b, const void* c, const int32_t* offs
            !misaligned(c, 16) && !misaligned(offsets, 4);
 }
 
+constexpr int32_t kZeroFlags = MOE_GEMM_ZERO_TAIL | MOE_GEMM_ZERO_HEAD;
+int32_t zero_of(int32_t flags) {
+    return ((flags & MOE_GEMM_ZERO_TAIL) ? moe::kZeroTail : 0) |
+           ((flags & MOE_GEMM_ZERO_HEAD) ? moe::kZeroHead : 0);
+}
+
 int status_of(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_ERR_HIP; }
 
 // Where the form that streams the weights (16-row tiles, the sum split over a
@@ -97,7 +103,7 @@ int run_gemm(moe::ExpertOp op, const void* rows, const void* w, const int32_t* o
         a.activation = activation;
         a.out = out;
         a.pre = pre;
-        a.zero_tail = (flags & MOE_GEMM_ZERO_TAIL) != 0;
+        a.zero = zero_of(flags);
         if (moe::expert_stream_grid(a) > moe::kMaxGrid) return MOE_ERR_INVALID_ARG;
         return status_of(moe::launch_expert_stream(a, static_cast<hipStream_t>(stream)));
     }
@@ -113,7 +119,7 @@ int run_gemm(moe::ExpertOp op, const void* rows, const void* w, const int32_t* o
     a.activation = activation;
     a.out = out;
     a.pre = pre;
-    a.zero_tail = (flags & MOE_GEMM_ZERO_TAIL) != 0;
+    a.zero = zero_of(flags);
     if (moe::expert_gemm_grid(a) > moe::kMaxGrid) return MOE_ERR_INVALID_ARG;
     return status_of(moe::launch_expert_gemm(a, static_cast<hipStream_t>(stream)));
 }
@@ -123,7 +129,7 @@ int run_mxfp4(bool gated, const void* rows, const void* packed, const int32_t* o
               int32_t flags, void* stream) {
     const int64_t packed_bytes = moe_mxfp4_weights_bytes(E, gated ? 2 * feats : feats, red);
     if (packed_bytes < 0) return MOE_ERR_INVALID_ARG;
-    if (max_rows < 0 || max_rows > INT32_MAX || (flags & ~MOE_GEMM_ZERO_TAIL))
+    if (max_rows < 0 || max_rows > INT32_MAX || (flags & ~kZeroFlags))
         return MOE_ERR_INVALID_ARG;
     if (max_rows == 0) return MOE_OK;
     if (!buffers_ok(rows, packed, out, offsets) ||
@@ -143,7 +149,7 @@ int run_mxfp4(bool gated, const void* rows, const void* packed, const int32_t* o
     a.activation = activation;
     a.out = out;
     a.pre = nullptr;
-    a.zero_tail = (flags & MOE_GEMM_ZERO_TAIL) != 0;
+    a.zero = zero_of(flags);
     if (stream_mxfp4(max_rows, E, gated ? int64_t(2) * feats : feats)) {
         if (moe::expert_stream_grid(a) > moe::kMaxGrid) return MOE_ERR_INVALID_ARG;
         return status_of(moe::launch_expert_stream(a, static_cast<hipStream_t>(stream)));
@@ -162,7 +168,7 @@ int moe_gated_grouped_gemm(const void* d_x_expert, const void* d_weights,
                            float* d_pre, int32_t flags, void* stream) {
     if (!experts_ok(num_experts) || !width_ok(k_in, 8) || !width_ok(n_hidden, 8) ||
         !activation_ok(activation) || max_rows < 0 || max_rows > INT32_MAX ||
-        (flags & ~MOE_GEMM_ZERO_TAIL))
+        (flags & ~kZeroFlags))
         return MOE_ERR_INVALID_ARG;
     if (max_rows == 0) return MOE_OK;
     if (!buffers_ok(d_x_expert, d_weights, d_h, d_offsets) || (d_pre && misaligned(d_pre, 16)))
@@ -183,7 +189,7 @@ int moe_grouped_gemm_forward(const void* d_x_expert, const void* d_weights,
                              int32_t k_in, int32_t n_out, void* d_out, int32_t flags,
                              void* stream) {
     if (!experts_ok(num_experts) || !width_ok(k_in, 8) || !width_ok(n_out, 8) || max_rows < 0 ||
-        max_rows > INT32_MAX || (flags & ~MOE_GEMM_ZERO_TAIL))
+        max_rows > INT32_MAX || (flags & ~kZeroFlags))
         return MOE_ERR_INVALID_ARG;
     if (max_rows == 0) return MOE_OK;
     if (!buffers_ok(d_x_expert, d_weights, d_out, d_offsets) ||
@@ -201,7 +207,7 @@ int moe_grouped_gemm_backward_input(const void* d_grad_out, const void* d_weight
                                     int64_t max_rows, int32_t k_in, int32_t n_out,
                                     void* d_grad_x, int32_t flags, void* stream) {
     if (!experts_ok(num_experts) || !width_ok(k_in, 8) || !width_ok(n_out, 8) || max_rows < 0 ||
-        max_rows > INT32_MAX || (flags & ~MOE_GEMM_ZERO_TAIL))
+        max_rows > INT32_MAX || (flags & ~kZeroFlags))
         return MOE_ERR_INVALID_ARG;
     if (max_rows == 0) return MOE_OK;
     if (!buffers_ok(d_grad_out, d_weights, d_grad_x, d_offsets) ||
@@ -221,7 +227,7 @@ int moe_gated_grouped_gemm_backward(const void* d_grad_out, const void* d_weight
                                     int32_t flags, void* stream) {
     if (!experts_ok(num_experts) || !width_ok(n_hidden, 8) || !width_ok(n_out, 8) ||
         !activation_ok(activation) || max_rows < 0 || max_rows > INT32_MAX ||
-        (flags & ~MOE_GEMM_ZERO_TAIL))
+        (flags & ~kZeroFlags))
         return MOE_ERR_INVALID_ARG;
     if (max_rows == 0) return MOE_OK;
     if (!buffers_ok(d_grad_out, d_weights, d_grad_pre, d_offsets) || !d_pre ||

@@ -78,7 +78,7 @@ __global__ __launch_bounds__(S::kWaves * 64, 2)
 void expert_gemm_kernel(const char* __restrict__ rows, const char* __restrict__ w,
                         const int32_t* __restrict__ offsets, int32_t E, int32_t max_rows,
                         int32_t red, int32_t feats, int32_t ftiles, int32_t act,
-                        char* __restrict__ out, float* __restrict__ pre, int32_t zero_tail) {
+                        char* __restrict__ out, float* __restrict__ pre, int32_t zero) {
     constexpr int kWaves = S::kWaves, kWavesF = S::kWavesF, kTileF = S::kTileF,
                   kTileR = S::kTileR;
     typedef typename WeightOperand<S, strided(OP)>::type Weights;
@@ -109,8 +109,8 @@ void expert_gemm_kernel(const char* __restrict__ rows, const char* __restrict__ 
     const int32_t nrows = __builtin_amdgcn_readfirstlane(info[3]);
     const int64_t out_pitch = int64_t(feats) * (OP == ExpertOp::kGatedGrad ? 4 : 2);
     if (e < 0) {
-        if (zero_tail)
-            expert_zero_tail(reinterpret_cast<v4i*>(out), row0, max_rows,
+        if (zero)
+            expert_zero_rows(reinterpret_cast<v4i*>(out), offsets, zero, row0, max_rows,
                              static_cast<int32_t>(out_pitch / 16), ft, int64_t(gridDim.x) - nrows);
         return;
     }
@@ -281,7 +281,7 @@ hipError_t launch_shape(const ExpertGemmArgs& a, hipStream_t stream) {
                        static_cast<const char*>(a.w), a.offsets, a.E,
                        static_cast<int32_t>(a.max_rows), a.red, a.feats,
                        static_cast<int32_t>(feature_tiles<S>(a)), a.activation,
-                       static_cast<char*>(a.out), a.pre, a.zero_tail ? 1 : 0);
+                       static_cast<char*>(a.out), a.pre, a.zero);
     return hipGetLastError();
 }
 

@@ -24,6 +24,10 @@ __host__ __device__ constexpr int32_t expert_row_parts(int32_t rows, uint32_t si
     return static_cast<int32_t>((static_cast<uint32_t>(rows) + size - 1) / size);
 }
 
+// Rows a product sets to +0.0 beside the ones it computes.
+constexpr int32_t kZeroTail = 1;        // from offsets[E] on
+constexpr int32_t kZeroHead = 2;        // before offsets[0]
+
 struct ExpertGemmArgs {
     ExpertOp op;
     const void* rows;       // bf16 [max_rows][red]
@@ -36,7 +40,7 @@ struct ExpertGemmArgs {
     int32_t activation;     // moe_activation
     void* out;              // bf16 [max_rows][feats], kGatedGrad: [max_rows][2 feats]
     float* pre;             // [max_rows][2 feats] or null
-    bool zero_tail;         // rows from offsets[E] on get +0.0
+    int32_t zero;           // kZeroTail, kZeroHead: rows outside the segments that get +0.0
 };
 hipError_t launch_expert_gemm(const ExpertGemmArgs& a, hipStream_t stream);
 // Work-items such a launch takes (workgroups times their threads); at most
@@ -100,7 +104,7 @@ struct ExpertStreamArgs {
     int32_t activation;
     void* out;              // bf16 [max_rows][feats]
     float* pre;             // gated: [max_rows][2 feats] or null
-    bool zero_tail;
+    int32_t zero;           // as above
 };
 hipError_t launch_expert_stream(const ExpertStreamArgs& a, hipStream_t stream);
 int64_t expert_stream_grid(const ExpertStreamArgs& a);

@@ -118,13 +118,19 @@ __device__ __forceinline__ int64_t expert_tile_number(int32_t chunk) {
     return ((idx / chunk) * kExpertXcds + x) * chunk + idx % chunk;
 }
 
-// +0.0 into rows [row0, max_rows) of `width` 16-byte chunks, spread over the
+// +0.0 into rows of no segment, of `width` 16-byte chunks each: from `end` on
+// (kZeroTail in `zero`), before the first segment (kZeroHead). Spread over the
 // workgroups without a tile (this one is number `index` of `count`).
-__device__ __forceinline__ void expert_zero_tail(v4i* out, int64_t row0, int64_t max_rows,
-                                                 int32_t width, int64_t index, int64_t count) {
-    const v4i zero = {0, 0, 0, 0};
-    for (int64_t r = row0 + index; r < max_rows; r += count)
-        for (int32_t c = threadIdx.x; c < width; c += blockDim.x) out[r * width + c] = zero;
+__device__ __forceinline__ void expert_zero_rows(v4i* out, const int32_t* offsets, int32_t zero,
+                                                 int64_t end, int64_t max_rows, int32_t width,
+                                                 int64_t index, int64_t count) {
+    const v4i nothing = {0, 0, 0, 0};
+    auto clear = [&](int64_t from, int64_t to) {
+        for (int64_t r = from + index; r < to; r += count)
+            for (int32_t c = threadIdx.x; c < width; c += blockDim.x) out[r * width + c] = nothing;
+    };
+    if (zero & kZeroTail) clear(end, max_rows);
+    if (zero & kZeroHead) clear(0, min(static_cast<int64_t>(offsets[0]), end));
 }
 
 typedef __attribute__((address_space(3))) v4i lds_v4i;

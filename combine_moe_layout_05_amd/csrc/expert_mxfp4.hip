@@ -38,7 +38,7 @@ __global__ __launch_bounds__(kWaves * 64, 2)
 void expert_mxfp4_kernel(const char* __restrict__ rows, const char* __restrict__ w,
                          const char* __restrict__ scales, const int32_t* __restrict__ offsets,
                          int32_t E, int32_t max_rows, int32_t red, int32_t feats, int32_t ftiles,
-                         int32_t act, char* __restrict__ out, int32_t zero_tail) {
+                         int32_t act, char* __restrict__ out, int32_t zero) {
     // Output features of a wavefront: half its blocks are up rows if gated.
     constexpr int kFeats = kBlocks * 16 / (GATED ? 2 : 1);
     __shared__ v4i lds[kStages * 2 * PackedOperand<kRowTile, kWaves>::kChunks];
@@ -62,9 +62,9 @@ void expert_mxfp4_kernel(const char* __restrict__ rows, const char* __restrict__
     const int32_t row0 = __builtin_amdgcn_readfirstlane(info[2]);
     const int32_t nrows = __builtin_amdgcn_readfirstlane(info[3]);
     if (e < 0) {
-        if (zero_tail)
-            expert_zero_tail(reinterpret_cast<v4i*>(out), row0, max_rows, feats / 8, ft,
-                             int64_t(gridDim.x) - nrows);
+        if (zero)
+            expert_zero_rows(reinterpret_cast<v4i*>(out), offsets, zero, row0, max_rows, feats / 8,
+                             ft, int64_t(gridDim.x) - nrows);
         return;
     }
     const int i = lane & 15, g = lane >> 4;
@@ -270,7 +270,7 @@ hipError_t launch_expert_mxfp4(const ExpertStreamArgs& a, hipStream_t stream) {
                        dim3(kWaves * 64), 0, stream, static_cast<const char*>(a.rows), w, scales,
                        a.offsets, a.E, static_cast<int32_t>(a.max_rows), a.red, a.feats,
                        static_cast<int32_t>(feature_tiles(a)), a.activation,
-                       static_cast<char*>(a.out), a.zero_tail ? 1 : 0);
+                       static_cast<char*>(a.out), a.zero);
     return hipGetLastError();
 }
 

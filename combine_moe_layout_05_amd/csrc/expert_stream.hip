@@ -60,7 +60,7 @@ void expert_stream_kernel(const char* __restrict__ rows, const char* __restrict_
                           const char* __restrict__ scales, const int32_t* __restrict__ offsets,
                           int32_t E, int32_t max_rows, int32_t red, int32_t feats, int32_t ftiles,
                           int32_t act, char* __restrict__ out, float* __restrict__ pre,
-                          int32_t zero_tail) {
+                          int32_t zero) {
     typedef Step<MXFP4> S;
     constexpr int kWaves = waves_of(MXFP4);
     constexpr int kFeatBlocks = GATED ? kBlocks / 2 : kBlocks;  // of the output
@@ -92,9 +92,9 @@ void expert_stream_kernel(const char* __restrict__ rows, const char* __restrict_
     const int32_t row0 = __builtin_amdgcn_readfirstlane(info[2]);
     const int32_t nrows = __builtin_amdgcn_readfirstlane(info[3]);
     if (e < 0) {
-        if (zero_tail)
-            expert_zero_tail(reinterpret_cast<v4i*>(out), row0, max_rows, feats / 8, ft,
-                             int64_t(gridDim.x) - nrows);
+        if (zero)
+            expert_zero_rows(reinterpret_cast<v4i*>(out), offsets, zero, row0, max_rows, feats / 8,
+                             ft, int64_t(gridDim.x) - nrows);
         return;
     }
     const int i = lane & 15, g = lane >> 4;
@@ -330,7 +330,7 @@ hipError_t launch_stream(const ExpertStreamArgs& a, hipStream_t stream) {
                        dim3(waves_of(MXFP4) * 64), 0, stream, static_cast<const char*>(a.rows), w,
                        scales, a.offsets, a.E, static_cast<int32_t>(a.max_rows), a.red, a.feats,
                        static_cast<int32_t>(stream_feature_tiles(a)), a.activation,
-                       static_cast<char*>(a.out), a.pre, a.zero_tail ? 1 : 0);
+                       static_cast<char*>(a.out), a.pre, a.zero);
     return hipGetLastError();
 }
 

@@ -8,8 +8,9 @@ For every expert e and row r with offsets[e] <= r < offsets[e+1]:
     y[r] = h[r] @ Wd[e].T
 The calls take the expert-major rows dispatch() returns and the offsets of
 layout(), both on the device; nothing is read back, so they can be captured in
-a graph. Where a call allocates its output, rows from offsets[E] on are zero;
-an output the caller passes keeps what it held there.
+a graph. Where a call allocates its output, the rows of no segment (from
+offsets[E] on, and before offsets[0], which is 0 in a layout) are zero; an
+output the caller passes keeps what it held there.
 """
 from __future__ import annotations
 
@@ -50,9 +51,9 @@ def _offsets(offsets: torch.Tensor, E: int, dev: torch.device) -> None:
 
 
 def _out(out: Optional[torch.Tensor], rows: int, width: int, dev: torch.device, name: str = "out"):
-    """The output and its flags: a fresh one is zero behind the last segment."""
+    """The output and its flags: a fresh one is zero outside the segments."""
     if out is None:
-        return torch.empty((rows, width), dtype=torch.bfloat16, device=dev), L.MOE_GEMM_ZERO_TAIL
+        return torch.empty((rows, width), dtype=torch.bfloat16, device=dev), L.MOE_GEMM_ZERO_OUTSIDE
     _rows(name, out, width, dev, rows)
     return out, 0
 

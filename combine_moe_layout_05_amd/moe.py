@@ -165,7 +165,7 @@ def _grouped_gemm_mxfp4(x_expert, weights: Mxfp4ExpertWeights, offsets, out, row
         raise ValueError("4-bit weights take no row_tile")
     flags = 0
     if out is None:
-        out, flags = x_expert.new_empty((R, n_out)), L.MOE_GEMM_ZERO_TAIL
+        out, flags = x_expert.new_empty((R, n_out)), L.MOE_GEMM_ZERO_OUTSIDE
     else:
         _check_rows("out", out, torch.bfloat16, 2, dev)
         if tuple(out.shape) != (R, n_out):
@@ -185,7 +185,7 @@ def grouped_gemm(x_expert: torch.Tensor, weights, offsets: torch.Tensor,
 
     x_expert bf16 [R, k_in]; weights bf16 [E, n_out, k_in] or the
     TiledExpertWeights of them (same results, faster), or 4-bit weights as
-    Mxfp4ExpertWeights (moe_grouped_gemm_mxfp4; rows from offsets[E] on of an
+    Mxfp4ExpertWeights (moe_grouped_gemm_mxfp4; the rows of no segment of an
     output it allocates are zero); offsets int32 [E+1]; out bf16 [R, n_out]
     (allocated with torch.empty if None)."""
     if isinstance(weights, Mxfp4ExpertWeights):

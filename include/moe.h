@@ -414,7 +414,8 @@ int moe_tile_expert_weights(const void *d_weights, int32_t num_experts, int32_t 
  *     moe_grouped_gemm (segments are clamped to [0, max_rows));
  *   - rows outside every segment are never read. They are not written either,
  *     except that MOE_GEMM_ZERO_TAIL sets the rows from offsets[num_experts]
- *     on to +0.0;
+ *     on to +0.0 and MOE_GEMM_ZERO_HEAD those before offsets[0] (a layout
+ *     has none);
  *   - 0 <= max_rows <= INT32_MAX; with max_rows == 0 nothing is enqueued
  *     (moe_grouped_gemm_backward_weight still writes its zeros);
  *   - widths are multiples of 8 (more where stated) from 8 to
@@ -427,6 +428,7 @@ int moe_tile_expert_weights(const void *d_weights, int32_t num_experts, int32_t 
 #define MOE_MAX_GEMM_WIDTH  (1 << 22)
 #define MOE_GEMM_ZERO_TAIL  1    /* +0.0 into the rows from offsets[num_experts] on */
 #define MOE_GEMM_ACCUMULATE 2    /* add to what the weight gradient holds */
+#define MOE_GEMM_ZERO_HEAD  8    /* +0.0 into the rows before offsets[0] */
 
 typedef enum moe_activation {
     MOE_ACT_SILU = 0,            /* g / (1 + exp(-g)) */
@@ -485,7 +487,7 @@ int moe_gated_grouped_gemm_backward(const void *d_grad_out, const void *d_weight
  * +0.0 for an expert without rows; with MOE_GEMM_ACCUMULATE the sum is added
  * to what d_grad_w holds (one rounding of the total), and an expert without
  * rows keeps its values. d_grad_w is [num_experts][n_out][k_in] of grad_dtype
- * (MOE_BF16 or MOE_F32). MOE_GEMM_ZERO_TAIL does not apply. */
+ * (MOE_BF16 or MOE_F32). The zero flags do not apply. */
 int moe_grouped_gemm_backward_weight(const void *d_grad_out, const void *d_x_expert,
                                      const int32_t *d_offsets, int32_t num_experts,
                                      int64_t max_rows, int32_t k_in, int32_t n_out,

@@ -50,3 +50,25 @@ def test_packed_size_limit():
     size = L.load().moe_mxfp4_weights_bytes
     assert size(1024, WIDE // 8, 1024) == -1
     assert size(1023, WIDE // 8, 1024) == 1023 * (WIDE // 8 // 16) * 8 * 1088
+
+
+@pytest.mark.parametrize("name, args", [
+    ("moe_grouped_gemm_forward", (X, W, OFF, 1, 0, 8, 8, OUT)),
+    ("moe_grouped_gemm_backward_input", (X, W, OFF, 1, 0, 8, 8, OUT)),
+    ("moe_gated_grouped_gemm", (X, W, OFF, 1, 0, 8, 8, 0, OUT, None)),
+    ("moe_gated_grouped_gemm_backward", (X, W, PRE, OFF, 1, 0, 8, 8, 0, OUT)),
+    ("moe_grouped_gemm_mxfp4", (X, W, OFF, 1, 0, 32, 8, OUT)),
+    ("moe_gated_grouped_gemm_mxfp4", (X, W, OFF, 1, 0, 32, 16, 0, OUT)),
+])
+def test_flags_of_the_products(name, args):
+    call = getattr(L.load(), name)
+    for flags in range(32):
+        known = flags & ~L.MOE_GEMM_ZERO_OUTSIDE == 0
+        assert call(*args, flags, None) == (L.MOE_OK if known else L.MOE_ERR_INVALID_ARG), flags
+    assert L.MOE_GEMM_ZERO_OUTSIDE == L.MOE_GEMM_ZERO_TAIL | L.MOE_GEMM_ZERO_HEAD == 9
+
+
+def test_the_weight_gradient_takes_no_zero_flags():
+    call = L.load().moe_grouped_gemm_backward_weight
+    for flags in (L.MOE_GEMM_ZERO_TAIL, L.MOE_GEMM_ZERO_HEAD):
+        assert call(X, W, OFF, 1, 8, 8, 8, L.MOE_F32, OUT, flags, None) == L.MOE_ERR_INVALID_ARG
