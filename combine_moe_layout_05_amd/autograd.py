@@ -184,7 +184,8 @@ class _ExpertFfn(torch.autograd.Function):
         return grad_x, grad_gate_up, grad_down, None, None
 
 
-# Marks a leaf's gradient accumulator as made by a call on the default stream.
+# Whether a leaf's gradient accumulator was made on the default stream, as far as
+# the calls here can tell: noted by the first of them that meets it.
 _ON_DEFAULT_STREAM = "combine_moe_layout.default_stream"
 
 
@@ -193,18 +194,18 @@ def _watch_accumulators(node, stream: int) -> None:
     leads to. The engine runs an accumulator on the stream it was made on, and
     it lives as long as any graph that reaches it. One made on the default
     stream cannot join a capture: the backward would fail inside the engine and
-    end the process, so such a capture is refused here."""
+    end the process, so such a capture is refused here. Calls that only use an
+    accumulator do not change where it belongs."""
     leaves = [fn for fn, _ in node.next_functions if hasattr(fn, "variable")]
-    if torch.cuda.is_current_stream_capturing():
-        if any(fn.metadata.get(_ON_DEFAULT_STREAM) for fn in leaves):
+    capturing = torch.cuda.is_current_stream_capturing()
+    for fn in leaves:
+        on_default = fn.metadata.setdefault(_ON_DEFAULT_STREAM, stream == 0 and not capturing)
+        if capturing and on_default:
             raise RuntimeError(
                 "expert_ffn cannot be captured while the output of an earlier call on the default "
                 "stream that reaches the same leaf tensors is alive: its gradient accumulators "
                 "belong to that stream. Delete that output first, or run the calls before the "
                 "capture on a side stream.")
-    elif stream == 0:
-        for fn in leaves:
-            fn.metadata[_ON_DEFAULT_STREAM] = True
 
 
 def expert_ffn(x_expert: torch.Tensor, w_gate_up: torch.Tensor, w_down: torch.Tensor,
@@ -225,8 +226,11 @@ def expert_ffn(x_expert: torch.Tensor, w_gate_up: torch.Tensor, w_down: torch.Te
     A step can be captured into a graph (forward and backward together) after
     warm-up calls on a side stream. While an output of a call on the default
     stream that takes the same leaf tensors is alive, the capture is refused.
-    (Of inputs that are computed from other leaves only the caller can know
-    that: keep no such output alive across the capture.)"""
+    Two cases only the caller can know of, and has to avoid, since such a
+    backward ends the process: a graph of another operation on the same leaves
+    (a penalty on a weight, say) that was made on the default stream and is
+    alive across the capture, and one of the leaves from which an input was
+    computed."""
     dev = x_expert.device
     act = _activation(activation)
     E, n2, k_in = _weights("w_gate_up", w_gate_up, dev)

@@ -219,3 +219,52 @@ def test_forward_mode_derivatives_are_refused(stubbed, which, grad):
         with torch.no_grad(), pytest.raises(NotImplementedError, match="forward"):
             moe.expert_ffn(*args, off)
         assert not stubbed                      # refused before any kernel
+
+
+def _leaves():
+    return [_cpu(4, 32).requires_grad_(True), _cpu(2, 32, 32).requires_grad_(True),
+            _cpu(2, 32, 16).requires_grad_(True)]
+
+
+def _on(monkeypatch, stream, capturing=False):
+    monkeypatch.setattr(autograd, "_stream", lambda dev: stream)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: capturing)
+
+
+def test_capture_after_a_side_stream_made_the_accumulators(stubbed, monkeypatch):
+    """The accumulators belong to the stream that made them, whoever uses them
+    afterwards: a call on the default stream does not spoil a later capture."""
+    off, leaves = _cpu(3, dtype=torch.int32), _leaves()
+    _on(monkeypatch, 7)
+    kept = moe.expert_ffn(*leaves, off)
+    _on(monkeypatch, 0)
+    moe.expert_ffn(*leaves, off)
+    _on(monkeypatch, 9, capturing=True)
+    moe.expert_ffn(*leaves, off)
+    del kept
+
+
+def test_capture_after_a_capture_made_the_accumulators(stubbed, monkeypatch):
+    off, leaves = _cpu(3, dtype=torch.int32), _leaves()
+    _on(monkeypatch, 9, capturing=True)
+    kept = moe.expert_ffn(*leaves, off)
+    _on(monkeypatch, 0)
+    moe.expert_ffn(*leaves, off)
+    _on(monkeypatch, 9, capturing=True)
+    moe.expert_ffn(*leaves, off)
+    del kept
+
+
+def test_capture_beside_accumulators_of_the_default_stream_is_refused(stubbed, monkeypatch):
+    """Also after calls on other streams have used them; once the output that
+    keeps them alive is gone, it works."""
+    off, leaves = _cpu(3, dtype=torch.int32), _leaves()
+    _on(monkeypatch, 0)
+    kept = moe.expert_ffn(*leaves, off)
+    _on(monkeypatch, 7)
+    moe.expert_ffn(*leaves, off)
+    _on(monkeypatch, 9, capturing=True)
+    with pytest.raises(RuntimeError, match="default stream"):
+        moe.expert_ffn(*leaves, off)
+    del kept
+    moe.expert_ffn(*leaves, off)
