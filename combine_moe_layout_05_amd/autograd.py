@@ -244,6 +244,9 @@ def expert_ffn(x_expert: torch.Tensor, w_gate_up: torch.Tensor, w_down: torch.Te
         raise NotImplementedError("expert_ffn has no forward-mode derivative")
     if torch.is_grad_enabled() and (x_expert.requires_grad or w_gate_up.requires_grad
                                     or w_down.requires_grad):
+        if n2 > L.MOE_MAX_GEMM_WIDTH and (x_expert.requires_grad or w_gate_up.requires_grad):
+            raise ValueError(f"n_hidden must be at most {L.MOE_MAX_GEMM_WIDTH // 2} for gradients "
+                             f"of x_expert and w_gate_up, got {hidden}")
         y = _ExpertFfn.apply(x_expert, w_gate_up, w_down, offsets, act)
         _watch_accumulators(y.grad_fn, _stream(dev))
         return y

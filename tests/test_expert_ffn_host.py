@@ -268,3 +268,30 @@ def test_capture_beside_accumulators_of_the_default_stream_is_refused(stubbed, m
         moe.expert_ffn(*leaves, off)
     del kept
     moe.expert_ffn(*leaves, off)
+
+
+def test_hidden_widths_that_the_backward_cannot_take_are_refused_at_the_call(stubbed):
+    """[g | u] is twice as wide as h, and it is a width of the backward's
+    products; without gradients only h's width counts."""
+    limit = MAX // 2
+    off = _cpu(3, dtype=torch.int32)
+    for hidden, fits in ((limit, True), (limit + 8, False)):
+        x = torch.empty(2, 8, dtype=torch.bfloat16)
+        w1 = torch.empty(1, 2 * hidden, 8, dtype=torch.bfloat16)
+        w2 = torch.empty(1, 8, hidden, dtype=torch.bfloat16)
+        moe.expert_ffn(x, w1, w2, off)
+        for leaf in (x, w1, w2):
+            leaf.requires_grad_(True)
+            if fits or leaf is w2:
+                # The gradient of w_down alone needs no product that wide.
+                y = moe.expert_ffn(x, w1, w2, off)
+                y.backward(torch.zeros_like(y))
+            else:
+                stubbed.clear()
+                with pytest.raises(ValueError, match="n_hidden"):
+                    moe.expert_ffn(x, w1, w2, off)
+                with torch.no_grad():
+                    moe.expert_ffn(x, w1, w2, off)
+                assert stubbed == ["moe_gated_grouped_gemm", "moe_grouped_gemm_forward"]
+            leaf.grad = None
+            leaf.requires_grad_(False)
