@@ -10,6 +10,30 @@
 #include "expert_kernels.h"
 #include "moe.h"
 
+namespace moe {
+
+// Where the form that streams the weights (16-row tiles, the sum split over a
+// workgroup's wavefronts) is the faster one. Measured on MI355X:
+//   - bf16, up to 64 rows: one expert of 4096 -> 2 x 2048 gated 19.6 us at 32
+//     rows, the tiled form 24.8 us from 65 to 256; at 128 rows 35.2 against
+//     24.4 us, so it ends there.
+//   - 4 bits, up to 8 rows per expert: 128 experts of 4096 -> 2 x 2048 at 1024
+//     rows 180 against 197 us, at 2048 rows 268 against 203 us.
+//   - 4 bits, while its workgroups are few (the tiled form then leaves CUs
+//     idle): one expert of 4096 -> 2 x 2048 at 256 rows (1024 workgroups) 18.0
+//     against 39.5 us, at 512 rows (2048) 39.3 against 40.6 us; 8 experts of
+//     4096 -> 2 x 1408 at 512 rows (1408) 38.2 against 40.2, at 1024 rows (2816)
+//     59.7 against 41.6 us.
+bool expert_streams_bf16(int64_t max_rows) { return max_rows <= 64; }
+bool expert_streams_mxfp4(int32_t E, int64_t max_rows, int64_t positions) {
+    if (max_rows <= int64_t(8) * E) return true;
+    const int64_t experts = max_rows < E ? max_rows : E;
+    const int64_t tiles = (max_rows + 15) / 16;
+    return (positions + 63) / 64 * (tiles > experts ? tiles : experts) <= 1536;
+}
+
+}  // namespace moe
+
 namespace {
 
 bool misaligned(const void* p, uintptr_t a) {
@@ -65,31 +89,11 @@ int32_t zero_of(int32_t flags) {
 
 int status_of(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_ERR_HIP; }
 
-// Where the form that streams the weights (16-row tiles, the sum split over a
-// workgroup's wavefronts) is the faster one. Measured on MI355X:
-//   - bf16, up to 64 rows: one expert of 4096 -> 2 x 2048 gated 19.6 us at 32
-//     rows, the tiled form 24.8 us from 65 to 256; at 128 rows 35.2 against
-//     24.4 us, so it ends there.
-//   - 4 bits, up to 8 rows per expert: 128 experts of 4096 -> 2 x 2048 at 1024
-//     rows 180 against 197 us, at 2048 rows 268 against 203 us.
-//   - 4 bits, while its workgroups are few (the tiled form then leaves CUs
-//     idle): one expert of 4096 -> 2 x 2048 at 256 rows (1024 workgroups) 18.0
-//     against 39.5 us, at 512 rows (2048) 39.3 against 40.6 us; 8 experts of
-//     4096 -> 2 x 1408 at 512 rows (1408) 38.2 against 40.2, at 1024 rows (2816)
-//     59.7 against 41.6 us.
-bool stream_bf16(int64_t max_rows) { return max_rows <= 64; }
-bool stream_mxfp4(int64_t max_rows, int32_t E, int64_t positions) {
-    if (max_rows <= int64_t(8) * E) return true;
-    const int64_t experts = max_rows < E ? max_rows : E;
-    const int64_t tiles = (max_rows + 15) / 16;
-    return (positions + 63) / 64 * (tiles > experts ? tiles : experts) <= 1536;
-}
-
 int run_gemm(moe::ExpertOp op, const void* rows, const void* w, const int32_t* offsets, int32_t E,
              int64_t max_rows, int32_t red, int32_t feats, int32_t activation, void* out,
              float* pre, int32_t flags, void* stream) {
     const bool forward = op == moe::ExpertOp::kPlain || op == moe::ExpertOp::kGated;
-    if (forward && stream_bf16(max_rows)) {
+    if (forward && moe::expert_streams_bf16(max_rows)) {
         moe::ExpertStreamArgs a;
         a.mxfp4 = false;
         a.gated = op == moe::ExpertOp::kGated;
@@ -150,7 +154,7 @@ int run_mxfp4(bool gated, const void* rows, const void* packed, const int32_t* o
     a.out = out;
     a.pre = nullptr;
     a.zero = zero_of(flags);
-    if (stream_mxfp4(max_rows, E, gated ? int64_t(2) * feats : feats)) {
+    if (moe::expert_streams_mxfp4(E, max_rows, gated ? int64_t(2) * feats : feats)) {
         if (moe::expert_stream_grid(a) > moe::kMaxGrid) return MOE_ERR_INVALID_ARG;
         return status_of(moe::launch_expert_stream(a, static_cast<hipStream_t>(stream)));
     }

@@ -240,9 +240,9 @@ void expert_gemm_kernel(const char* __restrict__ rows, const char* __restrict__ 
 }
 
 template <class S>
-int64_t feature_tiles(const ExpertGemmArgs& a) {
-    const int32_t per = S::feats(a.op);
-    return (int64_t(a.feats) + per - 1) / per;
+int64_t feature_tiles(ExpertOp op, int32_t feats) {
+    const int32_t per = S::feats(op);
+    return (int64_t(feats) + per - 1) / per;
 }
 
 template <class S>
@@ -251,10 +251,12 @@ int64_t grid_of(const ExpertGemmArgs& a) {
     // per expert with rows than the rows fill.
     const int64_t experts = a.max_rows < a.E ? a.max_rows : a.E;
     const int64_t tiles =
-        feature_tiles<S>(a) * ((a.max_rows + S::kTileR - 1) / S::kTileR + experts);
+        feature_tiles<S>(a.op, a.feats) * ((a.max_rows + S::kTileR - 1) / S::kTileR + experts);
     const int64_t unit = int64_t(kExpertXcds) * kXcdChunk;
     return (tiles + unit - 1) / unit * unit;
 }
+
+}  // namespace
 
 // The small shape where segments are short, or where the large one would leave
 // half the 256 CUs idle. Measured on MI355X, weights from HBM, large against
@@ -267,11 +269,17 @@ int64_t grid_of(const ExpertGemmArgs& a) {
 //     large tiles), 100 and 104 at 2048 (128), 135 and 201 at 4096 (256); 8 of
 //     100 rows 80.4 and 71.8 (128); 24 of 1992 -> 2 x 1000 60.7 and 70.1 at 92
 //     rows (192).
-bool use_small(const ExpertGemmArgs& a) {
-    if (a.max_rows <= int64_t(32) * a.E) return true;
-    const int64_t row_tiles = (a.max_rows + Large::kTileR - 1) / Large::kTileR;
-    const int64_t experts = a.max_rows < a.E ? a.max_rows : a.E;
-    return feature_tiles<Large>(a) * (row_tiles > experts ? row_tiles : experts) <= 128;
+bool expert_small_tile(ExpertOp op, int32_t E, int64_t max_rows, int32_t feats) {
+    if (max_rows <= int64_t(32) * E) return true;
+    const int64_t row_tiles = (max_rows + Large::kTileR - 1) / Large::kTileR;
+    const int64_t experts = max_rows < E ? max_rows : E;
+    return feature_tiles<Large>(op, feats) * (row_tiles > experts ? row_tiles : experts) <= 128;
+}
+
+namespace {
+
+bool small_tile(const ExpertGemmArgs& a) {
+    return expert_small_tile(a.op, a.E, a.max_rows, a.feats);
 }
 
 template <ExpertOp OP, class S>
@@ -280,20 +288,20 @@ hipError_t launch_shape(const ExpertGemmArgs& a, hipStream_t stream) {
                        dim3(S::kWaves * 64), 0, stream, static_cast<const char*>(a.rows),
                        static_cast<const char*>(a.w), a.offsets, a.E,
                        static_cast<int32_t>(a.max_rows), a.red, a.feats,
-                       static_cast<int32_t>(feature_tiles<S>(a)), a.activation,
+                       static_cast<int32_t>(feature_tiles<S>(a.op, a.feats)), a.activation,
                        static_cast<char*>(a.out), a.pre, a.zero);
     return hipGetLastError();
 }
 
 template <ExpertOp OP>
 hipError_t launch_op(const ExpertGemmArgs& a, hipStream_t stream) {
-    return use_small(a) ? launch_shape<OP, Small>(a, stream) : launch_shape<OP, Large>(a, stream);
+    return small_tile(a) ? launch_shape<OP, Small>(a, stream) : launch_shape<OP, Large>(a, stream);
 }
 
 }  // namespace
 
 int64_t expert_gemm_grid(const ExpertGemmArgs& a) {
-    return use_small(a) ? grid_of<Small>(a) * (Small::kWaves * 64)
+    return small_tile(a) ? grid_of<Small>(a) * (Small::kWaves * 64)
                         : grid_of<Large>(a) * (Large::kWaves * 64);
 }
 

@@ -42,6 +42,8 @@ struct ExpertGemmArgs {
     float* pre;             // [max_rows][2 feats] or null
     int32_t zero;           // kZeroTail, kZeroHead: rows outside the segments that get +0.0
 };
+// Whether it runs in the small tiles, by a rule on the sizes.
+bool expert_small_tile(ExpertOp op, int32_t E, int64_t max_rows, int32_t feats);
 hipError_t launch_expert_gemm(const ExpertGemmArgs& a, hipStream_t stream);
 // Work-items such a launch takes (workgroups times their threads); at most
 // kMaxGrid of them fit a launch.
@@ -106,6 +108,10 @@ struct ExpertStreamArgs {
     float* pre;             // gated: [max_rows][2 feats] or null
     int32_t zero;           // as above
 };
+// Whether a forward product is streamed, by a rule on the sizes; `positions`
+// are rows of weights (two per feature if gated).
+bool expert_streams_bf16(int64_t max_rows);
+bool expert_streams_mxfp4(int32_t E, int64_t max_rows, int64_t positions);
 hipError_t launch_expert_stream(const ExpertStreamArgs& a, hipStream_t stream);
 int64_t expert_stream_grid(const ExpertStreamArgs& a);
 // The same products with packed 4-bit weights for many rows per expert.

@@ -471,7 +471,8 @@ struct Accumulator {
 // act(g) and its derivative in fp32. silu(g) = g sigmoid(g); the tanh form of
 // gelu is g sigmoid(2z) with z = sqrt(2/pi) (g + 0.044715 g^3), which loses no
 // digits where 1 + tanh(z) would cancel. exp runs to infinity or zero at the
-// ends, where the sigmoid is exactly 0 or 1.
+// ends, where the sigmoid is exactly 0 or 1; one below 2^-126 (silu from g = -87.4
+// down, gelu from -10.0) becomes 0 too, since the reciprocal returns no denormals.
 constexpr int kActSilu = 0;
 constexpr int kActGelu = 1;
 __device__ __forceinline__ float sigmoid_f32(float z) {
