@@ -222,6 +222,9 @@ def expert_ffn(x_expert: torch.Tensor, w_gate_up: torch.Tensor, w_down: torch.Te
     sum). Between the kernels h = act(g) * u and, in the backward, the gradients
     of g and u are rounded to bf16: they are operands of matrix-core products.
     g and u themselves are kept in fp32. Forward-mode derivatives are refused.
+    x_expert is kept for the backward, not copied: rows in a MoeDispatcher's
+    buffer must not be dispatched anew before it (MoeTokenDispatcher watches for
+    that in combine()'s backward).
 
     A step can be captured into a graph (forward and backward together) after
     warm-up calls on a side stream. While an output of a call on the default

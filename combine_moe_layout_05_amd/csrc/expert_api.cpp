@@ -13,17 +13,20 @@
 namespace moe {
 
 // Where the form that streams the weights (16-row tiles, the sum split over a
-// workgroup's wavefronts) is the faster one. Measured on MI355X:
-//   - bf16, up to 64 rows: one expert of 4096 -> 2 x 2048 gated 19.6 us at 32
-//     rows, the tiled form 24.8 us from 65 to 256; at 128 rows 35.2 against
-//     24.4 us, so it ends there.
-//   - 4 bits, up to 8 rows per expert: 128 experts of 4096 -> 2 x 2048 at 1024
-//     rows 180 against 197 us, at 2048 rows 268 against 203 us.
+// workgroup's wavefronts) is the faster one. Measured on MI355X with other
+// weights in every call, so that they come from HBM, streamed against tiled:
+//   - bf16, up to 64 rows: one expert of 4096 -> 2 x 2048 gated 19.7 and 31.4 us
+//     at 32 rows, 19.7 and 32.9 at 64, 33.9 and 30.2 at 65, 64.0 and 31.9 at 256;
+//     one of 2048 -> 7168 13.3 and 18.1 at 32 rows, 19.9 and 19.1 at 64, 26.8 and
+//     17.8 at 65. With more experts they come near, on either side: at 64 rows 64
+//     of 7168 -> 2 x 2048 623 and 626, 8 of 4096 -> 2 x 2048 58.6 and 51.1.
+//   - 4 bits, up to 8 rows per expert: 128 experts of 4096 -> 2 x 2048 182 and 199
+//     us at 1024 rows, 203 and 202 at 2048.
 //   - 4 bits, while its workgroups are few (the tiled form then leaves CUs
-//     idle): one expert of 4096 -> 2 x 2048 at 256 rows (1024 workgroups) 18.0
-//     against 39.5 us, at 512 rows (2048) 39.3 against 40.6 us; 8 experts of
-//     4096 -> 2 x 1408 at 512 rows (1408) 38.2 against 40.2, at 1024 rows (2816)
-//     59.7 against 41.6 us.
+//     idle): one expert of 4096 -> 2 x 2048 20.3 and 40.2 us at 256 rows (1024
+//     workgroups), 39.0 and 40.6 at 512 (2048); 8 of 4096 -> 2 x 1408 31.5 and 42.9
+//     at 512 (1408), 48.6 and 39.9 at 768 (2112); one of 2048 -> 7168 21.2 and 23.0
+//     at 256 (1792), 38.2 and 23.8 at 512 (3584).
 bool expert_streams_bf16(int64_t max_rows) { return max_rows <= 64; }
 bool expert_streams_mxfp4(int32_t E, int64_t max_rows, int64_t positions) {
     if (max_rows <= int64_t(8) * E) return true;

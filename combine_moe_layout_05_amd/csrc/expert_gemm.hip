@@ -21,15 +21,19 @@
 // half the registers, the fragments of two half steps most of the rest.
 //
 // Measured on MI355X (a large library product reaches 1438 TFLOP/s, a large
-// copy 4.9 TB/s). 128 experts of 512 rows, 4096 -> 2 x 2048: gated 2.33 ms with
-// the fp32 projections written out for the backward (0.94 PFLOP/s and 1 GB of
-// them), 2.10 ms without, the second projection 1.10 ms (1.00 PFLOP/s), its gate
-// gradient 1.32 ms (0.83), the input gradient 2.09 ms (1.05). One expert of
+// copy 4.9 TB/s), two cards. 128 experts, 4096 -> 2 x 2048, 65536 rows routed at
+// random (512 per expert on average; some 60 experts end in a tile of at most 64
+// rows, 318 row tiles where the rows fill 256) and, behind the bar, exactly 512
+// rows per expert: gated 2.27 to 2.35 | 2.06 to 2.12 ms with the fp32 projections
+// written out for the backward (0.94 to 0.97 PFLOP/s and 1 GB of them), 2.10 to
+// 2.19 | 1.87 to 1.94 without, the second projection 1.11 to 1.15 | 1.00 to 1.04
+// (0.96 to 0.99 PFLOP/s), its gate gradient 1.33 to 1.39 | 1.19 to 1.21 (0.79 to
+// 0.83), the input gradient 2.08 to 2.24 | 1.89 to 1.97 (0.98 to 1.06). One expert of
 // 65536 rows: 1.27 to 1.34 PFLOP/s. 256 experts of 128 rows on average, skewed,
-// 7168 -> 2 x 2048: 3.23 ms for 15.6 GB (4.8 TB/s); of 2 rows: 1.37 ms for 8.0 GB
-// (5.8 TB/s). LDS bank conflicts count 0; at 512 rows per expert the matrix
-// cores are busy 59 % of the cycles at a clock that power holds near 1.7 GHz,
-// while 10 GB pass behind the L2 caches in 2.1 ms.
+// 7168 -> 2 x 2048: 3.28 to 3.37 ms for 15.6 GB (4.7 TB/s); of 2 rows: 1.36 to 1.38
+// ms for 8.0 GB (5.8 TB/s). LDS bank conflicts count 0; in the routed case the
+// matrix cores are busy 58 % of the cycles at a clock that power holds near 1.7
+// GHz, while 10 GB pass behind the L2 caches in 2.1 ms.
 #include "expert_kernels.h"
 #include "expert_mma.h"
 
@@ -172,6 +176,11 @@ void expert_gemm_kernel(const char* __restrict__ rows, const char* __restrict__ 
             // Two 16-feature blocks at a time: every lane ends up with eight
             // neighbouring features, which begin `at` features into the pair.
             const int at = (g & 1) * 16 + (g >> 1) * 8;
+            // Each result is rounded to bf16 here, once: h and the gradient of [g | u]
+            // are operands of the matrix-core products that follow, which take
+            // bf16; with more bits each would be two operands, at twice the products.
+            // [g | u], which only the epilogue of the gate gradient reads, is kept in
+            // fp32.
             if constexpr (OP == ExpertOp::kGated) {
                 static_assert(kBlkF == 4, "a pair of gate blocks, then their up blocks");
                 const int32_t f = f0 + wf * 32;

@@ -10,9 +10,10 @@
 //
 // Bound: the weights' bytes below some 100 rows per expert, then the matrix
 // cores. Measured on MI355X at 256 experts of 128 rows on average, skewed, 7168
-// -> 2 x 2048: 1.88 ms, 1.02 PFLOP/s, the matrix cores busy 67 % of the cycles,
-// LDS bank conflicts 0. Chunks of 16 to 128 tile numbers instead of 8 read up to
-// 15 % less behind the L2 caches (11.7 GB at 8) in the same time (1 %).
+// -> 2 x 2048: 1.80 to 1.88 ms, 1.02 to 1.07 PFLOP/s, the matrix cores busy 66 % of
+// the cycles, LDS bank conflicts 0; 2048 -> 7168 0.98 ms. Chunks of 16 to 128 tile
+// numbers instead of 8 read up to 15 % less behind the L2 caches (11.7 GB at 8) in
+// the same time (1 %).
 #include "expert_kernels.h"
 #include "expert_mma.h"
 #include "expert_mxfp4.h"

@@ -2,19 +2,22 @@
 // expert weights: with rows r of expert e, out[r] = x[r] W^T, or act(g) * u of
 // the two projections g and u.
 //
-// Bound: the bytes of the weights, each used for at most 16 rows. They go
-// straight from HBM into the registers the matrix cores read, never through
-// LDS: a workgroup takes 64 features, its wavefronts every n-th step of the sum
-// (consecutive weights, so that a workgroup's reads are one stream), and the
-// wavefronts' sums are joined in LDS in wavefront order. Splitting the sum gives
-// one token enough workgroups and loads in flight: 8 experts' 4096 features are
-// 512 workgroups of 8 wavefronts.
+// Bound: the bytes of the weights, each used for at most 16 rows; a segment's
+// weights are read once per 16 of its rows. They go straight into the registers
+// the matrix cores read, never through LDS: a workgroup takes 64 features, its
+// wavefronts every n-th step of the sum (consecutive weights, so that a
+// workgroup's reads are one stream), and the wavefronts' sums are joined in LDS
+// in wavefront order. Splitting the sum gives one token enough workgroups and
+// loads in flight: 8 experts' 4096 features are 512 workgroups of 8 wavefronts.
 //
-// Measured on MI355X, one token of 8 experts. bf16, 7168 -> 2 x 2048: 78.6 us for
-// 470 MB (6.0 TB/s; a large copy moves 4.9, an in-place update 6.0). 4 bits, 7168
-// -> 2 x 2048: 21.6 us for 125 MB (5.8 TB/s); 2048 -> 7168: 14.4 us for 63 MB
-// (4.4 TB/s), where a wavefront has four steps and start and end weigh most. 64
-// tokens over 256 experts at 4 bits: 353 us for 2.13 GB (6.0 TB/s).
+// Measured on MI355X, one token of 8 experts, other experts in every call, so that
+// the weights come from HBM (a large copy moves 4.9 TB/s, an in-place update 6.0).
+// bf16, 7168 -> 2 x 2048: 79.1 us for 470 MB (5.9 TB/s); 2048 -> 7168: 47.5 us for
+// 235 MB (4.9). 4 bits, 7168 -> 2 x 2048: 22.4 us for 125 MB (5.6 TB/s); 2048 ->
+// 7168: 14.2 us for 62 MB (4.4), where a wavefront has four steps and start and
+// end weigh most. The same experts again, out of the memory-side cache: 78.7, 38.4,
+// 20.4 and 12.7 us. 64 tokens over 256 experts at 4 bits: 330 to 350 us for 2.13 GB
+// (6.1 to 6.5 TB/s).
 #include "expert_kernels.h"
 #include "expert_mma.h"
 #include "expert_mxfp4.h"
@@ -25,9 +28,10 @@ namespace moe {
 namespace {
 
 // Wavefronts of a workgroup, splitting the sum. 4-bit weights leave each little
-// to read, and more, smaller workgroups start together: 15.5 against 21.2 us
-// with 8 at one token of 2048 -> 7168 (8 experts), 22.8 against 24.2 us at 7168
-// -> 2 x 2048; bf16 weights 83.6 against 80.2 us with 8 there.
+// to read, and more, smaller workgroups start together: 14.2 against 16.5 us
+// with 8 at one token of 2048 -> 7168 (8 experts, weights from HBM), 22.4 against
+// 22.6 us at 7168 -> 2 x 2048. With bf16 weights 4 or 8 make no difference there
+// (79.1 with 8, 78.9 with 4; 2048 -> 7168 47.5 and 46.7 us).
 constexpr int waves_of(bool mxfp4) { return mxfp4 ? 4 : 8; }
 constexpr int kBlocks = 4;              // 16-feature blocks per workgroup
 constexpr int kRows = 16;               // rows per workgroup

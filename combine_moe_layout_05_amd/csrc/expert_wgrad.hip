@@ -17,10 +17,17 @@
 // 2048 378 against 366); workgroups that stay and load the next tile early, 3.5.
 //
 // Measured on MI355X (a large library product reaches 1438 TFLOP/s), behind other
-// products as in a training step: 128 experts of 512 rows, 4096 x 2048 1.31 ms
-// (0.84 PFLOP/s), 4096 x 4096 2.58 ms (0.85); of 128 rows, 2048 x 1408 241 us,
-// 2816 x 2048 420 us (3.9 TB/s). One expert of 65536 rows: 1.23 to 1.31 PFLOP/s.
-// LDS bank conflicts count 0.
+// products as in a training step: 128 experts of 512 rows on average, routed at
+// random, 4096 x 2048 1.31 to 1.32 ms (0.83 PFLOP/s), 4096 x 4096 2.58 to 2.60 ms
+// (0.85); of 128 rows, 2048 x 1408 241 to 259 us, 2816 x 2048 420 to 484 us. Exactly
+// 512 rows per expert, by themselves: 1.24 and 2.51 ms where routed rows take 1.31
+// and 2.62. One expert of 65536 rows: 1.23 to 1.31 PFLOP/s. LDS bank conflicts
+// count 0.
+//
+// fp32 gradients are twice the bytes: 4096 x 4096 routed 3.29 ms against 2.70 in
+// bf16, 2816 x 2048 (128 rows on average) 0.51 against 0.41 ms. Adding reads the
+// gradient as well, and its lanes write pieces of 4 values where the other forms
+// write whole rows: 4.2 ms (bf16) and 5.1 ms (fp32), 1.07 and 1.33 ms.
 #include "expert_kernels.h"
 #include "expert_mma.h"
 

@@ -10,7 +10,8 @@ The calls take the expert-major rows dispatch() returns and the offsets of
 layout(), both on the device; nothing is read back, so they can be captured in
 a graph. Where a call allocates its output, the rows of no segment (from
 offsets[E] on, and before offsets[0], which is 0 in a layout) are zero; an
-output the caller passes keeps what it held there.
+output the caller passes keeps what it held there. None of them records a
+gradient or follows a tangent; expert_ffn is the differentiable block.
 """
 from __future__ import annotations
 
@@ -129,7 +130,15 @@ def gated_grouped_gemm(x_expert: torch.Tensor, weights: Union[torch.Tensor, Mxfp
 def grouped_gemm_forward(x_expert: torch.Tensor, weights: torch.Tensor, offsets: torch.Tensor,
                          out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Second half of the expert block (moe_grouped_gemm_forward): out[r] =
-    x[r] @ W[e].T with bf16 [E, n_out, k_in] weights."""
+    x[r] @ W[e].T with bf16 [E, n_out, k_in] weights.
+
+    The same product as grouped_gemm's, summed in another order, and the faster
+    one for row-major weights (MI355X, against grouped_gemm with row-major and
+    with tiled weights: 256 experts of 7168 -> 4096 at one token x 8 79 us
+    against 80 and 186, at 4096 tokens 3.34 ms against 4.03 and 3.23, at 32768
+    13.8 ms against 21.2 and 14.3; 128 of 2048 -> 4096 at 8192 tokens 1.16 ms
+    against 1.66 and 1.22). grouped_gemm is for weights in their tiled or 4-bit
+    form, and where its results have to stay what they were."""
     dev = x_expert.device
     E, n_out, k_in = _weights("weights", weights, dev)
     _rows("x_expert", x_expert, k_in, dev)

@@ -187,7 +187,9 @@ def grouped_gemm(x_expert: torch.Tensor, weights, offsets: torch.Tensor,
     TiledExpertWeights of them (same results, faster), or 4-bit weights as
     Mxfp4ExpertWeights (moe_grouped_gemm_mxfp4; the rows of no segment of an
     output it allocates are zero); offsets int32 [E+1]; out bf16 [R, n_out]
-    (allocated with torch.empty if None)."""
+    (allocated with torch.empty if None). For row-major weights
+    grouped_gemm_forward computes the same product faster, in another order of
+    the sums."""
     if isinstance(weights, Mxfp4ExpertWeights):
         return _grouped_gemm_mxfp4(x_expert, weights, offsets, out, int(row_tile))
     dev = x_expert.device

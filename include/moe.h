@@ -453,7 +453,8 @@ int moe_gated_grouped_gemm(const void *d_x_expert, const void *d_weights,
 
 /* Second half of the block: out[r] = x[r] W[e]^T with row-major weights
  * [num_experts][n_out][k_in], as moe_grouped_gemm computes it (another order
- * of the sums), with the flags of this family. */
+ * of the sums), with the flags of this family. It is the faster of the two for
+ * row-major weights; moe_grouped_gemm also takes tiled ones. */
 int moe_grouped_gemm_forward(const void *d_x_expert, const void *d_weights,
                              const int32_t *d_offsets, int32_t num_experts, int64_t max_rows,
                              int32_t k_in, int32_t n_out, void *d_out, int32_t flags,
