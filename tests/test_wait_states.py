@@ -68,7 +68,7 @@ def _violations(code):
             seen.add((p, states))
             if op.startswith("v_"):
                 # Destinations: the first operand, with a carry the second.
-                wide = "_co_" in op or "div_scale" in op
+                wide = any(k in op for k in ("_co_", "div_scale", "mad_u64", "mad_i64"))
                 dests = _registers(",".join(args.split(",")[:2 if wide else 1]))
                 if dests & regs:
                     return True
@@ -94,6 +94,17 @@ def test_the_check_sees_a_violation():
             "\tglobal_load_dword v2, v0, s[8:9] // 000000001008: DC508000 02080000\n")
     assert _violations(_functions(text.format(3))["k"])
     assert not _violations(_functions(text.format(4))["k"])
+
+
+def test_the_check_follows_jumps_and_carries():
+    text = ("0000000000001000 <k>:\n"
+            "\tv_mad_u64_u32 v[2:3], s[8:9], v4, v5, 0 // 000000001000: D1E80802 02020904\n"
+            "\ts_cbranch_scc1 2                // 000000001008: BF850002 <k+0x14>\n"
+            "\ts_nop 7                         // 00000000100C: BF800007\n"
+            "\ts_endpgm                        // 000000001010: BF810000\n"
+            "\tglobal_load_dword v2, v0, s[{}] // 000000001014: DC508000 02080000\n")
+    assert _violations(_functions(text.format("8:9"))["k"])
+    assert not _violations(_functions(text.format("6:7"))["k"])
 
 
 @pytest.mark.skipif(not os.path.exists(OBJDUMP), reason="llvm-objdump not available")
