@@ -18,3 +18,4 @@ from .experts import (  # noqa: F401
     grouped_gemm_backward_weight, grouped_gemm_forward, mxfp4_expert_weights,
 )
 from .autograd import MoeTokenDispatcher, expert_ffn  # noqa: F401
+from .router import Routing, route_topk, route_topk_backward  # noqa: F401

@@ -36,13 +36,17 @@ MOE_GEMM_ZERO_OUTSIDE = MOE_GEMM_ZERO_TAIL | MOE_GEMM_ZERO_HEAD
 MOE_MAX_GEMM_WIDTH = 1 << 22
 MOE_ACT_SILU = 0
 MOE_ACT_GELU_TANH = 1
+MOE_MAX_ROUTE_GROUPS = 64
+MOE_SCORE_SOFTMAX = 0
+MOE_SCORE_SIGMOID = 1
+MOE_ROUTE_RENORMALIZE = 1
 
 MOE_MAX_EXPERTS = 1024
 MOE_MAX_TOPK = 16
 MOE_WORKSPACE_ALIGN = 256
 
 # Entry points declared in include/moe.h: name -> (restype, argtypes).
-_i32, _i64, _vp, _int = C.c_int32, C.c_int64, C.c_void_p, C.c_int
+_i32, _i64, _vp, _int, _f32 = C.c_int32, C.c_int64, C.c_void_p, C.c_int, C.c_float
 
 
 class MoeConfig(C.Structure):
@@ -99,6 +103,10 @@ SIGNATURES = {
     "moe_grouped_gemm_mxfp4": (_int, [_vp, _vp, _vp, _i32, _i64, _i32, _i32, _vp, _i32, _vp]),
     "moe_gated_grouped_gemm_mxfp4": (_int, [_vp, _vp, _vp, _i32, _i64, _i32, _i32, _i32, _vp,
                                             _i32, _vp]),
+    "moe_route_topk": (_int, [_vp, _i32, _vp, _i32, _i32, _i32, _i32, _i32, _f32, _i32, _i32, _vp,
+                              _vp, _vp]),
+    "moe_route_topk_backward": (_int, [_vp, _i32, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _f32,
+                                       _vp, _vp]),
     "moe_set_tuning": (_int, [_vp, C.POINTER(MoeTuning)]),
     "moe_get_tuning": (_int, [_vp, C.POINTER(MoeTuning)]),
     "moe_ceil_div": (_i64, [_i64, _i64]),

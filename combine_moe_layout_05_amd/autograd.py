@@ -189,7 +189,7 @@ class _ExpertFfn(torch.autograd.Function):
 _ON_DEFAULT_STREAM = "combine_moe_layout.default_stream"
 
 
-def _watch_accumulators(node, stream: int) -> None:
+def _watch_accumulators(node, stream: int, name: str = "expert_ffn") -> None:
     """Looks at the gradient accumulators of the leaves that a call's node
     leads to. The engine runs an accumulator on the stream it was made on, and
     it lives as long as any graph that reaches it. One made on the default
@@ -202,7 +202,7 @@ def _watch_accumulators(node, stream: int) -> None:
         on_default = fn.metadata.setdefault(_ON_DEFAULT_STREAM, stream == 0 and not capturing)
         if capturing and on_default:
             raise RuntimeError(
-                "expert_ffn cannot be captured while the output of an earlier call on the default "
+                f"{name} cannot be captured while the output of an earlier call on the default "
                 "stream that reaches the same leaf tensors is alive: its gradient accumulators "
                 "belong to that stream. Delete that output first, or run the calls before the "
                 "capture on a side stream.")

@@ -5,8 +5,8 @@
 
 #include <climits>
 #include <cstdint>
-#include <initializer_list>
 
+#include "api_checks.h"
 #include "expert_kernels.h"
 #include "moe.h"
 
@@ -39,58 +39,24 @@ bool expert_streams_mxfp4(int32_t E, int64_t max_rows, int64_t positions) {
 
 namespace {
 
-bool misaligned(const void* p, uintptr_t a) {
-    return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0;
-}
-
-bool width_ok(int32_t n, int32_t multiple) {
-    return n >= 8 && n <= MOE_MAX_GEMM_WIDTH && n % multiple == 0;
-}
-
-bool experts_ok(int32_t E) { return E >= 1 && E <= MOE_MAX_EXPERTS; }
-
-bool activation_ok(int32_t a) { return a == MOE_ACT_SILU || a == MOE_ACT_GELU_TANH; }
-
-// Whether two buffers share a byte. The sizes stay below 2^56 bytes.
-bool overlap(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
-    if (a_bytes == 0 || b_bytes == 0) return false;
-    const uintptr_t pa = reinterpret_cast<uintptr_t>(a), pb = reinterpret_cast<uintptr_t>(b);
-    return pa < pb ? pb - pa < static_cast<uintptr_t>(a_bytes)
-                   : pa - pb < static_cast<uintptr_t>(b_bytes);
-}
-
-// A buffer a call reads.
-struct Input {
-    const void* p;
-    int64_t bytes;
-};
-Input rows_of(const void* p, int64_t rows, int64_t width, int64_t elem = 2) {
-    return {p, rows * width * elem};
-}
-Input weights_of(const void* p, int64_t E, int64_t n, int64_t k) { return {p, E * n * k * 2}; }
-Input offsets_of(const int32_t* p, int32_t E) { return {p, (int64_t(E) + 1) * 4}; }
-
-// An output that shares bytes with none of the inputs: other workgroups still
-// read those when it is written.
-bool apart(const void* out, int64_t bytes, std::initializer_list<Input> inputs) {
-    for (const Input& in : inputs)
-        if (overlap(out, bytes, in.p, in.bytes)) return false;
-    return true;
-}
+using moe::activation_ok;
+using moe::apart;
+using moe::experts_ok;
+using moe::Input;
+using moe::kZeroFlags;
+using moe::misaligned;
+using moe::offsets_of;
+using moe::rows_of;
+using moe::status_of;
+using moe::weights_of;
+using moe::width_ok;
+using moe::zero_of;
 
 // bf16 buffers every call of the family needs, with its offsets.
 bool buffers_ok(const void* a, const void* b, const void* c, const int32_t* offsets) {
     return a && b && c && offsets && !misaligned(a, 16) && !misaligned(b, 16) &&
            !misaligned(c, 16) && !misaligned(offsets, 4);
 }
-
-constexpr int32_t kZeroFlags = MOE_GEMM_ZERO_TAIL | MOE_GEMM_ZERO_HEAD;
-int32_t zero_of(int32_t flags) {
-    return ((flags & MOE_GEMM_ZERO_TAIL) ? moe::kZeroTail : 0) |
-           ((flags & MOE_GEMM_ZERO_HEAD) ? moe::kZeroHead : 0);
-}
-
-int status_of(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_ERR_HIP; }
 
 int run_gemm(moe::ExpertOp op, const void* rows, const void* w, const int32_t* offsets, int32_t E,
              int64_t max_rows, int32_t red, int32_t feats, int32_t activation, void* out,

@@ -523,6 +523,50 @@ int moe_gated_grouped_gemm_mxfp4(const void *d_x_expert, const void *d_packed,
                                  int64_t max_rows, int32_t k_in, int32_t n_hidden,
                                  int32_t activation, void *d_h, int32_t flags, void *stream);
 
+/* ---- Router ---------------------------------------------------------------
+ * The K experts of every token and their scores from the router's logits: the
+ * ids and scores that moe_layout, moe_dispatch and moe_combine take. An expert
+ * takes part in a token's choice unless its logit l is NaN or -inf. With
+ *   MOE_SCORE_SOFTMAX  p = exp(l) / sum of exp(l) over the experts taking part
+ *   MOE_SCORE_SIGMOID  p = 1 / (1 + exp(-l))
+ * the K experts with the largest v are chosen, in descending order, equal ones
+ * by ascending index. v is l, where p has the same order; with the sigmoid and a
+ * bias or groups it is p + bias, computed in 64 bits (an expert whose v is NaN or
+ * -inf is not chosen). The bias decides who is chosen and does not enter the
+ * scores. With num_groups > 1 the experts form groups of E / num_groups
+ * consecutive ones; only the topk_groups groups with the largest value (softmax:
+ * their largest v; sigmoid: the sum of their two largest v, of one where only one
+ * takes part; equal ones by index) can be chosen from. A slot for which no expert
+ * is left has id -1 and score 0.
+ *   scores = scale * p, with MOE_ROUTE_RENORMALIZE scale * p / (sum of the chosen
+ *   p), 0 where that sum is 0. Scores and sums are fp32.
+ *   d_logits  [T][E] of dtype (MOE_F32 or MOE_BF16), aligned to its elements
+ *   d_bias    float32 [E] or NULL (NULL for the softmax)
+ *   d_ids     int32 [T][K], d_scores float32 [T][K]
+ *   K         1 .. min(MOE_MAX_TOPK, E / num_groups * topk_groups)
+ *   num_groups  divides E, at most MOE_MAX_ROUTE_GROUPS; 1 <= topk_groups <=
+ *             num_groups; scale is finite; 0 <= T < 2^26 (0 enqueues nothing)
+ * No context and no workspace; an output shares no byte with an input or the
+ * other output. Violations: MOE_ERR_INVALID_ARG. */
+#define MOE_MAX_ROUTE_GROUPS  64
+#define MOE_SCORE_SOFTMAX     0
+#define MOE_SCORE_SIGMOID     1
+#define MOE_ROUTE_RENORMALIZE 1  /* divide the chosen experts' scores by their sum */
+
+int moe_route_topk(const void *d_logits, int32_t dtype, const float *d_bias, int32_t T, int32_t E,
+                   int32_t K, int32_t score, int32_t flags, float scale, int32_t num_groups,
+                   int32_t topk_groups, int32_t *d_ids, float *d_scores, void *stream);
+
+/* Gradient of the scores with respect to the logits, the ids being constants:
+ * d_grad_logits [T][E] of the logits' type, every element written, from the ids
+ * moe_route_topk wrote and d_grad_scores float32 [T][K]. The logits of experts
+ * that take no part, and the gradients of slots without an expert, are not read
+ * into any sum. score, flags and scale as in the forward call. */
+int moe_route_topk_backward(const void *d_logits, int32_t dtype, const int32_t *d_ids,
+                            const float *d_grad_scores, int32_t T, int32_t E, int32_t K,
+                            int32_t score, int32_t flags, float scale, void *d_grad_logits,
+                            void *stream);
+
 /* Launch shape tuning (optional). moe_create picks every default from the
  * context's sizes (measured on MI355X); moe_get_tuning reports them. Each
  * token row is split into `segments` wavefront work items (1..16) and

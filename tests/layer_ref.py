@@ -1,0 +1,108 @@
+"""Plain 64-bit forms of the router on the CPU, with bounds of the rounding
+errors of an fp32 evaluation.
+
+Bounds (u = 2^-24, fp32's half step). A score is an exponential of an exact or
+once rounded difference (off by (|difference| + 2) u relative), a sum of at most
+E of them in fp32 (gamma(E) and the terms' own errors), a division and a
+product with the scale: in all at most (2 |d| + 2 E + 16) u relative, |d| the
+largest difference of a logit to the largest one, or the largest |logit| for
+the sigmoid."""
+import math
+
+import torch
+
+U = 2.0 ** -24
+B = 2.0 ** -8
+
+
+def select(logits, K, score, bias=None, groups=1, kept=1):
+    """ids [T, K] (int64, -1 for none), one expert after the other."""
+    T, E = logits.shape
+    out = torch.full((T, K), -1)
+    size = E // groups
+    for t in range(T):
+        l = [float(x) for x in logits[t].double()]
+        part = [not math.isnan(x) and x != -math.inf for x in l]
+        if score == "sigmoid" and (bias is not None or groups > 1):
+            v = torch.sigmoid(logits[t].double())
+            if bias is not None:
+                v = v + bias.double()
+            v = v.tolist()
+        else:
+            v = l
+        ok = [e for e in range(E) if part[e] and not math.isnan(v[e]) and v[e] != -math.inf]
+        if groups > 1:
+            value = {}
+            for g in range(groups):
+                mine = sorted((v[e] for e in ok if e // size == g), reverse=True)
+                if mine:
+                    value[g] = sum(mine[:2]) if score == "sigmoid" else mine[0]
+            best = sorted(value, key=lambda g: (-value[g], g))[:kept]
+            ok = [e for e in ok if e // size in best]
+        for k, e in enumerate(sorted(ok, key=lambda e: (-v[e], e))[:K]):
+            out[t, k] = e
+    return out
+
+
+def probabilities(logits, score):
+    """p [T, E] in 64 bits, 0 where an expert takes no part, and the bound."""
+    l = logits.double()
+    part = ~torch.isnan(l) & (l != -math.inf)
+    if score == "sigmoid":
+        return torch.where(part, torch.sigmoid(l), torch.zeros_like(l)), part
+    l = torch.where(part, l, torch.full_like(l, -math.inf))
+    m = l.amax(dim=1, keepdim=True)
+    e = torch.where(part, torch.exp(l - torch.where(m == -math.inf, torch.zeros_like(m), m)),
+                    torch.zeros_like(l))
+    return e / e.sum(dim=1, keepdim=True).clamp(min=1e-300), part
+
+
+def scores(logits, ids, score, renormalize, scale):
+    """The scores of the ids in 64 bits and the relative error bound."""
+    p, part = probabilities(logits, score)
+    there = ids >= 0
+    q = torch.where(there, torch.gather(p, 1, ids.clamp(min=0)), torch.zeros(()).double())
+    if renormalize:
+        q = q / q.sum(dim=1, keepdim=True).clamp(min=1e-300)
+    return q * scale, bound(logits, part, score)
+
+
+def bound(logits, part, score):
+    l = logits.double()
+    l = l[part & torch.isfinite(l)]
+    if l.numel() == 0:
+        return 0.0
+    d = float(l.abs().max()) if score == "sigmoid" else float(l.max() - l.min())
+    return (2 * d + 2 * logits.shape[1] + 16) * U
+
+
+def gradient(logits, ids, grad, score, renormalize, scale):
+    """The logits' gradient in 64 bits by the formula, and a bound of the
+    absolute error before its last rounding: every factor of a term is off by
+    the scores' relative bound, the sum over K terms by gamma(K)."""
+    p, part = probabilities(logits, score)
+    rel = 4 * (bound(logits, part, score) + 32 * U)
+    there = ids >= 0
+    at = ids.clamp(min=0)
+    zero = torch.zeros((), dtype=torch.float64)
+    g = torch.where(there, grad.double() * scale, zero)
+    pk = torch.where(there, torch.gather(p, 1, at), zero)
+    total = pk.sum(dim=1, keepdim=True).clamp(min=1e-300)
+    q = pk / total if renormalize else pk
+    s = (g * q).sum(dim=1, keepdim=True)
+    s_mag = (g * q).abs().sum(dim=1, keepdim=True)
+    out, mag = torch.zeros_like(p), torch.zeros_like(p)
+    if score == "softmax":
+        if not renormalize:
+            out, mag = -p * s, p * s_mag
+            d, dm = q * g, q * g.abs()
+        else:
+            d, dm = q * (g - s), q * (g.abs() + s_mag)
+    else:
+        slope = pk * torch.sigmoid(-torch.gather(torch.nan_to_num(logits.double()), 1, at))
+        if renormalize:
+            d, dm = (g - s) / total * slope, (g.abs() + s_mag) / total * slope
+        else:
+            d, dm = g * slope, g.abs() * slope
+    d, dm = torch.where(there, d, zero), torch.where(there, dm, zero)
+    return out.scatter_add(1, at, d), rel * mag.scatter_add(1, at, dm)

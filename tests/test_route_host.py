@@ -1,0 +1,127 @@
+"""CPU tests of the router's host side: every refusal of the C entry points
+and of the Python binding happens before anything is enqueued."""
+import math
+
+import pytest
+import torch
+
+import combine_moe_layout_05_amd as moe
+from combine_moe_layout_05_amd import _lib as L
+
+P = 1 << 56                # a device address that is never dereferenced; buffers lie P apart
+OK, BAD = L.MOE_OK, L.MOE_ERR_INVALID_ARG
+
+FORWARD = dict(logits=P, dtype=L.MOE_F32, bias=None, T=0, E=64, K=8, score=L.MOE_SCORE_SIGMOID,
+               flags=1, scale=2.5, groups=8, kept=4, ids=2 * P, scores=3 * P, stream=None)
+BACKWARD = dict(logits=P, dtype=L.MOE_BF16, ids=2 * P, grad=3 * P, T=0, E=64, K=8,
+                score=L.MOE_SCORE_SOFTMAX, flags=0, scale=1.0, out=4 * P, stream=None)
+
+
+@pytest.fixture(scope="module")
+def lib():
+    return L.load()
+
+
+def test_sizes(lib):
+    fn = lib.moe_route_topk
+    assert fn(*FORWARD.values()) == OK
+    for key, value in [("dtype", 2), ("T", -1), ("T", 1 << 26), ("E", 0), ("E", 1025), ("K", 0),
+                       ("K", 17), ("E", 60), ("K", 33), ("score", 2), ("flags", 2),
+                       ("scale", math.inf), ("scale", math.nan), ("groups", 0), ("groups", 128),
+                       ("kept", 0), ("kept", 9)]:
+        assert fn(*dict(FORWARD, **{key: value}).values()) == BAD, (key, value)
+    # a bias goes with the sigmoid
+    assert fn(*dict(FORWARD, bias=4 * P).values()) == OK
+    assert fn(*dict(FORWARD, bias=4 * P, score=L.MOE_SCORE_SOFTMAX).values()) == BAD
+    # no more experts than the kept groups hold
+    assert fn(*dict(FORWARD, K=8, kept=1).values()) == OK
+    assert fn(*dict(FORWARD, K=9, kept=1).values()) == BAD
+    fn = lib.moe_route_topk_backward
+    assert fn(*BACKWARD.values()) == OK
+    for key, value in [("dtype", 2), ("T", -1), ("T", 1 << 26), ("E", 0), ("E", 1025), ("K", 0),
+                       ("K", 17), ("score", 2), ("flags", 2), ("scale", math.inf)]:
+        assert fn(*dict(BACKWARD, **{key: value}).values()) == BAD, (key, value)
+
+
+def test_pointers(lib):
+    fn, args = lib.moe_route_topk, dict(FORWARD, T=4, bias=4 * P)
+    for key in ("logits", "ids", "scores"):
+        assert fn(*dict(args, **{key: None}).values()) == BAD, key
+    for key in ("logits", "bias", "ids", "scores"):
+        assert fn(*dict(args, **{key: args[key] + 2}).values()) == BAD, key
+    assert fn(*dict(args, logits=P + 1, dtype=L.MOE_BF16).values()) == BAD
+    # outputs over an input's last bytes or over each other
+    for at in (P, P + 4 * 64 * 4 - 4, 4 * P, 4 * P + 252):
+        assert fn(*dict(args, ids=at).values()) == BAD
+        assert fn(*dict(args, scores=at).values()) == BAD
+    assert fn(*dict(args, scores=2 * P + 124).values()) == BAD
+    fn, args = lib.moe_route_topk_backward, dict(BACKWARD, T=4)
+    for key in ("logits", "ids", "grad", "out"):
+        assert fn(*dict(args, **{key: None}).values()) == BAD, key
+        assert fn(*dict(args, **{key: args[key] + 1}).values()) == BAD, key
+    for at in (P, P + 4 * 64 * 2 - 2, 2 * P, 2 * P + 126, 3 * P, 3 * P - 2):
+        assert fn(*dict(args, out=at).values()) == BAD, at
+
+
+def test_binding_refusals():
+    l = torch.zeros(4, 16)
+    with pytest.raises(ValueError, match="must be on a GPU"):
+        moe.route_topk(l, 2)
+    with pytest.raises(TypeError, match="logits must be one of"):
+        moe.route_topk(l.half(), 2)
+    with pytest.raises(ValueError, match="must be on a GPU"):
+        moe.route_topk_backward(torch.zeros(4, 2), l, torch.zeros(4, 2, dtype=torch.int32))
+
+
+class _Cuda(torch.Tensor):
+    """A CPU tensor that says it is on a GPU: what the checks see."""
+    is_cuda = property(lambda self: True)
+
+
+@pytest.fixture
+def fake(monkeypatch):
+    from combine_moe_layout_05_amd import router
+    calls = []
+    monkeypatch.setattr(router, "_call", lambda *a: calls.append(a))
+    make = lambda *shape, dtype=torch.float32: torch.zeros(*shape, dtype=dtype).as_subclass(_Cuda)
+    return make, calls
+
+
+def test_binding_checks(fake):
+    make, calls = fake
+    l = make(4, 16)
+    assert moe.route_topk(l, 2).ids.shape == (4, 2) and len(calls) == 1
+    bad = [
+        (ValueError, "score must be one of", dict(score="top")),
+        (ValueError, "bias goes with", dict(bias=make(16))),
+        (ValueError, "bias must have 16", dict(score="sigmoid", bias=make(8))),
+        (TypeError, "bias must be", dict(score="sigmoid", bias=make(16, dtype=torch.bfloat16))),
+        (ValueError, "contiguous", dict(score="sigmoid", bias=make(32)[::2])),
+    ]
+    for error, match, more in bad:
+        with pytest.raises(error, match=match):
+            moe.route_topk(l, 2, **more)
+    for k in (0, 17):
+        with pytest.raises(ValueError, match="topk must be"):
+            moe.route_topk(l, k)
+    with pytest.raises(ValueError, match="contiguous"):
+        moe.route_topk(make(16, 4).t(), 2)
+    with pytest.raises(ValueError, match="contiguous"):
+        moe.route_topk(make(16), 2)
+    ids = make(4, 2, dtype=torch.int32)
+    with pytest.raises(ValueError, match="shapes"):
+        moe.route_topk_backward(make(4, 3), l, ids)
+    with pytest.raises(ValueError, match="shapes"):
+        moe.route_topk_backward(make(3, 2), l, make(3, 2, dtype=torch.int32))
+    with pytest.raises(TypeError, match="ids must be"):
+        moe.route_topk_backward(make(4, 2), l, ids.long())
+    assert len(calls) == 1
+
+
+def test_forward_mode_is_refused(fake):
+    make, calls = fake
+    with torch.autograd.forward_ad.dual_level():
+        l = torch.autograd.forward_ad.make_dual(make(4, 16), make(4, 16))
+        with pytest.raises(NotImplementedError, match="forward-mode"):
+            moe.route_topk(l, 2)
+    assert not calls
