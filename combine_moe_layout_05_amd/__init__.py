@@ -8,14 +8,15 @@ The compute lives in libmoe_layout.so (hand-written HIP kernels behind the C
 ABI of include/moe.h); this package is its thin Python binding.
 """
 from .moe import (  # noqa: F401
-    Dispatched, Layout, MoeDispatcher, Mxfp4ExpertWeights, TiledExpertWeights, ceil_div,
-    grouped_gemm, layout_noalloc, num_max_tokens_infer, num_max_tokens_pretrain, round_up4,
+    Dispatched, Layout, MoeDispatcher, Mxfp4ExpertWeights, Mxfp4Rows, TiledExpertWeights,
+    ceil_div, grouped_gemm, layout_noalloc, num_max_tokens_infer, num_max_tokens_pretrain, round_up4,
     tile_expert_weights, validate_num_max,
 )
 from ._lib import MoeError, load  # noqa: F401
 from .experts import (  # noqa: F401
-    gated_grouped_gemm, gated_grouped_gemm_backward, grouped_gemm_backward_input,
-    grouped_gemm_backward_weight, grouped_gemm_forward, mxfp4_expert_weights,
+    dequantize_mxfp4, gated_grouped_gemm, gated_grouped_gemm_backward,
+    grouped_gemm_backward_input, grouped_gemm_backward_weight, grouped_gemm_forward,
+    mxfp4_expert_weights, quantize_mxfp4,
 )
 from .autograd import MoeTokenDispatcher, expert_ffn  # noqa: F401
 from .router import Routing, route_topk, route_topk_backward  # noqa: F401

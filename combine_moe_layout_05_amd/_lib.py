@@ -103,6 +103,12 @@ SIGNATURES = {
     "moe_grouped_gemm_mxfp4": (_int, [_vp, _vp, _vp, _i32, _i64, _i32, _i32, _vp, _i32, _vp]),
     "moe_gated_grouped_gemm_mxfp4": (_int, [_vp, _vp, _vp, _i32, _i64, _i32, _i32, _i32, _vp,
                                             _i32, _vp]),
+    "moe_quantize_mxfp4": (_int, [_vp, _i32, _i64, _i32, _vp, _vp, _vp]),
+    "moe_dequantize_mxfp4": (_int, [_vp, _vp, _i32, _i64, _i32, _vp, _vp]),
+    "moe_grouped_gemm_mxfp4_rows": (_int, [_vp, _vp, _vp, _vp, _i32, _i64, _i32, _i32, _vp, _i32,
+                                           _vp]),
+    "moe_gated_grouped_gemm_mxfp4_rows": (_int, [_vp, _vp, _vp, _vp, _i32, _i64, _i32, _i32, _i32,
+                                                 _vp, _i32, _vp]),
     "moe_route_topk": (_int, [_vp, _i32, _vp, _i32, _i32, _i32, _i32, _i32, _f32, _i32, _i32, _vp,
                               _vp, _vp]),
     "moe_route_topk_backward": (_int, [_vp, _i32, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _f32,

@@ -1,0 +1,425 @@
+// Expert products of 4-bit rows with packed 4-bit weights on gfx950: out[r] =
+// x[r] W^T, or act(g) * u of the two projections, both operands e2m1 with a
+// power-of-two scale per 32 elements of the sum, which the matrix cores apply
+// themselves.
+//
+// A matrix-core product takes 128 elements of the sum; lane (i, g) of an operand
+// holds position i's 32 values of scale group g, and that group's scale. Rows lie
+// in memory that way (16 bytes per group). The packed weights, which the products
+// with bf16 rows share, hold 8 values of each of the four groups in a lane: a
+// transpose of 4 x 4 dwords between the lanes of a feature (four register swaps)
+// puts them in place.
+//
+// Elements past the end of a sum meet weights of zero, which the packing put
+// there; what is read in their place is finite, or makes the row NaN anyway.
+#include "expert_kernels.h"
+#include "expert_mma.h"
+#include "layer_kernels.h"
+
+namespace moe {
+namespace {
+
+typedef int32_t v8i __attribute__((ext_vector_type(8)));
+
+constexpr int kBlocks = 4;              // 16-feature blocks per wavefront
+
+// c + a b over 128 elements; the scales' bytes in the low 8 bits.
+__device__ __forceinline__ f32x4 multiply4(v4i a, int32_t sa, v4i b, int32_t sb, f32x4 c) {
+    const v8i wa = {a[0], a[1], a[2], a[3], 0, 0, 0, 0};
+    const v8i wb = {b[0], b[1], b[2], b[3], 0, 0, 0, 0};
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wa, wb, c, 4, 4, 0, sa, 0, sb);
+}
+
+// Packed weights to an operand: dword s of lane group g and dword g of lane
+// group s change places.
+__device__ __forceinline__ v4i by_groups(v4i q) {
+    const auto a = __builtin_amdgcn_permlane32_swap(q[0], q[2], false, false);
+    const auto b = __builtin_amdgcn_permlane32_swap(q[1], q[3], false, false);
+    const auto lo = __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false);
+    const auto hi = __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false);
+    return v4i{static_cast<int32_t>(lo[0]), static_cast<int32_t>(lo[1]),
+               static_cast<int32_t>(hi[0]), static_cast<int32_t>(hi[1])};
+}
+
+// Weights of a 16-feature block over 128 elements.
+struct Weights4 {
+    v4i q;
+    int32_t scale;                      // of this lane's feature and group
+};
+
+
+// ---- Many rows per expert -------------------------------------------------
+
+constexpr int kWaves = 4;               // along the features
+constexpr int kRowTile = 64;
+constexpr int kStages = 3;              // 256-element steps of rows in LDS
+constexpr int kXcdChunk = 8;
+constexpr int kBand = 8;
+
+template <bool GATED>
+__global__ __launch_bounds__(kWaves * 64, 2)
+void expert_mx4_kernel(const char* __restrict__ rows, const uint8_t* __restrict__ row_scales,
+                       const char* __restrict__ w, const uint8_t* __restrict__ scales,
+                       const int32_t* __restrict__ offsets, int32_t E, int32_t max_rows,
+                       int32_t red, int32_t feats, int32_t ftiles, int32_t act,
+                       char* __restrict__ out, int32_t zero) {
+    // Output features of a wavefront: half its blocks are up rows if gated.
+    constexpr int kFeats = kBlocks * 16 / (GATED ? 2 : 1);
+    typedef PackedOperand<kRowTile, kWaves> Rows;
+    __shared__ v4i lds[kStages * Rows::kChunks];
+    __shared__ int32_t info[4];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t number = expert_tile_number(kXcdChunk);
+    if (wave == 0) {
+        const ExpertTile t =
+            expert_find_tile(offsets, E, max_rows, kRowTile, ftiles, kBand, number);
+        if (lane == 0) {
+            info[0] = t.e;
+            info[1] = t.f;
+            info[2] = t.row0;
+            info[3] = t.rows;
+        }
+    }
+    __syncthreads();
+    const int32_t e = __builtin_amdgcn_readfirstlane(info[0]);
+    const int32_t ft = __builtin_amdgcn_readfirstlane(info[1]);
+    const int32_t row0 = __builtin_amdgcn_readfirstlane(info[2]);
+    const int32_t nrows = __builtin_amdgcn_readfirstlane(info[3]);
+    if (e < 0) {
+        if (zero)
+            expert_zero_rows(reinterpret_cast<v4i*>(out), offsets, zero, row0, max_rows, feats / 8,
+                             ft, int64_t(gridDim.x) - nrows);
+        return;
+    }
+    const int i = lane & 15, g = lane >> 4;
+    const int32_t f0 = (ft * kWaves + wave) * kFeats;
+    const int32_t steps = (red + 255) / 256;
+    const int32_t halves = (red + kMxfp4Step - 1) / kMxfp4Step;
+    const int32_t groups = red / 32;
+
+    // This wavefront's blocks; those past the matrix read its last one and are
+    // not stored.
+    const char* wb[kBlocks];
+    const uint8_t* sb[kBlocks];
+#pragma unroll
+    for (int b = 0; b < kBlocks; ++b) {
+        const int32_t nb = (feats + 15) / 16;
+        const bool up = GATED && b >= kBlocks / 2;
+        const int32_t ob = min(f0 / 16 + (GATED ? b % (kBlocks / 2) : b), nb - 1);
+        const int64_t blk = (int64_t(e) * (GATED ? 2 : 1) + (up ? 1 : 0)) * nb + ob;
+        wb[b] = w + blk * halves * 1024;
+        sb[b] = scales + blk * halves * 64;
+    }
+
+    auto run = [&](auto row_blocks) {
+        constexpr int NB = decltype(row_blocks)::value;
+        constexpr int kHalfLoads = 2 * kBlocks + NB;
+        Rows rt;
+        const int64_t pitch = red / 2;
+        const char* rbase = rows + int64_t(row0) * pitch;
+        const uint8_t* sbase = row_scales + int64_t(row0) * groups;
+        rt.init(wave, lane, 0, pitch, [&](int) { return rbase; },
+                [&](int p) { return min(p, nrows - 1); });
+        uint32_t srow[NB];
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+            srow[b] = static_cast<uint32_t>(min(b * 16 + i, nrows - 1)) * groups;
+        f32x4 acc[kBlocks][NB];
+#pragma unroll
+        for (int a = 0; a < kBlocks; ++a)
+#pragma unroll
+            for (int b = 0; b < NB; ++b) acc[a][b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+        // What a half step of 128 elements takes from memory to registers.
+        struct Half {
+            Weights4 w[kBlocks];
+            int32_t rs[NB];
+        };
+        auto issue_rows = [&](int32_t t, int stage) {
+            v4i* buf = lds + stage * Rows::kChunks;
+            const int left = min(red / 4 - t * 64, 64);         // in pairs of bytes
+            if (left == 64)
+                rt.issue(t, buf);
+            else
+                rt.issue_partial(t, left, lane, buf);
+        };
+        auto load = [&](int32_t half, Half& d) {
+            // A uniform address and a 32-bit offset per lane.
+            uint32_t qo = lane * 16, so = i * 4 + g;
+            reform(qo);
+            reform(so);
+            const int32_t at = min(half, halves - 1);
+            const uint32_t group = min(4 * half + g, groups - 1);
+#pragma unroll
+            for (int b = 0; b < kBlocks; ++b) {
+                d.w[b].q = *reinterpret_cast<const v4i*>(wb[b] + int64_t(at) * 1024 + qo);
+                d.w[b].scale = (sb[b] + int64_t(at) * 64)[so];
+            }
+#pragma unroll
+            for (int b = 0; b < NB; ++b) d.rs[b] = sbase[srow[b] + group];
+        };
+        auto order = [&](Half& d) {
+#pragma unroll
+            for (int a = 0; a < kBlocks; ++a) d.w[a].q = by_groups(d.w[a].q);
+        };
+        auto multiply = [&](const Half& d, const v4i* buf, int h) {
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                const v4i x = __builtin_bit_cast(v4i, rt.frag(buf, b, h));
+#pragma unroll
+                for (int a = 0; a < kBlocks; ++a)
+                    acc[a][b] = multiply4(d.w[a].q, d.w[a].scale, x, d.rs[b], acc[a][b]);
+            }
+        };
+
+        Half lo, hi;
+        issue_rows(0, 0);
+        if (steps > 1) issue_rows(1, 1);
+        load(0, lo);
+        load(1, hi);
+        wait_loads<2 * kHalfLoads>();
+        step_barrier();
+        int stage = 0;
+        for (int32_t t = 0; t < steps; ++t) {
+            const int after = stage + 1 == kStages ? 0 : stage + 1;
+            const int free = after + 1 == kStages ? 0 : after + 1;
+            const v4i* buf = lds + stage * Rows::kChunks;
+            order(lo);
+            __builtin_amdgcn_sched_barrier(0);
+            // Behind the first use of this step's registers: what waits for
+            // them must not wait for these loads.
+            if (t + 2 < steps) issue_rows(t + 2, free);
+            multiply(lo, buf, 0);
+            __builtin_amdgcn_sched_barrier(0);
+            load(2 * t + 2, lo);
+            __builtin_amdgcn_sched_barrier(0);
+            order(hi);
+            if (2 * t + 1 >= halves) {
+                // A sum that ends in the first half.
+#pragma unroll
+                for (int a = 0; a < kBlocks; ++a) hi.w[a].q = v4i{0, 0, 0, 0};
+            }
+            multiply(hi, buf, 1);
+            __builtin_amdgcn_sched_barrier(0);
+            load(2 * t + 3, hi);
+            __builtin_amdgcn_sched_barrier(0);
+            // The next step's rows have landed: this step's registers, which
+            // were waited for, were loaded behind them.
+            step_barrier();
+            stage = after;
+        }
+        wait_loads<0>();
+
+        const int at = (g & 1) * 16 + (g >> 1) * 8;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            const int r = b * 16 + i;
+            if (r >= nrows) continue;
+            char* orow = out + int64_t(row0 + r) * feats * 2;
+            if constexpr (GATED) {
+                v2i h[2];
+#pragma unroll
+                for (int a = 0; a < 2; ++a) {
+                    f32x4 v;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        v[k] = activate(act, acc[a][b][k]) * acc[a + 2][b][k];
+                    h[a] = pack_bf16x4(v);
+                }
+                const v4i v = pair_blocks(h[0], h[1]);
+                if (f0 + at < feats) *reinterpret_cast<v4i*>(orow + int64_t(f0 + at) * 2) = v;
+            } else {
+#pragma unroll
+                for (int a = 0; a < kBlocks; a += 2) {
+                    const int32_t f = f0 + a * 16 + at;
+                    const v4i v = pair_blocks(pack_bf16x4(acc[a][b]), pack_bf16x4(acc[a + 1][b]));
+                    if (f < feats) *reinterpret_cast<v4i*>(orow + int64_t(f) * 2) = v;
+                }
+            }
+        }
+    };
+    // Short last tiles cost what their rows need.
+    if (nrows <= 16)
+        run(std::integral_constant<int, 1>{});
+    else if (nrows <= 32)
+        run(std::integral_constant<int, 2>{});
+    else if (nrows <= 48)
+        run(std::integral_constant<int, 3>{});
+    else
+        run(std::integral_constant<int, 4>{});
+}
+
+// ---- Few rows per expert --------------------------------------------------
+//
+// As the streamed products with bf16 rows: 64 features and up to 16 rows per
+// workgroup, the sum split over its wavefronts and joined in LDS in wavefront
+// order. Rows are small enough to come straight from the caches.
+
+constexpr int kStreamWaves = 4;
+constexpr int kStreamRows = 16;
+constexpr int kStreamChunk = 32;
+
+template <bool GATED>
+__global__ __launch_bounds__(kStreamWaves * 64, 4)
+void expert_mx4_stream_kernel(const char* __restrict__ rows, const uint8_t* __restrict__ row_scales,
+                              const char* __restrict__ w, const uint8_t* __restrict__ scales,
+                              const int32_t* __restrict__ offsets, int32_t E, int32_t max_rows,
+                              int32_t red, int32_t feats, int32_t ftiles, int32_t act,
+                              char* __restrict__ out, int32_t zero) {
+    constexpr int kFeatBlocks = GATED ? kBlocks / 2 : kBlocks;  // of the output
+    __shared__ f32x4 part[kStreamWaves][kBlocks][64];
+    __shared__ int32_t info[4];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t number = expert_tile_number(kStreamChunk);
+    if (wave == 0) {
+        const ExpertTile t = expert_find_tile(offsets, E, max_rows, kStreamRows, ftiles, 4, number);
+        if (lane == 0) {
+            info[0] = t.e;
+            info[1] = t.f;
+            info[2] = t.row0;
+            info[3] = t.rows;
+        }
+    }
+    __syncthreads();
+    const int32_t e = __builtin_amdgcn_readfirstlane(info[0]);
+    const int32_t ft = __builtin_amdgcn_readfirstlane(info[1]);
+    const int32_t row0 = __builtin_amdgcn_readfirstlane(info[2]);
+    const int32_t nrows = __builtin_amdgcn_readfirstlane(info[3]);
+    if (e < 0) {
+        if (zero)
+            expert_zero_rows(reinterpret_cast<v4i*>(out), offsets, zero, row0, max_rows, feats / 8,
+                             ft, int64_t(gridDim.x) - nrows);
+        return;
+    }
+    const int i = lane & 15, g = lane >> 4;
+    const int32_t f0 = ft * kFeatBlocks * 16;
+    const int32_t steps = (red + kMxfp4Step - 1) / kMxfp4Step;
+    const int32_t groups = red / 32;
+    const char* wb[kBlocks];
+    const uint8_t* sb[kBlocks];
+#pragma unroll
+    for (int b = 0; b < kBlocks; ++b) {
+        const int32_t nb = (feats + 15) / 16;
+        const bool up = GATED && b >= kFeatBlocks;
+        const int64_t blk = int64_t(e) * nb * (GATED ? 2 : 1) + (up ? nb : 0) +
+                            min(f0 / 16 + (GATED ? b % kFeatBlocks : b), nb - 1);
+        wb[b] = w + blk * steps * 1024 + lane * 16;
+        sb[b] = scales + blk * steps * 64 + i * 4 + g;
+    }
+    const int64_t row = row0 + min(i, nrows - 1);
+    const char* rbase = rows + row * (red / 2);
+    const uint8_t* sbase = row_scales + row * groups;
+
+    struct Step {
+        Weights4 w[kBlocks];
+        v4i x;
+        int32_t rs;
+    };
+    auto load = [&](int32_t t, Step& d) {
+        const int32_t group = min(4 * t + g, groups - 1);
+#pragma unroll
+        for (int b = 0; b < kBlocks; ++b) {
+            d.w[b].q = __builtin_nontemporal_load(
+                reinterpret_cast<const v4i*>(wb[b] + int64_t(t) * 1024));
+            d.w[b].scale = sb[b][int64_t(t) * 64];
+        }
+        d.x = *reinterpret_cast<const v4i*>(rbase + int64_t(group) * 16);
+        d.rs = sbase[group];
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    f32x4 acc[kBlocks];
+#pragma unroll
+    for (int b = 0; b < kBlocks; ++b) acc[b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    auto compute = [&](const Step& d) {
+#pragma unroll
+        for (int b = 0; b < kBlocks; ++b)
+            acc[b] = multiply4(by_groups(d.w[b].q), d.w[b].scale, d.x, d.rs, acc[b]);
+    };
+    // Wavefront w takes steps w, w + kStreamWaves, ..., two in flight.
+    Step even, odd;
+    int32_t t = wave;
+    if (t < steps) load(t, even);
+    if (t + kStreamWaves < steps) load(t + kStreamWaves, odd);
+    while (t < steps) {
+        compute(even);
+        if (t + 2 * kStreamWaves < steps) load(t + 2 * kStreamWaves, even);
+        t += kStreamWaves;
+        if (t >= steps) break;
+        compute(odd);
+        if (t + 2 * kStreamWaves < steps) load(t + 2 * kStreamWaves, odd);
+        t += kStreamWaves;
+    }
+
+#pragma unroll
+    for (int b = 0; b < kBlocks; ++b) part[wave][b][lane] = acc[b];
+    __syncthreads();
+    if (wave >= kFeatBlocks) return;
+    f32x4 v = part[0][wave][lane];
+#pragma unroll
+    for (int p = 1; p < kStreamWaves; ++p) v += part[p][wave][lane];
+    if constexpr (GATED) {
+        f32x4 u = part[0][wave + kFeatBlocks][lane];
+#pragma unroll
+        for (int p = 1; p < kStreamWaves; ++p) u += part[p][wave + kFeatBlocks][lane];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] = activate(act, v[k]) * u[k];
+    }
+    const int32_t f = f0 + wave * 16 + g * 4;
+    if (i >= nrows || f >= feats) return;
+    *reinterpret_cast<v2i*>(out + (int64_t(row0 + i) * feats + f) * 2) = pack_bf16x4(v);
+}
+
+int64_t round_up(int64_t n, int64_t unit) { return (n + unit - 1) / unit * unit; }
+int64_t active(const ExpertMx4Args& a) { return a.max_rows < a.E ? a.max_rows : a.E; }
+
+int64_t tile_features(const ExpertMx4Args& a) {
+    const int32_t per = kWaves * kBlocks * 16 / (a.gated ? 2 : 1);
+    return (int64_t(a.feats) + per - 1) / per;
+}
+int64_t tile_workgroups(const ExpertMx4Args& a) {
+    return round_up(tile_features(a) * ((a.max_rows + kRowTile - 1) / kRowTile + active(a)),
+                    int64_t(kExpertXcds) * kXcdChunk);
+}
+int64_t stream_features(const ExpertMx4Args& a) {
+    const int32_t per = (a.gated ? kBlocks / 2 : kBlocks) * 16;
+    return (int64_t(a.feats) + per - 1) / per;
+}
+int64_t stream_workgroups(const ExpertMx4Args& a) {
+    return round_up(stream_features(a) * ((a.max_rows + kStreamRows - 1) / kStreamRows + active(a)),
+                    int64_t(kExpertXcds) * kStreamChunk);
+}
+
+template <class Kernel>
+hipError_t launch(Kernel kernel, int64_t workgroups, int threads, int64_t ftiles,
+                  const ExpertMx4Args& a, hipStream_t stream) {
+    const char* w = static_cast<const char*>(a.w);
+    const char* scales = w + mxfp4_tiles(a.E, a.gated ? 2 * a.feats : a.feats, a.red) * 1024;
+    hipLaunchKernelGGL(kernel, dim3(static_cast<uint32_t>(workgroups)), dim3(threads), 0, stream,
+                       static_cast<const char*>(a.rows), static_cast<const uint8_t*>(a.row_scales),
+                       w, reinterpret_cast<const uint8_t*>(scales), a.offsets, a.E,
+                       static_cast<int32_t>(a.max_rows), a.red, a.feats,
+                       static_cast<int32_t>(ftiles), a.activation, static_cast<char*>(a.out),
+                       a.zero);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+int64_t expert_mx4_grid(const ExpertMx4Args& a) { return tile_workgroups(a) * (kWaves * 64); }
+int64_t expert_mx4_stream_grid(const ExpertMx4Args& a) {
+    return stream_workgroups(a) * (kStreamWaves * 64);
+}
+
+hipError_t launch_expert_mx4(const ExpertMx4Args& a, hipStream_t stream) {
+    return launch(a.gated ? expert_mx4_kernel<true> : expert_mx4_kernel<false>, tile_workgroups(a),
+                  kWaves * 64, tile_features(a), a, stream);
+}
+
+hipError_t launch_expert_mx4_stream(const ExpertMx4Args& a, hipStream_t stream) {
+    return launch(a.gated ? expert_mx4_stream_kernel<true> : expert_mx4_stream_kernel<false>,
+                  stream_workgroups(a), kStreamWaves * 64, stream_features(a), a, stream);
+}
+
+}  // namespace moe

@@ -13,11 +13,16 @@
 
 namespace {
 
+using moe::activation_ok;
 using moe::apart;
 using moe::experts_ok;
 using moe::Input;
+using moe::kZeroFlags;
 using moe::misaligned;
+using moe::offsets_of;
 using moe::status_of;
+using moe::width_ok;
+using moe::zero_of;
 
 bool route_ok(int32_t dtype, int32_t T, int32_t E, int32_t K, int32_t score, int32_t flags,
               float scale) {
@@ -32,7 +37,81 @@ Input logits_of(const void* p, int32_t dtype, int64_t T, int64_t E) {
     return {p, T * E * (dtype == MOE_F32 ? 4 : 2)};
 }
 
+int run_quant(bool back, const void* from, int32_t dtype, int64_t rows, int32_t width, void* values,
+              void* scales, void* to, void* stream) {
+    if ((dtype != MOE_F32 && dtype != MOE_BF16) || rows < 0 || width < 32 ||
+        width > MOE_MAX_GEMM_WIDTH || width % 32 != 0 ||
+        rows > moe::kMaxQuantBlocks / (width / 32))
+        return MOE_ERR_INVALID_ARG;
+    if (rows == 0) return MOE_OK;
+    const void* elements = back ? to : from;
+    if (!elements || !values || !scales || misaligned(elements, 16) || misaligned(values, 16))
+        return MOE_ERR_INVALID_ARG;
+    const int64_t blocks = rows * (width / 32);
+    const Input x = {elements, blocks * 32 * (dtype == MOE_F32 ? 4 : 2)};
+    const Input v = {values, blocks * 16}, s = {scales, blocks};
+    if (back ? !apart(to, x.bytes, {v, s}) : !apart(values, v.bytes, {x, s}) ||
+                                                 !apart(scales, s.bytes, {x}))
+        return MOE_ERR_INVALID_ARG;
+    moe::QuantArgs a;
+    a.src = from;
+    a.bf16 = dtype == MOE_BF16;
+    a.blocks = blocks;
+    a.values = values;
+    a.scales = static_cast<uint8_t*>(scales);
+    a.dst = to;
+    return status_of(back ? moe::launch_dequantize_mxfp4(a, static_cast<hipStream_t>(stream))
+                          : moe::launch_quantize_mxfp4(a, static_cast<hipStream_t>(stream)));
+}
+
+int run_mx4(bool gated, const void* values, const void* row_scales, const void* packed,
+            const int32_t* offsets, int32_t E, int64_t max_rows, int32_t red, int32_t feats,
+            int32_t activation, void* out, int32_t flags, void* stream) {
+    const int64_t packed_bytes = moe_mxfp4_weights_bytes(E, gated ? 2 * feats : feats, red);
+    if (packed_bytes < 0 || max_rows < 0 || max_rows > INT32_MAX || (flags & ~kZeroFlags))
+        return MOE_ERR_INVALID_ARG;
+    if (max_rows == 0) return MOE_OK;
+    if (!values || !row_scales || !packed || !offsets || !out || misaligned(values, 16) ||
+        misaligned(packed, 16) || misaligned(offsets, 4) || misaligned(out, 16) ||
+        !apart(out, max_rows * feats * 2,
+               {{values, max_rows * (red / 2)}, {row_scales, max_rows * (red / 32)},
+                {packed, packed_bytes}, offsets_of(offsets, E)}))
+        return MOE_ERR_INVALID_ARG;
+    moe::ExpertMx4Args a;
+    a.gated = gated;
+    a.rows = values;
+    a.row_scales = row_scales;
+    a.w = packed;
+    a.offsets = offsets;
+    a.E = E;
+    a.max_rows = max_rows;
+    a.red = red;
+    a.feats = feats;
+    a.activation = activation;
+    a.out = out;
+    a.zero = zero_of(flags);
+    if (moe::expert_mx4_streams(E, max_rows, gated ? int64_t(2) * feats : feats)) {
+        if (moe::expert_mx4_stream_grid(a) > moe::kMaxGrid) return MOE_ERR_INVALID_ARG;
+        return status_of(moe::launch_expert_mx4_stream(a, static_cast<hipStream_t>(stream)));
+    }
+    if (moe::expert_mx4_grid(a) > moe::kMaxGrid) return MOE_ERR_INVALID_ARG;
+    return status_of(moe::launch_expert_mx4(a, static_cast<hipStream_t>(stream)));
+}
+
 }  // namespace
+
+namespace moe {
+
+// Where the form that streams the weights is the faster one: the limits of the
+// products with bf16 rows.
+bool expert_mx4_streams(int32_t E, int64_t max_rows, int64_t positions) {
+    if (max_rows <= int64_t(8) * E) return true;
+    const int64_t experts = max_rows < E ? max_rows : E;
+    const int64_t tiles = (max_rows + 15) / 16;
+    return (positions + 63) / 64 * (tiles > experts ? tiles : experts) <= 1536;
+}
+
+}  // namespace moe
 
 extern "C" {
 
@@ -97,6 +176,36 @@ int moe_route_topk_backward(const void* d_logits, int32_t dtype, const int32_t* 
     a.scale = scale;
     a.grad_logits = d_grad_logits;
     return status_of(moe::launch_route_topk_grad(a, static_cast<hipStream_t>(stream)));
+}
+
+int moe_quantize_mxfp4(const void* d_x, int32_t dtype, int64_t rows, int32_t width, void* d_values,
+                       void* d_scales, void* stream) {
+    return run_quant(false, d_x, dtype, rows, width, d_values, d_scales, nullptr, stream);
+}
+
+int moe_dequantize_mxfp4(const void* d_values, const void* d_scales, int32_t dtype, int64_t rows,
+                         int32_t width, void* d_x, void* stream) {
+    return run_quant(true, nullptr, dtype, rows, width, const_cast<void*>(d_values),
+                     const_cast<void*>(d_scales), d_x, stream);
+}
+
+int moe_grouped_gemm_mxfp4_rows(const void* d_values, const void* d_scales, const void* d_packed,
+                                const int32_t* d_offsets, int32_t num_experts, int64_t max_rows,
+                                int32_t k_in, int32_t n_out, void* d_out, int32_t flags,
+                                void* stream) {
+    return run_mx4(false, d_values, d_scales, d_packed, d_offsets, num_experts, max_rows, k_in,
+                   n_out, MOE_ACT_SILU, d_out, flags, stream);
+}
+
+int moe_gated_grouped_gemm_mxfp4_rows(const void* d_values, const void* d_scales,
+                                      const void* d_packed, const int32_t* d_offsets,
+                                      int32_t num_experts, int64_t max_rows, int32_t k_in,
+                                      int32_t n_hidden, int32_t activation, void* d_h,
+                                      int32_t flags, void* stream) {
+    if (!width_ok(n_hidden, 16) || n_hidden > MOE_MAX_GEMM_WIDTH / 2 || !activation_ok(activation))
+        return MOE_ERR_INVALID_ARG;
+    return run_mx4(true, d_values, d_scales, d_packed, d_offsets, num_experts, max_rows, k_in,
+                   n_hidden, activation, d_h, flags, stream);
 }
 
 }  // extern "C"

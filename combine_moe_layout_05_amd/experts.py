@@ -20,7 +20,7 @@ from typing import Optional, Union
 import torch
 
 from . import _lib as L
-from .moe import Mxfp4ExpertWeights, _call, _check_rows
+from .moe import (Mxfp4ExpertWeights, Mxfp4Rows, _DTYPES, _call, _check_mxfp4_rows, _check_rows)
 
 ACTIVATIONS = {"silu": L.MOE_ACT_SILU, "gelu": L.MOE_ACT_GELU_TANH}
 
@@ -84,7 +84,47 @@ def mxfp4_expert_weights(values: torch.Tensor, scales: torch.Tensor) -> Mxfp4Exp
     return Mxfp4ExpertWeights(data, E, n_out, k_in)
 
 
-def gated_grouped_gemm(x_expert: torch.Tensor, weights: Union[torch.Tensor, Mxfp4ExpertWeights],
+def quantize_mxfp4(x: torch.Tensor) -> Mxfp4Rows:
+    """x in MXFP4 along its last axis (moe_quantize_mxfp4): for each 32
+    elements the scale 2^e, e = max(floor(log2(largest magnitude)) - 2, -127),
+    and the e2m1 numbers nearest to x / 2^e (ties to even, at most 6).
+
+    x fp32 or bf16 [..., k], contiguous, k a multiple of 32: expert-major rows
+    for grouped_gemm and gated_grouped_gemm, or weights [E, n_out, k_in] for
+    mxfp4_expert_weights(*quantize_mxfp4(w)). A block with a NaN or an infinity
+    becomes NaN. Records no gradient."""
+    if x.dtype not in _DTYPES:
+        raise TypeError(f"x must be one of {list(_DTYPES)}, got {x.dtype}")
+    dev = x.device
+    _check_rows("x", x, x.dtype, max(x.dim(), 1), dev)
+    k = x.shape[-1]
+    if k == 0 or k % 32 != 0:
+        raise ValueError(f"the last axis must be a multiple of 32, got {k}")
+    values = torch.empty((*x.shape[:-1], k // 2), dtype=torch.uint8, device=dev)
+    scales = torch.empty((*x.shape[:-1], k // 32), dtype=torch.uint8, device=dev)
+    _call("moe_quantize_mxfp4", dev, x.data_ptr(), _DTYPES[x.dtype], x.numel() // k, k,
+          values.data_ptr(), scales.data_ptr())
+    return Mxfp4Rows(values, scales)
+
+
+def dequantize_mxfp4(rows: Mxfp4Rows, dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
+    """The numbers that rows stand for (moe_dequantize_mxfp4), fp32 or bf16
+    [..., k]; exact in both."""
+    if dtype not in _DTYPES:
+        raise TypeError(f"dtype must be one of {list(_DTYPES)}, got {dtype}")
+    dev = rows.values.device
+    rows.check(dev, max(rows.values.dim(), 1))
+    k = 2 * rows.values.shape[-1]
+    if k == 0:
+        raise ValueError("the last axis is empty")
+    x = torch.empty((*rows.values.shape[:-1], k), dtype=dtype, device=dev)
+    _call("moe_dequantize_mxfp4", dev, rows.values.data_ptr(), rows.scales.data_ptr(),
+          _DTYPES[dtype], x.numel() // k, k, x.data_ptr())
+    return x
+
+
+def gated_grouped_gemm(x_expert: Union[torch.Tensor, Mxfp4Rows],
+                       weights: Union[torch.Tensor, Mxfp4ExpertWeights],
                        offsets: torch.Tensor, out: Optional[torch.Tensor] = None, *,
                        activation: str = "silu",
                        pre: Optional[torch.Tensor] = None) -> torch.Tensor:
@@ -93,12 +133,24 @@ def gated_grouped_gemm(x_expert: torch.Tensor, weights: Union[torch.Tensor, Mxfp
 
     x_expert bf16 [R, k_in]; weights bf16 [E, 2 n_hidden, k_in], the gate's
     rows first, or the Mxfp4ExpertWeights of such rows (n_hidden a multiple of
-    16); offsets int32 [E+1]; out bf16 [R, n_hidden]. activation "silu" or
+    16), which x_expert in 4 bits (quantize_mxfp4) needs; offsets int32 [E+1]; out bf16 [R, n_hidden]. activation "silu" or
     "gelu" (tanh form). pre, fp32 [R, 2 n_hidden], receives the projections
     [g | u] of the segments' rows for the backward (bf16 weights only). Not
     differentiable by itself; see expert_ffn."""
-    dev = x_expert.device
     act = _activation(activation)
+    if isinstance(x_expert, Mxfp4Rows):
+        dev = _check_mxfp4_rows(x_expert, weights, offsets)
+        n2, R = weights.n_out, x_expert.values.shape[0]
+        if n2 % 32 != 0:
+            raise ValueError(f"packed gate and up rows must be 2 * a multiple of 16, got {n2}")
+        if pre is not None:
+            raise ValueError("pre needs bf16 weights (4-bit weights have no backward)")
+        out, flags = _out(out, R, n2 // 2, dev)
+        _call("moe_gated_grouped_gemm_mxfp4_rows", dev, x_expert.values.data_ptr(),
+              x_expert.scales.data_ptr(), weights.data.data_ptr(), offsets.data_ptr(),
+              weights.num_experts, R, weights.k_in, n2 // 2, act, out.data_ptr(), flags)
+        return out
+    dev = x_expert.device
     packed = isinstance(weights, Mxfp4ExpertWeights)
     if packed:
         E, n2, k_in = weights.num_experts, weights.n_out, weights.k_in

@@ -152,6 +152,54 @@ class Mxfp4ExpertWeights(NamedTuple):
                              f"got {self.data.numel()}")
 
 
+class Mxfp4Rows(NamedTuple):
+    """Rows (or weights) in 4 bits (quantize_mxfp4): e2m1 numbers, two to a
+    byte, and a scale 2^(byte - 127) for each 32 of them."""
+    values: torch.Tensor     # uint8 [..., k / 2], element 2i in the low half of byte i
+    scales: torch.Tensor     # uint8 [..., k / 32]
+
+    def check(self, dev: torch.device, dim: int) -> None:
+        _check_rows("values", self.values, torch.uint8, dim, dev)
+        _check_rows("scales", self.scales, torch.uint8, dim, dev)
+        half = self.values.shape[-1]
+        if half % 16 != 0 or tuple(self.scales.shape) != (*self.values.shape[:-1], half // 16):
+            raise ValueError("shapes: values [..., k / 2], scales [..., k / 32], k a multiple of "
+                             f"32; got {tuple(self.values.shape)}, {tuple(self.scales.shape)}")
+
+
+def _check_mxfp4_rows(rows: Mxfp4Rows, weights, offsets) -> torch.device:
+    """Checks of a product of 4-bit rows: the device they are all on."""
+    dev = rows.values.device
+    if not isinstance(weights, Mxfp4ExpertWeights):
+        raise TypeError("rows in 4 bits need weights packed with mxfp4_expert_weights, got "
+                        f"{type(weights).__name__}")
+    rows.check(dev, 2)
+    weights.check(dev)
+    _check_rows("offsets", offsets, torch.int32, 1, dev)
+    if 2 * rows.values.shape[1] != weights.k_in or offsets.shape[0] != weights.num_experts + 1:
+        raise ValueError("shapes: values [R, k_in / 2], weights [E, n_out, k_in], offsets [E+1]")
+    return dev
+
+
+def _grouped_gemm_mxfp4_rows(rows: Mxfp4Rows, weights, offsets, out, row_tile: int):
+    dev = _check_mxfp4_rows(rows, weights, offsets)
+    if row_tile != 0:
+        raise ValueError("4-bit weights take no row_tile")
+    R, n_out = rows.values.shape[0], weights.n_out
+    flags = 0
+    if out is None:
+        out = torch.empty((R, n_out), dtype=torch.bfloat16, device=dev)
+        flags = L.MOE_GEMM_ZERO_OUTSIDE
+    else:
+        _check_rows("out", out, torch.bfloat16, 2, dev)
+        if tuple(out.shape) != (R, n_out):
+            raise ValueError(f"out must be a contiguous bf16 [{R}, {n_out}] tensor on {dev}")
+    _call("moe_grouped_gemm_mxfp4_rows", dev, rows.values.data_ptr(), rows.scales.data_ptr(),
+          weights.data.data_ptr(), offsets.data_ptr(), weights.num_experts, R, weights.k_in, n_out,
+          out.data_ptr(), flags)
+    return out
+
+
 def _grouped_gemm_mxfp4(x_expert, weights: Mxfp4ExpertWeights, offsets, out, row_tile: int):
     dev = x_expert.device
     weights.check(dev)
@@ -175,7 +223,7 @@ def _grouped_gemm_mxfp4(x_expert, weights: Mxfp4ExpertWeights, offsets, out, row
     return out
 
 
-def grouped_gemm(x_expert: torch.Tensor, weights, offsets: torch.Tensor,
+def grouped_gemm(x_expert, weights, offsets: torch.Tensor,
                  out: Optional[torch.Tensor] = None, *, row_tile: int = 0) -> torch.Tensor:
     """Expert step between dispatch and combine (moe_grouped_gemm): for each
     expert e, rows r in [offsets[e], offsets[e+1]) get
@@ -183,13 +231,16 @@ def grouped_gemm(x_expert: torch.Tensor, weights, offsets: torch.Tensor,
     offsets stays on the device (e.g. Layout.offsets); rows outside every
     segment keep what `out` held.
 
-    x_expert bf16 [R, k_in]; weights bf16 [E, n_out, k_in] or the
+    x_expert bf16 [R, k_in], or Mxfp4Rows of such rows with Mxfp4ExpertWeights
+    (moe_grouped_gemm_mxfp4_rows); weights bf16 [E, n_out, k_in] or the
     TiledExpertWeights of them (same results, faster), or 4-bit weights as
     Mxfp4ExpertWeights (moe_grouped_gemm_mxfp4; the rows of no segment of an
     output it allocates are zero); offsets int32 [E+1]; out bf16 [R, n_out]
     (allocated with torch.empty if None). For row-major weights
     grouped_gemm_forward computes the same product faster, in another order of
     the sums."""
+    if isinstance(x_expert, Mxfp4Rows):
+        return _grouped_gemm_mxfp4_rows(x_expert, weights, offsets, out, int(row_tile))
     if isinstance(weights, Mxfp4ExpertWeights):
         return _grouped_gemm_mxfp4(x_expert, weights, offsets, out, int(row_tile))
     dev = x_expert.device

@@ -523,6 +523,42 @@ int moe_gated_grouped_gemm_mxfp4(const void *d_x_expert, const void *d_packed,
                                  int64_t max_rows, int32_t k_in, int32_t n_hidden,
                                  int32_t activation, void *d_h, int32_t flags, void *stream);
 
+/* Rows (or weights before packing) to MXFP4 and back, along their last axis.
+ * With top the largest magnitude of 32 consecutive elements and
+ *   e = max(floor(log2(top)) - 2, -127)
+ * the scale byte is e + 127 and an element x becomes the e2m1 number nearest to
+ * x / 2^e, ties to the one with an even code, magnitudes above 6 to 6. A block of
+ * zeros has byte 0. A block with a NaN or an infinity has byte 255: all its
+ * elements are NaN from then on. Back, each element is its value times its
+ * scale, exact in either type where the result is a number the type holds.
+ *   d_x       [rows][width] of dtype (MOE_F32 or MOE_BF16), 16-byte aligned
+ *   d_values  uint8 [rows][width / 2], element 2i in the low half of byte i
+ *             (16-byte aligned)
+ *   d_scales  uint8 [rows][width / 32]
+ *   width     a multiple of 32, at most MOE_MAX_GEMM_WIDTH; rows * width < 2^35 -
+ *             2048 (rows == 0 enqueues nothing)
+ * No context and no workspace; no output shares a byte with another buffer.
+ * Violations: MOE_ERR_INVALID_ARG. */
+int moe_quantize_mxfp4(const void *d_x, int32_t dtype, int64_t rows, int32_t width,
+                       void *d_values, void *d_scales, void *stream);
+int moe_dequantize_mxfp4(const void *d_values, const void *d_scales, int32_t dtype, int64_t rows,
+                         int32_t width, void *d_x, void *stream);
+
+/* moe_grouped_gemm_mxfp4 and moe_gated_grouped_gemm_mxfp4 with rows in MXFP4
+ * too: d_values [max_rows][k_in / 2] (16-byte aligned) and d_scales [max_rows]
+ * [k_in / 32] as moe_quantize_mxfp4 writes them, the packed weights as those
+ * calls take them. Each product of two elements is exact, sums are fp32, the
+ * result is rounded once to bf16. A row with a scale byte of 255 becomes NaN. */
+int moe_grouped_gemm_mxfp4_rows(const void *d_values, const void *d_scales, const void *d_packed,
+                                const int32_t *d_offsets, int32_t num_experts, int64_t max_rows,
+                                int32_t k_in, int32_t n_out, void *d_out, int32_t flags,
+                                void *stream);
+int moe_gated_grouped_gemm_mxfp4_rows(const void *d_values, const void *d_scales,
+                                      const void *d_packed, const int32_t *d_offsets,
+                                      int32_t num_experts, int64_t max_rows, int32_t k_in,
+                                      int32_t n_hidden, int32_t activation, void *d_h,
+                                      int32_t flags, void *stream);
+
 /* ---- Router ---------------------------------------------------------------
  * The K experts of every token and their scores from the router's logits: the
  * ids and scores that moe_layout, moe_dispatch and moe_combine take. An expert

@@ -106,3 +106,56 @@ def gradient(logits, ids, grad, score, renormalize, scale):
             d, dm = g * slope, g.abs() * slope
     d, dm = torch.where(there, d, zero), torch.where(there, dm, zero)
     return out.scatter_add(1, at, d), rel * mag.scatter_add(1, at, dm)
+
+
+# ---- MXFP4 ------------------------------------------------------------------
+
+MIDDLES = torch.tensor([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0], dtype=torch.float64)
+UP = torch.tensor([False, True, False, True, False, True, False])   # a middle rounds to the even code
+
+
+def quantize(x):
+    """(values, scales) uint8 of x [..., k] by the definition, 64-bit
+    arithmetic; a block with a NaN or infinity gets zeros and 255."""
+    b = x.double().unflatten(-1, (-1, 32))
+    lost = ~torch.isfinite(b).all(dim=-1, keepdim=True)
+    b = torch.where(lost, torch.zeros_like(b), b)
+    top = b.abs().amax(dim=-1, keepdim=True)
+    e = torch.frexp(top)[1].double() - 3          # top = m 2^exponent, 1/2 <= m < 1
+    e = torch.where(top > 0, e, torch.full_like(e, -127)).clamp(min=-127)
+    t = (b.abs() * torch.exp2(-e)).unsqueeze(-1)
+    code = ((t > MIDDLES) | (UP & (t == MIDDLES))).sum(dim=-1)
+    code += 8 * torch.signbit(torch.where(lost, torch.zeros_like(b), b)).long()
+    code = code.flatten(-2).to(torch.uint8)
+    scales = torch.where(lost, torch.full_like(e, 255), e + 127).squeeze(-1).to(torch.uint8)
+    return code[..., 0::2] | (code[..., 1::2] << 4), scales
+
+
+def decode(values, scales):
+    """float64 [..., k]."""
+    import expert_ref
+    q = torch.stack((values & 15, values >> 4), dim=-1).flatten(-2).long()
+    s = torch.ldexp(torch.ones((), dtype=torch.float64), scales.int() - 127)
+    s = torch.where(scales == 255, torch.full_like(s, float("nan")), s)
+    return expert_ref.E2M1[q] * s.repeat_interleave(32, dim=-1)
+
+
+def product(x, w, off):
+    """out[r] = x[r] w[e]^T in 64 bits and the error bound of its sum in fp32 on
+    the matrix cores: each of the k additions loses at most a whole unit (2 u)
+    of the sum of the products' magnitudes, since they may truncate."""
+    import expert_ref
+    out, mag = expert_ref.linear(x, w, off)
+    return out, 2 * expert_ref.gamma(x.shape[1]) * mag
+
+
+def gate(pre, dpre, name):
+    """act(g) * u of pre = [g | u] with errors dpre, and the error before the
+    last rounding."""
+    import expert_ref as er
+    F = pre.shape[1] // 2
+    g, u, dg, du = pre[:, :F], pre[:, F:], dpre[:, :F], dpre[:, F:]
+    a = er.act(name, g)[0]
+    da = er.SLOPE * dg + er.act_error(name, g)[0]
+    h = a * u
+    return h, da * (u.abs() + du) + a.abs() * du + 2 * U * h.abs()
