@@ -20,3 +20,4 @@ from .experts import (  # noqa: F401
 )
 from .autograd import MoeTokenDispatcher, expert_ffn  # noqa: F401
 from .router import Routing, route_topk, route_topk_backward  # noqa: F401
+from .layer import moe_layer  # noqa: F401

@@ -29,6 +29,8 @@ MOE_F32 = 0
 MOE_BF16 = 1
 MOE_WEIGHTS_ROW_MAJOR = 0
 MOE_WEIGHTS_TILED = 1
+MOE_WEIGHTS_MXFP4 = 2
+MOE_MAX_LAYER_SLOTS = 512
 MOE_GEMM_ZERO_TAIL = 1
 MOE_GEMM_ACCUMULATE = 2
 MOE_GEMM_ZERO_HEAD = 8
@@ -113,6 +115,9 @@ SIGNATURES = {
                               _vp, _vp]),
     "moe_route_topk_backward": (_int, [_vp, _i32, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _f32,
                                        _vp, _vp]),
+    "moe_few_tokens_workspace_bytes": (_i64, [_i32, _i32, _i32]),
+    "moe_few_tokens_layer": (_int, [_vp, _vp, _vp, _i32, _i32, _vp, _vp, _i32, _i32, _i32, _i32,
+                                    _i32, _vp, _i64, _vp, _vp]),
     "moe_set_tuning": (_int, [_vp, C.POINTER(MoeTuning)]),
     "moe_get_tuning": (_int, [_vp, C.POINTER(MoeTuning)]),
     "moe_ceil_div": (_i64, [_i64, _i64]),

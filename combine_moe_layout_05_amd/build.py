@@ -22,7 +22,7 @@ INCLUDE = os.path.join(ROOT, "include")
 SOURCES = ["layout.hip", "dispatch.hip", "combine.hip", "combine_backward.hip", "routing_map.hip",
            "grouped_gemm.hip", "noalloc.hip",
            "expert_gemm.hip", "expert_wgrad.hip", "expert_stream.hip", "expert_mxfp4.hip",
-           "expert_mx4.hip", "mxfp4_rows.hip", "route.hip",
+           "expert_mx4.hip", "mxfp4_rows.hip", "route.hip", "few_tokens.hip",
            "moe_api.cpp", "expert_api.cpp", "layer_api.cpp"]
 HEADERS = [os.path.join(CSRC, "moe_kernels.h"), os.path.join(CSRC, "moe_lanes.h"),
            os.path.join(CSRC, "expert_kernels.h"), os.path.join(CSRC, "expert_mma.h"),

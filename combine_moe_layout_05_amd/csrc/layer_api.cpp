@@ -11,6 +11,10 @@
 #include "layer_kernels.h"
 #include "moe.h"
 
+static_assert(MOE_MAX_LAYER_SLOTS == moe::kMaxLayerSlots &&
+                  MOE_MAX_ROUTE_GROUPS == moe::kMaxRouteGroups,
+              "the kernels' limits");
+
 namespace {
 
 using moe::activation_ok;
@@ -21,6 +25,7 @@ using moe::kZeroFlags;
 using moe::misaligned;
 using moe::offsets_of;
 using moe::status_of;
+using moe::weights_of;
 using moe::width_ok;
 using moe::zero_of;
 
@@ -206,6 +211,62 @@ int moe_gated_grouped_gemm_mxfp4_rows(const void* d_values, const void* d_scales
         return MOE_ERR_INVALID_ARG;
     return run_mx4(true, d_values, d_scales, d_packed, d_offsets, num_experts, max_rows, k_in,
                    n_hidden, activation, d_h, flags, stream);
+}
+
+int64_t moe_few_tokens_workspace_bytes(int32_t T, int32_t K, int32_t n_hidden) {
+    if (T < 0 || K < 1 || K > MOE_MAX_TOPK || T > MOE_MAX_LAYER_SLOTS / K || !width_ok(n_hidden, 8) ||
+        n_hidden > MOE_MAX_GEMM_WIDTH / 2)
+        return -1;
+    return int64_t(T) * K * n_hidden * 4;
+}
+
+int moe_few_tokens_layer(const void* d_x, const float* d_topk_scores, const int32_t* d_topk_ids,
+                         int32_t T, int32_t K, const void* d_w_gate_up, const void* d_w_down,
+                         int32_t weight_layout, int32_t num_experts, int32_t hidden,
+                         int32_t n_hidden, int32_t activation, void* d_workspace,
+                         int64_t workspace_bytes, void* d_y, void* stream) {
+    const bool four = weight_layout == MOE_WEIGHTS_MXFP4;
+    const int64_t need = moe_few_tokens_workspace_bytes(T, K, n_hidden);
+    if (need < 0 || (!four && weight_layout != MOE_WEIGHTS_ROW_MAJOR) || !experts_ok(num_experts) ||
+        !width_ok(hidden, four ? 32 : 8) || !width_ok(n_hidden, four ? 32 : 8) ||
+        !activation_ok(activation))
+        return MOE_ERR_INVALID_ARG;
+    Input w1 = weights_of(d_w_gate_up, num_experts, int64_t(2) * n_hidden, hidden);
+    Input w2 = weights_of(d_w_down, num_experts, hidden, n_hidden);
+    if (four) {
+        w1.bytes = moe_mxfp4_weights_bytes(num_experts, 2 * n_hidden, hidden);
+        w2.bytes = moe_mxfp4_weights_bytes(num_experts, hidden, n_hidden);
+        if (w1.bytes < 0 || w2.bytes < 0) return MOE_ERR_INVALID_ARG;
+    }
+    if (T == 0) return MOE_OK;
+    if (workspace_bytes < need) return MOE_ERR_WORKSPACE;
+    if (!d_x || !d_topk_scores || !d_topk_ids || !d_w_gate_up || !d_w_down || !d_workspace ||
+        !d_y || misaligned(d_x, 16) || misaligned(d_topk_scores, 4) || misaligned(d_topk_ids, 4) ||
+        misaligned(d_w_gate_up, 16) || misaligned(d_w_down, 16) || misaligned(d_workspace, 16) ||
+        misaligned(d_y, 16))
+        return MOE_ERR_INVALID_ARG;
+    const Input x = {d_x, int64_t(T) * hidden * 2};
+    const Input s = {d_topk_scores, int64_t(T) * K * 4}, ids = {d_topk_ids, int64_t(T) * K * 4};
+    if (!apart(d_workspace, need, {x, s, ids, w1, w2}) ||
+        !apart(d_y, x.bytes, {x, s, ids, w1, w2, {d_workspace, need}}))
+        return MOE_ERR_INVALID_ARG;
+    moe::LayerArgs a;
+    a.x = d_x;
+    a.scores = d_topk_scores;
+    a.ids = d_topk_ids;
+    a.T = T;
+    a.K = K;
+    a.E = num_experts;
+    a.four = four;
+    a.w_gate_up = d_w_gate_up;
+    a.w_down = d_w_down;
+    a.D = hidden;
+    a.F = n_hidden;
+    a.activation = activation;
+    a.workspace = d_workspace;
+    a.y = d_y;
+    if (moe::few_tokens_grid(a) > moe::kMaxGrid) return MOE_ERR_INVALID_ARG;
+    return status_of(moe::launch_few_tokens(a, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -80,4 +80,25 @@ int64_t expert_mx4_grid(const ExpertMx4Args& a);
 hipError_t launch_expert_mx4_stream(const ExpertMx4Args& a, hipStream_t stream);
 int64_t expert_mx4_stream_grid(const ExpertMx4Args& a);
 
+// The whole expert layer for a few tokens.
+constexpr int32_t kMaxLayerSlots = 512;
+struct LayerArgs {
+    const void* x;          // bf16 [T][D]
+    const float* scores;    // [T][K]
+    const int32_t* ids;     // [T][K]
+    int32_t T;              // T K is 1 .. kMaxLayerSlots
+    int32_t K;
+    int32_t E;
+    bool four;              // weights are packed 4-bit, else bf16
+    const void* w_gate_up;  // [E][2 F][D]
+    const void* w_down;     // [E][D][F]
+    int32_t D;              // multiple of 8 (four: of 32)
+    int32_t F;              // multiple of 8 (four: of 32)
+    int32_t activation;
+    void* workspace;        // 4 T K F bytes
+    void* y;                // bf16 [T][D]
+};
+hipError_t launch_few_tokens(const LayerArgs& a, hipStream_t stream);
+int64_t few_tokens_grid(const LayerArgs& a);    // work-items of its larger launch
+
 }  // namespace moe

@@ -603,6 +603,41 @@ int moe_route_topk_backward(const void *d_logits, int32_t dtype, const int32_t *
                             int32_t score, int32_t flags, float scale, void *d_grad_logits,
                             void *stream);
 
+/* ---- The whole layer for a few tokens -------------------------------------
+ * A decoding step's expert layer in two launches, from the tokens' rows and
+ * their routing to the combined output, with no layout, dispatch or combine:
+ *   y[t] = sum over k of scores[t][k] *
+ *          ((act(x[t] Wg[e]^T) * (x[t] Wu[e]^T)) Wd[e]^T),  e = topk_ids[t][k]
+ * Slots whose id is outside [0, num_experts) add nothing and their score is not
+ * read; a token without an expert gets zeros. Sums and the activation are
+ * fp32, the gated product keeps 16 bits of significand between the launches, the
+ * slots' results stay fp32 and are added in slot order; one rounding to bf16.
+ * Equal calls give equal bits.
+ *   d_x            bf16 [T][hidden]
+ *   d_topk_scores  float32 [T][K], d_topk_ids int32 [T][K]; T * K <=
+ *                  MOE_MAX_LAYER_SLOTS (T == 0 enqueues nothing)
+ *   d_w_gate_up, d_w_down  weight_layout MOE_WEIGHTS_ROW_MAJOR: bf16
+ *                  [num_experts][2 * n_hidden][hidden] (gate rows, then up rows)
+ *                  and [num_experts][hidden][n_hidden]; MOE_WEIGHTS_MXFP4: those
+ *                  in 4 bits, each packed by moe_pack_mxfp4_weights
+ *   hidden, n_hidden  multiples of 8 (4 bits: of 32), n_hidden at most
+ *                  MOE_MAX_GEMM_WIDTH / 2
+ *   d_workspace    moe_few_tokens_workspace_bytes(T, K, n_hidden) bytes (-1 for
+ *                  sizes not supported), the call's own until it has run
+ *   d_y            bf16 [T][hidden]
+ * bf16 and packed buffers, the workspace and d_y are 16-byte aligned; d_y and the
+ * workspace share no byte with another buffer. MOE_ERR_WORKSPACE: the workspace
+ * is too small. Other violations: MOE_ERR_INVALID_ARG. */
+#define MOE_WEIGHTS_MXFP4   2    /* the output of moe_pack_mxfp4_weights */
+#define MOE_MAX_LAYER_SLOTS 512
+
+int64_t moe_few_tokens_workspace_bytes(int32_t T, int32_t K, int32_t n_hidden);
+int moe_few_tokens_layer(const void *d_x, const float *d_topk_scores, const int32_t *d_topk_ids,
+                         int32_t T, int32_t K, const void *d_w_gate_up, const void *d_w_down,
+                         int32_t weight_layout, int32_t num_experts, int32_t hidden,
+                         int32_t n_hidden, int32_t activation, void *d_workspace,
+                         int64_t workspace_bytes, void *d_y, void *stream);
+
 /* Launch shape tuning (optional). moe_create picks every default from the
  * context's sizes (measured on MI355X); moe_get_tuning reports them. Each
  * token row is split into `segments` wavefront work items (1..16) and

@@ -159,3 +159,36 @@ def gate(pre, dpre, name):
     da = er.SLOPE * dg + er.act_error(name, g)[0]
     h = a * u
     return h, da * (u.abs() + du) + a.abs() * du + 2 * U * h.abs()
+
+
+# ---- The whole layer ---------------------------------------------------------
+
+def layer(x, scores, ids, w13, w2, name):
+    """y [T, D] in 64 bits and the error bound before its last rounding, for
+    x [T, D], w13 [E, 2F, D], w2 [E, D, F] as numbers of any type.
+
+    h = act(g) * u is off by the fp32 evaluation (gate()); as two bf16 it loses
+    B^2 |h| more, and what lies below bf16's normal numbers (2^-126). Its sum
+    with w2 has 2 F terms of magnitude at most (1 + 2 B) |h w2|, joined from at
+    most 8 parts; the sum over the slots has K terms."""
+    import expert_ref as er
+    T, K = ids.shape
+    E, D, F = w2.shape
+    y, err = torch.zeros(T, D, dtype=torch.float64), torch.zeros(T, D, dtype=torch.float64)
+    mag = torch.zeros_like(y)
+    for e in range(E):
+        t, k = torch.nonzero(ids == e, as_tuple=True)
+        if len(t) == 0:
+            continue
+        off = [0, len(t)]
+        pre, m = er.linear(x[t], w13[e:e + 1], off)
+        h, dh = gate(pre, 2 * er.gamma(D + 8) * m, name)
+        dh = dh + B * B * h.abs() + 2.0 ** -126
+        w = w2[e].double()
+        p = h @ w.t()
+        pm = (1 + 2 * B) * (h.abs() + dh) @ w.abs().t()
+        s = scores[t, k].double()[:, None]
+        y.index_add_(0, t, s * p)
+        mag.index_add_(0, t, s.abs() * pm)
+        err.index_add_(0, t, s.abs() * (dh @ w.abs().t() + 2 * er.gamma(2 * F + 16) * pm))
+    return y, err + 2 * er.gamma(K + 1) * mag
