@@ -14,7 +14,10 @@
 // h goes between the kernels as two bf16, the rounded number and what the
 // rounding left, 16 bits of significand: the matrix cores take both as rows of
 // one product, whose 16 places a few tokens leave empty anyway, so the second
-// rounding that a bf16 h would bring costs nothing to avoid.
+// rounding that a bf16 h would bring costs nothing to avoid. Its rows lie in the
+// order of their experts, and in steps of the second kernel's sum: for each step
+// and row 32 rounded elements, their 32 rests, the next 32 and so on, so that the
+// loads of few or many rows all take whole cache lines.
 //
 // Bound: the bytes of the weights in use, read once each, straight into the
 // registers the matrix cores read.
@@ -23,21 +26,38 @@
 #include "expert_mxfp4.h"
 #include "layer_kernels.h"
 
+#include <type_traits>
+
 namespace moe {
 namespace {
 
 constexpr int kMaxWords = 32;           // of a bit per expert (1024)
 
-// What a step of the sum takes from memory for one 16-feature block.
+// What a step of the sum takes from memory for one 16-feature block; the scales
+// of 4-bit weights come apart from them.
 template <bool FOUR>
 struct Weights;
 template <>
-struct Weights<true> : Mxfp4Step {};
+struct Weights<true> {
+    v4i q;
+    __device__ bf16x8 frag(int s, uint32_t scale) const { return Mxfp4Step{q, scale}.frag(s); }
+};
 template <>
 struct Weights<false> {
     v4i q[2];
-    __device__ bf16x8 frag(int s) const { return __builtin_bit_cast(bf16x8, q[s]); }
+    __device__ bf16x8 frag(int s, uint32_t) const { return __builtin_bit_cast(bf16x8, q[s]); }
 };
+// A register of which lane group g holds value g of the 16 lanes' to four
+// registers that hold value 0, 1, 2 and 3 in all groups.
+__device__ __forceinline__ void spread(uint32_t v, uint32_t (&d)[4]) {
+    const auto half = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    const auto lo = __builtin_amdgcn_permlane16_swap(half[0], half[0], false, false);
+    const auto hi = __builtin_amdgcn_permlane16_swap(half[1], half[1], false, false);
+    d[0] = lo[0];
+    d[1] = lo[1];
+    d[2] = hi[0];
+    d[3] = hi[1];
+}
 template <bool FOUR>
 struct Step {
     static constexpr int kElems = FOUR ? kMxfp4Step : 64;
@@ -48,22 +68,17 @@ struct Step {
 template <bool FOUR>
 struct Block {
     const char* q;
-    const char* scale;
     // Lane (i, g)'s offsets, the same for all blocks of a kernel but for a
     // clamped row.
     static __device__ uint32_t offset(int lane, int32_t row, int64_t pitch) {
         return FOUR ? lane * 16 : static_cast<uint32_t>(row * pitch) + (lane >> 4) * 16;
     }
     __device__ __forceinline__ void load(int32_t t, uint32_t at, int lane, Weights<FOUR>& d) const {
+        reform(at);
         if constexpr (FOUR) {
-            uint32_t so = (lane & 15) * 4;
-            reform(at);
-            reform(so);
             d.q = __builtin_nontemporal_load(
                 reinterpret_cast<const v4i*>(q + int64_t(t) * 1024 + at));
-            d.scale = *reinterpret_cast<const uint32_t*>(scale + int64_t(t) * 64 + so);
         } else {
-            reform(at);
 #pragma unroll
             for (int s = 0; s < 2; ++s)
                 d.q[s] = *reinterpret_cast<const v4i*>(q + (int64_t(t) * 128 + s * 64) + at);
@@ -86,46 +101,77 @@ struct Block {
     }
 };
 
-// Rows of the other operand, bf16: 8 elements of this lane's row (offset `at` from
-// the uniform `base`) for each product of step t.
-template <bool FOUR>
-__device__ __forceinline__ void load_rows(const char* base, int32_t t, uint32_t at,
-                                          v4i (&d)[Step<FOUR>::kProducts]) {
-    reform(at);
+// Rows of the other operand, bf16, of which there are at most 16 / P at a time.
+// With few of them most of an operand's 16 places would stay empty, and every
+// load instruction takes the same time however few bytes are new in it; so lane
+// (i, g) loads for row i % (16 / P), and for product i / (16 / P) of P in turn, and
+// one load serves P products. Each of those has sums of its own, of which the 16
+// / P columns are valid that hold its own elements. Measured on MI355X, 4-bit
+// weights, 32 tokens on some 100 of 256 experts: see the down projection.
+template <bool FOUR, int P>
+struct Rows {
+    static constexpr int kRows = 16 / P;
+    static constexpr int kLoads = Step<FOUR>::kProducts / P;
+    // Byte of lane (i, g)'s elements in a step's first load.
+    static __device__ uint32_t within(int i, int g) { return (i / kRows) * 64 + g * 16; }
+    static __device__ __forceinline__ void load(const char* base, int32_t t, uint32_t at,
+                                                v4i (&d)[kLoads]) {
+        reform(at);
 #pragma unroll
-    for (int s = 0; s < Step<FOUR>::kProducts; ++s)
-        d[s] = *reinterpret_cast<const v4i*>(base + (int64_t(t) * (Step<FOUR>::kElems * 2) + s * 64) +
-                                             at);
-}
-template <bool FOUR>
-__device__ __forceinline__ void load_rows_last(const char* base, int32_t t, int left, uint32_t at,
-                                               int lane, v4i (&d)[Step<FOUR>::kProducts]) {
-#pragma unroll
-    for (int s = 0; s < Step<FOUR>::kProducts; ++s) {
-        d[s] = v4i{0, 0, 0, 0};
-        if (4 * s + (lane >> 4) < left)
-            d[s] = *reinterpret_cast<const v4i*>(
-                base + (int64_t(t) * (Step<FOUR>::kElems * 2) + s * 64) + at);
+        for (int j = 0; j < kLoads; ++j)
+            d[j] = *reinterpret_cast<const v4i*>(
+                base + (int64_t(t) * (Step<FOUR>::kElems * 2) + j * P * 64) + at);
     }
+    // The last step of a sum that ends inside it, `left` 8-element chunks.
+    static __device__ __forceinline__ void load_last(const char* base, int32_t t, int left,
+                                                     uint32_t at, int i, int g, v4i (&d)[kLoads]) {
+#pragma unroll
+        for (int j = 0; j < kLoads; ++j) {
+            d[j] = v4i{0, 0, 0, 0};
+            if ((j * P + i / kRows) * 4 + g < left)
+                d[j] = *reinterpret_cast<const v4i*>(
+                    base + (int64_t(t) * (Step<FOUR>::kElems * 2) + j * P * 64) + at);
+        }
+    }
+};
+// The P sums of a block joined: lane (i, g) gets row i % (16 / P)'s.
+template <int P>
+__device__ __forceinline__ f32x4 join_products(const f32x4 (&acc)[P], int lane) {
+    constexpr int R = 16 / P;
+    f32x4 v = acc[0];
+    if constexpr (P > 1) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            float sum = 0.0f;
+#pragma unroll
+            for (int q = 0; q < P; ++q)
+                sum += __shfl(acc[q][k], (lane & 48) + q * R + (lane & (R - 1)), 64);
+            v[k] = sum;
+        }
+    }
+    return v;
 }
 
-// The experts in use, in ascending order, from the slots' ids (a bit per expert
-// first). Every thread of the workgroup calls it.
+// The experts in use, in ascending order (found by a bit per expert). Every
+// thread of the workgroup calls it; `ids` are read once.
 struct InUse {
     uint32_t bits[kMaxWords];
-    int16_t expert[kMaxLayerSlots];
     int32_t count;
+    int16_t expert[kMaxLayerSlots];
+    int16_t id[kMaxLayerSlots];         // of each slot, -1 for none
 };
 __device__ inline void find_in_use(InUse& u, const int32_t* ids, int slots, int32_t E) {
+    const int lane = threadIdx.x & 63;
     if (threadIdx.x < kMaxWords) u.bits[threadIdx.x] = 0;
     __syncthreads();
     for (int p = threadIdx.x; p < slots; p += blockDim.x) {
         const int32_t e = ids[p];
-        if (e >= 0 && e < E) atomicOr(&u.bits[e >> 5], 1u << (e & 31));
+        const bool some = e >= 0 && e < E;
+        if (some) atomicOr(&u.bits[e >> 5], 1u << (e & 31));
+        u.id[p] = static_cast<int16_t>(some ? e : -1);
     }
     __syncthreads();
     if (threadIdx.x < 64) {
-        const int lane = threadIdx.x;
         uint32_t word = lane < kMaxWords ? u.bits[lane] : 0;
         const int mine = __popc(word);
         int incl = mine;
@@ -144,19 +190,24 @@ __device__ inline void find_in_use(InUse& u, const int32_t* ids, int slots, int3
     __syncthreads();
 }
 
-// Slots of expert e, ascending, into `list`; their number. A wavefront calls
-// it by itself.
-__device__ inline int find_slots(int16_t* list, const int32_t* ids, int slots, int32_t e) {
+// Slots of expert e, ascending, into `list`; their number and that of the slots
+// of lower experts. A wavefront calls it by itself.
+struct Found {
+    int n, before;
+};
+__device__ inline Found find_slots(int16_t* list, const InUse& u, int slots, int32_t e) {
     const int lane = threadIdx.x & 63;
-    int n = 0;
+    Found f = {0, 0};
     for (int p0 = 0; p0 < slots; p0 += 64) {
         const int p = p0 + lane;
-        const bool mine = p < slots && ids[p] == e;
-        const uint64_t all = __ballot(mine);
-        if (mine) list[n + __popcll(all & ((uint64_t(1) << lane) - 1))] = static_cast<int16_t>(p);
-        n += __popcll(all);
+        const int32_t id = p < slots ? u.id[p] : -1;
+        const uint64_t all = __ballot(id == e);
+        if (id == e)
+            list[f.n + __popcll(all & ((uint64_t(1) << lane) - 1))] = static_cast<int16_t>(p);
+        f.n += __popcll(all);
+        f.before += __popcll(__ballot(id >= 0 && id < e));
     }
-    return n;
+    return f;
 }
 // Between a wavefront's own LDS writes and reads by its other lanes.
 __device__ __forceinline__ void wave_sync() {
@@ -165,13 +216,21 @@ __device__ __forceinline__ void wave_sync() {
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
+// Where h keeps the 32 elements of group `group` of row `row` (their rests lie 64
+// bytes behind them).
+template <bool FOUR>
+__device__ __forceinline__ int64_t h_at(int32_t slots, int32_t row, int32_t group) {
+    constexpr int kGroups = Step<FOUR>::kProducts;
+    return ((int64_t(group / kGroups) * slots + row) * kGroups + group % kGroups) * 128;
+}
+
 // ---- Gate and up projections, the activation and the product ----------------
 
 constexpr int gate_waves(bool four) { return four ? 4 : 8; }
 constexpr int kGateBlocks = 4;          // two of gate rows, two of up rows
 
-template <bool FOUR, int NB>
-__global__ __launch_bounds__(gate_waves(FOUR) * 64, NB == 1 ? 4 : 2)
+template <bool FOUR, bool WIDE>
+__global__ __launch_bounds__(gate_waves(FOUR) * 64, WIDE ? 2 : 4)
 void few_tokens_gate_kernel(const char* __restrict__ x, const int32_t* __restrict__ ids, int32_t T,
                             int32_t K, int32_t E, const char* __restrict__ w,
                             const char* __restrict__ scales, int32_t D, int32_t F, int32_t ftiles,
@@ -180,7 +239,7 @@ void few_tokens_gate_kernel(const char* __restrict__ x, const int32_t* __restric
     constexpr int kWaves = gate_waves(FOUR);
     __shared__ InUse in_use;
     __shared__ int16_t list[kMaxLayerSlots];
-    __shared__ int32_t list_size;
+    __shared__ Found found;
     __shared__ f32x4 part[kWaves][kGateBlocks][64];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -190,11 +249,12 @@ void few_tokens_gate_kernel(const char* __restrict__ x, const int32_t* __restric
     if (which >= in_use.count) return;
     const int32_t e = __builtin_amdgcn_readfirstlane(in_use.expert[which]);
     if (wave == 0) {
-        const int n = find_slots(list, ids, slots, e);
-        if (lane == 0) list_size = n;
+        const Found f = find_slots(list, in_use, slots, e);
+        if (lane == 0) found = f;
     }
     __syncthreads();
-    const int n = __builtin_amdgcn_readfirstlane(list_size);
+    const int n = __builtin_amdgcn_readfirstlane(found.n);
+    const int row0 = __builtin_amdgcn_readfirstlane(found.before);
     const int i = lane & 15, g = lane >> 4;
     const int32_t f0 = ft * 32;
     const int32_t steps = (D + S::kElems - 1) / S::kElems;
@@ -211,47 +271,67 @@ void few_tokens_gate_kernel(const char* __restrict__ x, const int32_t* __restric
         if constexpr (FOUR) {
             const int64_t blk = int64_t(e) * nb * 2 + (up ? nb : 0) + ob;
             blocks[b].q = w + blk * steps * 1024;
-            blocks[b].scale = scales + blk * steps * 64;
         } else {
             blocks[b].q = w + (int64_t(e) * F * 2 + (up ? F : 0) + ob * 16) * (int64_t(D) * 2);
-            blocks[b].scale = nullptr;
         }
         at[b] = Block<FOUR>::offset(lane, min(i, F - 1 - ob * 16), int64_t(D) * 2);
     }
+    // Lane group g loads the scales of block g.
+    const char* scale = scales;
+    if constexpr (FOUR) {
+        const int32_t nb = (F + 15) / 16;
+        const int64_t blk =
+            int64_t(e) * nb * 2 + (g >= 2 ? nb : 0) + min(f0 / 16 + g % 2, nb - 1);
+        scale += blk * steps * 64 + i * 4;
+    }
 
-    // 16 NB of the slots, or what is left.
-    for (int first = 0; first < n; first += 16 * NB) {
+    // 16 NB / P of the slots from `first` on, or what is left.
+    auto run = [&](auto products, auto tiles, int first) {
+        constexpr int P = decltype(products)::value, NB = decltype(tiles)::value;
+        typedef Rows<FOUR, P> R;
         uint32_t xr[NB];                // below 2^32: 512 rows of at most 2^23 bytes
 #pragma unroll
         for (int b = 0; b < NB; ++b)
-            xr[b] = static_cast<uint32_t>(list[min(first + b * 16 + i, n - 1)] / K) *
-                        (static_cast<uint32_t>(D) * 2) + g * 16;
+            xr[b] = static_cast<uint32_t>(list[min(first + b * 16 + i % R::kRows, n - 1)] / K) *
+                        (static_cast<uint32_t>(D) * 2) + R::within(i, g);
         struct Data {
             Weights<FOUR> w[kGateBlocks];
-            v4i x[NB][S::kProducts];
+            uint32_t scale;
+            v4i x[NB][R::kLoads];
+        };
+        auto load_scale = [&](int32_t t, Data& d) {
+            d.scale = 0;
+            if constexpr (FOUR)
+                d.scale = *reinterpret_cast<const uint32_t*>(scale + int64_t(t) * 64);
         };
         auto load = [&](int32_t t, Data& d) {
+            load_scale(t, d);
 #pragma unroll
-            for (int b = 0; b < NB; ++b) load_rows<FOUR>(x, t, xr[b], d.x[b]);
+            for (int b = 0; b < NB; ++b) R::load(x, t, xr[b], d.x[b]);
 #pragma unroll
             for (int b = 0; b < kGateBlocks; ++b) blocks[b].load(t, at[b], lane, d.w[b]);
             __builtin_amdgcn_sched_barrier(0);
         };
-        f32x4 acc[kGateBlocks][NB];
+        f32x4 acc[kGateBlocks][NB][P];
 #pragma unroll
         for (int a = 0; a < kGateBlocks; ++a)
 #pragma unroll
-            for (int b = 0; b < NB; ++b) acc[a][b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int q = 0; q < P; ++q) acc[a][b][q] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         auto compute = [&](const Data& d) {
+            uint32_t sc[kGateBlocks];
+            spread(d.scale, sc);
 #pragma unroll
             for (int s = 0; s < S::kProducts; ++s)
 #pragma unroll
                 for (int a = 0; a < kGateBlocks; ++a) {
-                    const bf16x8 fw = d.w[a].frag(s);
+                    const bf16x8 fw = d.w[a].frag(s, sc[a]);
 #pragma unroll
                     for (int b = 0; b < NB; ++b)
-                        acc[a][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                            fw, __builtin_bit_cast(bf16x8, d.x[b][s]), acc[a][b], 0, 0, 0);
+                        acc[a][b][s % P] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                            fw, __builtin_bit_cast(bf16x8, d.x[b][s / P]), acc[a][b][s % P], 0, 0,
+                            0);
                 }
         };
         Data even, odd;
@@ -270,7 +350,8 @@ void few_tokens_gate_kernel(const char* __restrict__ x, const int32_t* __restric
         if (full < steps && wave == full % kWaves) {
             const int left = (D - full * S::kElems) / 8;
 #pragma unroll
-            for (int b = 0; b < NB; ++b) load_rows_last<FOUR>(x, full, left, xr[b], lane, even.x[b]);
+            for (int b = 0; b < NB; ++b) R::load_last(x, full, left, xr[b], i, g, even.x[b]);
+            load_scale(full, even);
 #pragma unroll
             for (int b = 0; b < kGateBlocks; ++b)
                 blocks[b].load_last(full, left, at[b], lane, even.w[b]);
@@ -282,7 +363,8 @@ void few_tokens_gate_kernel(const char* __restrict__ x, const int32_t* __restric
         for (int b = 0; b < NB; ++b) {
             __syncthreads();
 #pragma unroll
-            for (int a = 0; a < kGateBlocks; ++a) part[wave][a][lane] = acc[a][b];
+            for (int a = 0; a < kGateBlocks; ++a)
+                part[wave][a][lane] = join_products<P>(acc[a][b], lane);
             __syncthreads();
             if (wave < 2) {
                 f32x4 v = part[0][wave][lane], u = part[0][wave + 2][lane];
@@ -293,7 +375,7 @@ void few_tokens_gate_kernel(const char* __restrict__ x, const int32_t* __restric
                 }
                 const int r = first + b * 16 + i;
                 const int32_t f = f0 + wave * 16 + g * 4;
-                if (r < n && f < F) {
+                if (i < R::kRows && r < n && f < F) {
                     f32x4 rest;
 #pragma unroll
                     for (int k = 0; k < 4; ++k) v[k] = activate(act, v[k]) * u[k];
@@ -306,13 +388,16 @@ void few_tokens_gate_kernel(const char* __restrict__ x, const int32_t* __restric
                             __uint_as_float(k & 1 ? half & 0xFFFF0000u : half << 16);
                         rest[k] = fabsf(back) < INFINITY ? v[k] - back : 0.0f;
                     }
-                    char* at = h + (int64_t(list[r]) * F + f) * 2;
-                    *reinterpret_cast<v2i*>(at) = high;
-                    *reinterpret_cast<v2i*>(at + int64_t(slots) * F * 2) = pack_bf16x4(rest);
+                    char* to = h + h_at<FOUR>(slots, row0 + r, f / 32) + f % 32 * 2;
+                    *reinterpret_cast<v2i*>(to) = high;
+                    *reinterpret_cast<v2i*>(to + 64) = pack_bf16x4(rest);
                 }
             }
         }
-    }
+    };
+    const std::integral_constant<int, 1> one;
+    for (int first = 0; first < n; first += WIDE ? 32 : 16)
+        run(one, std::integral_constant<int, WIDE ? 2 : 1>{}, first);
 }
 
 // ---- Down projection and the sum over the slots ------------------------------
@@ -323,7 +408,7 @@ constexpr int kDownWaves = 8;
 // workgroup's LDS holds of their results.
 int most_parts(int slots) { return slots <= 64 ? 8 : slots <= 128 ? 4 : slots <= 256 ? 2 : 1; }
 
-template <bool FOUR, int NB>
+template <bool FOUR, bool WIDE>
 __global__ __launch_bounds__(kDownWaves * 64, 4)
 void few_tokens_down_kernel(const char* __restrict__ h, const int32_t* __restrict__ ids,
                             const float* __restrict__ scores, int32_t T, int32_t K, int32_t E,
@@ -355,78 +440,128 @@ void few_tokens_down_kernel(const char* __restrict__ h, const int32_t* __restric
         const int32_t to = static_cast<int32_t>(int64_t(steps) * (piece + 1) / parts);
         int16_t* list = lists[wave];
         wave_sync();                // the last task's reads of it are done
-        const int n = find_slots(list, ids, slots, e);
+        const Found f = find_slots(list, in_use, slots, e);
         wave_sync();
+        const int n = f.n;
         Block<FOUR> block;
+        const char* scale = scales;
         if constexpr (FOUR) {
             const int64_t blk = int64_t(e) * ((D + 15) / 16) + c0 / 16;
             block.q = w + blk * steps * 1024;
-            block.scale = scales + blk * steps * 64;
+            scale = scales + blk * steps * 64;
         } else {
             block.q = w + (int64_t(e) * D + c0) * (int64_t(F) * 2);
-            block.scale = nullptr;
         }
         const uint32_t at = Block<FOUR>::offset(lane, min(i, D - 1 - c0), int64_t(F) * 2);
-        // 8 NB of the slots, or what is left; lanes i < 8 take h's rounded
-        // numbers, the others what the rounding left.
-        for (int first = 0; first < n; first += 8 * NB) {
-            uint32_t hr[NB];            // below 2^32: 1024 rows of at most 2^22 bytes
+        // 8 NB / P of the slots from `first` on, or what is left: the first half of
+        // the rows are h's rounded numbers, the second what the rounding left.
+        auto run = [&](auto products, auto tiles, int first) {
+            constexpr int P = decltype(products)::value, NB = decltype(tiles)::value;
+            typedef Rows<FOUR, P> R;
+            constexpr int kSlots = R::kRows / 2;
+            // Rows of h: the slots in the order of their experts. A step's rows
+            // lie together, 128 bytes for each group of 32 elements.
+            constexpr int kRowBytes = S::kProducts * 128;
+            const char* hb = h + int64_t(f.before + first) * kRowBytes;
+            const int64_t pitch = int64_t(slots) * kRowBytes;
+            uint32_t hr[NB];
 #pragma unroll
             for (int b = 0; b < NB; ++b)
-                hr[b] = static_cast<uint32_t>(list[min(first + b * 8 + (i & 7), n - 1)] +
-                                              (i < 8 ? 0 : slots)) *
-                            (static_cast<uint32_t>(F) * 2) + g * 16;
+                hr[b] = min(b * 8 + i % kSlots, n - first - 1) * kRowBytes +
+                        i / R::kRows * 128 + (i % R::kRows < kSlots ? 0 : 64) + g * 16;
             struct Data {
                 Weights<FOUR> w;
-                v4i x[NB][S::kProducts];
+                v4i x[NB][R::kLoads];
             };
             auto load = [&](int32_t t, Data& d) {
                 block.load(t, at, lane, d.w);
 #pragma unroll
-                for (int b = 0; b < NB; ++b) load_rows<FOUR>(h, t, hr[b], d.x[b]);
+                for (int b = 0; b < NB; ++b) {
+                    uint32_t from = hr[b];
+                    reform(from);
+#pragma unroll
+                    for (int j = 0; j < R::kLoads; ++j)
+                        d.x[b][j] = *reinterpret_cast<const v4i*>(hb + (int64_t(t) * pitch + j * P * 128) +
+                                                                  from);
+                }
                 __builtin_amdgcn_sched_barrier(0);
             };
-            f32x4 acc[NB];
+            // The scales of 4 steps, lane group g's of step t + g.
+            auto load_scales = [&](int32_t t) -> uint32_t {
+                if constexpr (!FOUR) return 0;
+                uint32_t so = min(t + g, steps - 1) * 64 + i * 4;
+                return *reinterpret_cast<const uint32_t*>(scale + so);
+            };
+            f32x4 acc[NB][P];
 #pragma unroll
-            for (int b = 0; b < NB; ++b) acc[b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-            auto compute = [&](const Data& d) {
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int q = 0; q < P; ++q) acc[b][q] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            auto compute = [&](const Data& d, uint32_t sc) {
 #pragma unroll
                 for (int s = 0; s < S::kProducts; ++s) {
-                    const bf16x8 fw = d.w.frag(s);
+                    const bf16x8 fw = d.w.frag(s, sc);
 #pragma unroll
                     for (int b = 0; b < NB; ++b)
-                        acc[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                            fw, __builtin_bit_cast(bf16x8, d.x[b][s]), acc[b], 0, 0, 0);
+                        acc[b][s % P] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                            fw, __builtin_bit_cast(bf16x8, d.x[b][s / P]), acc[b][s % P], 0, 0, 0);
                 }
             };
             const int32_t end = min(to, full);
-            Data even, odd;
-            int32_t t = from;
-            if (t < end) load(t, even);
-            if (t + 1 < end) load(t + 1, odd);
-            while (t < end) {
-                compute(even);
-                if (t + 2 < end) load(t + 2, even);
-                if (++t >= end) break;
-                compute(odd);
-                if (t + 2 < end) load(t + 2, odd);
-                ++t;
+            // `kDepth` steps in flight, the scales of 4 at a time.
+            constexpr int kDepth = NB == 1 ? 4 : 2;
+            Data ring[kDepth];
+            uint32_t next = load_scales(from), sc[4];
+#pragma unroll
+            for (int j = 0; j < kDepth; ++j)
+                if (from + j < end) load(from + j, ring[j]);
+            for (int32_t t = from; t < end;) {
+                spread(next, sc);
+                if (t + 4 < steps) next = load_scales(t + 4);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if (t >= end) break;
+                    compute(ring[j % kDepth], sc[j]);
+                    if (t + kDepth < end) load(t + kDepth, ring[j % kDepth]);
+                    ++t;
+                }
             }
             if (full < to) {
                 const int left = (F - full * S::kElems) / 8;
 #pragma unroll
                 for (int b = 0; b < NB; ++b)
-                    load_rows_last<FOUR>(h, full, left, hr[b], lane, even.x[b]);
-                block.load_last(full, left, at, lane, even.w);
-                compute(even);
+#pragma unroll
+                    for (int j = 0; j < R::kLoads; ++j) {
+                        ring[0].x[b][j] = v4i{0, 0, 0, 0};
+                        if ((j * P + i / R::kRows) * 4 + g < left)
+                            ring[0].x[b][j] = *reinterpret_cast<const v4i*>(
+                                hb + (int64_t(full) * pitch + j * P * 128) + hr[b]);
+                    }
+                block.load_last(full, left, at, lane, ring[0].w);
+                spread(load_scales(full), sc);
+                compute(ring[0], sc[0]);
             }
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
-                f32x4 v = acc[b];
+                f32x4 v = join_products<P>(acc[b], lane);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) v[k] += __shfl_xor(v[k], 8, 64);
+                for (int k = 0; k < 4; ++k) v[k] += __shfl_xor(v[k], kSlots, 64);
                 const int r = first + b * 8 + i;
-                if (i < 8 && r < n) results[(piece * slots + list[r]) * 4 + g] = v;
+                if (i < kSlots && r < n) results[(piece * slots + list[r]) * 4 + g] = v;
+            }
+        };
+        const std::integral_constant<int, 1> one;
+        for (int first = 0; first < n;) {
+            const int left = n - first;
+            if (FOUR && left <= 2) {
+                run(std::integral_constant<int, S::kProducts>{}, one, first);
+                first += 2;
+            } else if (left <= 4) {
+                run(std::integral_constant<int, 2>{}, one, first);
+                first += 4;
+            } else {
+                run(one, std::integral_constant<int, WIDE ? 2 : 1>{}, first);
+                first += WIDE ? 16 : 8;
             }
         }
     }
@@ -454,12 +589,12 @@ int64_t gate_workgroups(const LayerArgs& a) {
     return gate_tiles(a) * (slots < a.E ? slots : a.E);
 }
 
-template <bool FOUR, int NB>
+template <bool FOUR, bool WIDE>
 hipError_t launch(const LayerArgs& a, hipStream_t stream) {
     const char* w1 = static_cast<const char*>(a.w_gate_up);
     const char* w2 = static_cast<const char*>(a.w_down);
     const int slots = a.T * a.K;
-    hipLaunchKernelGGL((few_tokens_gate_kernel<FOUR, NB>),
+    hipLaunchKernelGGL((few_tokens_gate_kernel<FOUR, WIDE>),
                        dim3(static_cast<uint32_t>(gate_workgroups(a))), dim3(gate_waves(FOUR) * 64),
                        0, stream, static_cast<const char*>(a.x), a.ids, a.T, a.K, a.E, w1,
                        w1 + mxfp4_tiles(a.E, 2 * a.F, a.D) * 1024, a.D, a.F,
@@ -468,7 +603,7 @@ hipError_t launch(const LayerArgs& a, hipStream_t stream) {
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     const int most = most_parts(slots);
-    hipLaunchKernelGGL((few_tokens_down_kernel<FOUR, NB>),
+    hipLaunchKernelGGL((few_tokens_down_kernel<FOUR, WIDE>),
                        dim3(static_cast<uint32_t>((a.D + 15) / 16)), dim3(kDownWaves * 64),
                        slots * most * 64, stream, static_cast<const char*>(a.workspace), a.ids,
                        a.scores, a.T, a.K, a.E, w2, w2 + mxfp4_tiles(a.E, a.D, a.F) * 1024, a.D,
@@ -483,8 +618,8 @@ int64_t few_tokens_grid(const LayerArgs& a) { return gate_workgroups(a) * (gate_
 hipError_t launch_few_tokens(const LayerArgs& a, hipStream_t stream) {
     // Twice the slots per pass over the weights where experts have many.
     if (int64_t(a.T) * a.K >= int64_t(4) * a.E)
-        return a.four ? launch<true, 2>(a, stream) : launch<false, 2>(a, stream);
-    return a.four ? launch<true, 1>(a, stream) : launch<false, 1>(a, stream);
+        return a.four ? launch<true, true>(a, stream) : launch<false, true>(a, stream);
+    return a.four ? launch<true, false>(a, stream) : launch<false, false>(a, stream);
 }
 
 }  // namespace moe

@@ -217,7 +217,7 @@ int64_t moe_few_tokens_workspace_bytes(int32_t T, int32_t K, int32_t n_hidden) {
     if (T < 0 || K < 1 || K > MOE_MAX_TOPK || T > MOE_MAX_LAYER_SLOTS / K || !width_ok(n_hidden, 8) ||
         n_hidden > MOE_MAX_GEMM_WIDTH / 2)
         return -1;
-    return int64_t(T) * K * n_hidden * 4;
+    return int64_t(T) * K * ((n_hidden + 127) / 128 * 128) * 4;
 }
 
 int moe_few_tokens_layer(const void* d_x, const float* d_topk_scores, const int32_t* d_topk_ids,

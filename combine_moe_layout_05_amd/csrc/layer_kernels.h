@@ -95,7 +95,7 @@ struct LayerArgs {
     int32_t D;              // multiple of 8 (four: of 32)
     int32_t F;              // multiple of 8 (four: of 32)
     int32_t activation;
-    void* workspace;        // 4 T K F bytes
+    void* workspace;        // 4 T K F bytes, F rounded up to 128
     void* y;                // bf16 [T][D]
 };
 hipError_t launch_few_tokens(const LayerArgs& a, hipStream_t stream);

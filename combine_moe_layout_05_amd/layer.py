@@ -59,8 +59,8 @@ def moe_layer(x_TD: torch.Tensor, topk_scores_TK: torch.Tensor, topk_expert_ids_
         raise ValueError(f"shapes: w_gate_up [E, 2 F, {D}], w_down [E, {D}, F]; got {shapes[0]}, "
                          f"{shapes[1]}")
     y = torch.empty_like(x_TD)
-    # h between the two launches: 4 bytes for each of its elements.
-    nbytes = 4 * T * K * F
+    # h between the two launches (moe_few_tokens_workspace_bytes).
+    nbytes = 4 * T * K * (-(-F // 128) * 128)
     h = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     _call("moe_few_tokens_layer", dev, x_TD.data_ptr(), topk_scores_TK.data_ptr(),
           topk_expert_ids_TK.data_ptr(), T, K, w1.data_ptr(), w2.data_ptr(),

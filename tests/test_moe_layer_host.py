@@ -39,11 +39,11 @@ def test_sizes(lib, layout):
 def test_workspace(lib):
     size = lib.moe_few_tokens_workspace_bytes
     assert size(1, 8, 2048) == 8 * 2048 * 4 and size(0, 1, 8) == 0
-    assert size(512, 1, 8) == 512 * 32 and size(513, 1, 8) == -1
+    assert size(512, 1, 8) == 512 * 512 and size(513, 1, 8) == -1
     for bad in [(-1, 8, 64), (65, 8, 64), (1, 0, 64), (1, 17, 64), (1, 8, 12), (1, 8, MAX)]:
         assert size(*bad) == -1, bad
     fn, args = lib.moe_few_tokens_layer, dict(CALL, T=4)
-    assert fn(*dict(args, bytes=4 * 8 * 32 * 4 - 1).values()) == L.MOE_ERR_WORKSPACE
+    assert fn(*dict(args, bytes=4 * 8 * 128 * 4 - 1).values()) == L.MOE_ERR_WORKSPACE
     assert fn(*dict(args, bytes=-1).values()) == L.MOE_ERR_WORKSPACE
 
 
@@ -54,7 +54,7 @@ def test_pointers(lib):
         by = 2 if key in ("scores", "ids") else 8
         assert fn(*dict(args, **{key: args[key] + by}).values()) == BAD, key
     sizes = dict(x=4 * 64 * 2, scores=128, ids=128, w1=16 * 64 * 64 * 2, w2=16 * 64 * 32 * 2,
-                 ws=4 * 8 * 32 * 4)
+                 ws=4 * 8 * 128 * 4)
     for key, size in sizes.items():
         for at in (args[key], args[key] + size - 16, args[key] + 16 - 4 * 64 * 2):
             assert fn(*dict(args, y=at).values()) == BAD, key
@@ -81,6 +81,12 @@ def test_binding_refusals(monkeypatch):
     p1 = moe.Mxfp4ExpertWeights(_fake(E * 4 * 1088, dtype=torch.uint8), E, 2 * F, D)
     p2 = moe.Mxfp4ExpertWeights(_fake(E * 4 * 1088, dtype=torch.uint8), E, D, F)
     assert moe.moe_layer(*good.values()).shape == (T, D)
+    # the workspace the binding gives is what the library asks for
+    size = L.load().moe_few_tokens_workspace_bytes
+    assert calls[0][-2] == size(T, K, F)
+    for f in (8, 128, 136, 2048):
+        moe.moe_layer(*dict(good, w1=_fake(E, 2 * f, D), w2=_fake(E, D, f)).values())
+        assert calls[-1][-2] == size(T, K, f)
     assert moe.moe_layer(*dict(good, w1=p1, w2=p2).values()).shape == (T, D)
     n = len(calls)
     i32, f32 = torch.int32, torch.float32
