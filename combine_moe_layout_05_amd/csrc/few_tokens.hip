@@ -408,20 +408,21 @@ constexpr int kDownWaves = 8;
 // workgroup's LDS holds of their results.
 int most_parts(int slots) { return slots <= 64 ? 8 : slots <= 128 ? 4 : slots <= 256 ? 2 : 1; }
 
-template <bool FOUR, bool WIDE>
-__global__ __launch_bounds__(kDownWaves * 64, 4)
+template <bool FOUR, bool WIDE, int CB>
+__global__ __launch_bounds__(kDownWaves * 64, CB == 1 ? 4 : 2)
 void few_tokens_down_kernel(const char* __restrict__ h, const int32_t* __restrict__ ids,
                             const float* __restrict__ scores, int32_t T, int32_t K, int32_t E,
                             const char* __restrict__ w, const char* __restrict__ scales, int32_t D,
                             int32_t F, int32_t most, __bf16* __restrict__ y) {
     typedef Step<FOUR> S;
-    extern __shared__ f32x4 results[];          // [part][slot][4 chunks of 4 columns]
+    extern __shared__ f32x4 results[];          // [part][slot][chunks of 4 columns]
     __shared__ InUse in_use;
     __shared__ int16_t lists[kDownWaves][kMaxLayerSlots];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int slots = T * K;
-    const int32_t c0 = blockIdx.x * 16;
+    constexpr int kColumns = 16 * CB;
+    const int32_t c0 = blockIdx.x * kColumns;
     find_in_use(in_use, ids, slots, E);
     const int count = __builtin_amdgcn_readfirstlane(in_use.count);
     const int i = lane & 15, g = lane >> 4;
@@ -443,16 +444,24 @@ void few_tokens_down_kernel(const char* __restrict__ h, const int32_t* __restric
         const Found f = find_slots(list, in_use, slots, e);
         wave_sync();
         const int n = f.n;
-        Block<FOUR> block;
-        const char* scale = scales;
-        if constexpr (FOUR) {
-            const int64_t blk = int64_t(e) * ((D + 15) / 16) + c0 / 16;
-            block.q = w + blk * steps * 1024;
-            scale = scales + blk * steps * 64;
-        } else {
-            block.q = w + (int64_t(e) * D + c0) * (int64_t(F) * 2);
+        // Blocks past the matrix read its last rows and are not stored.
+        Block<FOUR> blocks[CB];
+        const char* scale[CB];
+        uint32_t at[CB];
+#pragma unroll
+        for (int c = 0; c < CB; ++c) {
+            const int32_t nb = (D + 15) / 16;
+            const int32_t ob = min(c0 / 16 + c, nb - 1);
+            scale[c] = scales;
+            if constexpr (FOUR) {
+                const int64_t blk = int64_t(e) * nb + ob;
+                blocks[c].q = w + blk * steps * 1024;
+                scale[c] += blk * steps * 64;
+            } else {
+                blocks[c].q = w + (int64_t(e) * D + ob * 16) * (int64_t(F) * 2);
+            }
+            at[c] = Block<FOUR>::offset(lane, min(i, D - 1 - ob * 16), int64_t(F) * 2);
         }
-        const uint32_t at = Block<FOUR>::offset(lane, min(i, D - 1 - c0), int64_t(F) * 2);
         // 8 NB / P of the slots from `first` on, or what is left: the first half of
         // the rows are h's rounded numbers, the second what the rounding left.
         auto run = [&](auto products, auto tiles, int first) {
@@ -470,11 +479,12 @@ void few_tokens_down_kernel(const char* __restrict__ h, const int32_t* __restric
                 hr[b] = min(b * 8 + i % kSlots, n - first - 1) * kRowBytes +
                         i / R::kRows * 128 + (i % R::kRows < kSlots ? 0 : 64) + g * 16;
             struct Data {
-                Weights<FOUR> w;
+                Weights<FOUR> w[CB];
                 v4i x[NB][R::kLoads];
             };
             auto load = [&](int32_t t, Data& d) {
-                block.load(t, at, lane, d.w);
+#pragma unroll
+                for (int c = 0; c < CB; ++c) blocks[c].load(t, at[c], lane, d.w[c]);
 #pragma unroll
                 for (int b = 0; b < NB; ++b) {
                     uint32_t from = hr[b];
@@ -487,41 +497,52 @@ void few_tokens_down_kernel(const char* __restrict__ h, const int32_t* __restric
                 __builtin_amdgcn_sched_barrier(0);
             };
             // The scales of 4 steps, lane group g's of step t + g.
-            auto load_scales = [&](int32_t t) -> uint32_t {
-                if constexpr (!FOUR) return 0;
-                uint32_t so = min(t + g, steps - 1) * 64 + i * 4;
-                return *reinterpret_cast<const uint32_t*>(scale + so);
+            auto load_scales = [&](int32_t t, uint32_t (&d)[CB]) {
+                const uint32_t so = min(t + g, steps - 1) * 64 + i * 4;
+#pragma unroll
+                for (int c = 0; c < CB; ++c)
+                    d[c] = FOUR ? *reinterpret_cast<const uint32_t*>(scale[c] + so) : 0;
             };
-            f32x4 acc[NB][P];
+            f32x4 acc[CB][NB][P];
 #pragma unroll
-            for (int b = 0; b < NB; ++b)
+            for (int c = 0; c < CB; ++c)
 #pragma unroll
-                for (int q = 0; q < P; ++q) acc[b][q] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-            auto compute = [&](const Data& d, uint32_t sc) {
+                for (int b = 0; b < NB; ++b)
 #pragma unroll
-                for (int s = 0; s < S::kProducts; ++s) {
-                    const bf16x8 fw = d.w.frag(s, sc);
+                    for (int q = 0; q < P; ++q) acc[c][b][q] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            uint32_t next[CB], sc[CB][4];
+            auto spread_scales = [&] {
 #pragma unroll
-                    for (int b = 0; b < NB; ++b)
-                        acc[b][s % P] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                            fw, __builtin_bit_cast(bf16x8, d.x[b][s / P]), acc[b][s % P], 0, 0, 0);
-                }
+                for (int c = 0; c < CB; ++c) spread(next[c], sc[c]);
+            };
+            auto compute = [&](const Data& d, int j) {
+#pragma unroll
+                for (int s = 0; s < S::kProducts; ++s)
+#pragma unroll
+                    for (int c = 0; c < CB; ++c) {
+                        const bf16x8 fw = d.w[c].frag(s, sc[c][j]);
+#pragma unroll
+                        for (int b = 0; b < NB; ++b)
+                            acc[c][b][s % P] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                                fw, __builtin_bit_cast(bf16x8, d.x[b][s / P]), acc[c][b][s % P], 0,
+                                0, 0);
+                    }
             };
             const int32_t end = min(to, full);
             // `kDepth` steps in flight, the scales of 4 at a time.
             constexpr int kDepth = NB == 1 ? 4 : 2;
             Data ring[kDepth];
-            uint32_t next = load_scales(from), sc[4];
+            load_scales(from, next);
 #pragma unroll
             for (int j = 0; j < kDepth; ++j)
                 if (from + j < end) load(from + j, ring[j]);
             for (int32_t t = from; t < end;) {
-                spread(next, sc);
-                if (t + 4 < steps) next = load_scales(t + 4);
+                spread_scales();
+                if (t + 4 < steps) load_scales(t + 4, next);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     if (t >= end) break;
-                    compute(ring[j % kDepth], sc[j]);
+                    compute(ring[j % kDepth], j);
                     if (t + kDepth < end) load(t + kDepth, ring[j % kDepth]);
                     ++t;
                 }
@@ -537,18 +558,24 @@ void few_tokens_down_kernel(const char* __restrict__ h, const int32_t* __restric
                             ring[0].x[b][j] = *reinterpret_cast<const v4i*>(
                                 hb + (int64_t(full) * pitch + j * P * 128) + hr[b]);
                     }
-                block.load_last(full, left, at, lane, ring[0].w);
-                spread(load_scales(full), sc);
-                compute(ring[0], sc[0]);
+#pragma unroll
+                for (int c = 0; c < CB; ++c)
+                    blocks[c].load_last(full, left, at[c], lane, ring[0].w[c]);
+                load_scales(full, next);
+                spread_scales();
+                compute(ring[0], 0);
             }
 #pragma unroll
-            for (int b = 0; b < NB; ++b) {
-                f32x4 v = join_products<P>(acc[b], lane);
+            for (int b = 0; b < NB; ++b)
 #pragma unroll
-                for (int k = 0; k < 4; ++k) v[k] += __shfl_xor(v[k], kSlots, 64);
-                const int r = first + b * 8 + i;
-                if (i < kSlots && r < n) results[(piece * slots + list[r]) * 4 + g] = v;
-            }
+                for (int c = 0; c < CB; ++c) {
+                    f32x4 v = join_products<P>(acc[c][b], lane);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) v[k] += __shfl_xor(v[k], kSlots, 64);
+                    const int r = first + b * 8 + i;
+                    if (i < kSlots && r < n)
+                        results[((piece * slots + list[r]) * CB + c) * 4 + g] = v;
+                }
         };
         const std::integral_constant<int, 1> one;
         for (int first = 0; first < n;) {
@@ -567,16 +594,16 @@ void few_tokens_down_kernel(const char* __restrict__ h, const int32_t* __restric
     }
     __syncthreads();
     const float* sums = reinterpret_cast<const float*>(results);
-    for (int q = threadIdx.x; q < T * 16; q += kDownWaves * 64) {
-        const int t = q >> 4, c = q & 15;
+    for (int q = threadIdx.x; q < T * kColumns; q += kDownWaves * 64) {
+        const int t = q / kColumns, c = q % kColumns;
         if (c0 + c >= D) continue;
         float v = 0.0f;
         for (int k = 0; k < K; ++k) {
             const int p = t * K + k;
             const int32_t e = ids[p];
             if (e < 0 || e >= E) continue;
-            float one = sums[p * 16 + c];
-            for (int j = 1; j < parts; ++j) one += sums[(j * slots + p) * 16 + c];
+            float one = sums[p * kColumns + c];
+            for (int j = 1; j < parts; ++j) one += sums[(j * slots + p) * kColumns + c];
             v = __builtin_fmaf(scores[p], one, v);
         }
         y[int64_t(t) * D + c0 + c] = static_cast<__bf16>(v);
@@ -603,9 +630,14 @@ hipError_t launch(const LayerArgs& a, hipStream_t stream) {
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     const int most = most_parts(slots);
-    hipLaunchKernelGGL((few_tokens_down_kernel<FOUR, WIDE>),
-                       dim3(static_cast<uint32_t>((a.D + 15) / 16)), dim3(kDownWaves * 64),
-                       slots * most * 64, stream, static_cast<const char*>(a.workspace), a.ids,
+    auto down = few_tokens_down_kernel<FOUR, WIDE, 1>;
+    int columns = 16;
+    if (a.D > 16 * 256) {
+        down = few_tokens_down_kernel<FOUR, WIDE, 2>;
+        columns = 32;
+    }
+    hipLaunchKernelGGL(down, dim3(static_cast<uint32_t>((a.D + columns - 1) / columns)),
+                       dim3(kDownWaves * 64), slots * most * 4 * columns, stream, static_cast<const char*>(a.workspace), a.ids,
                        a.scores, a.T, a.K, a.E, w2, w2 + mxfp4_tiles(a.E, a.D, a.F) * 1024, a.D,
                        a.F, most, static_cast<__bf16*>(a.y));
     return hipGetLastError();

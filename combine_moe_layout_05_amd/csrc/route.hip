@@ -12,7 +12,9 @@
 // the `kept` best groups can be chosen, by the group's largest v (softmax) or the
 // sum of its two largest (sigmoid).
 //
-// One wavefront per token; lane j holds experts j, j + 64, ...
+// Up to 256 experts and 8 of them per token: 16 lanes per token, which select by
+// 32-bit keys and check the result, with the slow form for tokens that the check
+// does not clear. Else one wavefront per token; lane j holds experts j, j + 64, ...
 #include <cmath>
 
 #include "layer_kernels.h"
@@ -30,10 +32,47 @@ __device__ __forceinline__ float logit_at(const __bf16* p, int64_t i) {
 // Experts that take no part have a logit of -inf from here on.
 __device__ __forceinline__ float taking_part(float l) { return l == l ? l : -INFINITY; }
 
-__device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor(v, d, 64));
-    return v;
+// v moved between lanes by a data-parallel primitive; lanes it gives nothing keep
+// theirs.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int32_t moved(int32_t v) {
+    return __builtin_amdgcn_update_dpp(v, v, CTRL, ROWS, 0xF, false);
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float moved(float v) {
+    return __builtin_bit_cast(float, moved<CTRL, ROWS>(__builtin_bit_cast(int32_t, v)));
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double moved(double v) {
+    typedef int32_t two __attribute__((ext_vector_type(2)));
+    const two w = __builtin_bit_cast(two, v);
+    return __builtin_bit_cast(double,
+                              two{moved<CTRL, ROWS>(w[0]), moved<CTRL, ROWS>(w[1])});
+}
+__device__ __forceinline__ float last_lane(float v) {
+    return __builtin_bit_cast(
+        float, __builtin_amdgcn_readlane(__builtin_bit_cast(int32_t, v), 63));
+}
+__device__ __forceinline__ double last_lane(double v) {
+    typedef int32_t two __attribute__((ext_vector_type(2)));
+    const two w = __builtin_bit_cast(two, v);
+    return __builtin_bit_cast(double, two{__builtin_amdgcn_readlane(w[0], 63),
+                                          __builtin_amdgcn_readlane(w[1], 63)});
+}
+__device__ __forceinline__ float larger(float a, float b) { return fmaxf(a, b); }
+__device__ __forceinline__ double larger(double a, double b) { return fmax(a, b); }
+
+// The wavefront's largest value (none is a NaN), in every lane: within rows of 16
+// by shifts of 1, 2, 4 and 8, then from each row's last lane to the rows behind it.
+template <class V>
+__device__ __forceinline__ V wave_max(V v) {
+    v = larger(v, moved<0x111, 0xF>(v));
+    v = larger(v, moved<0x112, 0xF>(v));
+    v = larger(v, moved<0x114, 0xF>(v));
+    v = larger(v, moved<0x118, 0xF>(v));
+    v = larger(v, moved<0x142, 0xA>(v));
+    v = larger(v, moved<0x143, 0xC>(v));
+    return last_lane(v);
 }
 __device__ __forceinline__ float wave_sum(float v) {
 #pragma unroll
@@ -41,33 +80,19 @@ __device__ __forceinline__ float wave_sum(float v) {
     return v;
 }
 
-// The largest of the lanes' values and, of equal ones, the lowest index.
-template <class V>
-__device__ __forceinline__ void wave_best(V& v, int& at) {
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) {
-        const V ov = __shfl_xor(v, d, 64);
-        const int oi = __shfl_xor(at, d, 64);
-        if (ov > v || (ov == v && oi < at)) {
-            v = ov;
-            at = oi;
-        }
-    }
-}
-
-// The wavefront's best of v and its expert; at least one of the lanes' own
-// experts is named even where all hold -inf.
+// The wavefront's largest of v, and the lowest of the experts that have it.
 template <int VALS, class V>
-__device__ __forceinline__ void best_of(const V (&v)[VALS], int lane, V& top, int& at) {
+__device__ __forceinline__ void best_of(const V (&v)[VALS], V& top, int& at) {
     top = v[0];
-    at = lane;
 #pragma unroll
-    for (int i = 1; i < VALS; ++i)
-        if (v[i] > top) {
-            top = v[i];
-            at = i * 64 + lane;
-        }
-    wave_best(top, at);
+    for (int i = 1; i < VALS; ++i) top = larger(top, v[i]);
+    top = wave_max(top);
+    at = -1;
+#pragma unroll
+    for (int i = 0; i < VALS; ++i) {
+        const uint64_t here = __ballot(v[i] == top);
+        if (at < 0 && here) at = i * 64 + __ffsll(static_cast<unsigned long long>(here)) - 1;
+    }
 }
 
 template <int VALS, class V>
@@ -91,21 +116,22 @@ __device__ int select(V (&v)[VALS], int lane, int K, int E, int groups, int kept
                 const int e = i * 64 + lane;
                 w[i] = e >= g * size && e < (g + 1) * size ? v[i] : V(-INFINITY);
             }
-            V first, second = -INFINITY;
-            int at, unused;
-            best_of<VALS, V>(w, lane, first, at);
+            V first, second;
+            int at;
+            best_of<VALS, V>(w, first, at);
             if (pairs && size > 1) {
                 take_out<VALS, V>(w, lane, at);
-                best_of<VALS, V>(w, lane, second, unused);
+                best_of<VALS, V>(w, second, at);
                 if (second > V(-INFINITY)) first += second;
             }
             if (lane == g) value = first;
         }
         uint64_t open = 0;
         for (int j = 0; j < kept; ++j) {
-            V top = value;
-            int at = lane;
-            wave_best(top, at);
+            const V one[1] = {value};
+            V top;
+            int at;
+            best_of<1, V>(one, top, at);
             if (!(top > V(-INFINITY))) break;
             open |= uint64_t(1) << at;
             if (lane == at) value = -INFINITY;
@@ -120,7 +146,7 @@ __device__ int select(V (&v)[VALS], int lane, int K, int E, int groups, int kept
     for (int k = 0; k < K; ++k) {
         V top;
         int at;
-        best_of<VALS, V>(v, lane, top, at);
+        best_of<VALS, V>(v, top, at);
         if (!(top > V(-INFINITY))) break;
         if (lane == k) mine = at;
         take_out<VALS, V>(v, lane, at);
@@ -139,6 +165,32 @@ __device__ __forceinline__ float score_of(bool sigmoid, bool renormalize, int id
     return p;
 }
 
+// The choice of one token by a whole wavefront: lane k < K gets the k-th
+// expert or -1.
+template <int VALS, class L>
+__device__ int choose(const L* in, const float* bias, int lane, int32_t K, int32_t E, bool sigmoid,
+                      int32_t groups, int32_t kept) {
+    float l[VALS];
+#pragma unroll
+    for (int i = 0; i < VALS; ++i) {
+        const int e = i * 64 + lane;
+        l[i] = e < E ? taking_part(logit_at(in, e)) : -INFINITY;
+    }
+    if (!sigmoid || (!bias && groups == 1))
+        return select<VALS, float>(l, lane, K, E, groups, kept, sigmoid);
+    double v[VALS];
+#pragma unroll
+    for (int i = 0; i < VALS; ++i) {
+        v[i] = -INFINITY;
+        if (l[i] > -INFINITY) {
+            v[i] = 1.0 / (1.0 + exp(-static_cast<double>(l[i])));
+            if (bias) v[i] += static_cast<double>(bias[i * 64 + lane]);
+            if (!(v[i] == v[i])) v[i] = -INFINITY;
+        }
+    }
+    return select<VALS, double>(v, lane, K, E, groups, kept, true);
+}
+
 template <int VALS, class L>
 __global__ __launch_bounds__(kWaves * 64)
 void route_kernel(const L* __restrict__ logits, const float* __restrict__ bias, int32_t T,
@@ -149,48 +201,323 @@ void route_kernel(const L* __restrict__ logits, const float* __restrict__ bias, 
     const int64_t row = int64_t(blockIdx.x) * kWaves + (threadIdx.x >> 6);
     if (row >= T) return;
     const L* in = logits + row * E;
-    float l[VALS];
-#pragma unroll
-    for (int i = 0; i < VALS; ++i) {
-        const int e = i * 64 + lane;
-        l[i] = e < E ? taking_part(logit_at(in, e)) : -INFINITY;
-    }
-    float top = 0.0f, sum = 0.0f;
+    float top = -INFINITY, sum = 0.0f;
     if (!sigmoid) {
-        top = l[0];
-#pragma unroll
-        for (int i = 1; i < VALS; ++i) top = fmaxf(top, l[i]);
+        for (int e = lane; e < E; e += 64) top = fmaxf(top, taking_part(logit_at(in, e)));
         top = wave_max(top);
         if (!renormalize && top > -INFINITY) {
-#pragma unroll
-            for (int i = 0; i < VALS; ++i)
-                if (l[i] > -INFINITY) sum += expf(l[i] - top);
+            for (int e = lane; e < E; e += 64) {
+                const float v = taking_part(logit_at(in, e));
+                if (v > -INFINITY) sum += expf(v - top);
+            }
             sum = wave_sum(sum);
         }
     }
-    int id;
-    if (sigmoid && (bias || groups > 1)) {
-        double v[VALS];
-#pragma unroll
-        for (int i = 0; i < VALS; ++i) {
-            const int e = i * 64 + lane;
-            v[i] = -INFINITY;
-            if (l[i] > -INFINITY) {
-                v[i] = 1.0 / (1.0 + exp(-static_cast<double>(l[i])));
-                if (bias) v[i] += static_cast<double>(bias[e]);
-                if (!(v[i] == v[i])) v[i] = -INFINITY;
-            }
-        }
-        id = select<VALS, double>(v, lane, K, E, groups, kept, true);
-    } else {
-        id = select<VALS, float>(l, lane, K, E, groups, kept, sigmoid != 0);
-    }
+    const int id = choose<VALS, L>(in, bias, lane, K, E, sigmoid != 0, groups, kept);
     float p = 0.0f;
     if (id >= 0) p = logit_at(in, id);
     p = score_of(sigmoid, renormalize, id, p, top, sum);
     if (lane < K) {
         ids[row * K + lane] = id;
         scores[row * K + lane] = p * scale;
+    }
+}
+
+// ---- 16 lanes per token ------------------------------------------------------
+//
+// Lane j of a token holds experts VALS j .. VALS j + VALS - 1. Each value becomes a
+// key of 32 bits: its distance to the token's largest in 24 bits of 2^-20 (16 in
+// all), and the expert's index, so that keys differ and equal values go by index.
+// A lane sorts its keys, the lanes' lists of 8 are merged by rotations, after which
+// all hold the token's 8 largest keys in order: some 60 instructions per token
+// where 8 rounds of a search over the wavefront take several hundred.
+//
+// Then the choice is checked against the values themselves: neighbours in order
+// and every other expert below the last, by more than the error of a value in 32
+// bits where it is one (a sigmoid plus a bias), exactly where it is a logit. A token
+// that fails (two values nearer than that, fewer experts than slots, values more
+// than 16 apart, infinities) is chosen for by the whole wavefront.
+constexpr int kLanes = 16;
+constexpr int kList = 8;
+
+template <int N>
+__device__ __forceinline__ float ror(float v) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int32_t, v),
+                                                              0x120 + N, 0xF, 0xF, true));
+}
+template <int N>
+__device__ __forceinline__ uint32_t ror(uint32_t v) {
+    return static_cast<uint32_t>(
+        __builtin_amdgcn_mov_dpp(static_cast<int32_t>(v), 0x120 + N, 0xF, 0xF, true));
+}
+__device__ __forceinline__ float lanes_max(float v) {
+    v = fmaxf(v, ror<8>(v));
+    v = fmaxf(v, ror<4>(v));
+    v = fmaxf(v, ror<2>(v));
+    return fmaxf(v, ror<1>(v));
+}
+__device__ __forceinline__ float lanes_sum(float v) {
+    v += ror<8>(v);
+    v += ror<4>(v);
+    v += ror<2>(v);
+    return v + ror<1>(v);
+}
+
+// Lanes D, D + 1, ... before this one, in a circle, whose group goes before this
+// lane's: a larger value, or the same and a lower index.
+template <int D>
+__device__ __forceinline__ int lanes_ahead(float value, int j, int span) {
+    if constexpr (D == kLanes) {
+        return 0;
+    } else {
+        const float other = ror<D>(value);
+        const int at = (j - D) & (kLanes - 1);
+        const bool first = other > value || (other == value && at < (j & ~(span - 1)));
+        return first + lanes_ahead<D + 1>(value, j, span);
+    }
+}
+
+__device__ __forceinline__ void order(uint32_t& a, uint32_t& b) {   // a >= b
+    const uint32_t hi = max(a, b);
+    b = min(a, b);
+    a = hi;
+}
+// Descending order of N values (a power of two), by a bitonic network.
+template <int N>
+__device__ __forceinline__ void sort_keys(uint32_t* v) {
+#pragma unroll
+    for (int k = 2; k <= N; k *= 2)
+#pragma unroll
+        for (int j = k / 2; j > 0; j /= 2)
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                if ((i ^ j) > i) {
+                    if ((i & k) == 0)
+                        order(v[i], v[i ^ j]);
+                    else
+                        order(v[i ^ j], v[i]);
+                }
+}
+// The 8 largest of two descending lists, in order, into a. b is reversed
+// against a, which makes the larger ones of each pair a bitonic sequence.
+__device__ __forceinline__ void merge_keys(uint32_t (&a)[kList], const uint32_t (&b)[kList]) {
+#pragma unroll
+    for (int i = 0; i < kList; ++i) a[i] = max(a[i], b[kList - 1 - i]);
+#pragma unroll
+    for (int j = kList / 2; j > 0; j /= 2)
+#pragma unroll
+        for (int i = 0; i < kList; ++i)
+            if ((i ^ j) > i) order(a[i], a[i ^ j]);
+}
+template <int N>
+__device__ __forceinline__ void merge_lanes(uint32_t (&a)[kList]) {
+    uint32_t b[kList];
+#pragma unroll
+    for (int i = 0; i < kList; ++i) b[i] = ror<N>(a[i]);
+    merge_keys(a, b);
+}
+
+template <int VALS>
+__device__ __forceinline__ void load_values(const float* p, float (&v)[VALS]) {
+    struct alignas(VALS * 4 < 16 ? VALS * 4 : 16) Raw {
+        float v[VALS];
+    };
+    const Raw r = *reinterpret_cast<const Raw*>(p);
+#pragma unroll
+    for (int i = 0; i < VALS; ++i) v[i] = r.v[i];
+}
+template <int VALS>
+__device__ __forceinline__ void load_values(const __bf16* p, float (&v)[VALS]) {
+    struct alignas(VALS * 2 < 16 ? VALS * 2 : 16) Raw {
+        uint32_t v[VALS / 2];
+    };
+    const Raw r = *reinterpret_cast<const Raw*>(p);
+#pragma unroll
+    for (int i = 0; i < VALS; i += 2) {
+        v[i] = __uint_as_float(r.v[i / 2] << 16);
+        v[i + 1] = __uint_as_float(r.v[i / 2] & 0xFFFF0000u);
+    }
+}
+
+// GROUPED needs E = 16 VALS and groups of 1, 2, 4, 8 or 16 lanes (`span`).
+template <int VALS, class L, bool BY_VALUE, bool GROUPED>
+__global__ __launch_bounds__(kWaves * 64)
+void route_lanes_kernel(const L* __restrict__ logits, const float* __restrict__ bias, int32_t T,
+                        int32_t E, int32_t K, int32_t sigmoid, int32_t renormalize, float scale,
+                        int32_t groups, int32_t kept, int32_t span, int32_t whole,
+                        int32_t* __restrict__ ids, float* __restrict__ scores) {
+    const int lane = threadIdx.x & 63;
+    const int j = lane & (kLanes - 1);
+    const int64_t row0 =
+        (int64_t(blockIdx.x) * (blockDim.x >> 6) + (threadIdx.x >> 6)) * (64 / kLanes);
+    if (row0 >= T) return;
+    const int64_t row = row0 + (lane >> 4);
+    const bool there = row < T;
+    const L* in = logits + (there ? row : T - 1) * int64_t(E);
+
+    float l[VALS];
+    if (whole) {                        // E = 16 VALS, aligned
+        load_values<VALS>(in + j * VALS, l);
+    } else {
+#pragma unroll
+        for (int i = 0; i < VALS; ++i) {
+            const int e = j * VALS + i;
+            l[i] = e < E ? logit_at(in, e) : -INFINITY;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < VALS; ++i) l[i] = taking_part(l[i]);
+    // The softmax's statistics over all experts.
+    float top = -INFINITY, sum = 0.0f;
+    if (!sigmoid) {
+#pragma unroll
+        for (int i = 0; i < VALS; ++i) top = fmaxf(top, l[i]);
+        top = lanes_max(top);
+        if (!renormalize && top > -INFINITY) {
+#pragma unroll
+            for (int i = 0; i < VALS; ++i)
+                if (l[i] > -INFINITY) sum += __expf(l[i] - top);
+            sum = lanes_sum(sum);
+        }
+    }
+    // v in 32 bits: the exponential and the reciprocal are off by a unit each,
+    // the sums by half, |l| times half a unit enters the exponent where the
+    // sigmoid's slope makes 0.23 of it: 4 half units of 1, and one of the sum with
+    // the bias.
+    float v[VALS];
+#pragma unroll
+    for (int i = 0; i < VALS; ++i) {
+        v[i] = l[i];
+        if constexpr (BY_VALUE) {
+            if (l[i] > -INFINITY) {
+                v[i] = __builtin_amdgcn_rcpf(1.0f + __expf(-l[i]));
+                if (bias) v[i] += bias[j * VALS + i];
+                v[i] = taking_part(v[i]);
+            }
+        }
+    }
+    bool bad = false;
+    if constexpr (GROUPED) {
+        // The two largest of a group: of a lane, then of its lanes.
+        float first = -INFINITY, second = -INFINITY, largest = 0.0f;
+#pragma unroll
+        for (int i = 0; i < VALS; ++i) {
+            second = fmaxf(second, fminf(first, v[i]));
+            first = fmaxf(first, v[i]);
+        }
+        auto join = [&](float of, float os) {
+            second = fmaxf(fminf(first, of), fmaxf(second, os));
+            first = fmaxf(first, of);
+        };
+        if (span > 1) join(__shfl_xor(first, 1, 64), __shfl_xor(second, 1, 64));
+        if (span > 2) join(__shfl_xor(first, 2, 64), __shfl_xor(second, 2, 64));
+        if (span > 4) join(__shfl_xor(first, 4, 64), __shfl_xor(second, 4, 64));
+        if (span > 8) join(__shfl_xor(first, 8, 64), __shfl_xor(second, 8, 64));
+        float value = first;
+        if (BY_VALUE && second > -INFINITY) value += second;
+        if (BY_VALUE)
+            largest = lanes_max(fmaxf(fabsf(first), second > -INFINITY ? fabsf(second) : 0.0f));
+        const float margin = BY_VALUE ? (8.0f + 4.0f * largest) * 0x1p-22f : 0.0f;
+        const int ahead = lanes_ahead<1>(value, j, span);
+        const bool keep = ahead < kept * span;
+        if (BY_VALUE && kept < groups) {
+            const float least = -lanes_max(keep ? -value : -INFINITY);
+            const float next = lanes_max(keep ? -INFINITY : value);
+            bad = !(least - next > margin);
+        }
+#pragma unroll
+        for (int i = 0; i < VALS; ++i) v[i] = keep ? v[i] : -INFINITY;
+    }
+    float m = v[0];
+#pragma unroll
+    for (int i = 1; i < VALS; ++i) m = fmaxf(m, v[i]);
+    m = lanes_max(m);
+    uint32_t key[VALS < kList ? kList : VALS];
+#pragma unroll
+    for (int i = 0; i < VALS; ++i) {
+        // Below 0 and NaN become 0.
+        const float d = __builtin_fmaf(v[i] - m, 0x1p20f, 16777215.0f);
+        key[i] = (static_cast<uint32_t>(fmaxf(d, 0.0f)) << 8) | (255 - (j * VALS + i));
+    }
+    uint32_t list[kList];
+    {
+        uint32_t k[VALS < kList ? kList : VALS];
+#pragma unroll
+        for (int i = 0; i < VALS; ++i) k[i] = key[i];
+#pragma unroll
+        for (int i = VALS; i < kList; ++i) k[i] = 0;
+        if constexpr (VALS <= kList) {
+            sort_keys<VALS>(k);
+#pragma unroll
+            for (int i = 0; i < kList; ++i) list[i] = k[i];
+        } else {
+            static_assert(VALS == 2 * kList, "two lists");
+            sort_keys<kList>(k);
+            sort_keys<kList>(k + kList);
+            uint32_t b[kList];
+#pragma unroll
+            for (int i = 0; i < kList; ++i) {
+                list[i] = k[i];
+                b[i] = k[kList + i];
+            }
+            merge_keys(list, b);
+        }
+    }
+    merge_lanes<8>(list);
+    merge_lanes<4>(list);
+    merge_lanes<2>(list);
+    merge_lanes<1>(list);
+    uint32_t mine = 0, last = 0;
+#pragma unroll
+    for (int i = 0; i < kList; ++i) {
+        if (i == j) mine = list[i];
+        if (i == K - 1) last = list[i];
+    }
+    if (j >= K) mine = 0;
+    if (last < 256) bad = true;         // not K experts within 16 of the largest
+    int id = j < K ? 255 - static_cast<int>(mine & 255) : -1;
+    float chosen = 0.0f;
+    if (j < K && id < E) chosen = taking_part(logit_at(in, id));
+    // The choice against the values.
+    float value = chosen;
+    if constexpr (BY_VALUE) {
+        value = __builtin_amdgcn_rcpf(1.0f + __expf(-chosen));
+        if (bias && j < K && id < E) value += bias[id];
+    }
+    const float next = __shfl(value, lane + 1 < 64 ? lane + 1 : lane, 64);
+    const int next_id = __shfl(id, lane + 1 < 64 ? lane + 1 : lane, 64);
+    const float least = __shfl(value, (lane & 48) + K - 1, 64);
+    const float margin = BY_VALUE ? (4.0f + fabsf(m) + fabsf(least)) * 0x1p-22f : 0.0f;
+    if (j + 1 < K) {
+        if (BY_VALUE)
+            bad = bad || !(value - next > margin);
+        else
+            bad = bad || !(value > next || (value == next && id < next_id));
+    }
+#pragma unroll
+    for (int i = 0; i < VALS; ++i)
+        if (key[i] < last && v[i] > (BY_VALUE ? least - margin : least)) bad = true;
+
+    // Tokens that the check does not clear, one after the other.
+    const uint64_t failed = __ballot(bad && there);
+#pragma unroll 1
+    for (int r = 0; r < 64 / kLanes; ++r) {
+        if (!(failed >> (r * kLanes) & 0xFFFF)) continue;
+        const int slow = choose<(VALS + 3) / 4, L>(logits + (row0 + r) * E, bias, lane, K, E,
+                                                   sigmoid != 0, groups, kept);
+        const int here = __shfl(slow, j, 64);
+        if ((lane >> 4) == r) {
+            id = j < K ? here : -1;
+            chosen = id >= 0 ? logit_at(in, id) : 0.0f;
+        }
+    }
+    float p = 0.0f;
+    if (id >= 0) p = sigmoid ? 1.0f / (1.0f + expf(-chosen)) : expf(chosen - top);
+    if (renormalize) sum = lanes_sum(p);
+    if (renormalize || !sigmoid) p = sum == 0.0f ? 0.0f : p / sum;
+    if (there && j < K) {
+        ids[row * K + j] = id;
+        scores[row * K + j] = p * scale;
     }
 }
 
@@ -271,6 +598,33 @@ void route_grad_kernel(const L* __restrict__ logits, const int32_t* __restrict__
 }
 
 template <int VALS, class L>
+hipError_t launch_lanes(const RouteArgs& a, int32_t span, hipStream_t stream) {
+    const bool by_value = a.sigmoid && (a.bias || a.groups > 1), grouped = a.groups > 1;
+    auto kernel = by_value ? (grouped ? route_lanes_kernel<VALS, L, true, true>
+                                      : route_lanes_kernel<VALS, L, true, false>)
+                           : (grouped ? route_lanes_kernel<VALS, L, false, true>
+                                      : route_lanes_kernel<VALS, L, false, false>);
+    const bool whole = a.E == kLanes * VALS && reinterpret_cast<uintptr_t>(a.logits) % 16 == 0;
+    // A wavefront per workgroup until there is one for every CU.
+    const int waves = a.T <= 4 * 1024 ? 1 : kWaves;
+    const int64_t tokens = waves * (64 / kLanes);
+    hipLaunchKernelGGL(kernel, dim3(static_cast<uint32_t>((a.T + tokens - 1) / tokens)),
+                       dim3(waves * 64), 0, stream, static_cast<const L*>(a.logits), a.bias, a.T,
+                       a.E, a.K, a.sigmoid, a.renormalize, a.scale, a.groups, a.kept, span, whole,
+                       a.ids, a.scores);
+    return hipGetLastError();
+}
+
+// Lanes of a group if the 16 lanes of a token can take its groups, else 0.
+int32_t lanes_of_group(const RouteArgs& a, int vals) {
+    if (a.groups == 1) return kLanes;
+    const int32_t size = a.E / a.groups;
+    if (a.E != kLanes * vals || size % vals != 0) return 0;
+    const int32_t span = size / vals;
+    return (span & (span - 1)) == 0 ? span : 0;
+}
+
+template <int VALS, class L>
 hipError_t launch_route(const RouteArgs& a, hipStream_t stream) {
     hipLaunchKernelGGL((route_kernel<VALS, L>), dim3((static_cast<uint32_t>(a.T) + kWaves - 1) / kWaves),
                        dim3(kWaves * 64), 0, stream, static_cast<const L*>(a.logits), a.bias, a.T,
@@ -281,6 +635,15 @@ hipError_t launch_route(const RouteArgs& a, hipStream_t stream) {
 
 template <class L>
 hipError_t route(const RouteArgs& a, hipStream_t stream) {
+    if (a.E <= kLanes * 16 && a.K <= kList) {
+        const int vals = a.E <= kLanes * 2 ? 2 : a.E <= kLanes * 4 ? 4 : a.E <= kLanes * 8 ? 8 : 16;
+        if (const int32_t span = lanes_of_group(a, vals)) {
+            if (vals == 2) return launch_lanes<2, L>(a, span, stream);
+            if (vals == 4) return launch_lanes<4, L>(a, span, stream);
+            if (vals == 8) return launch_lanes<8, L>(a, span, stream);
+            return launch_lanes<16, L>(a, span, stream);
+        }
+    }
     if (a.E <= 64) return launch_route<1, L>(a, stream);
     if (a.E <= 128) return launch_route<2, L>(a, stream);
     if (a.E <= 256) return launch_route<4, L>(a, stream);

@@ -56,9 +56,12 @@ SHAPES = [
     (17, 3, 3, 160, 96, 0.0), (33, 4, 2, 96, 544, 0.1), (64, 8, 8, 64, 64, 0.0),
     (37, 64, 4, 288, 160, 0.2), (64, 256, 8, 96, 32, 0.0), (32, 300, 16, 64, 32, 0.1),
     (512, 5, 1, 32, 64, 0.0), (13, 1024, 7, 32, 32, 0.0), (40, 2, 2, 320, 2080, 0.0),
+    # wide outputs: 32 columns per workgroup
+    (1, 6, 4, 4128, 64, 0.0), (9, 12, 3, 4192, 160, 0.1), (64, 16, 8, 4128, 32, 0.0),
+    (30, 4, 2, 5152, 96, 0.0),
 ]
 ODD = [(1, 4, 2, 8, 8, 0.0), (7, 6, 3, 72, 40, 0.1), (20, 3, 2, 200, 136, 0.0),
-       (2, 9, 4, 1000, 328, 0.0)]        # multiples of 8 alone: bf16
+       (2, 9, 4, 1000, 328, 0.0), (6, 5, 2, 4104, 72, 0.0)]     # multiples of 8 alone: bf16
 
 
 @pytest.mark.parametrize("four, shape", [(f, s) for f in (False, True) for s in SHAPES]

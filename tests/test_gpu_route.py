@@ -19,6 +19,10 @@ SHAPES = [
     (7, 65, 3, 5, 3), (6, 128, 8, 1, 1), (9, 160, 6, 8, 3), (67, 256, 8, 1, 1),
     (70, 256, 8, 8, 4), (13, 257, 16, 1, 1), (5, 512, 7, 16, 2), (4, 1000, 16, 1, 1),
     (3, 1024, 8, 64, 5), (11, 96, 4, 3, 3), (130, 32, 4, 2, 1),
+    # 16 lanes per token: all widths, groups of one lane to all of them
+    (9, 17, 8, 1, 1), (33, 48, 5, 1, 1), (21, 200, 8, 1, 1), (18, 32, 3, 16, 5), (18, 64, 8, 8, 3),
+    (22, 128, 6, 2, 1), (22, 128, 8, 16, 4), (4100, 64, 4, 4, 2), (19, 256, 8, 16, 9),
+    (5, 256, 9, 8, 4), (6, 224, 8, 7, 3),
 ]
 KINDS = [("softmax", False), ("sigmoid", False), ("sigmoid", True)]
 
@@ -90,6 +94,33 @@ def test_near_values_keep_the_order_of_the_formula(G, kept):
     r = route_topk(l.to(DEV), 8, score="sigmoid", bias=bias.to(DEV), num_groups=G,
                    topk_groups=kept)
     assert torch.equal(r.ids.cpu().long(), want)
+
+
+@pytest.mark.parametrize("groups", [(1, 1), (8, 4)])
+def test_far_biases_and_near_sums(groups):
+    """Biases far below zero: a group's second value decides its sum, and the
+    sums of groups lie as near as fp32 numbers of their size."""
+    gen = torch.Generator().manual_seed(17)
+    T, E = 70, 256
+    l = torch.randn(T, E, generator=gen)
+    bias = torch.full((E,), -1e6) + torch.randint(0, 4, (E,), generator=gen) * 0.0625
+    bias[::32] = torch.randn(8, generator=gen)
+    for b in (bias, bias * 1e-3, torch.where(bias < -1, bias, bias - 3e4)):
+        want = ref.select(l, 8, "sigmoid", b, *groups)
+        r = route_topk(l.to(DEV), 8, score="sigmoid", bias=b.to(DEV), num_groups=groups[0],
+                       topk_groups=groups[1])
+        assert torch.equal(r.ids.cpu().long(), want)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_values_further_apart_than_a_key_holds(score):
+    """Distances above 16 and below 2^-20 between the chosen."""
+    gen = torch.Generator().manual_seed(18)
+    far = torch.randn(64, 256, generator=gen) * 1000
+    near = 3.0 + torch.randint(0, 1 << 14, (64, 256), generator=gen) * 2.0 ** -22
+    for l in (far, near, near - 1e5, near * 1e-8):
+        want = ref.select(l, 8, score)
+        assert torch.equal(route_topk(l.to(DEV), 8, score=score).ids.cpu().long(), want)
 
 
 @pytest.mark.parametrize("big", [0.0, 100.0, 1e6, -1e6])
