@@ -263,6 +263,14 @@ __device__ __forceinline__ float lanes_sum(float v) {
     return v + ror<1>(v);
 }
 
+// exp(x) with an error of a unit and of half of |x| units; below 2^-126 it is 0.
+__device__ __forceinline__ float exp_f32(float x) {
+    return __builtin_amdgcn_exp2f(x * 1.44269504088896340736f);
+}
+__device__ __forceinline__ float sigmoid_of(float l) {
+    return __builtin_amdgcn_rcpf(1.0f + exp_f32(-l));
+}
+
 // Lanes D, D + 1, ... before this one, in a circle, whose group goes before this
 // lane's: a larger value, or the same and a lower index.
 template <int D>
@@ -362,7 +370,8 @@ void route_lanes_kernel(const L* __restrict__ logits, const float* __restrict__ 
 #pragma unroll
         for (int i = 0; i < VALS; ++i) {
             const int e = j * VALS + i;
-            l[i] = e < E ? logit_at(in, e) : -INFINITY;
+            const float x = logit_at(in, min(e, E - 1));
+            l[i] = e < E ? x : -INFINITY;
         }
     }
 #pragma unroll
@@ -373,10 +382,10 @@ void route_lanes_kernel(const L* __restrict__ logits, const float* __restrict__ 
 #pragma unroll
         for (int i = 0; i < VALS; ++i) top = fmaxf(top, l[i]);
         top = lanes_max(top);
-        if (!renormalize && top > -INFINITY) {
+        if (!renormalize) {
+            const float from = top > -INFINITY ? top : 0.0f;
 #pragma unroll
-            for (int i = 0; i < VALS; ++i)
-                if (l[i] > -INFINITY) sum += __expf(l[i] - top);
+            for (int i = 0; i < VALS; ++i) sum += exp_f32(l[i] - from);
             sum = lanes_sum(sum);
         }
     }
@@ -385,16 +394,26 @@ void route_lanes_kernel(const L* __restrict__ logits, const float* __restrict__ 
     // sigmoid's slope makes 0.23 of it: 4 half units of 1, and one of the sum with
     // the bias.
     float v[VALS];
+    if constexpr (BY_VALUE) {
+        float b[VALS];
 #pragma unroll
-    for (int i = 0; i < VALS; ++i) {
-        v[i] = l[i];
-        if constexpr (BY_VALUE) {
-            if (l[i] > -INFINITY) {
-                v[i] = __builtin_amdgcn_rcpf(1.0f + __expf(-l[i]));
-                if (bias) v[i] += bias[j * VALS + i];
-                v[i] = taking_part(v[i]);
+        for (int i = 0; i < VALS; ++i) b[i] = 0.0f;
+        if (bias) {
+            if (whole) {
+                load_values<VALS>(bias + j * VALS, b);
+            } else {
+#pragma unroll
+                for (int i = 0; i < VALS; ++i) b[i] = bias[min(j * VALS + i, E - 1)];
             }
         }
+#pragma unroll
+        for (int i = 0; i < VALS; ++i) {
+            const float w = sigmoid_of(l[i]) + b[i];
+            v[i] = l[i] > -INFINITY && w == w ? w : -INFINITY;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < VALS; ++i) v[i] = l[i];
     }
     bool bad = false;
     if constexpr (GROUPED) {
@@ -481,7 +500,7 @@ void route_lanes_kernel(const L* __restrict__ logits, const float* __restrict__ 
     // The choice against the values.
     float value = chosen;
     if constexpr (BY_VALUE) {
-        value = __builtin_amdgcn_rcpf(1.0f + __expf(-chosen));
+        value = sigmoid_of(chosen);
         if (bias && j < K && id < E) value += bias[id];
     }
     const float next = __shfl(value, lane + 1 < 64 ? lane + 1 : lane, 64);
@@ -494,9 +513,11 @@ void route_lanes_kernel(const L* __restrict__ logits, const float* __restrict__ 
         else
             bad = bad || !(value > next || (value == next && id < next_id));
     }
+    const float limit = BY_VALUE ? least - margin : least;
+    float above = -INFINITY;            // the largest of those not chosen
 #pragma unroll
-    for (int i = 0; i < VALS; ++i)
-        if (key[i] < last && v[i] > (BY_VALUE ? least - margin : least)) bad = true;
+    for (int i = 0; i < VALS; ++i) above = fmaxf(above, key[i] < last ? v[i] : -INFINITY);
+    bad = bad || above > limit;
 
     // Tokens that the check does not clear, one after the other.
     const uint64_t failed = __ballot(bad && there);
@@ -604,7 +625,8 @@ hipError_t launch_lanes(const RouteArgs& a, int32_t span, hipStream_t stream) {
                                       : route_lanes_kernel<VALS, L, true, false>)
                            : (grouped ? route_lanes_kernel<VALS, L, false, true>
                                       : route_lanes_kernel<VALS, L, false, false>);
-    const bool whole = a.E == kLanes * VALS && reinterpret_cast<uintptr_t>(a.logits) % 16 == 0;
+    const bool whole = a.E == kLanes * VALS && reinterpret_cast<uintptr_t>(a.logits) % 16 == 0 &&
+                       reinterpret_cast<uintptr_t>(a.bias) % 16 == 0;
     // A wavefront per workgroup until there is one for every CU.
     const int waves = a.T <= 4 * 1024 ? 1 : kWaves;
     const int64_t tokens = waves * (64 / kLanes);
