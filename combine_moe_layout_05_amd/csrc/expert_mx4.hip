@@ -41,22 +41,34 @@ __device__ __forceinline__ v4i by_groups(v4i q) {
                static_cast<int32_t>(hi[0]), static_cast<int32_t>(hi[1])};
 }
 
-// Weights of a 16-feature block over 128 elements.
-struct Weights4 {
-    v4i q;
-    int32_t scale;                      // of this lane's feature and group
-};
-
+// A register of which lane group g holds value g of the 16 lanes' to four
+// registers that hold value 0, 1, 2 and 3 in all groups.
+__device__ __forceinline__ void spread(uint32_t v, uint32_t (&d)[4]) {
+    const auto half = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    const auto lo = __builtin_amdgcn_permlane16_swap(half[0], half[0], false, false);
+    const auto hi = __builtin_amdgcn_permlane16_swap(half[1], half[1], false, false);
+    d[0] = lo[0];
+    d[1] = lo[1];
+    d[2] = hi[0];
+    d[3] = hi[1];
+}
 
 // ---- Many rows per expert -------------------------------------------------
+//
+// A wavefront keeps 64 features' weights to itself, straight from memory into
+// registers, a step of 256 elements ahead; the rows, which the workgroup's four
+// wavefronts share, go through LDS, and so do their scales, all of a tile's at its
+// start. What bounds it is the number of load instructions: a CU takes some 30
+// cycles for each, whatever it brings, while 16 products of 16 cycles use up the
+// four loads of weights they need.
 
 constexpr int kWaves = 4;               // along the features
-constexpr int kRowTile = 64;
 constexpr int kStages = 3;              // 256-element steps of rows in LDS
 constexpr int kXcdChunk = 8;
 constexpr int kBand = 8;
+constexpr int kChunkGroups = 248;       // groups of 32 whose scales LDS holds
 
-template <bool GATED>
+template <bool GATED, int ROWS>
 __global__ __launch_bounds__(kWaves * 64, 2)
 void expert_mx4_kernel(const char* __restrict__ rows, const uint8_t* __restrict__ row_scales,
                        const char* __restrict__ w, const uint8_t* __restrict__ scales,
@@ -65,15 +77,15 @@ void expert_mx4_kernel(const char* __restrict__ rows, const uint8_t* __restrict_
                        char* __restrict__ out, int32_t zero) {
     // Output features of a wavefront: half its blocks are up rows if gated.
     constexpr int kFeats = kBlocks * 16 / (GATED ? 2 : 1);
-    typedef PackedOperand<kRowTile, kWaves> Rows;
+    typedef PackedOperand<ROWS, kWaves> Rows;
     __shared__ v4i lds[kStages * Rows::kChunks];
+    __shared__ uint32_t scale_lds[ROWS * kChunkGroups / 4];
     __shared__ int32_t info[4];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t number = expert_tile_number(kXcdChunk);
     if (wave == 0) {
-        const ExpertTile t =
-            expert_find_tile(offsets, E, max_rows, kRowTile, ftiles, kBand, number);
+        const ExpertTile t = expert_find_tile(offsets, E, max_rows, ROWS, ftiles, kBand, number);
         if (lane == 0) {
             info[0] = t.e;
             info[1] = t.f;
@@ -100,31 +112,43 @@ void expert_mx4_kernel(const char* __restrict__ rows, const uint8_t* __restrict_
 
     // This wavefront's blocks; those past the matrix read its last one and are
     // not stored.
-    const char* wb[kBlocks];
-    const uint8_t* sb[kBlocks];
-#pragma unroll
-    for (int b = 0; b < kBlocks; ++b) {
-        const int32_t nb = (feats + 15) / 16;
+    const int32_t nb = (feats + 15) / 16;
+    auto block_of = [&](int b) {
         const bool up = GATED && b >= kBlocks / 2;
         const int32_t ob = min(f0 / 16 + (GATED ? b % (kBlocks / 2) : b), nb - 1);
-        const int64_t blk = (int64_t(e) * (GATED ? 2 : 1) + (up ? 1 : 0)) * nb + ob;
-        wb[b] = w + blk * halves * 1024;
-        sb[b] = scales + blk * halves * 64;
-    }
+        return (int64_t(e) * (GATED ? 2 : 1) + (up ? 1 : 0)) * nb + ob;
+    };
+    const char* wb[kBlocks];
+#pragma unroll
+    for (int b = 0; b < kBlocks; ++b) wb[b] = w + block_of(b) * halves * 1024;
+    // Lane group g loads the scales of block g.
+    const uint8_t* sb = scales + block_of(g) * halves * 64 + i * 4;
+
+    // The rows' scales of groups [c0, c0 + len) to LDS, `pitch` bytes a row.
+    const uint8_t* sbase = row_scales + int64_t(row0) * groups;
+    const int32_t pitch4 = (min(groups, kChunkGroups) + 3) / 4;
+    auto load_scales = [&](int32_t c0) {
+        const int32_t len = min(groups - c0, kChunkGroups);
+        for (int q = threadIdx.x; q < nrows * pitch4; q += kWaves * 64) {
+            const int r = q / pitch4, at = q % pitch4 * 4;
+            const uint8_t* p = sbase + r * groups + c0 + at;
+            uint32_t v = 0;
+            if (at + 4 <= len) {
+                __builtin_memcpy(&v, p, 4);
+            } else {
+                for (int k = 0; k < len - at; ++k) v |= uint32_t(p[k]) << (8 * k);
+            }
+            scale_lds[q] = v;
+        }
+    };
 
     auto run = [&](auto row_blocks) {
         constexpr int NB = decltype(row_blocks)::value;
-        constexpr int kHalfLoads = 2 * kBlocks + NB;
         Rows rt;
         const int64_t pitch = red / 2;
         const char* rbase = rows + int64_t(row0) * pitch;
-        const uint8_t* sbase = row_scales + int64_t(row0) * groups;
         rt.init(wave, lane, 0, pitch, [&](int) { return rbase; },
                 [&](int p) { return min(p, nrows - 1); });
-        uint32_t srow[NB];
-#pragma unroll
-        for (int b = 0; b < NB; ++b)
-            srow[b] = static_cast<uint32_t>(min(b * 16 + i, nrows - 1)) * groups;
         f32x4 acc[kBlocks][NB];
 #pragma unroll
         for (int a = 0; a < kBlocks; ++a)
@@ -133,8 +157,8 @@ void expert_mx4_kernel(const char* __restrict__ rows, const uint8_t* __restrict_
 
         // What a half step of 128 elements takes from memory to registers.
         struct Half {
-            Weights4 w[kBlocks];
-            int32_t rs[NB];
+            v4i q[kBlocks];
+            uint32_t scale;
         };
         auto issue_rows = [&](int32_t t, int stage) {
             v4i* buf = lds + stage * Rows::kChunks;
@@ -146,61 +170,75 @@ void expert_mx4_kernel(const char* __restrict__ rows, const uint8_t* __restrict_
         };
         auto load = [&](int32_t half, Half& d) {
             // A uniform address and a 32-bit offset per lane.
-            uint32_t qo = lane * 16, so = i * 4 + g;
+            uint32_t qo = lane * 16;
             reform(qo);
-            reform(so);
             const int32_t at = min(half, halves - 1);
-            const uint32_t group = min(4 * half + g, groups - 1);
+            d.scale = *reinterpret_cast<const uint32_t*>(sb + int64_t(at) * 64);
 #pragma unroll
-            for (int b = 0; b < kBlocks; ++b) {
-                d.w[b].q = *reinterpret_cast<const v4i*>(wb[b] + int64_t(at) * 1024 + qo);
-                d.w[b].scale = (sb[b] + int64_t(at) * 64)[so];
+            for (int b = 0; b < kBlocks; ++b)
+                d.q[b] = *reinterpret_cast<const v4i*>(wb[b] + int64_t(at) * 1024 + qo);
+        };
+        const int shift = 8 * g;
+        auto order = [&](Half& d, uint32_t (&sc)[kBlocks]) {
+            spread(d.scale, sc);
+#pragma unroll
+            for (int a = 0; a < kBlocks; ++a) {
+                sc[a] >>= shift;
+                d.q[a] = by_groups(d.q[a]);
             }
-#pragma unroll
-            for (int b = 0; b < NB; ++b) d.rs[b] = sbase[srow[b] + group];
         };
-        auto order = [&](Half& d) {
-#pragma unroll
-            for (int a = 0; a < kBlocks; ++a) d.w[a].q = by_groups(d.w[a].q);
-        };
-        auto multiply = [&](const Half& d, const v4i* buf, int h) {
+        const uint8_t* scale_bytes = reinterpret_cast<const uint8_t*>(scale_lds);
+        auto multiply = [&](const Half& d, const uint32_t (&sc)[kBlocks], const v4i* buf, int h,
+                            int32_t group, int32_t first) {
+            // Behind the sum's end the last group's, which are there.
+            const uint8_t* mine = scale_bytes + min(group + g, groups - first - 1);
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
                 const v4i x = __builtin_bit_cast(v4i, rt.frag(buf, b, h));
+                const int32_t rs = mine[min(b * 16 + i, nrows - 1) * pitch4 * 4];
 #pragma unroll
                 for (int a = 0; a < kBlocks; ++a)
-                    acc[a][b] = multiply4(d.w[a].q, d.w[a].scale, x, d.rs[b], acc[a][b]);
+                    acc[a][b] = multiply4(d.q[a], sc[a], x, rs, acc[a][b]);
             }
         };
 
         Half lo, hi;
+        uint32_t sc[kBlocks];
         issue_rows(0, 0);
         if (steps > 1) issue_rows(1, 1);
+        load_scales(0);
         load(0, lo);
         load(1, hi);
-        wait_loads<2 * kHalfLoads>();
+        wait_loads<2 * (kBlocks + 1)>();
         step_barrier();
         int stage = 0;
+        int32_t first = 0;                      // group the scales in LDS begin with
         for (int32_t t = 0; t < steps; ++t) {
             const int after = stage + 1 == kStages ? 0 : stage + 1;
             const int free = after + 1 == kStages ? 0 : after + 1;
             const v4i* buf = lds + stage * Rows::kChunks;
-            order(lo);
+            if (8 * t - first == kChunkGroups) {
+                // Every wavefront is past the last barrier: the old ones are read.
+                first = 8 * t;
+                load_scales(first);
+                __syncthreads();
+            }
+            order(lo, sc);
             __builtin_amdgcn_sched_barrier(0);
             // Behind the first use of this step's registers: what waits for
             // them must not wait for these loads.
             if (t + 2 < steps) issue_rows(t + 2, free);
-            multiply(lo, buf, 0);
+            multiply(lo, sc, buf, 0, 8 * t - first, first);
             __builtin_amdgcn_sched_barrier(0);
             load(2 * t + 2, lo);
             __builtin_amdgcn_sched_barrier(0);
-            order(hi);
+            order(hi, sc);
             if (2 * t + 1 >= halves) {
                 // A sum that ends in the first half.
 #pragma unroll
-                for (int a = 0; a < kBlocks; ++a) hi.w[a].q = v4i{0, 0, 0, 0};
+                for (int a = 0; a < kBlocks; ++a) hi.q[a] = v4i{0, 0, 0, 0};
             }
-            multiply(hi, buf, 1);
+            multiply(hi, sc, buf, 1, 8 * t + 4 - first, first);
             __builtin_amdgcn_sched_barrier(0);
             load(2 * t + 3, hi);
             __builtin_amdgcn_sched_barrier(0);
@@ -244,10 +282,19 @@ void expert_mx4_kernel(const char* __restrict__ rows, const uint8_t* __restrict_
         run(std::integral_constant<int, 1>{});
     else if (nrows <= 32)
         run(std::integral_constant<int, 2>{});
-    else if (nrows <= 48)
-        run(std::integral_constant<int, 3>{});
-    else
-        run(std::integral_constant<int, 4>{});
+    else if (nrows <= 48 || ROWS == 64) {
+        if (nrows <= 48)
+            run(std::integral_constant<int, 3>{});
+        else
+            run(std::integral_constant<int, 4>{});
+    } else if constexpr (ROWS == 128) {
+        if (nrows <= 64)
+            run(std::integral_constant<int, 4>{});
+        else if (nrows <= 96)
+            run(std::integral_constant<int, 6>{});
+        else
+            run(std::integral_constant<int, 8>{});
+    }
 }
 
 // ---- Few rows per expert --------------------------------------------------
@@ -297,34 +344,35 @@ void expert_mx4_stream_kernel(const char* __restrict__ rows, const uint8_t* __re
     const int32_t f0 = ft * kFeatBlocks * 16;
     const int32_t steps = (red + kMxfp4Step - 1) / kMxfp4Step;
     const int32_t groups = red / 32;
-    const char* wb[kBlocks];
-    const uint8_t* sb[kBlocks];
-#pragma unroll
-    for (int b = 0; b < kBlocks; ++b) {
+    auto block_of = [&](int b) {
         const int32_t nb = (feats + 15) / 16;
         const bool up = GATED && b >= kFeatBlocks;
-        const int64_t blk = int64_t(e) * nb * (GATED ? 2 : 1) + (up ? nb : 0) +
-                            min(f0 / 16 + (GATED ? b % kFeatBlocks : b), nb - 1);
-        wb[b] = w + blk * steps * 1024 + lane * 16;
-        sb[b] = scales + blk * steps * 64 + i * 4 + g;
-    }
+        return int64_t(e) * nb * (GATED ? 2 : 1) + (up ? nb : 0) +
+               min(f0 / 16 + (GATED ? b % kFeatBlocks : b), nb - 1);
+    };
+    const char* wb[kBlocks];
+#pragma unroll
+    for (int b = 0; b < kBlocks; ++b) wb[b] = w + block_of(b) * steps * 1024;
+    const uint8_t* sb = scales + block_of(g) * steps * 64 + i * 4;
     const int64_t row = row0 + min(i, nrows - 1);
     const char* rbase = rows + row * (red / 2);
     const uint8_t* sbase = row_scales + row * groups;
 
     struct Step {
-        Weights4 w[kBlocks];
+        v4i q[kBlocks];
+        uint32_t scale;
         v4i x;
         int32_t rs;
     };
     auto load = [&](int32_t t, Step& d) {
         const int32_t group = min(4 * t + g, groups - 1);
+        uint32_t qo = lane * 16;
+        reform(qo);
 #pragma unroll
-        for (int b = 0; b < kBlocks; ++b) {
-            d.w[b].q = __builtin_nontemporal_load(
-                reinterpret_cast<const v4i*>(wb[b] + int64_t(t) * 1024));
-            d.w[b].scale = sb[b][int64_t(t) * 64];
-        }
+        for (int b = 0; b < kBlocks; ++b)
+            d.q[b] = __builtin_nontemporal_load(
+                reinterpret_cast<const v4i*>(wb[b] + int64_t(t) * 1024 + qo));
+        d.scale = *reinterpret_cast<const uint32_t*>(sb + int64_t(t) * 64);
         d.x = *reinterpret_cast<const v4i*>(rbase + int64_t(group) * 16);
         d.rs = sbase[group];
         __builtin_amdgcn_sched_barrier(0);
@@ -333,9 +381,11 @@ void expert_mx4_stream_kernel(const char* __restrict__ rows, const uint8_t* __re
 #pragma unroll
     for (int b = 0; b < kBlocks; ++b) acc[b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     auto compute = [&](const Step& d) {
+        uint32_t sc[kBlocks];
+        spread(d.scale, sc);
 #pragma unroll
         for (int b = 0; b < kBlocks; ++b)
-            acc[b] = multiply4(by_groups(d.w[b].q), d.w[b].scale, d.x, d.rs, acc[b]);
+            acc[b] = multiply4(by_groups(d.q[b]), sc[b] >> (8 * g), d.x, d.rs, acc[b]);
     };
     // Wavefront w takes steps w, w + kStreamWaves, ..., two in flight.
     Step even, odd;
@@ -378,8 +428,11 @@ int64_t tile_features(const ExpertMx4Args& a) {
     const int32_t per = kWaves * kBlocks * 16 / (a.gated ? 2 : 1);
     return (int64_t(a.feats) + per - 1) / per;
 }
+// Rows per tile, by what an expert has on average.
+int tile_rows(const ExpertMx4Args& a) { return a.max_rows > 64 * int64_t(a.E) ? 128 : 64; }
 int64_t tile_workgroups(const ExpertMx4Args& a) {
-    return round_up(tile_features(a) * ((a.max_rows + kRowTile - 1) / kRowTile + active(a)),
+    const int64_t rows = tile_rows(a);
+    return round_up(tile_features(a) * ((a.max_rows + rows - 1) / rows + active(a)),
                     int64_t(kExpertXcds) * kXcdChunk);
 }
 int64_t stream_features(const ExpertMx4Args& a) {
@@ -413,8 +466,10 @@ int64_t expert_mx4_stream_grid(const ExpertMx4Args& a) {
 }
 
 hipError_t launch_expert_mx4(const ExpertMx4Args& a, hipStream_t stream) {
-    return launch(a.gated ? expert_mx4_kernel<true> : expert_mx4_kernel<false>, tile_workgroups(a),
-                  kWaves * 64, tile_features(a), a, stream);
+    auto kernel = tile_rows(a) == 128
+                      ? (a.gated ? expert_mx4_kernel<true, 128> : expert_mx4_kernel<false, 128>)
+                      : (a.gated ? expert_mx4_kernel<true, 64> : expert_mx4_kernel<false, 64>);
+    return launch(kernel, tile_workgroups(a), kWaves * 64, tile_features(a), a, stream);
 }
 
 hipError_t launch_expert_mx4_stream(const ExpertMx4Args& a, hipStream_t stream) {
