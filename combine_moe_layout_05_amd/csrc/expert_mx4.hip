@@ -23,11 +23,12 @@ typedef int32_t v8i __attribute__((ext_vector_type(8)));
 
 constexpr int kBlocks = 4;              // 16-feature blocks per wavefront
 
-// c + a b over 128 elements; the scales' bytes in the low 8 bits.
+// c + a b over 128 elements; a's scale is the low byte of sa, b's byte BYTE of sb.
+template <int BYTE>
 __device__ __forceinline__ f32x4 multiply4(v4i a, int32_t sa, v4i b, int32_t sb, f32x4 c) {
     const v8i wa = {a[0], a[1], a[2], a[3], 0, 0, 0, 0};
     const v8i wb = {b[0], b[1], b[2], b[3], 0, 0, 0, 0};
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wa, wb, c, 4, 4, 0, sa, 0, sb);
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wa, wb, c, 4, 4, 0, sa, BYTE, sb);
 }
 
 // Packed weights to an operand: dword s of lane group g and dword g of lane
@@ -64,9 +65,9 @@ __device__ __forceinline__ void spread(uint32_t v, uint32_t (&d)[4]) {
 
 constexpr int kWaves = 4;               // along the features
 constexpr int kStages = 3;              // 256-element steps of rows in LDS
-constexpr int kXcdChunk = 8;
 constexpr int kBand = 8;
-constexpr int kChunkGroups = 248;       // groups of 32 whose scales LDS holds
+constexpr int kChunkGroups = 240;       // groups of 32 whose scales LDS holds
+constexpr int kRowWords = kChunkGroups / 4;
 
 template <bool GATED, int ROWS>
 __global__ __launch_bounds__(kWaves * 64, 2)
@@ -74,7 +75,7 @@ void expert_mx4_kernel(const char* __restrict__ rows, const uint8_t* __restrict_
                        const char* __restrict__ w, const uint8_t* __restrict__ scales,
                        const int32_t* __restrict__ offsets, int32_t E, int32_t max_rows,
                        int32_t red, int32_t feats, int32_t ftiles, int32_t act,
-                       char* __restrict__ out, int32_t zero) {
+                       char* __restrict__ out, int32_t zero, int32_t chunk) {
     // Output features of a wavefront: half its blocks are up rows if gated.
     constexpr int kFeats = kBlocks * 16 / (GATED ? 2 : 1);
     typedef PackedOperand<ROWS, kWaves> Rows;
@@ -83,7 +84,7 @@ void expert_mx4_kernel(const char* __restrict__ rows, const uint8_t* __restrict_
     __shared__ int32_t info[4];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t number = expert_tile_number(kXcdChunk);
+    const int64_t number = expert_tile_number(chunk);
     if (wave == 0) {
         const ExpertTile t = expert_find_tile(offsets, E, max_rows, ROWS, ftiles, kBand, number);
         if (lane == 0) {
@@ -124,21 +125,38 @@ void expert_mx4_kernel(const char* __restrict__ rows, const uint8_t* __restrict_
     // Lane group g loads the scales of block g.
     const uint8_t* sb = scales + block_of(g) * halves * 64 + i * 4;
 
-    // The rows' scales of groups [c0, c0 + len) to LDS, `pitch` bytes a row.
+    // The rows' scales of kChunkGroups groups from c0 on to LDS. Of row r, word 15
+    // g + q holds scale group g of the four half steps from 4 q on, a byte each: what
+    // lane group g needs for two steps, one of whose bytes a product picks by
+    // itself. 60 words a row and 15 a group put the 64 lanes into as many banks.
+    // Groups behind the sum's end get 1: they meet weights of zero.
     const uint8_t* sbase = row_scales + int64_t(row0) * groups;
-    const int32_t pitch4 = (min(groups, kChunkGroups) + 3) / 4;
     auto load_scales = [&](int32_t c0) {
         const int32_t len = min(groups - c0, kChunkGroups);
-        for (int q = threadIdx.x; q < nrows * pitch4; q += kWaves * 64) {
-            const int r = q / pitch4, at = q % pitch4 * 4;
+        const int32_t quads = (len + 15) / 16;
+        for (int q = threadIdx.x; q < nrows * quads; q += kWaves * 64) {
+            const int r = q / quads, at = q % quads * 16;
             const uint8_t* p = sbase + r * groups + c0 + at;
-            uint32_t v = 0;
-            if (at + 4 <= len) {
-                __builtin_memcpy(&v, p, 4);
+            v4i v;
+            if (at + 16 <= len) {
+                __builtin_memcpy(&v, p, 16);
             } else {
-                for (int k = 0; k < len - at; ++k) v |= uint32_t(p[k]) << (8 * k);
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                    const uint32_t byte = at + k < len ? p[k] : 127;
+                    const uint32_t word = k % 4 == 0 ? 0 : static_cast<uint32_t>(v[k / 4]);
+                    v[k / 4] = static_cast<int32_t>(word | byte << (8 * (k % 4)));
+                }
             }
-            scale_lds[q] = v;
+            const uint32_t a = __builtin_amdgcn_perm(v[1], v[0], 0x05010400u);
+            const uint32_t b = __builtin_amdgcn_perm(v[3], v[2], 0x05010400u);
+            const uint32_t c = __builtin_amdgcn_perm(v[1], v[0], 0x07030602u);
+            const uint32_t d = __builtin_amdgcn_perm(v[3], v[2], 0x07030602u);
+            uint32_t* to = scale_lds + r * kRowWords + at / 16;
+            to[0] = __builtin_amdgcn_perm(b, a, 0x05040100u);
+            to[kRowWords / 4] = __builtin_amdgcn_perm(b, a, 0x07060302u);
+            to[kRowWords / 2] = __builtin_amdgcn_perm(d, c, 0x05040100u);
+            to[kRowWords / 4 * 3] = __builtin_amdgcn_perm(d, c, 0x07060302u);
         }
     };
 
@@ -187,18 +205,35 @@ void expert_mx4_kernel(const char* __restrict__ rows, const uint8_t* __restrict_
                 d.q[a] = by_groups(d.q[a]);
             }
         };
-        const uint8_t* scale_bytes = reinterpret_cast<const uint8_t*>(scale_lds);
-        auto multiply = [&](const Half& d, const uint32_t (&sc)[kBlocks], const v4i* buf, int h,
-                            int32_t group, int32_t first) {
-            // Behind the sum's end the last group's, which are there.
-            const uint8_t* mine = scale_bytes + min(group + g, groups - first - 1);
+        // Two row blocks' operands, read while the products of the two before them
+        // run.
+        constexpr int kPair = NB == 1 ? 1 : 2;
+        struct Pair {
+            v4i x[kPair];
+        };
+        auto fetch = [&](Pair& d, const v4i* buf, int b, int h) {
 #pragma unroll
-            for (int b = 0; b < NB; ++b) {
-                const v4i x = __builtin_bit_cast(v4i, rt.frag(buf, b, h));
-                const int32_t rs = mine[min(b * 16 + i, nrows - 1) * pitch4 * 4];
+            for (int k = 0; k < kPair; ++k)
+                if (b + k < NB) d.x[k] = __builtin_bit_cast(v4i, rt.frag(buf, b + k, h));
+        };
+        int32_t rs[NB];                         // the rows' scales of four half steps
+        auto multiply = [&](const Half& d, const uint32_t (&sc)[kBlocks], const v4i* buf,
+                            auto half) {
+            constexpr int kHalf = decltype(half)::value;        // of four
+            Pair p[2];
+            fetch(p[0], buf, 0, kHalf & 1);
 #pragma unroll
-                for (int a = 0; a < kBlocks; ++a)
-                    acc[a][b] = multiply4(d.q[a], sc[a], x, rs, acc[a][b]);
+            for (int b = 0; b < NB; b += kPair) {
+                if (b + kPair < NB) fetch(p[b / kPair % 2 ^ 1], buf, b + kPair, kHalf & 1);
+                __builtin_amdgcn_sched_barrier(0);
+                const Pair& now = p[b / kPair % 2];
+#pragma unroll
+                for (int k = 0; k < kPair; ++k)
+#pragma unroll
+                    for (int a = 0; a < kBlocks; ++a)
+                        if (b + k < NB)
+                            acc[a][b + k] = multiply4<kHalf>(d.q[a], sc[a], now.x[k], rs[b + k],
+                                                             acc[a][b + k]);
             }
         };
 
@@ -206,29 +241,23 @@ void expert_mx4_kernel(const char* __restrict__ rows, const uint8_t* __restrict_
         uint32_t sc[kBlocks];
         issue_rows(0, 0);
         if (steps > 1) issue_rows(1, 1);
-        load_scales(0);
         load(0, lo);
         load(1, hi);
-        wait_loads<2 * (kBlocks + 1)>();
+        load_scales(0);
+        wait_loads<0>();
         step_barrier();
         int stage = 0;
-        int32_t first = 0;                      // group the scales in LDS begin with
-        for (int32_t t = 0; t < steps; ++t) {
+        auto step = [&](auto odd, int32_t t) {
+            constexpr int kOdd = decltype(odd)::value;
             const int after = stage + 1 == kStages ? 0 : stage + 1;
             const int free = after + 1 == kStages ? 0 : after + 1;
             const v4i* buf = lds + stage * Rows::kChunks;
-            if (8 * t - first == kChunkGroups) {
-                // Every wavefront is past the last barrier: the old ones are read.
-                first = 8 * t;
-                load_scales(first);
-                __syncthreads();
-            }
             order(lo, sc);
             __builtin_amdgcn_sched_barrier(0);
             // Behind the first use of this step's registers: what waits for
             // them must not wait for these loads.
             if (t + 2 < steps) issue_rows(t + 2, free);
-            multiply(lo, sc, buf, 0, 8 * t - first, first);
+            multiply(lo, sc, buf, std::integral_constant<int, 2 * kOdd>{});
             __builtin_amdgcn_sched_barrier(0);
             load(2 * t + 2, lo);
             __builtin_amdgcn_sched_barrier(0);
@@ -238,7 +267,7 @@ void expert_mx4_kernel(const char* __restrict__ rows, const uint8_t* __restrict_
 #pragma unroll
                 for (int a = 0; a < kBlocks; ++a) hi.q[a] = v4i{0, 0, 0, 0};
             }
-            multiply(hi, sc, buf, 1, 8 * t + 4 - first, first);
+            multiply(hi, sc, buf, std::integral_constant<int, 2 * kOdd + 1>{});
             __builtin_amdgcn_sched_barrier(0);
             load(2 * t + 3, hi);
             __builtin_amdgcn_sched_barrier(0);
@@ -246,6 +275,21 @@ void expert_mx4_kernel(const char* __restrict__ rows, const uint8_t* __restrict_
             // were waited for, were loaded behind them.
             step_barrier();
             stage = after;
+        };
+        int32_t first = 0;                      // group the scales in LDS begin with
+        for (int32_t t = 0; t < steps; t += 2) {
+            if (8 * t - first == kChunkGroups) {
+                // Every wavefront is past the last barrier: the old ones are read.
+                first = 8 * t;
+                load_scales(first);
+                __syncthreads();
+            }
+#pragma unroll
+            for (int b = 0; b < NB; ++b)        // rows past the last are not stored
+                rs[b] = static_cast<int32_t>(
+                    scale_lds[(b * 16 + i) * kRowWords + g * (kRowWords / 4) + (8 * t - first) / 16]);
+            step(std::integral_constant<int, 0>{}, t);
+            if (t + 1 < steps) step(std::integral_constant<int, 1>{}, t + 1);
         }
         wait_loads<0>();
 
@@ -313,13 +357,13 @@ void expert_mx4_stream_kernel(const char* __restrict__ rows, const uint8_t* __re
                               const char* __restrict__ w, const uint8_t* __restrict__ scales,
                               const int32_t* __restrict__ offsets, int32_t E, int32_t max_rows,
                               int32_t red, int32_t feats, int32_t ftiles, int32_t act,
-                              char* __restrict__ out, int32_t zero) {
+                              char* __restrict__ out, int32_t zero, int32_t chunk) {
     constexpr int kFeatBlocks = GATED ? kBlocks / 2 : kBlocks;  // of the output
     __shared__ f32x4 part[kStreamWaves][kBlocks][64];
     __shared__ int32_t info[4];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t number = expert_tile_number(kStreamChunk);
+    const int64_t number = expert_tile_number(chunk);
     if (wave == 0) {
         const ExpertTile t = expert_find_tile(offsets, E, max_rows, kStreamRows, ftiles, 4, number);
         if (lane == 0) {
@@ -385,7 +429,7 @@ void expert_mx4_stream_kernel(const char* __restrict__ rows, const uint8_t* __re
         spread(d.scale, sc);
 #pragma unroll
         for (int b = 0; b < kBlocks; ++b)
-            acc[b] = multiply4(by_groups(d.q[b]), sc[b] >> (8 * g), d.x, d.rs, acc[b]);
+            acc[b] = multiply4<0>(by_groups(d.q[b]), sc[b] >> (8 * g), d.x, d.rs, acc[b]);
     };
     // Wavefront w takes steps w, w + kStreamWaves, ..., two in flight.
     Step even, odd;
@@ -421,19 +465,34 @@ void expert_mx4_stream_kernel(const char* __restrict__ rows, const uint8_t* __re
     *reinterpret_cast<v2i*>(out + (int64_t(row0 + i) * feats + f) * 2) = pack_bf16x4(v);
 }
 
+int64_t tile_features(bool gated, int32_t feats) {
+    const int32_t per = kWaves * kBlocks * 16 / (gated ? 2 : 1);
+    return (int64_t(feats) + per - 1) / per;
+}
+int64_t tiles_of(bool gated, int32_t E, int64_t max_rows, int32_t feats, int rows) {
+    return tile_features(gated, feats) * ((max_rows + rows - 1) / rows + (max_rows < E ? max_rows : E));
+}
+int tile_rows(const ExpertMx4Args& a) {
+    return expert_mx4_tile_rows(a.gated, a.E, a.max_rows, a.feats);
+}
+int64_t tiles_of(const ExpertMx4Args& a) {
+    return tiles_of(a.gated, a.E, a.max_rows, a.feats, tile_rows(a));
+}
 int64_t round_up(int64_t n, int64_t unit) { return (n + unit - 1) / unit * unit; }
 int64_t active(const ExpertMx4Args& a) { return a.max_rows < a.E ? a.max_rows : a.E; }
 
-int64_t tile_features(const ExpertMx4Args& a) {
-    const int32_t per = kWaves * kBlocks * 16 / (a.gated ? 2 : 1);
-    return (int64_t(a.feats) + per - 1) / per;
+// Neighbouring tiles that one XCD takes together: with 64 an expert's rows are
+// read into few L2 caches (256 experts of 7168 -> 2 x 2048 at 1024 rows each 4.49
+// ms, with 8 4.65; 64 rows each 0.72 with both). Fewer where that would leave an
+// XCD fewer than 8 such pieces.
+int32_t tile_chunk(const ExpertMx4Args& a) {
+    const int64_t tiles = tiles_of(a);
+    int32_t chunk = 1;
+    while (chunk < 64 && tiles >= int64_t(chunk) * 2 * kExpertXcds * 8) chunk *= 2;
+    return chunk;
 }
-// Rows per tile, by what an expert has on average.
-int tile_rows(const ExpertMx4Args& a) { return a.max_rows > 64 * int64_t(a.E) ? 128 : 64; }
 int64_t tile_workgroups(const ExpertMx4Args& a) {
-    const int64_t rows = tile_rows(a);
-    return round_up(tile_features(a) * ((a.max_rows + rows - 1) / rows + active(a)),
-                    int64_t(kExpertXcds) * kXcdChunk);
+    return round_up(tiles_of(a), int64_t(kExpertXcds) * tile_chunk(a));
 }
 int64_t stream_features(const ExpertMx4Args& a) {
     const int32_t per = (a.gated ? kBlocks / 2 : kBlocks) * 16;
@@ -445,7 +504,7 @@ int64_t stream_workgroups(const ExpertMx4Args& a) {
 }
 
 template <class Kernel>
-hipError_t launch(Kernel kernel, int64_t workgroups, int threads, int64_t ftiles,
+hipError_t launch(Kernel kernel, int64_t workgroups, int threads, int64_t ftiles, int32_t chunk,
                   const ExpertMx4Args& a, hipStream_t stream) {
     const char* w = static_cast<const char*>(a.w);
     const char* scales = w + mxfp4_tiles(a.E, a.gated ? 2 * a.feats : a.feats, a.red) * 1024;
@@ -454,11 +513,21 @@ hipError_t launch(Kernel kernel, int64_t workgroups, int threads, int64_t ftiles
                        w, reinterpret_cast<const uint8_t*>(scales), a.offsets, a.E,
                        static_cast<int32_t>(a.max_rows), a.red, a.feats,
                        static_cast<int32_t>(ftiles), a.activation, static_cast<char*>(a.out),
-                       a.zero);
+                       a.zero, chunk);
     return hipGetLastError();
 }
 
 }  // namespace
+
+// Measured on MI355X, 64 against 128 rows per tile, other weights in every call: 64
+// experts of 7168 -> 2 x 2048 at 32 rows each 176 and 177 us, at 64 212 and 183, at
+// 256 398 and 354; 8 of 4096 -> 2 x 1408 at 128 24.1 and 29.8 (176 tiles of 128
+// rows), at 256 30.8 and 30.9 (264), at 512 42.8 and 41.8 (440); 24 of 1984 -> 1000
+// at 256 21.4 and 21.9 (288), at 512 37.7 and 31.7 (480).
+int expert_mx4_tile_rows(bool gated, int32_t E, int64_t max_rows, int32_t feats) {
+    return max_rows >= 64 * int64_t(E) && tiles_of(gated, E, max_rows, feats, 128) >= 320 ? 128
+                                                                                          : 64;
+}
 
 int64_t expert_mx4_grid(const ExpertMx4Args& a) { return tile_workgroups(a) * (kWaves * 64); }
 int64_t expert_mx4_stream_grid(const ExpertMx4Args& a) {
@@ -469,12 +538,13 @@ hipError_t launch_expert_mx4(const ExpertMx4Args& a, hipStream_t stream) {
     auto kernel = tile_rows(a) == 128
                       ? (a.gated ? expert_mx4_kernel<true, 128> : expert_mx4_kernel<false, 128>)
                       : (a.gated ? expert_mx4_kernel<true, 64> : expert_mx4_kernel<false, 64>);
-    return launch(kernel, tile_workgroups(a), kWaves * 64, tile_features(a), a, stream);
+    return launch(kernel, tile_workgroups(a), kWaves * 64, tile_features(a.gated, a.feats), tile_chunk(a),
+                  a, stream);
 }
 
 hipError_t launch_expert_mx4_stream(const ExpertMx4Args& a, hipStream_t stream) {
     return launch(a.gated ? expert_mx4_stream_kernel<true> : expert_mx4_stream_kernel<false>,
-                  stream_workgroups(a), kStreamWaves * 64, stream_features(a), a, stream);
+                  stream_workgroups(a), kStreamWaves * 64, stream_features(a), kStreamChunk, a, stream);
 }
 
 }  // namespace moe

@@ -107,13 +107,21 @@ int run_mx4(bool gated, const void* values, const void* row_scales, const void* 
 
 namespace moe {
 
-// Where the form that streams the weights is the faster one: the limits of the
-// products with bf16 rows.
+// Where the form that streams the weights (16-row tiles, the sum split over a
+// workgroup's wavefronts) is the faster one. Measured on MI355X with other weights
+// in every call, streamed against tiled:
+//   - up to 8 rows per expert: 64 experts of 7168 -> 2 x 2048 145 and 171 us at 8
+//     rows each, 230 and 173 at 16; 256 of 2048 -> 7168 315 and 346, 465 and 360.
+//   - while its workgroups are few (the tiled form then leaves CUs idle): one expert
+//     of 4096 -> 2 x 2048 18.5 and 21.9 us at 256 rows (1024 workgroups), 31.3 and
+//     22.1 at 512 (2048); one of 2048 -> 7168 12.4 and 13.5 at 128 (896), 20.1 and
+//     14.0 at 256 (1792); 24 of 1984 -> 1000 12.5 and 14.4 at 768 (768), 19.7 and
+//     15.6 at 1536 (1536).
 bool expert_mx4_streams(int32_t E, int64_t max_rows, int64_t positions) {
     if (max_rows <= int64_t(8) * E) return true;
     const int64_t experts = max_rows < E ? max_rows : E;
     const int64_t tiles = (max_rows + 15) / 16;
-    return (positions + 63) / 64 * (tiles > experts ? tiles : experts) <= 1536;
+    return (positions + 63) / 64 * (tiles > experts ? tiles : experts) <= 1024;
 }
 
 }  // namespace moe

@@ -75,6 +75,9 @@ struct ExpertMx4Args {
 // Tiles of many rows, or weights streamed for up to 16 rows each; a rule on the
 // sizes chooses. The grids are work-items of a launch.
 bool expert_mx4_streams(int32_t E, int64_t max_rows, int64_t positions);
+// Rows of a tile: 128 from 64 rows per expert on average, unless the tiles
+// become too few for the CUs, else 64.
+int expert_mx4_tile_rows(bool gated, int32_t E, int64_t max_rows, int32_t feats);
 hipError_t launch_expert_mx4(const ExpertMx4Args& a, hipStream_t stream);
 int64_t expert_mx4_grid(const ExpertMx4Args& a);
 hipError_t launch_expert_mx4_stream(const ExpertMx4Args& a, hipStream_t stream);

@@ -127,7 +127,15 @@ SHAPES = [
     ([1100, 17], 9, 1312, 800, 1608),
     ([530, 49, 600], 0, 1408, 704, 1336),
     ([64, 1000, 65], 1, 2880, 720, 1400),
+    # sums longer than the row scales that LDS holds at a time (7680)
+    ([600, 90, 700], 5, 8032, 656, 1256),
+    ([300, 1100], 0, 15424, 656, 1256),
+    # 128-row tiles; last ones of one to eight 16-row blocks
+    ([138, 148, 296, 60, 474, 376, 256], 7, 96, 2064, 4104),
+    ([1200, 700, 77], 0, 1312, 2560, 5128),
+    ([1500, 1000], 3, 7712, 2048, 4096),
 ]
+TILES_128 = 3              # of these
 
 
 def _operands(i):

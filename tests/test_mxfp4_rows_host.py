@@ -138,6 +138,15 @@ def test_both_forms_are_tested(lib):
         for counts, behind, K, F, N in shapes:
             rows = sum(counts) + behind
             assert rule(len(counts), rows, N) == rule(len(counts), rows, 2 * F) == streams
+    tile = getattr(lib, "_ZN3moe20expert_mx4_tile_rowsEbili")
+    tile.argtypes, tile.restype = [C.c_bool, C.c_int32, C.c_int64, C.c_int32], C.c_int
+    for i, (counts, behind, K, F, N) in enumerate(many):
+        E, rows = len(counts), sum(counts) + behind
+        want = 128 if i >= len(many) - gpu.TILES_128 else 64
+        assert tile(False, E, rows, N) == tile(True, E, rows, F) == want, i
+    large = many[-gpu.TILES_128:]
+    assert {-(-(c % 128) // 16) for counts, *_ in large for c in counts} >= {0, 1, 2, 3, 4, 6, 8}
+    assert any(K > 7680 for _, _, K, _, _ in large)
     # whole and partial sums of odd and even numbers of 128-element halves, and
     # last row tiles of one to four 16-row blocks
     assert {(-(-K // 128) % 2, K % 128 != 0) for _, _, K, _, _ in many} == {
