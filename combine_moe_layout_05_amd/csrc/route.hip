@@ -347,6 +347,27 @@ __device__ __forceinline__ void load_values(const __bf16* p, float (&v)[VALS]) {
     }
 }
 
+template <int VALS>
+__device__ __forceinline__ void store_values(float* p, const float (&v)[VALS]) {
+    struct alignas(VALS * 4 < 16 ? VALS * 4 : 16) Raw {
+        float v[VALS];
+    };
+    Raw r;
+#pragma unroll
+    for (int i = 0; i < VALS; ++i) r.v[i] = v[i];
+    *reinterpret_cast<Raw*>(p) = r;
+}
+template <int VALS>
+__device__ __forceinline__ void store_values(__bf16* p, const float (&v)[VALS]) {
+    struct alignas(VALS * 2 < 16 ? VALS * 2 : 16) Raw {
+        __bf16 v[VALS];
+    };
+    Raw r;
+#pragma unroll
+    for (int i = 0; i < VALS; ++i) r.v[i] = static_cast<__bf16>(v[i]);
+    *reinterpret_cast<Raw*>(p) = r;
+}
+
 // GROUPED needs E = 16 VALS and groups of 1, 2, 4, 8 or 16 lanes (`span`).
 template <int VALS, class L, bool BY_VALUE, bool GROUPED>
 __global__ __launch_bounds__(kWaves * 64)
@@ -618,6 +639,100 @@ void route_grad_kernel(const L* __restrict__ logits, const int32_t* __restrict__
     }
 }
 
+// The same for up to 256 experts, 16 lanes per token as in the choice; lane j also
+// holds slot j.
+template <int VALS, class L>
+__global__ __launch_bounds__(kWaves * 64)
+void route_grad_lanes_kernel(const L* __restrict__ logits, const int32_t* __restrict__ ids,
+                             const float* __restrict__ grad, int32_t T, int32_t E, int32_t K,
+                             int32_t sigmoid, int32_t renormalize, float scale, int32_t whole,
+                             L* __restrict__ out) {
+    const int lane = threadIdx.x & 63;
+    const int j = lane & (kLanes - 1);
+    const int64_t row0 =
+        (int64_t(blockIdx.x) * (blockDim.x >> 6) + (threadIdx.x >> 6)) * (64 / kLanes);
+    if (row0 >= T) return;
+    const bool there = row0 + (lane >> 4) < T;
+    const int64_t row = there ? row0 + (lane >> 4) : T - 1;
+    const L* in = logits + row * E;
+    const bool dense = !sigmoid && !renormalize;
+    int id = -1;
+    float g = 0.0f, l = -INFINITY;
+    if (j < K) {
+        id = ids[row * K + j];
+        g = grad[row * K + j] * scale;
+        if (id < 0 || id >= E) id = -1;
+        if (id >= 0) l = taking_part(logit_at(in, id));
+        if (!(l > -INFINITY)) id = -1;
+        if (id < 0) g = 0.0f;
+    }
+    float v[VALS];
+    float top = -INFINITY, sum = 0.0f;
+    if (dense) {
+        if (whole) {
+            load_values<VALS>(in + j * VALS, v);
+        } else {
+#pragma unroll
+            for (int i = 0; i < VALS; ++i) {
+                const int e = j * VALS + i;
+                const float x = logit_at(in, min(e, E - 1));
+                v[i] = e < E ? x : -INFINITY;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < VALS; ++i) top = fmaxf(top, v[i] = taking_part(v[i]));
+        top = lanes_max(top);
+        const float from = top > -INFINITY ? top : 0.0f;
+#pragma unroll
+        for (int i = 0; i < VALS; ++i) sum += v[i] = exp_f32(v[i] - from);
+        sum = lanes_sum(sum);
+    } else if (!sigmoid) {
+        top = lanes_max(l);
+    }
+    const float p = id < 0 ? 0.0f : sigmoid ? 1.0f / (1.0f + expf(-l)) : expf(l - top);
+    if (renormalize) sum = lanes_sum(p);
+    float d, s = 0.0f;
+    if (sigmoid) {
+        const float slope = id < 0 ? 0.0f : p / (1.0f + expf(l));
+        if (renormalize) {
+            s = lanes_sum(sum == 0.0f ? 0.0f : g * (p / sum));
+            d = sum == 0.0f ? 0.0f : (g - s) / sum * slope;
+        } else {
+            d = g * slope;
+        }
+    } else {
+        const float q = sum == 0.0f ? 0.0f : p / sum;
+        s = lanes_sum(g * q);
+        d = dense ? g * q : (g - s) * q;
+    }
+    if (id < 0) d = 0.0f;
+    const float share = dense && sum > 0.0f ? -s / sum : 0.0f;
+#pragma unroll
+    for (int i = 0; i < VALS; ++i) v[i] = dense ? v[i] * share : 0.0f;
+    const int first = j * VALS;
+    for (int k = 0; k < K; ++k) {
+        const float dk = __shfl(d, (lane & 48) + k, 64);
+        const int at = __shfl(id, (lane & 48) + k, 64) - first;
+#pragma unroll
+        for (int i = 0; i < VALS; ++i)
+            if (at == i) v[i] += dk;
+    }
+    if (!there) return;
+    if (whole) {
+        store_values<VALS>(out + row * E + first, v);
+    } else {
+#pragma unroll
+        for (int i = 0; i < VALS; ++i)
+            if (first + i < E) store_grad(out, row * E + first + i, v[i]);
+    }
+}
+
+// A wavefront per workgroup until there is one for every CU.
+int lane_waves(int32_t T) { return T <= 4 * 1024 ? 1 : kWaves; }
+int lane_values(int32_t E) {
+    return E <= kLanes * 2 ? 2 : E <= kLanes * 4 ? 4 : E <= kLanes * 8 ? 8 : 16;
+}
+
 template <int VALS, class L>
 hipError_t launch_lanes(const RouteArgs& a, int32_t span, hipStream_t stream) {
     const bool by_value = a.sigmoid && (a.bias || a.groups > 1), grouped = a.groups > 1;
@@ -627,8 +742,7 @@ hipError_t launch_lanes(const RouteArgs& a, int32_t span, hipStream_t stream) {
                                       : route_lanes_kernel<VALS, L, false, false>);
     const bool whole = a.E == kLanes * VALS && reinterpret_cast<uintptr_t>(a.logits) % 16 == 0 &&
                        reinterpret_cast<uintptr_t>(a.bias) % 16 == 0;
-    // A wavefront per workgroup until there is one for every CU.
-    const int waves = a.T <= 4 * 1024 ? 1 : kWaves;
+    const int waves = lane_waves(a.T);
     const int64_t tokens = waves * (64 / kLanes);
     hipLaunchKernelGGL(kernel, dim3(static_cast<uint32_t>((a.T + tokens - 1) / tokens)),
                        dim3(waves * 64), 0, stream, static_cast<const L*>(a.logits), a.bias, a.T,
@@ -658,7 +772,7 @@ hipError_t launch_route(const RouteArgs& a, hipStream_t stream) {
 template <class L>
 hipError_t route(const RouteArgs& a, hipStream_t stream) {
     if (a.E <= kLanes * 16 && a.K <= kList) {
-        const int vals = a.E <= kLanes * 2 ? 2 : a.E <= kLanes * 4 ? 4 : a.E <= kLanes * 8 ? 8 : 16;
+        const int vals = lane_values(a.E);
         if (const int32_t span = lanes_of_group(a, vals)) {
             if (vals == 2) return launch_lanes<2, L>(a, span, stream);
             if (vals == 4) return launch_lanes<4, L>(a, span, stream);
@@ -675,6 +789,22 @@ hipError_t route(const RouteArgs& a, hipStream_t stream) {
 
 template <class L>
 hipError_t route_grad(const RouteGradArgs& a, hipStream_t stream) {
+    if (a.E <= kLanes * 16) {
+        const int vals = lane_values(a.E), waves = lane_waves(a.T);
+        auto kernel = vals == 2   ? route_grad_lanes_kernel<2, L>
+                      : vals == 4 ? route_grad_lanes_kernel<4, L>
+                      : vals == 8 ? route_grad_lanes_kernel<8, L>
+                                  : route_grad_lanes_kernel<16, L>;
+        const bool whole = a.E == kLanes * vals &&
+                           reinterpret_cast<uintptr_t>(a.logits) % 16 == 0 &&
+                           reinterpret_cast<uintptr_t>(a.grad_logits) % 16 == 0;
+        const int64_t tokens = waves * (64 / kLanes);
+        hipLaunchKernelGGL(kernel, dim3(static_cast<uint32_t>((a.T + tokens - 1) / tokens)),
+                           dim3(waves * 64), 0, stream, static_cast<const L*>(a.logits), a.ids,
+                           a.grad, a.T, a.E, a.K, a.sigmoid, a.renormalize, a.scale, whole,
+                           static_cast<L*>(a.grad_logits));
+        return hipGetLastError();
+    }
     hipLaunchKernelGGL((route_grad_kernel<L>), dim3((static_cast<uint32_t>(a.T) + kWaves - 1) / kWaves),
                        dim3(kWaves * 64), 0, stream, static_cast<const L*>(a.logits), a.ids, a.grad,
                        a.T, a.E, a.K, a.sigmoid, a.renormalize, a.scale,

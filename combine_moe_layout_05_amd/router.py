@@ -53,11 +53,15 @@ class _RouteTopk(torch.autograd.Function):
         ctx.save_for_backward(logits, ids)
         ctx.args = score, flags, scale
         ctx.mark_non_differentiable(ids)
+        # No zeros for the ids' gradient, which is none: that would be a launch.
+        ctx.set_materialize_grads(False)
         return ids, scores
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, _grad_ids, grad_scores):
+        if grad_scores is None:
+            return (None,) * 8
         logits, ids = ctx.saved_tensors
         score, flags, scale = ctx.args
         grad = _backward(grad_scores.contiguous(), logits, ids, score, flags, scale)
