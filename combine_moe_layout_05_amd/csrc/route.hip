@@ -5,12 +5,12 @@
 // neither NaN nor -inf:
 //   softmax   p = exp(l - m) / sum of exp(l - m), m the largest l
 //   sigmoid   p = 1 / (1 + exp(-l))
-// The K largest of v are chosen, equal ones by index; v is l where p only has
-// to keep its order, else sigmoid(l) + bias. That is computed in 64 bits, so
-// that the order of near values is that of the formula and not that of an
-// exponential's last digit. With groups of consecutive experts only those of
-// the `kept` best groups can be chosen, by the group's largest v (softmax) or the
-// sum of its two largest (sigmoid).
+// The K largest of v are chosen, equal ones by index; v is l, which has p's order,
+// or with a bias sigmoid(l) + bias. That is computed in 64 bits, so that the order
+// of near values is that of the formula and not that of an exponential's last
+// digit. With groups of consecutive experts only those of the `kept` best groups
+// can be chosen, by the group's largest v (softmax) or the sum of the sigmoids,
+// plus their bias, of its two largest (sigmoid), in 64 bits.
 //
 // Up to 256 experts and 8 of them per token: 16 lanes per token, which select by
 // 32-bit keys and check the result, with the slow form for tokens that the check
@@ -102,13 +102,19 @@ __device__ __forceinline__ void take_out(V (&v)[VALS], int lane, int at) {
         if (i * 64 + lane == at) v[i] = -INFINITY;
 }
 
-// The experts chosen by v (destroyed): lane k gets the k-th, or -1.
+__device__ __forceinline__ double sigmoid_64(double l) { return 1.0 / (1.0 + exp(-l)); }
+// What a value counts in its group's sum: a logit its sigmoid, others themselves.
+__device__ __forceinline__ double in_sum(float l) { return sigmoid_64(l); }
+__device__ __forceinline__ double in_sum(double v) { return v; }
+
+// The experts chosen by v (destroyed): lane k gets the k-th, or -1. Groups go by
+// their largest value, or, with `pairs`, by the sum of what their two largest count.
 template <int VALS, class V>
 __device__ int select(V (&v)[VALS], int lane, int K, int E, int groups, int kept, bool pairs) {
     if (groups > 1) {
         const int size = E / groups;
         // Lane g holds group g's value; groups without an expert keep -inf.
-        V value = -INFINITY;
+        double value = -INFINITY;
         for (int g = 0; g < groups; ++g) {
             V w[VALS];
 #pragma unroll
@@ -119,20 +125,22 @@ __device__ int select(V (&v)[VALS], int lane, int K, int E, int groups, int kept
             V first, second;
             int at;
             best_of<VALS, V>(w, first, at);
-            if (pairs && size > 1) {
+            double sum = first;
+            if (pairs && first > V(-INFINITY)) {
+                sum = in_sum(first);
                 take_out<VALS, V>(w, lane, at);
                 best_of<VALS, V>(w, second, at);
-                if (second > V(-INFINITY)) first += second;
+                if (second > V(-INFINITY)) sum += in_sum(second);
             }
-            if (lane == g) value = first;
+            if (lane == g) value = sum;
         }
         uint64_t open = 0;
         for (int j = 0; j < kept; ++j) {
-            const V one[1] = {value};
-            V top;
+            const double one[1] = {value};
+            double top;
             int at;
-            best_of<1, V>(one, top, at);
-            if (!(top > V(-INFINITY))) break;
+            best_of<1, double>(one, top, at);
+            if (!(top > -INFINITY)) break;
             open |= uint64_t(1) << at;
             if (lane == at) value = -INFINITY;
         }
@@ -166,25 +174,24 @@ __device__ __forceinline__ float score_of(bool sigmoid, bool renormalize, int id
 }
 
 // The choice of one token by a whole wavefront: lane k < K gets the k-th
-// expert or -1.
+// expert or -1. Only experts e with bit e / per of `open` are looked at.
 template <int VALS, class L>
 __device__ int choose(const L* in, const float* bias, int lane, int32_t K, int32_t E, bool sigmoid,
-                      int32_t groups, int32_t kept) {
+                      int32_t groups, int32_t kept, uint32_t open = 1, int32_t per = 1024) {
     float l[VALS];
 #pragma unroll
     for (int i = 0; i < VALS; ++i) {
         const int e = i * 64 + lane;
-        l[i] = e < E ? taking_part(logit_at(in, e)) : -INFINITY;
+        l[i] = e < E && (open >> (e / per) & 1) ? taking_part(logit_at(in, e)) : -INFINITY;
     }
-    if (!sigmoid || (!bias && groups == 1))
+    if (!sigmoid || !bias)
         return select<VALS, float>(l, lane, K, E, groups, kept, sigmoid);
     double v[VALS];
 #pragma unroll
     for (int i = 0; i < VALS; ++i) {
         v[i] = -INFINITY;
         if (l[i] > -INFINITY) {
-            v[i] = 1.0 / (1.0 + exp(-static_cast<double>(l[i])));
-            if (bias) v[i] += static_cast<double>(bias[i * 64 + lane]);
+            v[i] = sigmoid_64(l[i]) + static_cast<double>(bias[i * 64 + lane]);
             if (!(v[i] == v[i])) v[i] = -INFINITY;
         }
     }
@@ -233,10 +240,12 @@ void route_kernel(const L* __restrict__ logits, const float* __restrict__ bias, 
 // where 8 rounds of a search over the wavefront take several hundred.
 //
 // Then the choice is checked against the values themselves: neighbours in order
-// and every other expert below the last, by more than the error of a value in 32
-// bits where it is one (a sigmoid plus a bias), exactly where it is a logit. A token
-// that fails (two values nearer than that, fewer experts than slots, values more
-// than 16 apart, infinities) is chosen for by the whole wavefront.
+// and every other expert below the last, exactly where they are logits, by more
+// than the error of a value in 32 bits where they are sigmoids plus a bias.
+// Neighbours nearer than that are put in order by their values in 64 bits. A token
+// that fails otherwise (an expert too near to the last or a group to the last kept,
+// fewer experts than slots, values more than 16 apart, infinities) is chosen for by
+// the whole wavefront.
 constexpr int kLanes = 16;
 constexpr int kList = 8;
 
@@ -417,15 +426,11 @@ void route_lanes_kernel(const L* __restrict__ logits, const float* __restrict__ 
     float v[VALS];
     if constexpr (BY_VALUE) {
         float b[VALS];
+        if (whole) {
+            load_values<VALS>(bias + j * VALS, b);
+        } else {
 #pragma unroll
-        for (int i = 0; i < VALS; ++i) b[i] = 0.0f;
-        if (bias) {
-            if (whole) {
-                load_values<VALS>(bias + j * VALS, b);
-            } else {
-#pragma unroll
-                for (int i = 0; i < VALS; ++i) b[i] = bias[min(j * VALS + i, E - 1)];
-            }
+            for (int i = 0; i < VALS; ++i) b[i] = bias[min(j * VALS + i, E - 1)];
         }
 #pragma unroll
         for (int i = 0; i < VALS; ++i) {
@@ -436,7 +441,8 @@ void route_lanes_kernel(const L* __restrict__ logits, const float* __restrict__ 
 #pragma unroll
         for (int i = 0; i < VALS; ++i) v[i] = l[i];
     }
-    bool bad = false;
+    uint64_t open = ~uint64_t(0);       // lanes of the kept groups
+    bool open_bad = false;
     if constexpr (GROUPED) {
         // The two largest of a group: of a lane, then of its lanes.
         float first = -INFINITY, second = -INFINITY, largest = 0.0f;
@@ -454,16 +460,23 @@ void route_lanes_kernel(const L* __restrict__ logits, const float* __restrict__ 
         if (span > 4) join(__shfl_xor(first, 4, 64), __shfl_xor(second, 4, 64));
         if (span > 8) join(__shfl_xor(first, 8, 64), __shfl_xor(second, 8, 64));
         float value = first;
-        if (BY_VALUE && second > -INFINITY) value += second;
-        if (BY_VALUE)
+        if (sigmoid) {
+            // Without a bias the two largest logits are those of the largest sigmoids.
+            if (!BY_VALUE && first > -INFINITY) {
+                first = sigmoid_of(first);
+                if (second > -INFINITY) second = sigmoid_of(second);
+            }
+            value = second > -INFINITY ? first + second : first;
             largest = lanes_max(fmaxf(fabsf(first), second > -INFINITY ? fabsf(second) : 0.0f));
-        const float margin = BY_VALUE ? (8.0f + 4.0f * largest) * 0x1p-22f : 0.0f;
+        }
+        const float margin = sigmoid ? (8.0f + 4.0f * largest) * 0x1p-22f : 0.0f;
         const int ahead = lanes_ahead<1>(value, j, span);
         const bool keep = ahead < kept * span;
-        if (BY_VALUE && kept < groups) {
+        open = __ballot(keep);
+        if (sigmoid && kept < groups) {
             const float least = -lanes_max(keep ? -value : -INFINITY);
             const float next = lanes_max(keep ? -INFINITY : value);
-            bad = !(least - next > margin);
+            open_bad = !(least - next > margin);
         }
 #pragma unroll
         for (int i = 0; i < VALS; ++i) v[i] = keep ? v[i] : -INFINITY;
@@ -514,7 +527,7 @@ void route_lanes_kernel(const L* __restrict__ logits, const float* __restrict__ 
         if (i == K - 1) last = list[i];
     }
     if (j >= K) mine = 0;
-    if (last < 256) bad = true;         // not K experts within 16 of the largest
+    bool bad = open_bad || last < 256;  // not K experts within 16 of the largest
     int id = j < K ? 255 - static_cast<int>(mine & 255) : -1;
     float chosen = 0.0f;
     if (j < K && id < E) chosen = taking_part(logit_at(in, id));
@@ -522,31 +535,52 @@ void route_lanes_kernel(const L* __restrict__ logits, const float* __restrict__ 
     float value = chosen;
     if constexpr (BY_VALUE) {
         value = sigmoid_of(chosen);
-        if (bias && j < K && id < E) value += bias[id];
+        if (j < K && id < E) value += bias[id];
     }
     const float next = __shfl(value, lane + 1 < 64 ? lane + 1 : lane, 64);
     const int next_id = __shfl(id, lane + 1 < 64 ? lane + 1 : lane, 64);
     const float least = __shfl(value, (lane & 48) + K - 1, 64);
     const float margin = BY_VALUE ? (4.0f + fabsf(m) + fabsf(least)) * 0x1p-22f : 0.0f;
-    if (j + 1 < K) {
-        if (BY_VALUE)
-            bad = bad || !(value - next > margin);
-        else
-            bad = bad || !(value > next || (value == next && id < next_id));
+    if constexpr (BY_VALUE) {
+        if (__any(j + 1 < K && !(value - next > margin))) {
+            // In order by the values in 64 bits; equal ones by index.
+            double v64 = -INFINITY;
+            if (j < K && id < E) {
+                v64 = sigmoid_64(chosen) + static_cast<double>(bias[id]);
+            }
+            int before = 0;
+            for (int k = 0; k < K; ++k) {
+                const double other = __shfl(v64, (lane & 48) + k, 64);
+                const int other_id = __shfl(id, (lane & 48) + k, 64);
+                before += other > v64 || (other == v64 && other_id < id);
+            }
+            const int to = (lane & 48) + (j < K ? before : j);
+            id = __builtin_amdgcn_ds_permute(to * 4, id);
+            chosen = __builtin_bit_cast(
+                float, __builtin_amdgcn_ds_permute(to * 4, __builtin_bit_cast(int32_t, chosen)));
+        }
+    } else if (j + 1 < K) {
+        bad = bad || !(value > next || (value == next && id < next_id));
     }
-    const float limit = BY_VALUE ? least - margin : least;
+    // The last key's value may be above another's by what a key does not hold.
+    const float limit = BY_VALUE ? least - margin - 0x1p-20f : least;
     float above = -INFINITY;            // the largest of those not chosen
 #pragma unroll
     for (int i = 0; i < VALS; ++i) above = fmaxf(above, key[i] < last ? v[i] : -INFINITY);
     bad = bad || above > limit;
 
     // Tokens that the check does not clear, one after the other.
-    const uint64_t failed = __ballot(bad && there);
+    const uint64_t failed = __ballot(bad && there), unsure = __ballot(open_bad);
 #pragma unroll 1
     for (int r = 0; r < 64 / kLanes; ++r) {
         if (!(failed >> (r * kLanes) & 0xFFFF)) continue;
-        const int slow = choose<(VALS + 3) / 4, L>(logits + (row0 + r) * E, bias, lane, K, E,
-                                                   sigmoid != 0, groups, kept);
+        // Groups that are certain stay as they are.
+        const uint32_t certain =
+            GROUPED && !(unsure >> (r * kLanes) & 1)
+                ? static_cast<uint32_t>(open >> (r * kLanes)) & 0xFFFF : 0;
+        const int slow = choose<(VALS + 3) / 4, L>(
+            logits + (row0 + r) * E, bias, lane, K, E, sigmoid != 0, certain ? 1 : groups, kept,
+            certain ? certain : 1, certain ? VALS : 1024);
         const int here = __shfl(slow, j, 64);
         if ((lane >> 4) == r) {
             id = j < K ? here : -1;
@@ -735,7 +769,7 @@ int lane_values(int32_t E) {
 
 template <int VALS, class L>
 hipError_t launch_lanes(const RouteArgs& a, int32_t span, hipStream_t stream) {
-    const bool by_value = a.sigmoid && (a.bias || a.groups > 1), grouped = a.groups > 1;
+    const bool by_value = a.sigmoid && a.bias, grouped = a.groups > 1;
     auto kernel = by_value ? (grouped ? route_lanes_kernel<VALS, L, true, true>
                                       : route_lanes_kernel<VALS, L, true, false>)
                            : (grouped ? route_lanes_kernel<VALS, L, false, true>

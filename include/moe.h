@@ -566,12 +566,12 @@ int moe_gated_grouped_gemm_mxfp4_rows(const void *d_values, const void *d_scales
  *   MOE_SCORE_SOFTMAX  p = exp(l) / sum of exp(l) over the experts taking part
  *   MOE_SCORE_SIGMOID  p = 1 / (1 + exp(-l))
  * the K experts with the largest v are chosen, in descending order, equal ones
- * by ascending index. v is l, where p has the same order; with the sigmoid and a
- * bias or groups it is p + bias, computed in 64 bits (an expert whose v is NaN or
- * -inf is not chosen). The bias decides who is chosen and does not enter the
- * scores. With num_groups > 1 the experts form groups of E / num_groups
- * consecutive ones; only the topk_groups groups with the largest value (softmax:
- * their largest v; sigmoid: the sum of their two largest v, of one where only one
+ * by ascending index. v is l, which has the order of p, or with a bias (sigmoid
+ * only) p + bias, computed in 64 bits; an expert whose v is NaN or -inf is not
+ * chosen. The bias decides who is chosen and does not enter the scores. With
+ * num_groups > 1 the experts form groups of E / num_groups consecutive ones; only
+ * the topk_groups groups with the largest value (softmax: their largest v; sigmoid:
+ * the sum of p + bias over their two largest v, in 64 bits, of one where only one
  * takes part; equal ones by index) can be chosen from. A slot for which no expert
  * is left has id -1 and score 0.
  *   scores = scale * p, with MOE_ROUTE_RENORMALIZE scale * p / (sum of the chosen

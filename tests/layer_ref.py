@@ -23,20 +23,20 @@ def select(logits, K, score, bias=None, groups=1, kept=1):
     for t in range(T):
         l = [float(x) for x in logits[t].double()]
         part = [not math.isnan(x) and x != -math.inf for x in l]
-        if score == "sigmoid" and (bias is not None or groups > 1):
-            v = torch.sigmoid(logits[t].double())
+        counts = v = l
+        if score == "sigmoid":
+            counts = torch.sigmoid(logits[t].double())
             if bias is not None:
-                v = v + bias.double()
-            v = v.tolist()
-        else:
-            v = l
+                counts = counts + bias.double()
+                v = counts.tolist()
+            counts = counts.tolist()
         ok = [e for e in range(E) if part[e] and not math.isnan(v[e]) and v[e] != -math.inf]
         if groups > 1:
             value = {}
             for g in range(groups):
-                mine = sorted((v[e] for e in ok if e // size == g), reverse=True)
+                mine = sorted((e for e in ok if e // size == g), key=lambda e: (-v[e], e))
                 if mine:
-                    value[g] = sum(mine[:2]) if score == "sigmoid" else mine[0]
+                    value[g] = sum(counts[e] for e in mine[:2 if score == "sigmoid" else 1])
             best = sorted(value, key=lambda g: (-value[g], g))[:kept]
             ok = [e for e in ok if e // size in best]
         for k, e in enumerate(sorted(ok, key=lambda e: (-v[e], e))[:K]):

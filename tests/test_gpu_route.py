@@ -112,6 +112,22 @@ def test_far_biases_and_near_sums(groups):
         assert torch.equal(r.ids.cpu().long(), want)
 
 
+@pytest.mark.parametrize("E, G, kept", [(256, 8, 4), (256, 1, 1), (128, 4, 2), (160, 8, 3)])
+def test_saturated_sigmoids(E, G, kept):
+    """Sigmoids that are 1 in 64 bits: without a bias the logits decide, with
+    one the index does between them."""
+    gen = torch.Generator().manual_seed(E)
+    l = 60.0 + torch.randn(40, E, generator=gen)
+    l[:, ::7] = torch.randn(40, len(range(0, E, 7)), generator=gen)
+    for dtype in (torch.float32, BF):
+        for bias in (None, torch.zeros(E)):
+            x = l.to(dtype)
+            want = ref.select(x, 6, "sigmoid", bias, G, kept)
+            r = route_topk(x.to(DEV), 6, score="sigmoid", num_groups=G, topk_groups=kept,
+                           bias=None if bias is None else bias.to(DEV))
+            assert torch.equal(r.ids.cpu().long(), want)
+
+
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 def test_values_further_apart_than_a_key_holds(score):
     """Distances above 16 and below 2^-20 between the chosen."""
