@@ -19,8 +19,14 @@
 // and row 32 rounded elements, their 32 rests, the next 32 and so on, so that the
 // loads of few or many rows all take whole cache lines.
 //
-// Bound: the bytes of the weights in use, read once each, straight into the
-// registers the matrix cores read.
+// Bound: the bytes of the weights in use, read once per 16 (first kernel) or 8
+// slots of an expert, straight into the registers the matrix cores read; with 4 bits
+// also the load instructions, of which a CU takes one in some 30 cycles. Measured on
+// MI355X, 256 experts of 7168 -> 2048, 8 per token, us for both kernels: one token 127
+// (705 MB, 5.5 TB/s), in 4 bits 40 (187 MB, 4.7 TB/s), of which the start and end of
+// the two launches are some 12; 16 tokens 1548 and 356. Where an expert has several
+// slots the separate calls read its weights fewer times: 64 tokens on 8 experts of
+// 4096 -> 4096 take 230 us here and 162 there.
 #include "expert_kernels.h"
 #include "expert_mma.h"
 #include "expert_mxfp4.h"
@@ -106,8 +112,13 @@ struct Block {
 // load instruction takes the same time however few bytes are new in it; so lane
 // (i, g) loads for row i % (16 / P), and for product i / (16 / P) of P in turn, and
 // one load serves P products. Each of those has sums of its own, of which the 16
-// / P columns are valid that hold its own elements. Measured on MI355X, 4-bit
-// weights, 32 tokens on some 100 of 256 experts: see the down projection.
+// / P columns are valid that hold its own elements. The second kernel, whose rows
+// come twice, packs up to 2 slots fourfold and up to 4 twofold; the first, with four
+// blocks of weights per load of rows, does not (its registers spill). Measured on
+// MI355X, both kernels, packed and not, us: 256 experts of 7168 -> 2048, 4 bits, 4
+// tokens 119 and 123, 16 tokens 356 and 371, 64 tokens 825 and 847; 64 of 2048 ->
+// 1408, 8 tokens 50.4 and 55.7 (bf16 137 and 143); 32 of 256 -> 128, 16 tokens 15.6
+// and 15.0.
 template <bool FOUR, int P>
 struct Rows {
     static constexpr int kRows = 16 / P;
@@ -631,6 +642,11 @@ hipError_t launch(const LayerArgs& a, hipStream_t stream) {
     if (e != hipSuccess) return e;
     const int most = most_parts(slots);
     auto down = few_tokens_down_kernel<FOUR, WIDE, 1>;
+    // 16 columns of y per workgroup, or 32 where 16 give every CU more than one: every
+    // row of h then serves twice the weights. Measured on MI355X, 16 and 32, us: 256
+    // experts of 7168 -> 2048, 4 bits, 1 token 40.1 and 40.3, 64 tokens 881 and 825; 8 of
+    // 4096 -> 4096, 8 tokens 43.9 and 48.4 (bf16 154 and 175); 64 of 2048 -> 1408, 32
+    // tokens 85 and 100 (239 and 312).
     int columns = 16;
     if (a.D > 16 * 256) {
         down = few_tokens_down_kernel<FOUR, WIDE, 2>;
@@ -648,8 +664,13 @@ hipError_t launch(const LayerArgs& a, hipStream_t stream) {
 int64_t few_tokens_grid(const LayerArgs& a) { return gate_workgroups(a) * (gate_waves(a.four) * 64); }
 
 hipError_t launch_few_tokens(const LayerArgs& a, hipStream_t stream) {
-    // Twice the slots per pass over the weights where experts have many.
-    if (int64_t(a.T) * a.K >= int64_t(4) * a.E)
+    // Twice the slots per pass over the weights where experts have many: fewer passes,
+    // but half the wavefronts per CU and twice the products of a pass that has few.
+    // Measured on MI355X, both kernels, one against two times 16 (8) slots, us: 8 experts
+    // of 4096 -> 4096 at 4 slots each 170 and 175 (4 bits 51 and 59), at 8 194 and 189
+    // (69 and 74), at 16 286 and 230 (115 and 110); 64 of 2048 -> 1408 at 6 each 292 and
+    // 331 (121 and 149).
+    if (int64_t(a.T) * a.K >= int64_t(12) * a.E)
         return a.four ? launch<true, true>(a, stream) : launch<false, true>(a, stream);
     return a.four ? launch<true, false>(a, stream) : launch<false, false>(a, stream);
 }

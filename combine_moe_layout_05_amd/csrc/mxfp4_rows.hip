@@ -6,7 +6,11 @@
 // makes all its elements NaN. x / 2^e is exact but where it falls below 2^-126,
 // far under the smallest e2m1 number: one rounding in all.
 //
-// Bound: the bytes. Four lanes share a block, eight elements each.
+// Bound: the bytes. Four lanes share a block, eight elements each, so that a lane's
+// loads and stores are 16 or 32 bytes of the rows and 4 of the values, and the scale
+// needs two exchanges within the four. Measured on MI355X: 32768 rows of 7168 in bf16,
+// 595 MB, 116 us there and 104 us back (5.1 and 5.7 TB/s, a large copy 4.7); 613 rows of
+// 1984 in fp32 2.3 and 3.2 us, a launch's time.
 #include "expert_mma.h"
 #include "layer_kernels.h"
 

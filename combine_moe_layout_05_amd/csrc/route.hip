@@ -15,6 +15,13 @@
 // Up to 256 experts and 8 of them per token: 16 lanes per token, which select by
 // 32-bit keys and check the result, with the slow form for tokens that the check
 // does not clear. Else one wavefront per token; lane j holds experts j, j + 64, ...
+//
+// Bound: for a few tokens a launch, its loads and the chain of the selection (one
+// token of 256 experts, 8 groups 4.3 us); for many the vector instructions of the
+// selection, not the bytes. Measured on MI355X, 32768 tokens of 256 experts, fp32, 8
+// each: softmax 11.3 us (35.7 MB, 3.2 TB/s), sigmoid with bias 15.8, in 8 groups 19.1
+// (a wavefront per token 178); bf16 sigmoid in groups without a bias 21.8, as more of
+// its tokens are near ties.
 #include <cmath>
 
 #include "layer_kernels.h"
@@ -674,7 +681,8 @@ void route_grad_kernel(const L* __restrict__ logits, const int32_t* __restrict__
 }
 
 // The same for up to 256 experts, 16 lanes per token as in the choice; lane j also
-// holds slot j.
+// holds slot j. Bound: the launch; 8191 tokens of 128 experts, 8 each, bf16, softmax
+// renormalized 4.2 us on MI355X.
 template <int VALS, class L>
 __global__ __launch_bounds__(kWaves * 64)
 void route_grad_lanes_kernel(const L* __restrict__ logits, const int32_t* __restrict__ ids,

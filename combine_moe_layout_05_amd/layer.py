@@ -24,6 +24,8 @@ def moe_layer(x_TD: torch.Tensor, topk_scores_TK: torch.Tensor, topk_expert_ids_
     x bf16 [T, D]; scores fp32 and ids int32 [T, K] (e.g. route_topk's), T * K
     at most 512; a slot whose id is no expert's adds nothing. Weights bf16
     [E, 2 F, D] (gate rows first) and [E, D, F], or both as Mxfp4ExpertWeights.
+    Made for the few tokens of a decoding step: with some 8 slots or more per
+    expert (T * K / E) the separate calls are the faster ones.
     activation "silu" or "gelu" (tanh form). Result bf16 [T, D]. Records no
     gradient: training goes through MoeTokenDispatcher and expert_ffn."""
     dev = x_TD.device
