@@ -2,7 +2,9 @@
 dispatch also fused into two launches: MoeDispatcher.layout_dispatch), their
 backward, and the expert step between them (grouped GEMMs driven by the
 device-side offsets): one linear map per expert, or the gated feed-forward
-block with its backward; weights in bf16 or in 4 bits.
+block with its backward; weights in bf16 or in 4 bits, rows in bf16 or, for
+the forward products, in 4 bits. Before them the router (route_topk); for the
+few tokens of a decoding step the whole layer in two launches (moe_layer).
 
 The compute lives in libmoe_layout.so (hand-written HIP kernels behind the C
 ABI of include/moe.h); this package is its thin Python binding.

@@ -84,12 +84,12 @@ def route_topk(logits: torch.Tensor, topk: int, *, score: str = "softmax",
 
     logits fp32 or bf16 [T, E]. With p = softmax(logits) or sigmoid(logits) the
     experts with the largest p + bias are chosen (without a bias those with the
-    largest logits), equal ones by ascending index; scores = scale * p, divided by the sum of the chosen p if renormalize. bias,
-    fp32 [E], goes with the sigmoid only; it decides who is chosen, does not
-    enter the scores and gets no gradient. num_groups > 1: only the experts of
-    the topk_groups best of num_groups groups of neighbouring experts can be
-    chosen, by the group's largest p (softmax) or the sum of its two largest p +
-    bias (sigmoid).
+    largest logits), equal ones by ascending index; scores = scale * p, divided by
+    the sum of the chosen p if renormalize. bias, fp32 [E], goes with the sigmoid
+    only; it decides who is chosen, does not enter the scores and gets no
+    gradient. num_groups > 1: only the experts of the topk_groups best of
+    num_groups groups of neighbouring experts can be chosen, by the group's
+    largest p (softmax) or the sum of its two largest p + bias (sigmoid).
 
     A logit of NaN or -inf takes its expert out of the token's choice (and out
     of the softmax's sum); a slot for which no expert is left has id -1 and
