@@ -24,6 +24,7 @@
 // its tokens are near ties.
 #include <cmath>
 
+#include "expert_kernels.h"
 #include "layer_kernels.h"
 
 namespace moe {
@@ -212,7 +213,7 @@ void route_kernel(const L* __restrict__ logits, const float* __restrict__ bias, 
                   int32_t groups, int32_t kept, int32_t* __restrict__ ids,
                   float* __restrict__ scores) {
     const int lane = threadIdx.x & 63;
-    const int64_t row = int64_t(blockIdx.x) * kWaves + (threadIdx.x >> 6);
+    const int64_t row = int64_t(blockIdx.x) * (blockDim.x >> 6) + (threadIdx.x >> 6);
     if (row >= T) return;
     const L* in = logits + row * E;
     float top = -INFINITY, sum = 0.0f;
@@ -622,7 +623,7 @@ void route_grad_kernel(const L* __restrict__ logits, const int32_t* __restrict__
                        const float* __restrict__ grad, int32_t T, int32_t E, int32_t K,
                        int32_t sigmoid, int32_t renormalize, float scale, L* __restrict__ out) {
     const int lane = threadIdx.x & 63;
-    const int64_t row = int64_t(blockIdx.x) * kWaves + (threadIdx.x >> 6);
+    const int64_t row = int64_t(blockIdx.x) * (blockDim.x >> 6) + (threadIdx.x >> 6);
     if (row >= T) return;
     const L* in = logits + row * E;
     const bool dense = !sigmoid && !renormalize;
@@ -802,12 +803,17 @@ int32_t lanes_of_group(const RouteArgs& a, int vals) {
     return (span & (span - 1)) == 0 ? span : 0;
 }
 
+// Wavefronts per workgroup with one token each: one where whole workgroups of kWaves
+// would make a launch of 2^32 threads.
+uint32_t token_waves(int32_t T) { return (int64_t(T) + kWaves - 1) * 64 > kMaxGrid ? 1 : kWaves; }
+
 template <int VALS, class L>
 hipError_t launch_route(const RouteArgs& a, hipStream_t stream) {
-    hipLaunchKernelGGL((route_kernel<VALS, L>), dim3((static_cast<uint32_t>(a.T) + kWaves - 1) / kWaves),
-                       dim3(kWaves * 64), 0, stream, static_cast<const L*>(a.logits), a.bias, a.T,
-                       a.E, a.K, a.sigmoid, a.renormalize, a.scale, a.groups, a.kept, a.ids,
-                       a.scores);
+    const uint32_t waves = token_waves(a.T);
+    hipLaunchKernelGGL((route_kernel<VALS, L>),
+                       dim3((static_cast<uint32_t>(a.T) + waves - 1) / waves), dim3(waves * 64), 0,
+                       stream, static_cast<const L*>(a.logits), a.bias, a.T, a.E, a.K, a.sigmoid,
+                       a.renormalize, a.scale, a.groups, a.kept, a.ids, a.scores);
     return hipGetLastError();
 }
 
@@ -847,9 +853,10 @@ hipError_t route_grad(const RouteGradArgs& a, hipStream_t stream) {
                            static_cast<L*>(a.grad_logits));
         return hipGetLastError();
     }
-    hipLaunchKernelGGL((route_grad_kernel<L>), dim3((static_cast<uint32_t>(a.T) + kWaves - 1) / kWaves),
-                       dim3(kWaves * 64), 0, stream, static_cast<const L*>(a.logits), a.ids, a.grad,
-                       a.T, a.E, a.K, a.sigmoid, a.renormalize, a.scale,
+    const uint32_t waves = token_waves(a.T);
+    hipLaunchKernelGGL((route_grad_kernel<L>),
+                       dim3((static_cast<uint32_t>(a.T) + waves - 1) / waves), dim3(waves * 64), 0,
+                       stream, static_cast<const L*>(a.logits), a.ids, a.grad, a.T, a.E, a.K, a.sigmoid, a.renormalize, a.scale,
                        static_cast<L*>(a.grad_logits));
     return hipGetLastError();
 }

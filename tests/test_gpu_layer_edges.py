@@ -46,6 +46,25 @@ def test_router_past_4_gib(dtype):
     assert torch.equal(d[-4000:], want)
 
 
+def test_router_of_the_most_tokens():
+    """2^26 - 1 tokens, a wavefront each: whole workgroups of four would be a
+    launch of 2^32 threads."""
+    T, E, last = (1 << 26) - 1, 257, 9
+    note(f"router of {T} tokens of {E} experts")
+    l = torch.zeros(T, E, dtype=BF, device=DEV)
+    l[-last:] = torch.randn(last, E, generator=_gpu_gen(2), device=DEV).to(BF)
+    r = route_topk(l, 1, renormalize=False)
+    alone = route_topk(l[-last:].clone(), 1, renormalize=False)
+    assert torch.equal(r.ids[-last:], alone.ids) and torch.equal(r.scores[-last:], alone.scores)
+    assert (r.ids[:-last] == 0).all()
+    grad = route_topk_backward(torch.ones_like(r.scores), l, r.ids, renormalize=False)
+    want = route_topk_backward(torch.ones_like(alone.scores), l[-last:].clone(), alone.ids,
+                               renormalize=False)
+    assert torch.equal(grad[-last:], want) and torch.equal(grad[5], grad[0])
+    del l, r, grad
+    torch.cuda.empty_cache()
+
+
 def test_quantisation_past_4_gib():
     """2^31 elements and some: bf16 values, fp32 ones past 8 GiB, and back."""
     R, K = (1 << 31) // 7168 + 40, 7168
