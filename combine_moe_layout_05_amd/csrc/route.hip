@@ -19,9 +19,10 @@
 // Bound: for a few tokens a launch, its loads and the chain of the selection (one
 // token of 256 experts, 8 groups 4.3 us); for many the vector instructions of the
 // selection, not the bytes. Measured on MI355X, 32768 tokens of 256 experts, fp32, 8
-// each: softmax 11.3 us (35.7 MB, 3.2 TB/s), sigmoid with bias 15.8, in 8 groups 19.1
-// (a wavefront per token 178); bf16 sigmoid in groups without a bias 21.8, as more of
-// its tokens are near ties.
+// each: softmax 11.3 us (35.7 MB, 3.2 TB/s), sigmoid with bias 14.5, in 8 groups 17.4
+// (a wavefront per token 178), bf16 sigmoid in groups without a bias 14.0. One token of
+// the slow form at the end of a launch costs some 5 us: with near neighbours, near
+// groups and one expert near the last all going there these took 15.8, 23 and 78.
 #include <cmath>
 
 #include "expert_kernels.h"
@@ -250,10 +251,11 @@ void route_kernel(const L* __restrict__ logits, const float* __restrict__ bias, 
 // Then the choice is checked against the values themselves: neighbours in order
 // and every other expert below the last, exactly where they are logits, by more
 // than the error of a value in 32 bits where they are sigmoids plus a bias.
-// Neighbours nearer than that are put in order by their values in 64 bits. A token
-// that fails otherwise (an expert too near to the last or a group to the last kept,
-// fewer experts than slots, values more than 16 apart, infinities) is chosen for by
-// the whole wavefront.
+// Neighbours nearer than that, among them one expert too near to the last, are put
+// in order by their values in 64 bits, and so are groups too near to the last kept.
+// A token that fails otherwise (two experts too near to the last, three in a group
+// too near to each other, fewer experts than slots, values more than 16 apart,
+// infinities) is chosen for by the whole wavefront.
 constexpr int kLanes = 16;
 constexpr int kList = 8;
 
@@ -290,15 +292,23 @@ __device__ __forceinline__ float sigmoid_of(float l) {
 
 // Lanes D, D + 1, ... before this one, in a circle, whose group goes before this
 // lane's: a larger value, or the same and a lower index.
-template <int D>
-__device__ __forceinline__ int lanes_ahead(float value, int j, int span) {
+template <int N>
+__device__ __forceinline__ double ror(double v) {
+    typedef int32_t two __attribute__((ext_vector_type(2)));
+    const two w = __builtin_bit_cast(two, v);
+    return __builtin_bit_cast(
+        double, two{__builtin_amdgcn_mov_dpp(w[0], 0x120 + N, 0xF, 0xF, true),
+                    __builtin_amdgcn_mov_dpp(w[1], 0x120 + N, 0xF, 0xF, true)});
+}
+template <int D, class V>
+__device__ __forceinline__ int lanes_ahead(V value, int j, int span) {
     if constexpr (D == kLanes) {
         return 0;
     } else {
-        const float other = ror<D>(value);
+        const V other = ror<D>(value);
         const int at = (j - D) & (kLanes - 1);
-        const bool first = other > value || (other == value && at < (j & ~(span - 1)));
-        return first + lanes_ahead<D + 1>(value, j, span);
+        const bool first = (other > value) | ((other == value) & (at < (j & ~(span - 1))));
+        return first + lanes_ahead<D + 1, V>(value, j, span);
     }
 }
 
@@ -470,22 +480,55 @@ void route_lanes_kernel(const L* __restrict__ logits, const float* __restrict__ 
         float value = first;
         if (sigmoid) {
             // Without a bias the two largest logits are those of the largest sigmoids.
-            if (!BY_VALUE && first > -INFINITY) {
-                first = sigmoid_of(first);
-                if (second > -INFINITY) second = sigmoid_of(second);
+            float a = first, b = second;
+            if (!BY_VALUE) {
+                if (a > -INFINITY) a = sigmoid_of(a);
+                if (b > -INFINITY) b = sigmoid_of(b);
             }
-            value = second > -INFINITY ? first + second : first;
-            largest = lanes_max(fmaxf(fabsf(first), second > -INFINITY ? fabsf(second) : 0.0f));
+            value = b > -INFINITY ? a + b : a;
+            largest = lanes_max(fmaxf(fabsf(a), b > -INFINITY ? fabsf(b) : 0.0f));
         }
         const float margin = sigmoid ? (8.0f + 4.0f * largest) * 0x1p-22f : 0.0f;
-        const int ahead = lanes_ahead<1>(value, j, span);
-        const bool keep = ahead < kept * span;
-        open = __ballot(keep);
+        bool keep = lanes_ahead<1, float>(value, j, span) < kept * span;
         if (sigmoid && kept < groups) {
             const float least = -lanes_max(keep ? -value : -INFINITY);
             const float next = lanes_max(keep ? -INFINITY : value);
             open_bad = !(least - next > margin);
+            if (__any(open_bad)) {
+                // The groups' values in 64 bits.
+                double exact = 0.0;
+                bool sure = true;
+                if constexpr (BY_VALUE) {
+                    // Its two largest, if no third is near the second.
+                    const float from = second - margin;
+                    int found = 0, one = 0, two = 0;
+#pragma unroll
+                    for (int i = 0; i < VALS; ++i)
+                        if (v[i] > -INFINITY && v[i] >= from) {
+                            two = one;
+                            one = j * VALS + i;
+                            ++found;
+                        }
+                    auto counts = [&](int e) {
+                        return sigmoid_64(logit_at(in, e)) + static_cast<double>(bias[e]);
+                    };
+                    if (found > 0) exact = counts(one);
+                    if (found > 1) exact += counts(two);
+                    for (int d = 1; d < span; d *= 2) {
+                        exact += __shfl_xor(exact, d, 64);
+                        found += __shfl_xor(found, d, 64);
+                    }
+                    sure = found == (first > -INFINITY) + (second > -INFINITY);
+                } else {
+                    if (first > -INFINITY) exact = in_sum(first);
+                    if (second > -INFINITY) exact += in_sum(second);
+                }
+                if (!(first > -INFINITY)) exact = -INFINITY;
+                keep = lanes_ahead<1, double>(exact, j, span) < kept * span;
+                open_bad = (__ballot(!sure) >> (lane & 48) & 0xFFFF) != 0;
+            }
         }
+        open = __ballot(keep);
 #pragma unroll
         for (int i = 0; i < VALS; ++i) v[i] = keep ? v[i] : -INFINITY;
     }
@@ -549,33 +592,50 @@ void route_lanes_kernel(const L* __restrict__ logits, const float* __restrict__ 
     const int next_id = __shfl(id, lane + 1 < 64 ? lane + 1 : lane, 64);
     const float least = __shfl(value, (lane & 48) + K - 1, 64);
     const float margin = BY_VALUE ? (4.0f + fabsf(m) + fabsf(least)) * 0x1p-22f : 0.0f;
-    if constexpr (BY_VALUE) {
-        if (__any(j + 1 < K && !(value - next > margin))) {
-            // In order by the values in 64 bits; equal ones by index.
-            double v64 = -INFINITY;
-            if (j < K && id < E) {
-                v64 = sigmoid_64(chosen) + static_cast<double>(bias[id]);
-            }
-            int before = 0;
-            for (int k = 0; k < K; ++k) {
-                const double other = __shfl(v64, (lane & 48) + k, 64);
-                const int other_id = __shfl(id, (lane & 48) + k, 64);
-                before += other > v64 || (other == v64 && other_id < id);
-            }
-            const int to = (lane & 48) + (j < K ? before : j);
-            id = __builtin_amdgcn_ds_permute(to * 4, id);
-            chosen = __builtin_bit_cast(
-                float, __builtin_amdgcn_ds_permute(to * 4, __builtin_bit_cast(int32_t, chosen)));
-        }
-    } else if (j + 1 < K) {
-        bad = bad || !(value > next || (value == next && id < next_id));
-    }
     // The last key's value may be above another's by what a key does not hold.
     const float limit = BY_VALUE ? least - margin - 0x1p-20f : least;
     float above = -INFINITY;            // the largest of those not chosen
 #pragma unroll
     for (int i = 0; i < VALS; ++i) above = fmaxf(above, key[i] < last ? v[i] : -INFINITY);
-    bad = bad || above > limit;
+    if constexpr (BY_VALUE) {
+        if (__any(above > limit || (j + 1 < K && !(value - next > margin)))) {
+            // One more that may belong to the chosen goes to lane K.
+            int over = 0, at = -1;
+#pragma unroll
+            for (int i = 0; i < VALS; ++i)
+                if (key[i] < last && v[i] > limit) {
+                    ++over;
+                    at = j * VALS + i;
+                }
+            const uint32_t some = static_cast<uint32_t>(__ballot(over > 0) >> (lane & 48)) & 0xFFFF;
+            const uint32_t many = static_cast<uint32_t>(__ballot(over > 1) >> (lane & 48)) & 0xFFFF;
+            const bool one = __popc(some) == 1 && many == 0;
+            const int more = __shfl(at, (lane & 48) + (one ? __ffs(some) - 1 : 0), 64);
+            bad = bad || (some != 0 && !one);
+            const int n = K + one;
+            if (one && j == K) {
+                id = more;
+                chosen = logit_at(in, id);
+            }
+            // In order by the values in 64 bits; equal ones by index.
+            double v64 = -INFINITY;
+            if (j < n && id < E) v64 = sigmoid_64(chosen) + static_cast<double>(bias[id]);
+            int before = 0;
+            for (int k = 0; k <= K; ++k) {
+                const double other = __shfl(v64, (lane & 48) + k, 64);
+                const int other_id = __shfl(id, (lane & 48) + k, 64);
+                before += other > v64 || (other == v64 && other_id < id);
+            }
+            const int to = (lane & 48) + (j < n ? before : j);
+            id = __builtin_amdgcn_ds_permute(to * 4, id);
+            chosen = __builtin_bit_cast(
+                float, __builtin_amdgcn_ds_permute(to * 4, __builtin_bit_cast(int32_t, chosen)));
+            if (j >= K) id = -1;
+        }
+    } else {
+        bad = bad || above > limit ||
+              (j + 1 < K && !(value > next || (value == next && id < next_id)));
+    }
 
     // Tokens that the check does not clear, one after the other.
     const uint64_t failed = __ballot(bad && there), unsure = __ballot(open_bad);

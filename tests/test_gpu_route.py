@@ -96,6 +96,65 @@ def test_near_values_keep_the_order_of_the_formula(G, kept):
     assert torch.equal(r.ids.cpu().long(), want)
 
 
+@pytest.mark.parametrize("E", [256, 128, 23])
+@pytest.mark.parametrize("K", [1, 5, 8])
+def test_one_expert_near_to_the_last(K, E):
+    """The K-th and the next expert alone lie nearer than fp32 can tell, the
+    lower or the higher index ahead by the bias, or both equal."""
+    gen = torch.Generator().manual_seed(E + K)
+    T = 60
+    l = torch.stack([torch.randperm(E, generator=gen) for _ in range(T)]).float() / E * 3 - 1.5
+    bias = torch.zeros(E)
+    bias[1::3], bias[2::3] = 2.0 ** -28, 2.0 ** -29
+    order = l.argsort(dim=1, descending=True)
+    rows = torch.arange(T)
+    l[rows, order[:, K]] = l[rows, order[:, K - 1]]
+    want = ref.select(l, K, "sigmoid", bias)
+    r = route_topk(l.to(DEV), K, score="sigmoid", bias=bias.to(DEV))
+    assert torch.equal(r.ids.cpu().long(), want)
+    # a second one, and a third
+    l[rows, order[:, K + 1]] = l[rows, order[:, K]]
+    l[::2][torch.arange(T // 2), order[::2, K + 2]] = l[::2][torch.arange(T // 2), order[::2, K]]
+    want = ref.select(l, K, "sigmoid", bias)
+    r = route_topk(l.to(DEV), K, score="sigmoid", bias=bias.to(DEV))
+    assert torch.equal(r.ids.cpu().long(), want)
+
+
+@pytest.mark.parametrize("E, G, kept", [(256, 8, 4), (256, 16, 3), (64, 4, 1), (128, 4, 2),
+                                        (32, 16, 8), (256, 2, 1), (160, 8, 3)])
+@pytest.mark.parametrize("biased", [True, False])
+def test_groups_near_to_the_last_kept(E, G, kept, biased):
+    """The groups' two largest are the same numbers in two, three or all
+    groups, or apart by a bias of 2^-28; some groups hold three equal ones, or
+    one expert alone."""
+    gen = torch.Generator().manual_seed(E + G)
+    T, size = 64, E // G
+    l = torch.randn(T, G, size, generator=gen) - 2.0
+    top = torch.rand(T, G, 2, generator=gen) + 1.0
+    top[:24, 1] = top[:24, 0]
+    if G > 2:
+        top[8:24, 2] = top[8:24, 0].flip(-1)
+    top[24:40] = top[24:40, :1]
+    for t in range(T):
+        for g in range(G):
+            at = torch.randperm(size, generator=gen)[:3]
+            l[t, g, at[:2]] = top[t, g][:len(at[:2])]
+            if t % 4 == 3 and size > 2:
+                l[t, g, at[2]] = top[t, g].min()
+    l[40:44, ::2, 1:] = float("-inf")
+    l = l.reshape(T, E)
+    bias = None
+    if biased:
+        bias = torch.zeros(E)
+        bias[torch.randint(0, E, (E // 8,), generator=gen)] = 2.0 ** -28
+    K = min(6, size * kept)
+    for x in (l, l.to(BF)):
+        want = ref.select(x, K, "sigmoid", bias, G, kept)
+        r = route_topk(x.to(DEV), K, score="sigmoid", num_groups=G, topk_groups=kept,
+                       bias=None if bias is None else bias.to(DEV))
+        assert torch.equal(r.ids.cpu().long(), want)
+
+
 @pytest.mark.parametrize("groups", [(1, 1), (8, 4)])
 def test_far_biases_and_near_sums(groups):
     """Biases far below zero: a group's second value decides its sum, and the
