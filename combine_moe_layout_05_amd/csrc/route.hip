@@ -21,8 +21,9 @@
 // selection, not the bytes. Measured on MI355X, 32768 tokens of 256 experts, fp32, 8
 // each: softmax 11.3 us (35.7 MB, 3.2 TB/s), sigmoid with bias 14.5, in 8 groups 17.4
 // (a wavefront per token 178), bf16 sigmoid in groups without a bias 14.0. One token of
-// the slow form at the end of a launch costs some 5 us: with near neighbours, near
-// groups and one expert near the last all going there these took 15.8, 23 and 78.
+// the slow form at the end of a launch costs some 5 us: before groups near the last kept
+// and an expert near the last chosen were settled in their lanes, the latter two took
+// 18.8 and 22.
 #include <cmath>
 
 #include "expert_kernels.h"
