@@ -242,7 +242,7 @@ void route_kernel(const L* __restrict__ logits, const float* __restrict__ bias, 
 
 // ---- 16 lanes per token ------------------------------------------------------
 //
-// Lane j of a token holds experts VALS j .. VALS j + VALS - 1. Each value becomes a
+// Lane j of a token holds up to VALS experts in a row. Each value becomes a
 // key of 32 bits: its distance to the token's largest in 24 bits of 2^-20 (16 in
 // all), and the expert's index, so that keys differ and equal values go by index.
 // A lane sorts its keys, the lanes' lists of 8 are merged by rotations, after which
@@ -396,12 +396,13 @@ __device__ __forceinline__ void store_values(__bf16* p, const float (&v)[VALS]) 
     *reinterpret_cast<Raw*>(p) = r;
 }
 
-// GROUPED needs E = 16 VALS and groups of 1, 2, 4, 8 or 16 lanes (`span`).
+// A lane holds `per` of the experts, VALS or fewer. GROUPED needs E = 16 per and
+// groups of 1, 2, 4, 8 or 16 lanes (`span`).
 template <int VALS, class L, bool BY_VALUE, bool GROUPED>
 __global__ __launch_bounds__(kWaves * 64)
 void route_lanes_kernel(const L* __restrict__ logits, const float* __restrict__ bias, int32_t T,
                         int32_t E, int32_t K, int32_t sigmoid, int32_t renormalize, float scale,
-                        int32_t groups, int32_t kept, int32_t span, int32_t whole,
+                        int32_t groups, int32_t kept, int32_t span, int32_t per, int32_t whole,
                         int32_t* __restrict__ ids, float* __restrict__ scores) {
     const int lane = threadIdx.x & 63;
     const int j = lane & (kLanes - 1);
@@ -413,14 +414,15 @@ void route_lanes_kernel(const L* __restrict__ logits, const float* __restrict__ 
     const L* in = logits + (there ? row : T - 1) * int64_t(E);
 
     float l[VALS];
+    const int base = j * per;           // this lane's first expert
     if (whole) {                        // E = 16 VALS, aligned
-        load_values<VALS>(in + j * VALS, l);
+        load_values<VALS>(in + base, l);
     } else {
 #pragma unroll
         for (int i = 0; i < VALS; ++i) {
-            const int e = j * VALS + i;
+            const int e = base + i;
             const float x = logit_at(in, min(e, E - 1));
-            l[i] = e < E ? x : -INFINITY;
+            l[i] = i < per && e < E ? x : -INFINITY;
         }
     }
 #pragma unroll
@@ -446,10 +448,10 @@ void route_lanes_kernel(const L* __restrict__ logits, const float* __restrict__ 
     if constexpr (BY_VALUE) {
         float b[VALS];
         if (whole) {
-            load_values<VALS>(bias + j * VALS, b);
+            load_values<VALS>(bias + base, b);
         } else {
 #pragma unroll
-            for (int i = 0; i < VALS; ++i) b[i] = bias[min(j * VALS + i, E - 1)];
+            for (int i = 0; i < VALS; ++i) b[i] = bias[min(base + i, E - 1)];
         }
 #pragma unroll
         for (int i = 0; i < VALS; ++i) {
@@ -507,7 +509,7 @@ void route_lanes_kernel(const L* __restrict__ logits, const float* __restrict__ 
                     for (int i = 0; i < VALS; ++i)
                         if (v[i] > -INFINITY && v[i] >= from) {
                             two = one;
-                            one = j * VALS + i;
+                            one = base + i;
                             ++found;
                         }
                     auto counts = [&](int e) {
@@ -542,7 +544,7 @@ void route_lanes_kernel(const L* __restrict__ logits, const float* __restrict__ 
     for (int i = 0; i < VALS; ++i) {
         // Below 0 and NaN become 0.
         const float d = __builtin_fmaf(v[i] - m, 0x1p20f, 16777215.0f);
-        key[i] = (static_cast<uint32_t>(fmaxf(d, 0.0f)) << 8) | (255 - (j * VALS + i));
+        key[i] = (static_cast<uint32_t>(fmaxf(d, 0.0f)) << 8) | (255 - (base + i));
     }
     uint32_t list[kList];
     {
@@ -606,7 +608,7 @@ void route_lanes_kernel(const L* __restrict__ logits, const float* __restrict__ 
             for (int i = 0; i < VALS; ++i)
                 if (key[i] < last && v[i] > limit) {
                     ++over;
-                    at = j * VALS + i;
+                    at = base + i;
                 }
             const uint32_t some = static_cast<uint32_t>(__ballot(over > 0) >> (lane & 48)) & 0xFFFF;
             const uint32_t many = static_cast<uint32_t>(__ballot(over > 1) >> (lane & 48)) & 0xFFFF;
@@ -649,7 +651,7 @@ void route_lanes_kernel(const L* __restrict__ logits, const float* __restrict__ 
                 ? static_cast<uint32_t>(open >> (r * kLanes)) & 0xFFFF : 0;
         const int slow = choose<(VALS + 3) / 4, L>(
             logits + (row0 + r) * E, bias, lane, K, E, sigmoid != 0, certain ? 1 : groups, kept,
-            certain ? certain : 1, certain ? VALS : 1024);
+            certain ? certain : 1, certain ? per : 1024);
         const int here = __shfl(slow, j, 64);
         if ((lane >> 4) == r) {
             id = j < K ? here : -1;
@@ -838,7 +840,7 @@ int lane_values(int32_t E) {
 }
 
 template <int VALS, class L>
-hipError_t launch_lanes(const RouteArgs& a, int32_t span, hipStream_t stream) {
+hipError_t launch_lanes(const RouteArgs& a, int32_t per, hipStream_t stream) {
     const bool by_value = a.sigmoid && a.bias, grouped = a.groups > 1;
     auto kernel = by_value ? (grouped ? route_lanes_kernel<VALS, L, true, true>
                                       : route_lanes_kernel<VALS, L, true, false>)
@@ -850,18 +852,15 @@ hipError_t launch_lanes(const RouteArgs& a, int32_t span, hipStream_t stream) {
     const int64_t tokens = waves * (64 / kLanes);
     hipLaunchKernelGGL(kernel, dim3(static_cast<uint32_t>((a.T + tokens - 1) / tokens)),
                        dim3(waves * 64), 0, stream, static_cast<const L*>(a.logits), a.bias, a.T,
-                       a.E, a.K, a.sigmoid, a.renormalize, a.scale, a.groups, a.kept, span, whole,
-                       a.ids, a.scores);
+                       a.E, a.K, a.sigmoid, a.renormalize, a.scale, a.groups, a.kept,
+                       kLanes / a.groups, per, whole, a.ids, a.scores);
     return hipGetLastError();
 }
 
-// Lanes of a group if the 16 lanes of a token can take its groups, else 0.
-int32_t lanes_of_group(const RouteArgs& a, int vals) {
-    if (a.groups == 1) return kLanes;
-    const int32_t size = a.E / a.groups;
-    if (a.E != kLanes * vals || size % vals != 0) return 0;
-    const int32_t span = size / vals;
-    return (span & (span - 1)) == 0 ? span : 0;
+// Experts of a lane if the 16 lanes of a token can take its groups, else 0.
+int32_t lane_experts(const RouteArgs& a, int vals) {
+    if (a.groups == 1) return vals;
+    return a.E % kLanes == 0 && kLanes % a.groups == 0 ? a.E / kLanes : 0;
 }
 
 // Wavefronts per workgroup with one token each: one where whole workgroups of kWaves
@@ -882,11 +881,11 @@ template <class L>
 hipError_t route(const RouteArgs& a, hipStream_t stream) {
     if (a.E <= kLanes * 16 && a.K <= kList) {
         const int vals = lane_values(a.E);
-        if (const int32_t span = lanes_of_group(a, vals)) {
-            if (vals == 2) return launch_lanes<2, L>(a, span, stream);
-            if (vals == 4) return launch_lanes<4, L>(a, span, stream);
-            if (vals == 8) return launch_lanes<8, L>(a, span, stream);
-            return launch_lanes<16, L>(a, span, stream);
+        if (const int32_t per = lane_experts(a, vals)) {
+            if (vals == 2) return launch_lanes<2, L>(a, per, stream);
+            if (vals == 4) return launch_lanes<4, L>(a, per, stream);
+            if (vals == 8) return launch_lanes<8, L>(a, per, stream);
+            return launch_lanes<16, L>(a, per, stream);
         }
     }
     if (a.E <= 64) return launch_route<1, L>(a, stream);

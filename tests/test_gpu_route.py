@@ -23,6 +23,9 @@ SHAPES = [
     (9, 17, 8, 1, 1), (33, 48, 5, 1, 1), (21, 200, 8, 1, 1), (18, 32, 3, 16, 5), (18, 64, 8, 8, 3),
     (22, 128, 6, 2, 1), (22, 128, 8, 16, 4), (4100, 64, 4, 4, 2), (19, 256, 8, 16, 9),
     (5, 256, 9, 8, 4), (6, 224, 8, 7, 3),
+    # lanes that hold fewer experts than they have places for
+    (25, 48, 5, 4, 2), (9, 144, 8, 16, 7), (30, 16, 2, 8, 3), (40, 160, 6, 2, 1),
+    (12, 240, 8, 4, 2), (17, 80, 3, 16, 3), (16, 96, 8, 2, 2),
 ]
 KINDS = [("softmax", False), ("sigmoid", False), ("sigmoid", True)]
 
@@ -121,7 +124,8 @@ def test_one_expert_near_to_the_last(K, E):
 
 
 @pytest.mark.parametrize("E, G, kept", [(256, 8, 4), (256, 16, 3), (64, 4, 1), (128, 4, 2),
-                                        (32, 16, 8), (256, 2, 1), (160, 8, 3)])
+                                        (32, 16, 8), (256, 2, 1), (160, 8, 3), (48, 4, 2),
+                                        (96, 3, 1)])
 @pytest.mark.parametrize("biased", [True, False])
 def test_groups_near_to_the_last_kept(E, G, kept, biased):
     """The groups' two largest are the same numbers in two, three or all
