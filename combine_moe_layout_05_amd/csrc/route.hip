@@ -678,8 +678,10 @@ __device__ __forceinline__ void store_grad(__bf16* p, int64_t i, float v) {
 //   softmax              dl_j = q_j (g_j - s) if j was chosen, else -p_j s
 //   softmax, renormalized   dl_j = q_j (g_j - s), s = sum of g q, else 0
 //   sigmoid              dl_j = g_j p_j (1 - p_j)
-//   sigmoid, renormalized   dl_j = (g_j - s) / S p_j (1 - p_j)
-// A row is written whole; an expert in two slots gets the sum of both.
+//   sigmoid, renormalized   dl_j = q_j (g_j - s) (1 - p_j)
+// In the last one q_j stands for p_j / S, at most 1, since (g_j - s) / S alone
+// leaves fp32 where S is small. A row is written whole; an expert in two slots gets
+// the sum of both.
 template <class L>
 __global__ __launch_bounds__(kWaves * 64)
 void route_grad_kernel(const L* __restrict__ logits, const int32_t* __restrict__ ids,
@@ -715,13 +717,14 @@ void route_grad_kernel(const L* __restrict__ logits, const int32_t* __restrict__
     if (renormalize) sum = wave_sum(p);
     float d = 0.0f, s = 0.0f;
     if (sigmoid) {
-        // p (1 - p) without the difference, which loses p's last digits near 1.
-        const float slope = id < 0 ? 0.0f : p / (1.0f + expf(l));
+        // 1 - p without the difference, which loses its last digits near 1.
+        const float rest = id < 0 ? 0.0f : 1.0f / (1.0f + expf(l));
         if (renormalize) {
-            s = wave_sum(sum == 0.0f ? 0.0f : g * (p / sum));
-            d = sum == 0.0f ? 0.0f : (g - s) / sum * slope;
+            const float q = sum == 0.0f ? 0.0f : p / sum;
+            s = wave_sum(g * q);
+            d = sum == 0.0f ? 0.0f : (g - s) * (q * rest);
         } else {
-            d = g * slope;
+            d = g * (p * rest);
         }
     } else {
         const float q = sum == 0.0f ? 0.0f : p / sum;
@@ -799,12 +802,13 @@ void route_grad_lanes_kernel(const L* __restrict__ logits, const int32_t* __rest
     if (renormalize) sum = lanes_sum(p);
     float d, s = 0.0f;
     if (sigmoid) {
-        const float slope = id < 0 ? 0.0f : p / (1.0f + expf(l));
+        const float rest = id < 0 ? 0.0f : 1.0f / (1.0f + expf(l));      // 1 - p
         if (renormalize) {
-            s = lanes_sum(sum == 0.0f ? 0.0f : g * (p / sum));
-            d = sum == 0.0f ? 0.0f : (g - s) / sum * slope;
+            const float q = sum == 0.0f ? 0.0f : p / sum;
+            s = lanes_sum(g * q);
+            d = sum == 0.0f ? 0.0f : (g - s) * (q * rest);
         } else {
-            d = g * slope;
+            d = g * (p * rest);
         }
     } else {
         const float q = sum == 0.0f ? 0.0f : p / sum;
