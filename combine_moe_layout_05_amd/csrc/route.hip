@@ -172,13 +172,45 @@ __device__ int select(V (&v)[VALS], int lane, int K, int E, int groups, int kept
     return mine;
 }
 
+// 1 - sigmoid(l) and sigmoid(l), from an exponential that does not overflow: a
+// sigmoid below 2^-127 is not lost. The former without the difference, which loses its
+// last digits near 1.
+__device__ __forceinline__ float sigmoid_rest(float l) {
+    const float e = expf(-fabsf(l));
+    return (l > 0.0f ? e : 1.0f) / (1.0f + e);
+}
+__device__ __forceinline__ float sigmoid_32(float l) { return sigmoid_rest(-l); }
+
+// The sigmoids of a token's chosen experts (id >= 0, logit l) and, to renormalize
+// them, their sum over its lanes. A sum below 2^-24 is formed again with every sigmoid
+// times exp(-top), `top` the largest chosen logit: only the quotients count, and
+// numbers near 2^-149 have few digits. Sigmoids that are all 0 in fp32 stay 0.
+template <class Max, class Sum>
+__device__ __forceinline__ float chosen_sigmoid(int id, float l, bool renormalize, float& sum,
+                                                Max max_of, Sum sum_of) {
+    float p = id >= 0 ? sigmoid_32(l) : 0.0f;
+    if (!renormalize) return p;
+    sum = sum_of(p);
+    if (sum < 0x1p-24f) {
+        const float top = max_of(id >= 0 ? l : -INFINITY);
+        const bool some = id >= 0 && top >= -103.972077083991796f;      // 2^-150
+        p = some ? expf(l - top) / (1.0f + expf(l)) : 0.0f;
+        sum = sum_of(p);
+    }
+    return p;
+}
+
 // The score of a chosen expert in lanes 0 .. K - 1 (id >= 0, logit l), before
 // the scale; `top` and `sum` are the softmax's over all experts.
 __device__ __forceinline__ float score_of(bool sigmoid, bool renormalize, int id, float l,
                                           float top, float sum) {
     float p = 0.0f;
-    if (id >= 0) p = sigmoid ? 1.0f / (1.0f + expf(-l)) : expf(l - top);
-    if (renormalize) sum = wave_sum(p);
+    if (sigmoid) {
+        p = chosen_sigmoid(id, l, renormalize, sum, wave_max<float>, wave_sum);
+    } else {
+        if (id >= 0) p = expf(l - top);
+        if (renormalize) sum = wave_sum(p);
+    }
     if (renormalize || !sigmoid) p = sum == 0.0f ? 0.0f : p / sum;
     return p;
 }
@@ -659,8 +691,12 @@ void route_lanes_kernel(const L* __restrict__ logits, const float* __restrict__ 
         }
     }
     float p = 0.0f;
-    if (id >= 0) p = sigmoid ? 1.0f / (1.0f + expf(-chosen)) : expf(chosen - top);
-    if (renormalize) sum = lanes_sum(p);
+    if (sigmoid) {
+        p = chosen_sigmoid(id, chosen, renormalize, sum, lanes_max, lanes_sum);
+    } else {
+        if (id >= 0) p = expf(chosen - top);
+        if (renormalize) sum = lanes_sum(p);
+    }
     if (renormalize || !sigmoid) p = sum == 0.0f ? 0.0f : p / sum;
     if (there && j < K) {
         ids[row * K + j] = id;
@@ -713,12 +749,16 @@ void route_grad_kernel(const L* __restrict__ logits, const int32_t* __restrict__
     } else if (!sigmoid) {
         top = wave_max(l);
     }
-    const float p = id < 0 ? 0.0f : sigmoid ? 1.0f / (1.0f + expf(-l)) : expf(l - top);
-    if (renormalize) sum = wave_sum(p);
+    float p = 0.0f;
+    if (sigmoid) {
+        p = chosen_sigmoid(id, l, renormalize, sum, wave_max<float>, wave_sum);
+    } else {
+        if (id >= 0) p = expf(l - top);
+        if (renormalize) sum = wave_sum(p);
+    }
     float d = 0.0f, s = 0.0f;
     if (sigmoid) {
-        // 1 - p without the difference, which loses its last digits near 1.
-        const float rest = id < 0 ? 0.0f : 1.0f / (1.0f + expf(l));
+        const float rest = id < 0 ? 0.0f : sigmoid_rest(l);
         if (renormalize) {
             const float q = sum == 0.0f ? 0.0f : p / sum;
             s = wave_sum(g * q);
@@ -798,11 +838,16 @@ void route_grad_lanes_kernel(const L* __restrict__ logits, const int32_t* __rest
     } else if (!sigmoid) {
         top = lanes_max(l);
     }
-    const float p = id < 0 ? 0.0f : sigmoid ? 1.0f / (1.0f + expf(-l)) : expf(l - top);
-    if (renormalize) sum = lanes_sum(p);
+    float p = 0.0f;
+    if (sigmoid) {
+        p = chosen_sigmoid(id, l, renormalize, sum, lanes_max, lanes_sum);
+    } else {
+        if (id >= 0) p = expf(l - top);
+        if (renormalize) sum = lanes_sum(p);
+    }
     float d, s = 0.0f;
     if (sigmoid) {
-        const float rest = id < 0 ? 0.0f : 1.0f / (1.0f + expf(l));      // 1 - p
+        const float rest = id < 0 ? 0.0f : sigmoid_rest(l);
         if (renormalize) {
             const float q = sum == 0.0f ? 0.0f : p / sum;
             s = lanes_sum(g * q);

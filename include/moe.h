@@ -575,7 +575,8 @@ int moe_gated_grouped_gemm_mxfp4_rows(const void *d_values, const void *d_scales
  * takes part; equal ones by index) can be chosen from. A slot for which no expert
  * is left has id -1 and score 0.
  *   scores = scale * p, with MOE_ROUTE_RENORMALIZE scale * p / (sum of the chosen
- *   p), 0 where that sum is 0. Scores and sums are fp32.
+ *   p), 0 where each of those rounds to 0 in fp32 (sigmoids below 2^-150). Scores
+ *   and sums are fp32.
  *   d_logits  [T][E] of dtype (MOE_F32 or MOE_BF16), aligned to its elements
  *   d_bias    float32 [E] or NULL (NULL for the softmax)
  *   d_ids     int32 [T][K], d_scores float32 [T][K]

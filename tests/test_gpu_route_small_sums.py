@@ -28,14 +28,15 @@ def _rows(chosen, E):
     return l
 
 
-def _check_gradient(l, K, grad, scale=1.0):
+def _check_gradient(l, K, grad, scale=1.0, renormalize=True):
     ids = ref.select(l, K, "sigmoid")
-    want, err = ref.gradient(l, ids, grad, "sigmoid", True, scale)
+    want, err = ref.gradient(l, ids, grad, "sigmoid", renormalize, scale)
     leaf = l.to(DEV).requires_grad_(True)
-    r = route_topk(leaf, K, score="sigmoid", scale=scale)
+    r = route_topk(leaf, K, score="sigmoid", renormalize=renormalize, scale=scale)
     assert torch.equal(r.ids.cpu().long(), ids)
     got, = torch.autograd.grad(r.scores, leaf, grad.to(DEV))
-    direct = route_topk_backward(grad.to(DEV), leaf.detach(), r.ids, score="sigmoid", scale=scale)
+    direct = route_topk_backward(grad.to(DEV), leaf.detach(), r.ids, score="sigmoid",
+                                 renormalize=renormalize, scale=scale)
     sync_or_fail()
     assert torch.isfinite(got).all() and torch.equal(got, direct)
     got = got.double().cpu()
@@ -74,3 +75,59 @@ def test_gradient_of_a_sum_of_zero(E):
     got, = torch.autograd.grad(r.scores, leaf, grad)
     sync_or_fail()
     assert (got == 0).all()
+
+
+def _far(T, K, seed):
+    """Rows of chosen logits from -103 to -86: sigmoids that fp32 holds in few
+    bits or in none of an exponential's of the other sign; in some rows beside
+    ordinary ones and ones that saturate."""
+    l = -86.0 - 17.0 * torch.rand(T, K, generator=_gen(seed))
+    l[1::4, 0] = 2.0
+    l[2::8, -1] = 95.0
+    l[3::8] += 20.0
+    return l
+
+
+# E, K: 16 lanes per token, a wavefront per token
+FAR = [(32, 3), (200, 8), (64, 12), (300, 2), (257, 16)]
+
+
+@pytest.mark.parametrize("renormalize", [True, False])
+@pytest.mark.parametrize("E, K", FAR)
+def test_scores_of_small_sigmoids(E, K, renormalize):
+    """Off by the relative bound of fp32, and by units of its last place where
+    there are no more: one of the exponential times the scale, halves of the
+    division and of the product, together less than 4."""
+    note(f"small sigmoids E={E} K={K} renormalize={renormalize}")
+    l = _rows(_far(64, K, E + K), E)
+    ids = ref.select(l, K, "sigmoid")
+    want, rel = ref.scores(l, ids, "sigmoid", renormalize, 2.5)
+    r = route_topk(l.to(DEV), K, score="sigmoid", renormalize=renormalize, scale=2.5)
+    sync_or_fail()
+    assert torch.equal(r.ids.cpu().long(), ids)
+    off = (r.scores.double().cpu() - want).abs()
+    assert (off <= rel * want + 4 * 2.0 ** -149).all()
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("renormalize", [True, False])
+@pytest.mark.parametrize("E, K", FAR)
+def test_gradient_of_small_sigmoids(E, K, renormalize, bf16):
+    note(f"gradient of small sigmoids E={E} K={K} renormalize={renormalize} bf16={bf16}")
+    l = _rows(_far(64, K, 3 * E + K), E)
+    grad = torch.randn(64, K, generator=_gen(E)) * 64
+    _check_gradient(l.to(BF) if bf16 else l, K, grad, 2.5, renormalize)
+
+
+def test_below_the_range_of_fp32_all_scores_are_zero():
+    """exp(-103.97) is half of the smallest fp32 number: a token without a
+    larger chosen sigmoid has scores and a gradient of 0."""
+    l = torch.full((2, 40), -300.0)
+    l[0, :4] = -104.0
+    l[1, :4] = torch.tensor([-104.0, -103.9, -104.0, -104.0])
+    leaf = l.to(DEV).requires_grad_(True)
+    r = route_topk(leaf, 4, score="sigmoid")
+    got, = torch.autograd.grad(r.scores, leaf, torch.randn(2, 4, generator=_gen(1)).to(DEV))
+    sync_or_fail()
+    assert (r.scores[0] == 0).all() and (got[0] == 0).all()
+    assert float((r.scores.detach()[1].sum() - 1).abs()) <= 8 * ref.U
