@@ -521,14 +521,16 @@ void route_lanes_kernel(const L* __restrict__ logits, const float* __restrict__ 
                 if (b > -INFINITY) b = sigmoid_of(b);
             }
             value = b > -INFINITY ? a + b : a;
-            largest = lanes_max(fmaxf(fabsf(a), b > -INFINITY ? fabsf(b) : 0.0f));
+            largest = lanes_max(
+                fmaxf(a > -INFINITY ? fabsf(a) : 0.0f, b > -INFINITY ? fabsf(b) : 0.0f));
         }
         const float margin = sigmoid ? (8.0f + 4.0f * largest) * 0x1p-22f : 0.0f;
         bool keep = lanes_ahead<1, float>(value, j, span) < kept * span;
         if (sigmoid && kept < groups) {
             const float least = -lanes_max(keep ? -value : -INFINITY);
             const float next = lanes_max(keep ? -INFINITY : value);
-            open_bad = !(least - next > margin);
+            // Groups without an expert are no choice.
+            open_bad = next > -INFINITY && !(least - next > margin);
             if (__any(open_bad)) {
                 // The groups' values in 64 bits.
                 double exact = 0.0;
