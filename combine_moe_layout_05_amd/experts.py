@@ -20,7 +20,8 @@ from typing import Optional, Union
 import torch
 
 from . import _lib as L
-from .moe import (Mxfp4ExpertWeights, Mxfp4Rows, _DTYPES, _call, _check_mxfp4_rows, _check_rows)
+from .moe import (Mxfp4ExpertWeights, Mxfp4Rows, _DTYPES, _call, _check_mxfp4_rows, _check_rows,
+                  _refuse_tangents)
 
 ACTIVATIONS = {"silu": L.MOE_ACT_SILU, "gelu": L.MOE_ACT_GELU_TANH}
 
@@ -92,7 +93,7 @@ def quantize_mxfp4(x: torch.Tensor) -> Mxfp4Rows:
     x fp32 or bf16 [..., k], contiguous, k a multiple of 32: expert-major rows
     for grouped_gemm and gated_grouped_gemm, or weights [E, n_out, k_in] for
     mxfp4_expert_weights(*quantize_mxfp4(w)). A block with a NaN or an infinity
-    becomes NaN. Records no gradient."""
+    becomes NaN. Records no gradient; forward-mode derivatives are refused."""
     if x.dtype not in _DTYPES:
         raise TypeError(f"x must be one of {list(_DTYPES)}, got {x.dtype}")
     dev = x.device
@@ -100,6 +101,7 @@ def quantize_mxfp4(x: torch.Tensor) -> Mxfp4Rows:
     k = x.shape[-1]
     if k == 0 or k % 32 != 0:
         raise ValueError(f"the last axis must be a multiple of 32, got {k}")
+    _refuse_tangents("quantize_mxfp4", x)
     values = torch.empty((*x.shape[:-1], k // 2), dtype=torch.uint8, device=dev)
     scales = torch.empty((*x.shape[:-1], k // 32), dtype=torch.uint8, device=dev)
     _call("moe_quantize_mxfp4", dev, x.data_ptr(), _DTYPES[x.dtype], x.numel() // k, k,

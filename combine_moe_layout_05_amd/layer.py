@@ -8,7 +8,7 @@ import torch
 
 from . import _lib as L
 from .experts import _activation
-from .moe import Mxfp4ExpertWeights, _call, _check_rows
+from .moe import Mxfp4ExpertWeights, _call, _check_rows, _refuse_tangents
 
 
 def moe_layer(x_TD: torch.Tensor, topk_scores_TK: torch.Tensor, topk_expert_ids_TK: torch.Tensor,
@@ -27,7 +27,8 @@ def moe_layer(x_TD: torch.Tensor, topk_scores_TK: torch.Tensor, topk_expert_ids_
     Made for the few tokens of a decoding step: with some 8 slots or more per
     expert (T * K / E) the separate calls are the faster ones.
     activation "silu" or "gelu" (tanh form). Result bf16 [T, D]. Records no
-    gradient: training goes through MoeTokenDispatcher and expert_ffn."""
+    gradient: training goes through MoeTokenDispatcher and expert_ffn.
+    Forward-mode derivatives are refused."""
     dev = x_TD.device
     act = _activation(activation)
     _check_rows("x_TD", x_TD, torch.bfloat16, 2, dev)
@@ -60,6 +61,7 @@ def moe_layer(x_TD: torch.Tensor, topk_scores_TK: torch.Tensor, topk_expert_ids_
     if shapes != ((E, 2 * F, D), (E, D, F)):
         raise ValueError(f"shapes: w_gate_up [E, 2 F, {D}], w_down [E, {D}, F]; got {shapes[0]}, "
                          f"{shapes[1]}")
+    _refuse_tangents("moe_layer", x_TD, topk_scores_TK, w1, w2)
     y = torch.empty_like(x_TD)
     # h between the two launches (moe_few_tokens_workspace_bytes).
     nbytes = 4 * T * K * (-(-F // 128) * 128)

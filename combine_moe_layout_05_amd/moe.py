@@ -19,6 +19,7 @@ import ctypes as C
 from typing import NamedTuple, Optional
 
 import torch
+from torch.autograd import forward_ad
 
 from . import _lib as L
 
@@ -133,6 +134,15 @@ def _check_rows(name: str, t: torch.Tensor, dtype: torch.dtype, dim: int,
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.dim() != dim or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dim}-d tensor")
+
+
+def _refuse_tangents(name: str, *tensors: torch.Tensor) -> None:
+    """A call that would drop its inputs' forward-mode derivatives is refused.
+    Outside of a dual level, where nothing has any, one comparison."""
+    if getattr(forward_ad, "_current_level", 0) < 0:
+        return
+    if any(forward_ad.unpack_dual(t).tangent is not None for t in tensors):
+        raise NotImplementedError(f"{name} has no forward-mode derivative")
 
 
 class Mxfp4ExpertWeights(NamedTuple):

@@ -6,11 +6,10 @@ from __future__ import annotations
 from typing import NamedTuple, Optional
 
 import torch
-from torch.autograd import forward_ad
 
 from . import _lib as L
 from .autograd import _watch_accumulators
-from .moe import _DTYPES, _call, _check_rows, _stream
+from .moe import _DTYPES, _call, _check_rows, _refuse_tangents, _stream
 
 SCORES = {"softmax": L.MOE_SCORE_SOFTMAX, "sigmoid": L.MOE_SCORE_SIGMOID}
 
@@ -109,8 +108,7 @@ def route_topk(logits: torch.Tensor, topk: int, *, score: str = "softmax",
         raise ValueError(f"topk must be 1 to {L.MOE_MAX_TOPK}, got {topk}")
     args = (topk, kind, bias, L.MOE_ROUTE_RENORMALIZE if renormalize else 0, float(scale),
             int(num_groups), int(topk_groups))
-    if forward_ad.unpack_dual(logits).tangent is not None:
-        raise NotImplementedError("route_topk has no forward-mode derivative")
+    _refuse_tangents("route_topk", logits)
     if torch.is_grad_enabled() and logits.requires_grad:
         out = Routing(*_RouteTopk.apply(logits, *args))
         _watch_accumulators(out.scores.grad_fn, _stream(dev), "route_topk")
@@ -124,7 +122,8 @@ def route_topk_backward(grad_scores: torch.Tensor, logits: torch.Tensor, ids: to
     """Gradient of route_topk's scores with respect to the logits
     (moe_route_topk_backward), [T, E] of the logits' type: grad_scores fp32
     [T, K], logits and ids as route_topk took and gave them. The call that
-    route_topk's own backward makes."""
+    route_topk's own backward makes. Records no gradient; forward-mode
+    derivatives are refused."""
     dev = logits.device
     _check_logits(logits)
     kind = _score(score)
@@ -133,5 +132,6 @@ def route_topk_backward(grad_scores: torch.Tensor, logits: torch.Tensor, ids: to
     if ids.shape[0] != logits.shape[0] or grad_scores.shape != ids.shape:
         raise ValueError("shapes: logits [T, E], ids and grad_scores [T, K]; got "
                          f"{tuple(logits.shape)}, {tuple(ids.shape)}, {tuple(grad_scores.shape)}")
+    _refuse_tangents("route_topk_backward", grad_scores, logits)
     return _backward(grad_scores, logits, ids, kind,
                      L.MOE_ROUTE_RENORMALIZE if renormalize else 0, float(scale))

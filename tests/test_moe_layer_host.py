@@ -114,3 +114,21 @@ def test_binding_refusals(monkeypatch):
     with pytest.raises(ValueError, match="must be on a GPU"):
         moe.moe_layer(*dict(good, x=torch.zeros(T, D, dtype=torch.bfloat16)).values())
     assert len(calls) == n
+
+
+def test_forward_mode_is_refused(monkeypatch):
+    from combine_moe_layout_05_amd import layer
+    calls = []
+    monkeypatch.setattr(layer, "_call", lambda *a: calls.append(a))
+    T, E, K, D, F = 4, 3, 2, 64, 32
+    i = _fake(T, K, dtype=torch.int32)
+    good = [_fake(T, D), _fake(T, K, dtype=torch.float32), i, _fake(E, 2 * F, D), _fake(E, D, F)]
+    with torch.autograd.forward_ad.dual_level():
+        for k in (0, 1, 3, 4):
+            args = list(good)
+            args[k] = torch.autograd.forward_ad.make_dual(good[k], torch.ones_like(good[k]))
+            with pytest.raises(NotImplementedError, match="moe_layer has no forward-mode"):
+                moe.moe_layer(*args)
+        assert not calls
+        assert moe.moe_layer(*good).shape == (T, D)
+    assert moe.moe_layer(*good).shape == (T, D) and len(calls) == 2

@@ -152,3 +152,18 @@ def test_both_forms_are_tested(lib):
     assert {(-(-K // 128) % 2, K % 128 != 0) for _, _, K, _, _ in many} == {
         (0, False), (0, True), (1, False), (1, True)}
     assert {-(-(c % 64) // 16) for counts, *_ in many for c in counts if c % 64} == {1, 2, 3, 4}
+
+
+def test_forward_mode_is_refused(monkeypatch):
+    from combine_moe_layout_05_amd import experts
+    calls = []
+    monkeypatch.setattr(experts, "_call", lambda *a: calls.append(a))
+    x = _fake(2, 32, dtype=torch.float32)
+    with torch.autograd.forward_ad.dual_level():
+        dual = torch.autograd.forward_ad.make_dual(x, torch.ones_like(x))
+        with pytest.raises(NotImplementedError, match="quantize_mxfp4 has no forward-mode"):
+            moe.quantize_mxfp4(dual)
+        assert not calls
+        moe.quantize_mxfp4(x)
+    moe.quantize_mxfp4(x)
+    assert len(calls) == 2

@@ -125,3 +125,16 @@ def test_forward_mode_is_refused(fake):
         with pytest.raises(NotImplementedError, match="forward-mode"):
             moe.route_topk(l, 2)
     assert not calls
+
+
+def test_forward_mode_of_the_backward_call_is_refused(fake):
+    make, calls = fake
+    l, grad, ids = make(4, 16), make(4, 2), make(4, 2, dtype=torch.int32)
+    dual = lambda t: torch.autograd.forward_ad.make_dual(t, torch.ones_like(t))
+    with torch.autograd.forward_ad.dual_level():
+        for args in ((dual(grad), l, ids), (grad, dual(l), ids)):
+            with pytest.raises(NotImplementedError, match="route_topk_backward has no forward"):
+                moe.route_topk_backward(*args)
+        assert not calls
+        assert moe.route_topk_backward(grad, l, ids).shape == (4, 16)
+    assert len(calls) == 1
