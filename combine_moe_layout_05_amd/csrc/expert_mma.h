@@ -502,6 +502,18 @@ __device__ __forceinline__ v2i pack_bf16x4(f32x4 v) {
     return __builtin_bit_cast(v2i, __builtin_convertvector(v, bf16x4));
 }
 
+// A register of which lane group g holds value g of the 16 lanes' to four
+// registers that hold value 0, 1, 2 and 3 in all groups.
+__device__ __forceinline__ void spread(uint32_t v, uint32_t (&d)[4]) {
+    const auto half = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    const auto lo = __builtin_amdgcn_permlane16_swap(half[0], half[0], false, false);
+    const auto hi = __builtin_amdgcn_permlane16_swap(half[1], half[1], false, false);
+    d[0] = lo[0];
+    d[1] = lo[1];
+    d[2] = hi[0];
+    d[3] = hi[1];
+}
+
 // Four bf16 of block a and of the next block per lane (lane group g holds
 // elements 4g .. 4g + 3 of each, of one row), exchanged between groups 0 and 1
 // and between 2 and 3 so that every lane holds eight neighbours: elements

@@ -42,18 +42,6 @@ __device__ __forceinline__ v4i by_groups(v4i q) {
                static_cast<int32_t>(hi[0]), static_cast<int32_t>(hi[1])};
 }
 
-// A register of which lane group g holds value g of the 16 lanes' to four
-// registers that hold value 0, 1, 2 and 3 in all groups.
-__device__ __forceinline__ void spread(uint32_t v, uint32_t (&d)[4]) {
-    const auto half = __builtin_amdgcn_permlane32_swap(v, v, false, false);
-    const auto lo = __builtin_amdgcn_permlane16_swap(half[0], half[0], false, false);
-    const auto hi = __builtin_amdgcn_permlane16_swap(half[1], half[1], false, false);
-    d[0] = lo[0];
-    d[1] = lo[1];
-    d[2] = hi[0];
-    d[3] = hi[1];
-}
-
 // ---- Many rows per expert -------------------------------------------------
 //
 // A wavefront keeps 64 features' weights to itself, straight from memory into
@@ -477,7 +465,8 @@ int64_t tile_features(bool gated, int32_t feats) {
     return (int64_t(feats) + per - 1) / per;
 }
 int64_t tiles_of(bool gated, int32_t E, int64_t max_rows, int32_t feats, int rows) {
-    return tile_features(gated, feats) * ((max_rows + rows - 1) / rows + (max_rows < E ? max_rows : E));
+    return tile_features(gated, feats) *
+           ((max_rows + rows - 1) / rows + (max_rows < E ? max_rows : E));
 }
 int tile_rows(const ExpertMx4Args& a) {
     return expert_mx4_tile_rows(a.gated, a.E, a.max_rows, a.feats);
@@ -545,13 +534,14 @@ hipError_t launch_expert_mx4(const ExpertMx4Args& a, hipStream_t stream) {
     auto kernel = tile_rows(a) == 128
                       ? (a.gated ? expert_mx4_kernel<true, 128> : expert_mx4_kernel<false, 128>)
                       : (a.gated ? expert_mx4_kernel<true, 64> : expert_mx4_kernel<false, 64>);
-    return launch(kernel, tile_workgroups(a), kWaves * 64, tile_features(a.gated, a.feats), tile_chunk(a),
-                  a, stream);
+    return launch(kernel, tile_workgroups(a), kWaves * 64, tile_features(a.gated, a.feats),
+                  tile_chunk(a), a, stream);
 }
 
 hipError_t launch_expert_mx4_stream(const ExpertMx4Args& a, hipStream_t stream) {
     return launch(a.gated ? expert_mx4_stream_kernel<true> : expert_mx4_stream_kernel<false>,
-                  stream_workgroups(a), kStreamWaves * 64, stream_features(a), kStreamChunk, a, stream);
+                  stream_workgroups(a), kStreamWaves * 64, stream_features(a), kStreamChunk, a,
+                  stream);
 }
 
 }  // namespace moe

@@ -53,17 +53,6 @@ struct Weights<false> {
     v4i q[2];
     __device__ bf16x8 frag(int s, uint32_t) const { return __builtin_bit_cast(bf16x8, q[s]); }
 };
-// A register of which lane group g holds value g of the 16 lanes' to four
-// registers that hold value 0, 1, 2 and 3 in all groups.
-__device__ __forceinline__ void spread(uint32_t v, uint32_t (&d)[4]) {
-    const auto half = __builtin_amdgcn_permlane32_swap(v, v, false, false);
-    const auto lo = __builtin_amdgcn_permlane16_swap(half[0], half[0], false, false);
-    const auto hi = __builtin_amdgcn_permlane16_swap(half[1], half[1], false, false);
-    d[0] = lo[0];
-    d[1] = lo[1];
-    d[2] = hi[0];
-    d[3] = hi[1];
-}
 template <bool FOUR>
 struct Step {
     static constexpr int kElems = FOUR ? kMxfp4Step : 64;
@@ -502,8 +491,8 @@ void few_tokens_down_kernel(const char* __restrict__ h, const int32_t* __restric
                     reform(from);
 #pragma unroll
                     for (int j = 0; j < R::kLoads; ++j)
-                        d.x[b][j] = *reinterpret_cast<const v4i*>(hb + (int64_t(t) * pitch + j * P * 128) +
-                                                                  from);
+                        d.x[b][j] = *reinterpret_cast<const v4i*>(
+                            hb + (int64_t(t) * pitch + j * P * 128) + from);
                 }
                 __builtin_amdgcn_sched_barrier(0);
             };
@@ -653,9 +642,10 @@ hipError_t launch(const LayerArgs& a, hipStream_t stream) {
         columns = 32;
     }
     hipLaunchKernelGGL(down, dim3(static_cast<uint32_t>((a.D + columns - 1) / columns)),
-                       dim3(kDownWaves * 64), slots * most * 4 * columns, stream, static_cast<const char*>(a.workspace), a.ids,
-                       a.scores, a.T, a.K, a.E, w2, w2 + mxfp4_tiles(a.E, a.D, a.F) * 1024, a.D,
-                       a.F, most, static_cast<__bf16*>(a.y));
+                       dim3(kDownWaves * 64), slots * most * 4 * columns, stream,
+                       static_cast<const char*>(a.workspace), a.ids, a.scores, a.T, a.K, a.E, w2,
+                       w2 + mxfp4_tiles(a.E, a.D, a.F) * 1024, a.D, a.F, most,
+                       static_cast<__bf16*>(a.y));
     return hipGetLastError();
 }
 

@@ -323,8 +323,6 @@ __device__ __forceinline__ float sigmoid_of(float l) {
     return __builtin_amdgcn_rcpf(1.0f + exp_f32(-l));
 }
 
-// Lanes D, D + 1, ... before this one, in a circle, whose group goes before this
-// lane's: a larger value, or the same and a lower index.
 template <int N>
 __device__ __forceinline__ double ror(double v) {
     typedef int32_t two __attribute__((ext_vector_type(2)));
@@ -333,6 +331,8 @@ __device__ __forceinline__ double ror(double v) {
         double, two{__builtin_amdgcn_mov_dpp(w[0], 0x120 + N, 0xF, 0xF, true),
                     __builtin_amdgcn_mov_dpp(w[1], 0x120 + N, 0xF, 0xF, true)});
 }
+// Lanes D, D + 1, ... before this one, in a circle, whose group goes before this
+// lane's: a larger value, or the same and a lower index.
 template <int D, class V>
 __device__ __forceinline__ int lanes_ahead(V value, int j, int span) {
     if constexpr (D == kLanes) {
@@ -884,7 +884,7 @@ void route_grad_lanes_kernel(const L* __restrict__ logits, const int32_t* __rest
     }
 }
 
-// A wavefront per workgroup until there is one for every CU.
+// A wavefront per workgroup until there is one for every SIMD.
 int lane_waves(int32_t T) { return T <= 4 * 1024 ? 1 : kWaves; }
 int lane_values(int32_t E) {
     return E <= kLanes * 2 ? 2 : E <= kLanes * 4 ? 4 : E <= kLanes * 8 ? 8 : 16;
@@ -967,8 +967,8 @@ hipError_t route_grad(const RouteGradArgs& a, hipStream_t stream) {
     const uint32_t waves = token_waves(a.T);
     hipLaunchKernelGGL((route_grad_kernel<L>),
                        dim3((static_cast<uint32_t>(a.T) + waves - 1) / waves), dim3(waves * 64), 0,
-                       stream, static_cast<const L*>(a.logits), a.ids, a.grad, a.T, a.E, a.K, a.sigmoid, a.renormalize, a.scale,
-                       static_cast<L*>(a.grad_logits));
+                       stream, static_cast<const L*>(a.logits), a.ids, a.grad, a.T, a.E, a.K,
+                       a.sigmoid, a.renormalize, a.scale, static_cast<L*>(a.grad_logits));
     return hipGetLastError();
 }
 

@@ -136,9 +136,10 @@ def gated_grouped_gemm(x_expert: Union[torch.Tensor, Mxfp4Rows],
     x_expert bf16 [R, k_in]; weights bf16 [E, 2 n_hidden, k_in], the gate's
     rows first, or the Mxfp4ExpertWeights of such rows (n_hidden a multiple of
     16), which x_expert in 4 bits (quantize_mxfp4) needs; offsets int32 [E+1];
-    out bf16 [R, n_hidden]. activation "silu" or "gelu" (tanh form). pre, fp32 [R, 2 n_hidden], receives the projections
-    [g | u] of the segments' rows for the backward (bf16 weights only). Not
-    differentiable by itself; see expert_ffn."""
+    out bf16 [R, n_hidden]. activation "silu" or "gelu" (tanh form). pre, fp32
+    [R, 2 n_hidden], receives the projections [g | u] of the segments' rows for
+    the backward (bf16 weights only). Not differentiable by itself; see
+    expert_ffn."""
     act = _activation(activation)
     if isinstance(x_expert, Mxfp4Rows):
         dev = _check_mxfp4_rows(x_expert, weights, offsets)
