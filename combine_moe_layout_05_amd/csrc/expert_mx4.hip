@@ -45,17 +45,22 @@ __device__ __forceinline__ v4i by_groups(v4i q) {
 // ---- Many rows per expert -------------------------------------------------
 //
 // A wavefront keeps 64 features' weights to itself, straight from memory into
-// registers, a step of 256 elements ahead; the rows, which the workgroup's four
-// wavefronts share, go through LDS, and so do their scales, all of a tile's at its
-// start. What bounds it is the number of load instructions: a CU takes some 30
-// cycles for each, whatever it brings, while 16 products of 16 cycles use up the
-// four loads of weights they need.
+// registers; the rows, which the workgroup's four wavefronts share, go through LDS,
+// and so do their scales, all of a tile's at its start.
 //
-// Measured on MI355X, 256 experts of 7168 -> 2 x 2048: 32768 tokens x 8 rows 4.35 ms
-// (15.4 TFLOP, 3.5 PFLOP/s; the matrix cores busy 46 % at a clock held near 1.9 GHz),
+// What bounds it where rows are many: the waits of a step. The branch between a
+// step's two halves ends a block of code, and the compiler moves the first half's
+// products past it: as built, all 64 products of a wavefront's step stand behind the
+// wait for the second half's weights, which has nothing beside it. That wait counts
+// the row loads of step t + 2 as well, which went out just before, so their latency
+// lies open in every step and the third stage hides nothing; and both halves'
+// operands are live together (246 registers at 128 rows, 160 at 64).
+//
+// Measured on MI355X, 256 experts of 7168 -> 2 x 2048: 32768 tokens x 8 rows 4.38 ms
+// (15.4 TFLOP, 3.5 PFLOP/s; the matrix cores busy 45 % at a clock held near 1.9 GHz),
 // 4096 tokens x 8 skewed 0.97 ms (4.25 GB, 4.4 TB/s). A version of the former that took
 // 4.5 ms took 3.2 without its loads, 3.6 without the weights', 4.0 without the rows',
-// 4.1 without the exchange of dwords: no single one of them holds it.
+// 4.1 without the exchange of dwords: what those cost beside these waits.
 constexpr int kWaves = 4;               // along the features
 constexpr int kStages = 3;              // 256-element steps of rows in LDS
 constexpr int kBand = 8;
@@ -247,8 +252,8 @@ void expert_mx4_kernel(const char* __restrict__ rows, const uint8_t* __restrict_
             const v4i* buf = lds + stage * Rows::kChunks;
             order(lo, sc);
             __builtin_amdgcn_sched_barrier(0);
-            // Behind the first use of this step's registers: what waits for
-            // them must not wait for these loads.
+            // Behind the first use of this step's registers: the wait for the first
+            // half does not wait for these loads. The one for the second half does.
             if (t + 2 < steps) issue_rows(t + 2, free);
             multiply(lo, sc, buf, std::integral_constant<int, 2 * kOdd>{});
             __builtin_amdgcn_sched_barrier(0);
@@ -256,7 +261,8 @@ void expert_mx4_kernel(const char* __restrict__ rows, const uint8_t* __restrict_
             __builtin_amdgcn_sched_barrier(0);
             order(hi, sc);
             if (2 * t + 1 >= halves) {
-                // A sum that ends in the first half.
+                // A sum that ends in the first half. The first half's products are
+                // placed behind this branch.
 #pragma unroll
                 for (int a = 0; a < kBlocks; ++a) hi.q[a] = v4i{0, 0, 0, 0};
             }

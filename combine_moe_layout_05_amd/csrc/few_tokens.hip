@@ -24,9 +24,11 @@
 // also the load instructions, of which a CU takes one in some 30 cycles. Measured on
 // MI355X, 256 experts of 7168 -> 2048, 8 per token, us for both kernels: one token 127
 // (705 MB, 5.5 TB/s), in 4 bits 40 (187 MB, 4.7 TB/s), of which the start and end of
-// the two launches are some 12; 16 tokens 1548 and 356. Where an expert has several
-// slots the separate calls read its weights fewer times: 64 tokens on 8 experts of
-// 4096 -> 4096 take 230 us here and 162 there.
+// the two launches are some 12; 16 tokens 1512 and 375. Where an expert has several
+// slots the separate calls read its weights fewer times: with these experts they are
+// level at 4 tokens in bf16 (455 us) and ahead from 16 on (1457), in 4 bits ahead at 64
+// (796 against 818) and not at 32 (598 against 587); 64 tokens x 2 on 8 experts of 4096
+// -> 4096 take 227 us here and 163 there, in 4 bits 109 and 70.
 #include "expert_kernels.h"
 #include "expert_mma.h"
 #include "expert_mxfp4.h"

@@ -17,10 +17,12 @@
 // does not clear. Else one wavefront per token; lane j holds experts j, j + 64, ...
 //
 // Bound: for a few tokens a launch, its loads and the chain of the selection (one
-// token of 256 experts, 8 groups 4.3 us); for many the vector instructions of the
+// token of 256 experts, 8 groups 4.4 us); for many the vector instructions of the
 // selection, not the bytes. Measured on MI355X, 32768 tokens of 256 experts, fp32, 8
-// each: softmax 11.3 us (35.7 MB, 3.2 TB/s), sigmoid with bias 14.5, in 8 groups 17.4
-// (a wavefront per token 178), bf16 sigmoid in groups without a bias 14.0. One token of
+// each: softmax 11.5 us (35.7 MB, 3.1 TB/s), sigmoid with bias 14.1, in 8 groups 17.0
+// (a wavefront per token 178), in groups without a bias 14.0. A wavefront per token,
+// 8192 tokens of 512 experts, 8 each: softmax 15.7, sigmoid 13.5, with bias 24, in 8
+// groups 46 and without a bias 40; the gradient 17.2. One token of
 // the slow form at the end of a launch costs some 5 us: before groups near the last kept
 // and an expert near the last chosen were settled in their lanes, the latter two took
 // 18.8 and 22.
@@ -791,7 +793,7 @@ void route_grad_kernel(const L* __restrict__ logits, const int32_t* __restrict__
 
 // The same for up to 256 experts, 16 lanes per token as in the choice; lane j also
 // holds slot j. Bound: the launch; 8191 tokens of 128 experts, 8 each, bf16, softmax
-// renormalized 4.2 us on MI355X.
+// renormalized 4.4 us on MI355X.
 template <int VALS, class L>
 __global__ __launch_bounds__(kWaves * 64)
 void route_grad_lanes_kernel(const L* __restrict__ logits, const int32_t* __restrict__ ids,

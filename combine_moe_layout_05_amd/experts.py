@@ -111,7 +111,8 @@ def quantize_mxfp4(x: torch.Tensor) -> Mxfp4Rows:
 
 def dequantize_mxfp4(rows: Mxfp4Rows, dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
     """The numbers that rows stand for (moe_dequantize_mxfp4), fp32 or bf16
-    [..., k]; exact in both."""
+    [..., k], exact in both but for those past their range, which become
+    infinities (scale bytes 253 and 254)."""
     if dtype not in _DTYPES:
         raise TypeError(f"dtype must be one of {list(_DTYPES)}, got {dtype}")
     dev = rows.values.device
